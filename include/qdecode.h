@@ -378,6 +378,101 @@ qd_status qd_embed(qd_fmt fmt, const void* E, int64_t vocab, int64_t dim, const 
                    float* x, qd_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* Verification of a tree of drafted tokens (no counterpart on the pages: the   */
+/* decode step's operations for many drafted tokens in one pass).  A draft      */
+/* proposes for each sequence a tree of up to QD_MAX_TREE tokens; node 0 is the */
+/* last token sampled (its K and V are not cached yet), every other node        */
+/* continues its parent, and a parent's index is smaller than its children's.   */
+/* Per layer, qd_tree_append rotates the nodes' q and k and stores k and v in   */
+/* the layer's draft buffers, and qd_tree_attn attends; after the head,         */
+/* qd_token_logprobs scores the drafted tokens and names the greedy ones, and   */
+/* qd_tree_commit accepts a path and copies its rows of every layer into the    */
+/* caches.  Draft buffers: f32 or (kv_f16 = 1) binary16                         */
+/* [batch][n_kv_heads][n_nodes][head_dim], of the caches' type; caches as in    */
+/* qd_kv_append, of either type.  The cache itself holds accepted rows only, so */
+/* a rejected draft leaves no trace in it.                                      */
+/* n_valid (device int32 [batch], may be NULL: n_nodes each): the number of     */
+/* nodes of each sequence; a value outside [0, n_nodes] is taken as the nearer  */
+/* of the two.  Rows of nodes behind it are not read, and not written either.   */
+/* No input may overlap an output.                                              */
+/* ------------------------------------------------------------------------- */
+#define QD_MAX_TREE 64
+
+/* Host: ancestor masks and depths of one tree.  parent_host[i] (i >= 1) is the index of
+ * node i's parent, 0 <= parent_host[i] < i (else QD_ERR_INVALID_ARG); parent_host[0] is
+ * not read.  mask_host[i]: bit j set when node j is node i or one of its ancestors;
+ * depth_host[i]: the number of its ancestors.  1 <= n_nodes <= QD_MAX_TREE. */
+qd_status qd_tree_plan(const int32_t* parent_host, int n_nodes, uint64_t* mask_host, int32_t* depth_host);
+
+/* Node i of sequence b, at rope position p = pos[b] + depth[b][i]: q rotated by p's angles
+ * into q_out (f32 [batch][n_nodes][n_heads][head_dim]), k rotated and v into draft slot i
+ * (rounded once to binary16 with kv_f16).  q, k, v: f32 rows of n_heads (n_kv_heads) heads
+ * at b*batch_stride + i*node_stride (e.g. three parts of one fused projection); depth:
+ * device int32 [batch][n_nodes]; cos_sin as in qd_rope.  head_dim a multiple of 8, at most
+ * 1024; strides multiples of 4.  A node whose p is outside [0, max_ctx), and every node of
+ * a sequence whose pos[b] is, writes nothing. */
+qd_status qd_tree_append(const float* q, const float* k, const float* v, int64_t batch_stride, int64_t node_stride,
+                         float* q_out, void* k_draft, void* v_draft, int kv_f16, int n_heads, int n_kv_heads,
+                         int head_dim, const int32_t* pos, const int32_t* depth, const int32_t* n_valid, int n_nodes,
+                         qd_rope_pairing pairing, const float* cos_sin, int max_ctx, int batch, qd_stream_t stream);
+
+/* Attention of the tree (the sums of qd_gqa_decode_attn over another set of positions):
+ * node i of sequence b sees cached positions 0..pos[b]-1 and the draft slots j whose bit j
+ * of mask[b][i] is set (device uint64 [batch][n_nodes], 8-byte aligned; bits at or above the
+ * sequence's n_valid are ignored).  q: f32 [n_nodes][n_heads][head_dim] per sequence, at
+ * b*q_batch_stride (a multiple of 4); out: f32 [batch][n_nodes][n_heads][head_dim].
+ * head_dim 64; n_heads % n_kv_heads == 0, group size <= 8.  A node that sees nothing gives
+ * zeros, as do the nodes of a sequence with pos[b] outside [0, max_ctx].  A non-finite q
+ * gives NaN in its own row alone, and what a slot holds that a node does not see, NaN and
+ * infinities included, does not reach that node's row.  The result does not depend on what
+ * the caches hold at or behind pos[b].  Results are the same bits on every run.
+ * workspace (device): qd_tree_attn_workspace bytes (0: a shape the call does not take); two
+ * calls that can run at the same time need one each. */
+size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch);
+qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cache, const void* v_cache,
+                       const void* k_draft, const void* v_draft, int kv_f16, float* out, int n_heads, int n_kv_heads,
+                       int head_dim, const int32_t* pos, const uint64_t* mask, const int32_t* n_valid, int n_nodes,
+                       int max_ctx, int batch, void* workspace, size_t workspace_bytes, qd_stream_t stream);
+
+/* Log probabilities under each row's softmax.  logits: f32 rows of vocab values, row r at
+ * r*row_stride (any stride >= vocab; 1 <= vocab <= QD_MAX_VOCAB; 1 <= rows <=
+ * QD_MAX_GEMM_TOKENS); -INFINITY rules a token out.
+ *  - logprob[r][t] = log p(tokens[r][t]) for t < n_tokens (device, [rows][n_tokens],
+ *    0 <= n_tokens <= QD_MAX_TREE); -INFINITY for an id outside [0, vocab) (padding).
+ *  - entropy[r] = -sum p log p in nats (may be NULL).
+ *  - top_idx, top_logprob [rows][top_k], 0 <= top_k <= min(QD_MAX_TOP, vocab): the largest
+ *    logits in falling order, the lower index first among equal ones.
+ * Sums are f32.  A row that holds a NaN, or whose largest value is infinite, gives NaN log
+ * probabilities (of ids inside the vocabulary) and entropy; its top_idx still follow the
+ * order, NaN behind every number.  Pointers of outputs that are not asked for (n_tokens 0,
+ * top_k 0) may be NULL. */
+#define QD_MAX_TOP 32
+#define QD_MAX_VOCAB (1 << 24)
+qd_status qd_token_logprobs(const float* logits, int64_t row_stride, int64_t vocab, int rows, const int32_t* tokens,
+                            int n_tokens, float* logprob, float* entropy, int top_k, int32_t* top_idx,
+                            float* top_logprob, qd_stream_t stream);
+
+/* Accept a path of each sequence's tree and copy its rows into the caches.  tokens, parent:
+ * device int32 [batch][n_nodes]; chosen: the token that the model chose after each node
+ * (greedy or sampled), that of node i of sequence b at (b*n_nodes + i)*chosen_stride, so the
+ * top_idx of qd_token_logprobs can be passed with chosen_stride = top_k.  The path starts at
+ * node 0 and goes on to the first node c behind the current one with parent c = the current
+ * node and tokens[c] = its chosen token, until there is none or the cache is full
+ * (pos[b] + length = max_ctx).  Its node i goes to cache position pos[b] + i, in each of
+ * `layers` layers: draft buffers [layers][batch][n_kv_heads][n_nodes][head_dim], caches
+ * [batch][n_kv_heads][max_ctx][head_dim] with layer l at l*cache_layer_stride elements.
+ * Outputs (device int32): path [batch][n_nodes] (-1 behind its end), n_accept [batch] (its
+ * length), next_token [batch] (the token chosen after its last node: the next tree's node 0;
+ * -1 for an empty path), pos_out [batch] = pos[b] + n_accept[b] (not pos itself).  A
+ * sequence with n_valid 0 or pos[b] outside [0, max_ctx] has an empty path.  head_dim a
+ * multiple of 8, at most 1024. */
+qd_status qd_tree_commit(const int32_t* tokens, const int32_t* parent, const int32_t* chosen, int64_t chosen_stride,
+                         const int32_t* n_valid, int n_nodes, const void* k_draft, const void* v_draft, void* k_cache,
+                         void* v_cache, int kv_f16, int layers, int64_t cache_layer_stride, int n_kv_heads,
+                         int head_dim, const int32_t* pos, int max_ctx, int batch, int32_t* path, int32_t* n_accept,
+                         int32_t* next_token, int32_t* pos_out, qd_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Model and decode step ([llmoxide] 7, 11, 12; [dasLLAMA] 8.7.1.6 forward,    */
 /* 8.7.1.7; [go-llm] CPU.Forward / Reset / Pos, "Design points").             */
 /* ------------------------------------------------------------------------- */

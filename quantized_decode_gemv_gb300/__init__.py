@@ -29,7 +29,8 @@ EXPORTS = ["qd_status_str", "qd_abi_version", "qd_f16_to_f32", "qd_bf16_to_f32",
            "qd_quantize_q8", "qd_q_gemv_q8", "qd_rmsnorm",
            "qd_rope_table", "qd_rope", "qd_kv_append", "qd_gqa_decode_attn_workspace", "qd_gqa_decode_attn",
            "qd_gqa_decode_attn_noalloc",
-           "qd_swiglu", "qd_argmax", "qd_embed", "qd_model_weight_bytes", "qd_model_state_bytes",
+           "qd_swiglu", "qd_argmax", "qd_embed", "qd_tree_plan", "qd_tree_append", "qd_tree_attn_workspace",
+           "qd_tree_attn", "qd_token_logprobs", "qd_tree_commit", "qd_model_weight_bytes", "qd_model_state_bytes",
            "qd_model_create", "qd_model_destroy", "qd_decode_step", "qd_prefill_workspace", "qd_prefill",
            "qd_model_reset", "qd_model_set_pos",
            "qd_model_pos", "qd_model_kv_cache", "qd_model_act_q8_buffer", "qd_model_check",
@@ -37,6 +38,8 @@ EXPORTS = ["qd_status_str", "qd_abi_version", "qd_f16_to_f32", "qd_bf16_to_f32",
            "qd_model_cluster_available"]
 STEP_AUTO, STEP_KERNEL_CHAIN, STEP_CLUSTER = 0, 1, 2
 PREFILL_EXACT = 1
+MAX_TREE = 64
+MAX_TOP = 32
 
 
 class QDError(RuntimeError):
@@ -102,6 +105,13 @@ def load():
         "qd_swiglu": ([p, p, p, i64, i32, p], i32),
         "qd_argmax": ([p, i64, i32, p, p], i32),
         "qd_embed": ([i32, p, i64, i64, p, i32, p, p], i32),
+        "qd_tree_plan": ([p, i32, p, p], i32),
+        "qd_tree_append": ([p, p, p, i64, i64, p, p, p, i32, i32, i32, i32, p, p, p, i32, i32, p, i32, i32, p], i32),
+        "qd_tree_attn_workspace": ([i32] * 6, sz),
+        "qd_tree_attn": ([p, i64, p, p, p, p, i32, p, i32, i32, i32, p, p, p, i32, i32, i32, p, sz, p], i32),
+        "qd_token_logprobs": ([p, i64, i64, i32, p, i32, p, p, i32, p, p, p], i32),
+        "qd_tree_commit": ([p, p, p, i64, p, i32, p, p, p, p, i32, i32, i64, i32, i32, p, i32, i32, p, p, p, p, p],
+                           i32),
         "qd_model_weight_bytes": ([ctypes.POINTER(Config)], sz),
         "qd_model_state_bytes": ([ctypes.POINTER(Config)], sz),
         "qd_model_create": ([ctypes.POINTER(Config), p, p, sz, p, sz, p, ctypes.POINTER(p)], i32),
@@ -305,6 +315,116 @@ def argmax(logits, n, batch, out_idx, stream=None):
 def embed(fmt, E, vocab, dim, tokens, batch, x, stream=None):
     _check("qd_embed", load().qd_embed(FMT[fmt], _ptr(E), vocab, dim, _ptr(tokens), batch, _ptr(x),
                                        _stream(stream)))
+
+
+def _room(fn, name, t, dtypes, n, stepped=False):
+    """Pointer of t after a look at what only the tensor tells: its type, its device and that
+    n elements lie behind its pointer, so that a tensor too small is an error here and not a
+    read out of bounds on the device.  Only a `stepped` argument, whose strides the call is
+    given, may be a view with gaps.  Raw pointers and None pass as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} has type {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+    if not stepped and not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    have = t.numel() if not stepped else t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if have < n:
+        raise ValueError(f"{fn}: {name} holds {have} elements, the call takes {n}")
+    return t.data_ptr()
+
+
+def tree_plan(parent):
+    """Ancestor masks (int64 bit patterns) and depths (int32) of the tree parent[i], as CPU tensors."""
+    import torch
+
+    par = torch.as_tensor(parent, dtype=torch.int32, device="cpu").contiguous()
+    mask, depth = torch.empty(par.numel(), dtype=torch.int64), torch.empty(par.numel(), dtype=torch.int32)
+    _check("qd_tree_plan", load().qd_tree_plan(par.data_ptr(), par.numel(), mask.data_ptr(), depth.data_ptr()))
+    return mask, depth
+
+
+def tree_append(q, k, v, batch_stride, node_stride, q_out, k_draft, v_draft, n_heads, n_kv_heads, head_dim, pos, depth,
+                n_valid, n_nodes, pairing, cos_sin, max_ctx, batch, kv_f16=False, stream=None):
+    """Rotated queries into q_out, rotated keys and values into the draft buffers (see qdecode.h)."""
+    import torch
+
+    fn, f32, i32 = "qd_tree_append", (torch.float32,), (torch.int32,)
+    kv = (torch.float16,) if kv_f16 else f32
+    last = (batch - 1) * batch_stride + (n_nodes - 1) * node_stride
+    qn, kn = n_heads * head_dim, n_kv_heads * head_dim
+    _check(fn, load().qd_tree_append(
+        _room(fn, "q", q, f32, last + qn, True), _room(fn, "k", k, f32, last + kn, True),
+        _room(fn, "v", v, f32, last + kn, True), batch_stride, node_stride,
+        _room(fn, "q_out", q_out, f32, batch * n_nodes * qn), _room(fn, "k_draft", k_draft, kv, batch * n_nodes * kn),
+        _room(fn, "v_draft", v_draft, kv, batch * n_nodes * kn), 1 if kv_f16 else 0, n_heads, n_kv_heads, head_dim,
+        _room(fn, "pos", pos, i32, batch), _room(fn, "depth", depth, i32, batch * n_nodes),
+        _room(fn, "n_valid", n_valid, i32, batch), n_nodes, PAIRING[pairing],
+        _room(fn, "cos_sin", cos_sin, f32, max_ctx * head_dim), max_ctx, batch, _stream(stream)))
+
+
+def tree_attn_workspace(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch) -> int:
+    return int(load().qd_tree_attn_workspace(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch))
+
+
+def tree_attn(q, q_batch_stride, k_cache, v_cache, k_draft, v_draft, out, n_heads, n_kv_heads, head_dim, pos, mask,
+              n_valid, n_nodes, max_ctx, batch, workspace, workspace_bytes=None, kv_f16=False, stream=None):
+    """Attention of the tree over the cache and its own drafts (see qdecode.h)."""
+    import torch
+
+    fn, f32, i32 = "qd_tree_attn", (torch.float32,), (torch.int32,)
+    kv = (torch.float16,) if kv_f16 else f32
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    qn, kn, cn = n_nodes * n_heads * head_dim, batch * n_nodes * n_kv_heads * head_dim, \
+        batch * n_kv_heads * max_ctx * head_dim
+    _check(fn, load().qd_tree_attn(
+        _room(fn, "q", q, f32, (batch - 1) * q_batch_stride + qn, True), q_batch_stride,
+        _room(fn, "k_cache", k_cache, kv, cn), _room(fn, "v_cache", v_cache, kv, cn),
+        _room(fn, "k_draft", k_draft, kv, kn), _room(fn, "v_draft", v_draft, kv, kn), 1 if kv_f16 else 0,
+        _room(fn, "out", out, f32, batch * qn), n_heads, n_kv_heads, head_dim, _room(fn, "pos", pos, i32, batch),
+        _room(fn, "mask", mask, (torch.int64, torch.uint64), batch * n_nodes),
+        _room(fn, "n_valid", n_valid, i32, batch), n_nodes, max_ctx, batch,
+        _room(fn, "workspace", workspace, (torch.uint8,), workspace_bytes), workspace_bytes, _stream(stream)))
+
+
+def token_logprobs(logits, row_stride, vocab, rows, tokens, n_tokens, logprob, entropy, top_k, top_idx, top_logprob,
+                   stream=None):
+    """Log probabilities of tokens, entropy and the top alternatives of each row of logits (see qdecode.h)."""
+    import torch
+
+    fn, f32, i32 = "qd_token_logprobs", (torch.float32,), (torch.int32,)
+    _check(fn, load().qd_token_logprobs(
+        _room(fn, "logits", logits, f32, (rows - 1) * row_stride + vocab, True), row_stride, vocab, rows,
+        _room(fn, "tokens", tokens, i32, rows * n_tokens), n_tokens,
+        _room(fn, "logprob", logprob, f32, rows * n_tokens), _room(fn, "entropy", entropy, f32, rows), top_k,
+        _room(fn, "top_idx", top_idx, i32, rows * top_k), _room(fn, "top_logprob", top_logprob, f32, rows * top_k),
+        _stream(stream)))
+
+
+def tree_commit(tokens, parent, chosen, chosen_stride, n_valid, n_nodes, k_draft, v_draft, k_cache, v_cache, layers,
+                cache_layer_stride, n_kv_heads, head_dim, pos, max_ctx, batch, path, n_accept, next_token, pos_out,
+                kv_f16=False, stream=None):
+    """Accept a path of each tree and copy its rows of every layer into the caches (see qdecode.h)."""
+    import torch
+
+    fn, i32 = "qd_tree_commit", (torch.int32,)
+    kv = (torch.float16,) if kv_f16 else (torch.float32,)
+    nodes, dn = batch * n_nodes, layers * batch * n_nodes * n_kv_heads * head_dim
+    cn = (layers - 1) * cache_layer_stride + batch * n_kv_heads * max_ctx * head_dim
+    _check(fn, load().qd_tree_commit(
+        _room(fn, "tokens", tokens, i32, nodes), _room(fn, "parent", parent, i32, nodes),
+        _room(fn, "chosen", chosen, i32, (nodes - 1) * chosen_stride + 1, True), chosen_stride,
+        _room(fn, "n_valid", n_valid, i32, batch), n_nodes, _room(fn, "k_draft", k_draft, kv, dn),
+        _room(fn, "v_draft", v_draft, kv, dn), _room(fn, "k_cache", k_cache, kv, cn, True),
+        _room(fn, "v_cache", v_cache, kv, cn, True), 1 if kv_f16 else 0, layers, cache_layer_stride, n_kv_heads,
+        head_dim, _room(fn, "pos", pos, i32, batch), max_ctx, batch, _room(fn, "path", path, i32, nodes),
+        _room(fn, "n_accept", n_accept, i32, batch), _room(fn, "next_token", next_token, i32, batch),
+        _room(fn, "pos_out", pos_out, i32, batch), _stream(stream)))
 
 
 def make_config(cfg: dict, max_ctx: int, max_batch: int, tied: bool = True, kv_f16: bool | None = None,
