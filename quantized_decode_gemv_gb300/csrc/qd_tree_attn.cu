@@ -1,69 +1,780 @@
 // Attention of a tree of drafted tokens over the cache: node i of sequence b sees the pos[b]
 // cached positions and the draft slots j with bit j of its mask set,
 //   o = sum_p softmax_p(q . k_p / sqrt(head_dim)) v_p.
+//
+// The rows that share a kv head (nodes x query heads of the group) walk its positions together,
+// 64 at a time, with an online softmax: s = q k^T and o += p v as m16n8k16 binary16 matrix
+// products with f32 accumulators.  A binary16 operand alone is 2^-12 off, so what is f32 enters
+// as two binary16 parts (hi = rn(x), lo = rn(x - hi): 2^-22 of the operand's scale):
+//  - q, scaled by a power of two per row, in two parts;
+//  - the weights p = 2^(s - m + 12) in two parts (the 2^12 keeps the low part of small weights
+//    above binary16's subnormal step; it cancels in o / l);
+//  - a binary16 cache exactly; an f32 cache in two parts, k scaled by a power of two per
+//    position and v per group of positions, converted once per tile by the whole CTA.
+// So a tile costs 2 + 2 matrix products on a binary16 cache and 3 + 3 on an f32 one.  Scores,
+// running maxima, sums and o are f32.  The matrix unit cuts its f32 sums off instead of rounding
+// them, so a tile's products of the high parts start from zero, those with a low part have
+// accumulators of their own, and both are added to o with rounded f32 additions (one accumulator
+// through a whole walk of 4080 positions: 1.4e-6 relative error of o).
+//
+// Work: the walks of all (sequence, kv head, block of rows) are laid end to end in units of a
+// tile and cut evenly over the CTAs, whatever the lengths; a walk's start (its queries, its
+// result) counts as kStart units.  A CTA that holds a part of a walk writes (m, l, o) to the
+// workspace and a second kernel joins the parts in order.
+#include <algorithm>
+
 #include "qd_internal.cuh"
+#include "qd_tc.cuh"
 
 namespace qd {
 namespace {
 
 constexpr int kHd = 64;
+constexpr int kTile = 64;     // positions of a tile; the drafts (at most 64) are one tile
+constexpr int kThreads = 128;  // 4 warps: WM blocks of 16 rows x WN shares of the positions
+constexpr float kBias = 12.f;  // log2 of the weights' scale
+constexpr int kStart = 3;      // what the start of a walk costs, in tiles
+constexpr int kMinPer = 4;     // units of a CTA at least
+static_assert(QD_MAX_TREE <= kTile, "the drafts fit one tile");
 
-template <typename KV>
-__device__ __forceinline__ float2 load2(const KV* p);
-template <>
-__device__ __forceinline__ float2 load2<float>(const float* p) {
-  return *reinterpret_cast<const float2*>(p);
+struct TreeAttnArgs {
+  const float* q;
+  int64_t q_batch_stride;
+  const void *kc, *vc, *kd, *vd;
+  float* out;
+  int n_kv, group;
+  const int32_t* pos;
+  const uint64_t* mask;
+  const int32_t* n_valid;
+  int n_nodes, max_ctx, batch;
+  float* ws;
+};
+
+// Work of the sequences: nt tiles for each of n_kv * rb walks (0 when pos is out of range).
+struct Plan {
+  int off[QD_MAX_BATCH + 1];  // in units
+  int nt[QD_MAX_BATCH], rb[QD_MAX_BATCH], p0[QD_MAX_BATCH], cnt[QD_MAX_BATCH];
+};
+
+// Filled by one warp; `bm` rows to a block.
+__device__ __forceinline__ void make_plan(const TreeAttnArgs& a, int bm, Plan* p) {
+  const int b = threadIdx.x & 31;
+  int units = 0;
+  if (b < a.batch) {
+    const int cnt = a.n_valid ? min(max(a.n_valid[b], 0), a.n_nodes) : a.n_nodes;
+    const int p0 = a.pos[b];
+    const int rb = (cnt * a.group + bm - 1) / bm;
+    const int nt = p0 < 0 || p0 > a.max_ctx ? 0 : (p0 + kTile - 1) / kTile + 1;
+    p->cnt[b] = cnt;
+    p->p0[b] = p0;
+    p->rb[b] = rb;
+    p->nt[b] = nt;
+    units = nt ? (nt + kStart) * rb * a.n_kv : 0;
+  }
+  int sum = units;
+#pragma unroll
+  for (int o = 1; o < QD_MAX_BATCH; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (b >= o) sum += v;
+  }
+  if (b < QD_MAX_BATCH) p->off[b + 1] = sum;
+  if (b == 0) p->off[0] = 0;
 }
-template <>
-__device__ __forceinline__ float2 load2<__half>(const __half* p) {
-  return __half22float2(*reinterpret_cast<const __half2*>(p));
+__device__ __forceinline__ int units_per_cta(int total, int ctas) { return max((total + ctas - 1) / ctas, kMinPer); }
+
+// Floats of one partial: m and l of each row, then o.
+__host__ __device__ constexpr int part_floats(int bm) { return bm * (kHd + 2); }
+
+// ------------------------------------------------------------------ building blocks
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 16 bytes global -> shared, or 16 zero bytes
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// (x, y) -> two binary16 parts, hi = rn(x), lo = rn(x - hi)
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+// Exponent e of a largest magnitude (given by its bits), so that x 2^-e is below 4: finite
+// values only, an infinity or NaN keeps e = 126 and stays what it is.
+__device__ __forceinline__ int scale_exp(uint32_t abs_bits) { return min(max((int)(abs_bits >> 23) - 127, -100), 126); }
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Byte offset of 16-byte chunk c of row r in a tile of 64 rows of 64 binary16 values: chunks
+// permuted within a row so that 8 rows' same chunk (a matrix of ldmatrix) hits all banks.
+__device__ __forceinline__ uint32_t tile_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// A CTA's place in the units: the tile t of a walk (sequence, kv head, block of rows) and its unit.
+struct Cursor {
+  int b, h, r, t, u;
+};
+// The first tile at or behind unit u.
+__device__ __forceinline__ Cursor cursor_at(const Plan& p, int u) {
+  Cursor c;
+  c.b = 0;
+  while (u >= p.off[c.b + 1]) ++c.b;  // u < off[QD_MAX_BATCH]
+  const int len = p.nt[c.b] + kStart, in = u - p.off[c.b], walk = in / len;
+  c.t = max(in % len - kStart, 0);
+  c.u = p.off[c.b] + walk * len + kStart + c.t;
+  c.h = walk / p.rb[c.b];
+  c.r = walk % p.rb[c.b];
+  return c;
+}
+__device__ __forceinline__ void advance(const Plan& p, int n_kv, Cursor& c) {
+  ++c.u;
+  if (++c.t < p.nt[c.b]) return;
+  c.u += kStart;
+  c.t = 0;
+  if (++c.r < p.rb[c.b]) return;
+  c.r = 0;
+  if (++c.h < n_kv) return;
+  c.h = 0;
+  do ++c.b;
+  while (c.b < QD_MAX_BATCH - 1 && p.off[c.b] == p.off[c.b + 1]);
 }
 
-// One warp per (head, node, sequence); a lane holds dimensions 2 lane, 2 lane + 1.
-template <typename KV>
-__global__ void __launch_bounds__(32) k_tree_attn(const float* __restrict__ q, int64_t q_batch_stride,
-                                                  const KV* __restrict__ kc, const KV* __restrict__ vc,
-                                                  const KV* __restrict__ kd, const KV* __restrict__ vd,
-                                                  float* __restrict__ out, int n_kv, const int32_t* __restrict__ pos,
-                                                  const uint64_t* __restrict__ mask,
-                                                  const int32_t* __restrict__ n_valid, int n_nodes, int max_ctx) {
-  const int h = blockIdx.x, node = blockIdx.y, b = blockIdx.z, lane = threadIdx.x;
-  const int n_heads = gridDim.x, kvh = h / (n_heads / n_kv);
-  const int cnt = n_valid ? min(max(n_valid[b], 0), n_nodes) : n_nodes;
-  if (node >= cnt) return;
-  const int p0 = pos[b];
-  float2* dst = reinterpret_cast<float2*>(out + (((int64_t)b * n_nodes + node) * n_heads + h) * kHd) + lane;
-  if (p0 < 0 || p0 > max_ctx) {
+// Shared memory.  Binary16 cache: a ring of K and V tiles as they are.  f32 cache: a ring of
+// raw tiles, each chunk read back by the thread that copied it, and one converted tile.
+template <bool F16>
+struct Smem;
+template <>
+struct Smem<true> {
+  static constexpr int kStages = 3;
+  uint4 tile[kStages][2][kTile * 8];  // K, V
+  float merge[4][part_floats(16)];
+  unsigned long long bad;
+  Plan plan;
+};
+template <>
+struct Smem<false> {
+  static constexpr int kStages = 2;
+  float4 raw[kStages][2][kTile * 16];
+  union {
+    uint4 tile[4][kTile * 8];  // K hi, K lo, V hi, V lo
+    float merge[4][part_floats(16)];
+  };
+  float kscale[kTile], vscale[kTile];
+  unsigned long long bad;
+  Plan plan;
+};
+
+template <bool F16, int WM, int WN>
+__global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArgs a) {
+  using KV = typename std::conditional<F16, __half, float>::type;
+  using S = Smem<F16>;
+  constexpr int BM = 16 * WM;
+  constexpr int NP = kTile / WN;  // positions of a warp's share of a tile
+  constexpr int NT = NP / 8;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wm = warp % WM, wn = warp / WM;
+  const int qr = lane >> 2, qc = lane & 3;  // row and column pair of the lane in a fragment
+
+  pdl_trigger();
+  if (warp == 0) make_plan(a, BM, &sm.plan);
+  if (tid == 0) sm.bad = 0;
+  __syncthreads();
+  const int total = sm.plan.off[QD_MAX_BATCH];
+  const int per = units_per_cta(total, gridDim.x);
+  const int64_t first = (int64_t)blockIdx.x * per;
+  if (first >= total) return;
+  const int end = min((int)first + per, total);
+  Cursor cur = cursor_at(sm.plan, (int)first), pre = cur;
+
+  const KV* kc = static_cast<const KV*>(a.kc);
+  const KV* vc = static_cast<const KV*>(a.vc);
+  const KV* kd = static_cast<const KV*>(a.kd);
+  const KV* vd = static_cast<const KV*>(a.vd);
+
+  // copy the tile at `pre` into ring slot s and move on; rows behind its end become zeros
+  auto produce = [&](int s) {
+    if (pre.u < end) {
+      const int p0 = sm.plan.p0[pre.b];
+      const bool draft = pre.t == sm.plan.nt[pre.b] - 1;
+      const int64_t head = (int64_t)pre.b * a.n_kv + pre.h;
+      const int row0 = draft ? 0 : pre.t * kTile;
+      const int rows = draft ? sm.plan.cnt[pre.b] : min(kTile, p0 - row0);
+      const int64_t base = draft ? head * a.n_nodes * kHd : (head * a.max_ctx + row0) * kHd;
+      const KV* ks = (draft ? kd : kc) + base;
+      const KV* vs = (draft ? vd : vc) + base;
+      constexpr int kPer = F16 ? 8 : 16;           // 16-byte chunks of a row
+      constexpr int kIter = kTile * kPer / kThreads;
+      const int c = tid % kPer, r0 = tid / kPer;
+      uint32_t dk, dv;
+      if constexpr (F16) {
+        dk = tc::smem_u32(sm.tile[s][0]);
+        dv = tc::smem_u32(sm.tile[s][1]);
+      } else {
+        dk = tc::smem_u32(sm.raw[s][0]);
+        dv = tc::smem_u32(sm.raw[s][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int r = r0 + i * (kThreads / kPer);
+        const bool live = r < rows;
+        const int64_t src = live ? (int64_t)r * kHd + c * (16 / (int)sizeof(KV)) : 0;
+        const uint32_t off = F16 ? tile_off(r, c) : (uint32_t)(r * 256 + c * 16);
+        cp16(dk + off, ks + src, live);
+        cp16(dv + off, vs + src, live);
+      }
+      advance(sm.plan, a.n_kv, pre);
+    }
+    cp_commit();
+  };
+
+#pragma unroll
+  for (int s = 0; s < (F16 ? S::kStages - 1 : S::kStages); ++s) produce(s);
+
+  uint32_t qh[4][4], ql[4][4];
+  float o[8][4];
+  float m[2], l[2], rs[2];
+  uint64_t vis[2];
+  float vunit[2];     // o is in these units (f32 cache; powers of two)
+  int t_begin = -1;   // first tile of this CTA's part of the walk; -1: a new walk begins
+
+  for (int it = 0; cur.u < end; ++it) {
+    const int p0 = sm.plan.p0[cur.b], cnt = sm.plan.cnt[cur.b], nt = sm.plan.nt[cur.b];
+    const bool draft = cur.t == nt - 1;
+    const bool more = cur.u + 1 + (draft ? kStart : 0) < end;  // this CTA has another tile
+    const int rows = cnt * a.group;
+    if (t_begin < 0) {
+      t_begin = cur.t;
+      const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = cur.r * BM + wm * 16 + qr + 8 * i;
+        const int node = r / a.group, g = r % a.group;
+        const bool live = r < rows;
+        const float* src = a.q + (int64_t)cur.b * a.q_batch_stride +
+                           ((int64_t)node * a.n_kv * a.group + cur.h * a.group + g) * kHd;
+        float2 x[8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          x[c] = live ? __ldcg(reinterpret_cast<const float2*>(src + c * 8) + qc) : make_float2(0.f, 0.f);
+          x[c].x *= scale;
+          x[c].y *= scale;
+          mx = max(mx, max(abs_bits(x[c].x), abs_bits(x[c].y)));
+        }
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = scale_exp(mx);
+        rs[i] = pow2(e);
+        const float f = pow2(-e);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)  // columns 8c..8c+7: k step c / 2, its low or high half
+          split2(x[c].x * f, x[c].y * f, qh[c >> 1][i + 2 * (c & 1)], ql[c >> 1][i + 2 * (c & 1)]);
+        vis[i] = live ? a.mask[(int64_t)cur.b * a.n_nodes + node] : 0ull;
+        if (cnt < 64) vis[i] &= (1ull << cnt) - 1;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        vunit[i] = pow2(-100);
+      }
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    }
+
+    // ---- the tile arrives
+    uint32_t k_hi, k_lo = 0, v_hi, v_lo = 0;
+    if constexpr (F16) {
+      const int s = it % S::kStages;
+      cp_wait<S::kStages - 2>();
+      __syncthreads();
+      produce((it + S::kStages - 1) % S::kStages);
+      k_hi = tc::smem_u32(sm.tile[s][0]);
+      v_hi = tc::smem_u32(sm.tile[s][1]);
+      if (draft) {
+        // a value row with an infinity or NaN would reach every row of the product (0 times
+        // it is NaN): such rows are taken out here and added below where they are seen
+        __half* vt = reinterpret_cast<__half*>(sm.tile[s][1]);
+        const int r = tid >> 1;
+        uint32_t mx = 0;
+        uint4* row = reinterpret_cast<uint4*>(vt + r * 64) + (tid & 1) * 4;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 w = row[c];
+          mx |= (((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
+                 ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u)) &
+                0x80008000u;
+        }
+        mx |= __shfl_xor_sync(0xffffffffu, mx, 1);
+        if (mx) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) row[c] = make_uint4(0, 0, 0, 0);
+          if (!(tid & 1)) atomicOr(&sm.bad, 1ull << r);
+        }
+        __syncthreads();
+      }
+    } else {
+      const int s = it % S::kStages;
+      cp_wait<S::kStages - 1>();  // this thread's own chunks of tile `it`
+      if (it) __syncthreads();    // the last tile's products are done with the converted tile
+      const int c = tid & 15, r0 = tid >> 4;
+      uint2* kh = reinterpret_cast<uint2*>(sm.tile[0]);
+      uint2* kl = reinterpret_cast<uint2*>(sm.tile[1]);
+      uint2* vh = reinterpret_cast<uint2*>(sm.tile[2]);
+      uint2* vl = reinterpret_cast<uint2*>(sm.tile[3]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 8 * i;
+        const float4 x = sm.raw[s][0][r * 16 + c];
+        uint32_t mx = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const int e = scale_exp(mx);
+        const float f = pow2(-e);
+        uint2 hi, lo;
+        split2(x.x * f, x.y * f, hi.x, lo.x);
+        split2(x.z * f, x.w * f, hi.y, lo.y);
+        const uint32_t at = tile_off(r, c >> 1) / 8 + (c & 1);
+        kh[at] = hi;
+        kl[at] = lo;
+        if (c == 0) sm.kscale[r] = pow2(e);
+      }
+      // v rows: cached ones, which every row of the tile sees, with one scale for the rows of a
+      // warp; drafts, which some rows do not see, each with its own
+      uint32_t mx = 0;
+      if (!draft) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 x = sm.raw[s][1][(r0 + 8 * i) * 16 + c];
+          const uint32_t rm = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+          mx = max(mx, rm >= kInfBits ? 0u : rm);
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 8 * i;
+        float4 x = sm.raw[s][1][r * 16 + c];
+        if (draft) {
+          mx = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+#pragma unroll
+          for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          if (mx >= kInfBits) {  // as above: a row with an infinity or NaN is taken out
+            x = make_float4(0.f, 0.f, 0.f, 0.f);
+            mx = 0;
+            if (c == 0) atomicOr(&sm.bad, 1ull << r);
+          }
+        }
+        const int e = scale_exp(mx);
+        const float f = pow2(-e);
+        uint2 hi, lo;
+        split2(x.x * f, x.y * f, hi.x, lo.x);
+        split2(x.z * f, x.w * f, hi.y, lo.y);
+        const uint32_t at = tile_off(r, c >> 1) / 8 + (c & 1);
+        vh[at] = hi;
+        vl[at] = lo;
+        if (c == 0) sm.vscale[r] = pow2(e);
+      }
+      produce(s);  // the slot's chunks of this thread are read
+      __syncthreads();
+      k_hi = tc::smem_u32(sm.tile[0]);
+      k_lo = tc::smem_u32(sm.tile[1]);
+      v_hi = tc::smem_u32(sm.tile[2]);
+      v_lo = tc::smem_u32(sm.tile[3]);
+    }
+
+    // ---- scores
+    float s[NT][4];
+    {
+      float sl[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = sl[j][e] = 0.f;
+      const int kr = wn * NP + (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
+          const uint32_t off = tile_off(kr + j * 8, 2 * ks + ((lane >> 3) & 1));
+          uint32_t b[4];
+          ldsm4(k_hi + off, b);
+          mma(s[j], qh[ks], b[0], b[1]);
+          mma(s[j + 1], qh[ks], b[2], b[3]);
+          mma(sl[j], ql[ks], b[0], b[1]);
+          mma(sl[j + 1], ql[ks], b[2], b[3]);
+          if constexpr (!F16) {
+            ldsm4(k_lo + off, b);
+            mma(sl[j], qh[ks], b[0], b[1]);
+            mma(sl[j + 1], qh[ks], b[2], b[3]);
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] += sl[j][e];
+    }
+    if constexpr (!F16) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float2 f = *reinterpret_cast<const float2*>(&sm.kscale[wn * NP + j * 8 + 2 * qc]);
+        s[j][0] *= f.x;
+        s[j][1] *= f.y;
+        s[j][2] *= f.x;
+        s[j][3] *= f.y;
+      }
+    }
+    if (draft || p0 - cur.t * kTile < kTile) {
+      const uint64_t in = draft ? ~0ull : (1ull << (p0 - cur.t * kTile)) - 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t see = (draft ? vis[i] : in) >> (wn * NP + 2 * qc);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (!(see >> (8 * j) & 1)) s[j][2 * i] = -INFINITY;
+          if (!(see >> (8 * j + 1) & 1)) s[j][2 * i + 1] = -INFINITY;
+        }
+      }
+    }
+
+    // ---- online softmax
+    float corr[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+      for (int j = 1; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[i], mx * rs[i]);
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      corr[i] = ex2(m[i] - mu);
+      m[i] = mn;
+      const float bias = kBias - mu;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        s[j][2 * i] = ex2(fmaf(s[j][2 * i], rs[i], bias));
+        s[j][2 * i + 1] = ex2(fmaf(s[j][2 * i + 1], rs[i], bias));
+        sum += s[j][2 * i] + s[j][2 * i + 1];
+      }
+      l[i] = fmaf(l[i], corr[i], sum);
+    }
+    // f32 cache: the weights take over the scale of their v rows, in units of the largest that
+    // the row sees
+    float2 vs[F16 ? 1 : NT];
+    float vinv[2] = {1.f, 1.f};
+    if constexpr (!F16) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) vs[j] = *reinterpret_cast<const float2*>(&sm.vscale[wn * NP + j * 8 + 2 * qc]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t see = (draft ? vis[i] : ~0ull) >> (wn * NP + 2 * qc);
+        float top = vunit[i];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          top = fmaxf(top, fmaxf(see >> (8 * j) & 1 ? vs[j].x : 0.f, see >> (8 * j + 1) & 1 ? vs[j].y : 0.f));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        vinv[i] = __uint_as_float((254u << 23) - __float_as_uint(top));  // 1 / top, a power of two
+        corr[i] *= vunit[i] * vinv[i];
+        vunit[i] = top;
+      }
+    }
+
+    // ---- weighted values
+    const unsigned long long bad = draft ? sm.bad : 0ull;
+    if (bad) {
+      const KV* vrow = vd + ((int64_t)cur.b * a.n_kv + cur.h) * a.n_nodes * kHd;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (vis[i] & bad) {  // the other rows keep every bit
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            o[d][2 * i] *= corr[i];
+            o[d][2 * i + 1] *= corr[i];
+          }
+          corr[i] = 1.f;
+        }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int slot = wn * NP + j;
+        if (!(bad >> slot & 1)) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p = __shfl_sync(0xffffffffu, s[j / 8][2 * i + (j & 1)], (lane & 28) | ((j & 7) >> 1));
+          if (!(vis[i] >> slot & 1)) continue;
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              o[d][2 * i + e] += p * ((float)vrow[(int64_t)slot * kHd + d * 8 + 2 * qc + e] * vinv[i]);
+        }
+      }
+    }
+    uint32_t ph[NT / 2][4], pl[NT / 2][4];
+#pragma unroll
+    for (int pk = 0; pk < NT / 2; ++pk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // (row, row + 8) of n tile 2 pk, then of 2 pk + 1
+        const int j = 2 * pk + (e >> 1);
+        float x = s[j][2 * (e & 1)], y = s[j][2 * (e & 1) + 1];
+        if constexpr (!F16) {
+          x = x * vinv[e & 1] * vs[j].x;
+          y = y * vinv[e & 1] * vs[j].y;
+        }
+        split2(x, y, ph[pk][e], pl[pk][e]);
+      }
+    const int vr = wn * NP + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int d = 0; d < 8; d += 2) {
+      float t[2][4], tl[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[0][e] = t[1][e] = tl[0][e] = tl[1][e] = 0.f;
+#pragma unroll
+      for (int pk = 0; pk < NT / 2; ++pk) {
+        const uint32_t off = tile_off(vr + pk * 16, d + ((lane >> 4) & 1));
+        uint32_t b[4];
+        ldsm4t(v_hi + off, b);
+        mma(t[0], ph[pk], b[0], b[1]);
+        mma(t[1], ph[pk], b[2], b[3]);
+        mma(tl[0], pl[pk], b[0], b[1]);
+        mma(tl[1], pl[pk], b[2], b[3]);
+        if constexpr (!F16) {
+          ldsm4t(v_lo + off, b);
+          mma(tl[0], ph[pk], b[0], b[1]);
+          mma(tl[1], ph[pk], b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d + x][e] = fmaf(o[d + x][e], corr[e >> 1], t[x][e] + tl[x][e]);
+    }
+
+    // ---- the end of this CTA's part of the walk
+    if (draft || !more) {
+      const bool whole = t_begin == 0 && draft;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      }
+      const float unit[2] = {F16 ? 1.f : vunit[0], F16 ? 1.f : vunit[1]};
+      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(BM);
+      auto out_row = [&](int r) {  // row r of the block
+        const int at = cur.r * BM + r, node = at / a.group, g = at % a.group;
+        return a.out + (((int64_t)cur.b * a.n_nodes + node) * a.n_kv * a.group + cur.h * a.group + g) * kHd;
+      };
+      if constexpr (WN == 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = wm * 16 + qr + 8 * i;
+          if (whole) {
+            if (cur.r * BM + r < rows) {
+              const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+              float2* dst = reinterpret_cast<float2*>(out_row(r)) + qc;
+#pragma unroll
+              for (int d = 0; d < 8; ++d)
+                dst[4 * d] = l[i] == 0.f ? make_float2(0.f, 0.f)
+                                         : make_float2(o[d][2 * i] * inv * unit[i], o[d][2 * i + 1] * inv * unit[i]);
+            }
+          } else {
+            if (qc == 0) {
+              part[r] = m[i];
+              part[BM + r] = l[i];
+            }
+            float2* dst = reinterpret_cast<float2*>(part + 2 * BM + r * kHd) + qc;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) dst[4 * d] = make_float2(o[d][2 * i] * unit[i], o[d][2 * i + 1] * unit[i]);
+          }
+        }
+      } else {
+        // join the warps' shares of the positions
+        __syncthreads();
+        float* mine = sm.merge[warp];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = qr + 8 * i;
+          if (qc == 0) {
+            mine[r] = m[i];
+            mine[16 + r] = l[i];
+          }
+          float2* dst = reinterpret_cast<float2*>(mine + 32 + r * kHd) + qc;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) dst[4 * d] = make_float2(o[d][2 * i] * unit[i], o[d][2 * i + 1] * unit[i]);
+        }
+        __syncthreads();
+        for (int x = tid; x < BM * (kHd / 4); x += kThreads) {
+          const int r = x / (kHd / 4), c = x % (kHd / 4);
+          const int w0 = r / 16, rr = r % 16;
+          float mt = -INFINITY, lt = 0.f;
+          float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < WN; ++w) mt = fmaxf(mt, sm.merge[w0 + w * WM][rr]);
+#pragma unroll
+          for (int w = 0; w < WN; ++w) {
+            const float* src = sm.merge[w0 + w * WM];
+            const float mw = src[rr], lw = src[16 + rr];
+            const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
+            const float4 ow = *(reinterpret_cast<const float4*>(src + 32 + rr * kHd) + c);
+            lt = fmaf(lw, f, lt);
+            ot.x = fmaf(ow.x, f, ot.x);
+            ot.y = fmaf(ow.y, f, ot.y);
+            ot.z = fmaf(ow.z, f, ot.z);
+            ot.w = fmaf(ow.w, f, ot.w);
+          }
+          if (whole) {
+            if (cur.r * BM + r < rows) {
+              const float inv = lt == 0.f ? 0.f : 1.f / lt;
+              reinterpret_cast<float4*>(out_row(r))[c] =
+                  lt == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(ot.x * inv, ot.y * inv, ot.z * inv, ot.w * inv);
+            }
+          } else {
+            if (c == 0) {
+              part[r] = mt;
+              part[BM + r] = lt;
+            }
+            reinterpret_cast<float4*>(part + 2 * BM + r * kHd)[c] = ot;
+          }
+        }
+        if (more) __syncthreads();
+      }
+      t_begin = -1;
+      if (draft && more) {
+        __syncthreads();  // every warp has read `bad`
+        if (tid == 0) sm.bad = 0;
+      }
+    }
+    advance(sm.plan, a.n_kv, cur);
+  }
+  cp_wait<0>();
+}
+
+// Joins the parts of the walks that more than one CTA took (a warp to a row), and writes the
+// zeros of sequences whose position is out of range.
+template <int BM>
+__global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int ctas, int blocks) {
+  __shared__ Plan plan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) make_plan(a, BM, &plan);
+  __syncthreads();
+  pdl_wait();  // in every CTA: the end of this kernel is the end of both
+  const int walk = blockIdx.x;  // (sequence, kv head, block of rows)
+  const int b = walk / (a.n_kv * blocks), h = walk / blocks % a.n_kv, rb = walk % blocks;
+  const int r = blockIdx.y * 4 + warp, at = rb * BM + r;
+  if (at >= plan.cnt[b] * a.group) return;
+  float2* dst = reinterpret_cast<float2*>(
+                    a.out + (((int64_t)b * a.n_nodes + at / a.group) * a.n_kv * a.group + h * a.group + at % a.group) *
+                                kHd) +
+                lane;
+  const int nt = plan.nt[b];
+  if (!nt) {
     *dst = make_float2(0.f, 0.f);
     return;
   }
-  const float2 qv =
-      load2(q + (int64_t)b * q_batch_stride + ((int64_t)node * n_heads + h) * kHd + 2 * lane);
-  const int64_t head = (int64_t)b * n_kv + kvh;
-  const uint64_t sees = mask[(int64_t)b * n_nodes + node];
-  float m = -INFINITY, l = 0.f;
-  float2 o = make_float2(0.f, 0.f);
-  auto step = [&](const KV* k, const KV* v) {
-    const float2 kv = load2(k + 2 * lane);
-    const float s = warp_sum(qv.x * kv.x + qv.y * kv.y) * (1.4426950408889634f * 0.125f);
-    const float mn = fmaxf(m, s);
-    const float corr = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - mn);
-    const float2 vv = load2(v + 2 * lane);
-    l = l * corr + w;
-    o.x = o.x * corr + w * vv.x;
-    o.y = o.y * corr + w * vv.y;
-    m = mn;
-  };
-  for (int p = 0; p < p0; ++p) {
-    const int64_t at = (head * max_ctx + p) * kHd;
-    step(kc + at, vc + at);
+  const int per = units_per_cta(plan.off[QD_MAX_BATCH], ctas);
+  const int g0 = plan.off[b] + (h * plan.rb[b] + rb) * (nt + kStart) + kStart;  // the first tile's unit
+  const int c0 = g0 / per, c1 = (g0 + nt - 1) / per;
+  if (c0 == c1) return;
+  // the walk begins in its first CTA (slot 1: that CTA's last part) and is the first part of the others
+  auto part = [&](int c) { return a.ws + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats(BM); };
+  float mt = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) mt = fmaxf(mt, __ldcg(part(c) + r));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+  float lt = 0.f;
+  float2 ot = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float* p = part(c);
+    const float mc = __ldcg(p + r), lc = __ldcg(p + BM + r);
+    const float2 oc = __ldcg(reinterpret_cast<const float2*>(p + 2 * BM + r * kHd) + lane);
+    const float f = mc == -INFINITY ? lc : ex2(mc - mt);
+    lt = fmaf(lc, f, lt);
+    ot.x = fmaf(oc.x, f, ot.x);
+    ot.y = fmaf(oc.y, f, ot.y);
   }
-  for (int j = 0; j < cnt; ++j)
-    if (sees >> j & 1) {
-      const int64_t at = (head * n_nodes + j) * kHd;
-      step(kd + at, vd + at);
-    }
-  *dst = l == 0.f ? make_float2(0.f, 0.f) : make_float2(o.x / l, o.y / l);
+  *dst = lt == 0.f ? make_float2(0.f, 0.f) : make_float2(ot.x / lt, ot.y / lt);
+}
+
+// Rows to a block: all of them up to 64.
+inline int block_rows(int n_nodes, int group) {
+  const int r = n_nodes * group;
+  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+}
+inline int blocks_of(int n_nodes, int group) {
+  const int bm = block_rows(n_nodes, group);
+  return (n_nodes * group + bm - 1) / bm;
+}
+constexpr int kMaxCtas = 3;  // CTAs to an SM at most
+// CTAs of a call: what fits the device at once, and no more than there can be units for.
+inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, int per_sm) {
+  const int64_t units =
+      (int64_t)batch * n_kv * blocks_of(n_nodes, group) * ((max_ctx + (int64_t)kTile - 1) / kTile + 1 + kStart);
+  return (int)std::min<int64_t>((int64_t)attn_sm_count() * per_sm, (units + kMinPer - 1) / kMinPer);
+}
+
+template <bool F16, int WM, int WN>
+qd_status launch(const TreeAttnArgs& a, int blocks, cudaStream_t st) {
+  static_assert(WM * WN * 32 == kThreads, "four warps");
+  auto kern = k_tree_attn<F16, WM, WN>;
+  const int smem = (int)sizeof(Smem<F16>);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QD_ERR_CUDA;
+  const int ctas = tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, F16 ? 3 : 2);
+  kern<<<ctas, kThreads, smem, st>>>(a);
+  const qd_status s = launch_status();
+  if (s != QD_OK) return s;
+  const dim3 grid((unsigned)(a.batch * a.n_kv * blocks), (unsigned)(16 * WM / 4));
+  return launch_k(k_tree_attn_join<16 * WM>, grid, dim3(kThreads), 0, st, true, a, ctas, blocks);
+}
+
+template <bool F16>
+qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
+  const int blocks = blocks_of(a.n_nodes, a.group);
+  switch (block_rows(a.n_nodes, a.group)) {
+    case 16: return launch<F16, 1, 4>(a, blocks, st);
+    case 32: return launch<F16, 2, 2>(a, blocks, st);
+    default: return launch<F16, 4, 1>(a, blocks, st);
+  }
+}
+
+// The units of a call must fit an int.
+inline bool tree_shape_ok(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch) {
+  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 8 || head_dim != kHd ||
+      n_nodes < 1 || n_nodes > QD_MAX_TREE || max_ctx < 1 || batch < 1 || batch > QD_MAX_BATCH)
+    return false;
+  const int64_t walks = (int64_t)batch * n_kv_heads * blocks_of(n_nodes, n_heads / n_kv_heads);
+  return walks <= (1 << 20) && walks * ((int64_t)max_ctx / kTile + 2 + kStart) <= (1 << 30);
 }
 
 }  // namespace
@@ -74,10 +785,10 @@ using namespace qd;
 extern "C" {
 
 size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch) {
-  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 8 || head_dim != kHd ||
-      n_nodes < 1 || n_nodes > QD_MAX_TREE || max_ctx < 1 || batch < 1 || batch > QD_MAX_BATCH)
-    return 0;
-  return 256;
+  if (!tree_shape_ok(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch)) return 0;
+  const int group = n_heads / n_kv_heads;
+  return (size_t)tree_ctas(n_kv_heads, group, n_nodes, max_ctx, batch, kMaxCtas) * 2 *
+         part_floats(block_rows(n_nodes, group)) * sizeof(float);
 }
 
 qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cache, const void* v_cache,
@@ -89,7 +800,7 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   if (kv_f16 != 0 && kv_f16 != 1) return QD_ERR_INVALID_ARG;
   if (head_dim != kHd) return QD_ERR_UNSUPPORTED;
   const size_t need = qd_tree_attn_workspace(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch);
-  if (!need || n_heads > 65535) return QD_ERR_SHAPE;
+  if (!need) return QD_ERR_SHAPE;
   if (batch > 1 && q_batch_stride < (int64_t)n_nodes * n_heads * head_dim) return QD_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_draft) || !aligned16(v_draft) ||
       !aligned16(out) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(mask) & 7) ||
@@ -97,19 +808,24 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
     return QD_ERR_ALIGN;
   if (batch > 1 && q_batch_stride % 4) return QD_ERR_ALIGN;
   if (workspace_bytes < need) return QD_ERR_NOMEM;
-  const dim3 grid((unsigned)n_heads, (unsigned)n_nodes, (unsigned)batch);
-  cudaStream_t st = (cudaStream_t)stream;
-  if (kv_f16)
-    k_tree_attn<__half><<<grid, 32, 0, st>>>(q, q_batch_stride, static_cast<const __half*>(k_cache),
-                                             static_cast<const __half*>(v_cache), static_cast<const __half*>(k_draft),
-                                             static_cast<const __half*>(v_draft), out, n_kv_heads, pos, mask, n_valid,
-                                             n_nodes, max_ctx);
-  else
-    k_tree_attn<float><<<grid, 32, 0, st>>>(q, q_batch_stride, static_cast<const float*>(k_cache),
-                                            static_cast<const float*>(v_cache), static_cast<const float*>(k_draft),
-                                            static_cast<const float*>(v_draft), out, n_kv_heads, pos, mask, n_valid,
-                                            n_nodes, max_ctx);
-  return launch_status();
+  TreeAttnArgs a;
+  a.q = q;
+  a.q_batch_stride = q_batch_stride;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.kd = k_draft;
+  a.vd = v_draft;
+  a.out = out;
+  a.n_kv = n_kv_heads;
+  a.group = n_heads / n_kv_heads;
+  a.pos = pos;
+  a.mask = mask;
+  a.n_valid = n_valid;
+  a.n_nodes = n_nodes;
+  a.max_ctx = max_ctx;
+  a.batch = batch;
+  a.ws = static_cast<float*>(workspace);
+  return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
 }
 
 }  // extern "C"
