@@ -317,18 +317,28 @@ def embed(fmt, E, vocab, dim, tokens, batch, x, stream=None):
                                        _stream(stream)))
 
 
-def _room(fn, name, t, dtypes, n, stepped=False):
+def _here(stream):
+    """(raw stream, index of the current device); `stream` as in _stream."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    if stream is None:  # what torch.cuda.current_stream() wraps, without the wrapper's 3 us
+        return torch._C._cuda_getCurrentRawStream(dev), dev
+    return _stream(stream), dev
+
+
+def _room(fn, name, t, dtype, dev, n, stepped=False):
     """Pointer of t after a look at what only the tensor tells: its type, its device and that
     n elements lie behind its pointer, so that a tensor too small is an error here and not a
     read out of bounds on the device.  Only a `stepped` argument, whose strides the call is
     given, may be a view with gaps.  Raw pointers and None pass as they are."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    import torch
-
-    if t.dtype not in dtypes:
-        raise ValueError(f"{fn}: {name} has type {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} has type {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
     if not stepped and not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
@@ -353,18 +363,19 @@ def tree_append(q, k, v, batch_stride, node_stride, q_out, k_draft, v_draft, n_h
     """Rotated queries into q_out, rotated keys and values into the draft buffers (see qdecode.h)."""
     import torch
 
-    fn, f32, i32 = "qd_tree_append", (torch.float32,), (torch.int32,)
-    kv = (torch.float16,) if kv_f16 else f32
+    fn, f32, i32, (st, dev) = "qd_tree_append", torch.float32, torch.int32, _here(stream)
+    kv = torch.float16 if kv_f16 else f32
     last = (batch - 1) * batch_stride + (n_nodes - 1) * node_stride
     qn, kn = n_heads * head_dim, n_kv_heads * head_dim
     _check(fn, load().qd_tree_append(
-        _room(fn, "q", q, f32, last + qn, True), _room(fn, "k", k, f32, last + kn, True),
-        _room(fn, "v", v, f32, last + kn, True), batch_stride, node_stride,
-        _room(fn, "q_out", q_out, f32, batch * n_nodes * qn), _room(fn, "k_draft", k_draft, kv, batch * n_nodes * kn),
-        _room(fn, "v_draft", v_draft, kv, batch * n_nodes * kn), 1 if kv_f16 else 0, n_heads, n_kv_heads, head_dim,
-        _room(fn, "pos", pos, i32, batch), _room(fn, "depth", depth, i32, batch * n_nodes),
-        _room(fn, "n_valid", n_valid, i32, batch), n_nodes, PAIRING[pairing],
-        _room(fn, "cos_sin", cos_sin, f32, max_ctx * head_dim), max_ctx, batch, _stream(stream)))
+        _room(fn, "q", q, f32, dev, last + qn, True), _room(fn, "k", k, f32, dev, last + kn, True),
+        _room(fn, "v", v, f32, dev, last + kn, True), batch_stride, node_stride,
+        _room(fn, "q_out", q_out, f32, dev, batch * n_nodes * qn),
+        _room(fn, "k_draft", k_draft, kv, dev, batch * n_nodes * kn),
+        _room(fn, "v_draft", v_draft, kv, dev, batch * n_nodes * kn), 1 if kv_f16 else 0, n_heads, n_kv_heads,
+        head_dim, _room(fn, "pos", pos, i32, dev, batch), _room(fn, "depth", depth, i32, dev, batch * n_nodes),
+        _room(fn, "n_valid", n_valid, i32, dev, batch), n_nodes, PAIRING[pairing],
+        _room(fn, "cos_sin", cos_sin, f32, dev, max_ctx * head_dim), max_ctx, batch, st))
 
 
 def tree_attn_workspace(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch) -> int:
@@ -376,20 +387,20 @@ def tree_attn(q, q_batch_stride, k_cache, v_cache, k_draft, v_draft, out, n_head
     """Attention of the tree over the cache and its own drafts (see qdecode.h)."""
     import torch
 
-    fn, f32, i32 = "qd_tree_attn", (torch.float32,), (torch.int32,)
-    kv = (torch.float16,) if kv_f16 else f32
+    fn, f32, i32, (st, dev) = "qd_tree_attn", torch.float32, torch.int32, _here(stream)
+    kv = torch.float16 if kv_f16 else f32
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    qn, kn, cn = n_nodes * n_heads * head_dim, batch * n_nodes * n_kv_heads * head_dim, \
-        batch * n_kv_heads * max_ctx * head_dim
+    qn, kn = n_nodes * n_heads * head_dim, batch * n_nodes * n_kv_heads * head_dim
+    cn = batch * n_kv_heads * max_ctx * head_dim
     _check(fn, load().qd_tree_attn(
-        _room(fn, "q", q, f32, (batch - 1) * q_batch_stride + qn, True), q_batch_stride,
-        _room(fn, "k_cache", k_cache, kv, cn), _room(fn, "v_cache", v_cache, kv, cn),
-        _room(fn, "k_draft", k_draft, kv, kn), _room(fn, "v_draft", v_draft, kv, kn), 1 if kv_f16 else 0,
-        _room(fn, "out", out, f32, batch * qn), n_heads, n_kv_heads, head_dim, _room(fn, "pos", pos, i32, batch),
-        _room(fn, "mask", mask, (torch.int64, torch.uint64), batch * n_nodes),
-        _room(fn, "n_valid", n_valid, i32, batch), n_nodes, max_ctx, batch,
-        _room(fn, "workspace", workspace, (torch.uint8,), workspace_bytes), workspace_bytes, _stream(stream)))
+        _room(fn, "q", q, f32, dev, (batch - 1) * q_batch_stride + qn, True), q_batch_stride,
+        _room(fn, "k_cache", k_cache, kv, dev, cn), _room(fn, "v_cache", v_cache, kv, dev, cn),
+        _room(fn, "k_draft", k_draft, kv, dev, kn), _room(fn, "v_draft", v_draft, kv, dev, kn), 1 if kv_f16 else 0,
+        _room(fn, "out", out, f32, dev, batch * qn), n_heads, n_kv_heads, head_dim,
+        _room(fn, "pos", pos, i32, dev, batch), _room(fn, "mask", mask, torch.int64, dev, batch * n_nodes),
+        _room(fn, "n_valid", n_valid, i32, dev, batch), n_nodes, max_ctx, batch,
+        _room(fn, "workspace", workspace, torch.uint8, dev, workspace_bytes), workspace_bytes, st))
 
 
 def token_logprobs(logits, row_stride, vocab, rows, tokens, n_tokens, logprob, entropy, top_k, top_idx, top_logprob,
@@ -397,13 +408,13 @@ def token_logprobs(logits, row_stride, vocab, rows, tokens, n_tokens, logprob, e
     """Log probabilities of tokens, entropy and the top alternatives of each row of logits (see qdecode.h)."""
     import torch
 
-    fn, f32, i32 = "qd_token_logprobs", (torch.float32,), (torch.int32,)
+    fn, f32, i32, (st, dev) = "qd_token_logprobs", torch.float32, torch.int32, _here(stream)
     _check(fn, load().qd_token_logprobs(
-        _room(fn, "logits", logits, f32, (rows - 1) * row_stride + vocab, True), row_stride, vocab, rows,
-        _room(fn, "tokens", tokens, i32, rows * n_tokens), n_tokens,
-        _room(fn, "logprob", logprob, f32, rows * n_tokens), _room(fn, "entropy", entropy, f32, rows), top_k,
-        _room(fn, "top_idx", top_idx, i32, rows * top_k), _room(fn, "top_logprob", top_logprob, f32, rows * top_k),
-        _stream(stream)))
+        _room(fn, "logits", logits, f32, dev, (rows - 1) * row_stride + vocab, True), row_stride, vocab, rows,
+        _room(fn, "tokens", tokens, i32, dev, rows * n_tokens), n_tokens,
+        _room(fn, "logprob", logprob, f32, dev, rows * n_tokens), _room(fn, "entropy", entropy, f32, dev, rows), top_k,
+        _room(fn, "top_idx", top_idx, i32, dev, rows * top_k),
+        _room(fn, "top_logprob", top_logprob, f32, dev, rows * top_k), st))
 
 
 def tree_commit(tokens, parent, chosen, chosen_stride, n_valid, n_nodes, k_draft, v_draft, k_cache, v_cache, layers,
@@ -412,19 +423,19 @@ def tree_commit(tokens, parent, chosen, chosen_stride, n_valid, n_nodes, k_draft
     """Accept a path of each tree and copy its rows of every layer into the caches (see qdecode.h)."""
     import torch
 
-    fn, i32 = "qd_tree_commit", (torch.int32,)
-    kv = (torch.float16,) if kv_f16 else (torch.float32,)
+    fn, i32, (st, dev) = "qd_tree_commit", torch.int32, _here(stream)
+    kv = torch.float16 if kv_f16 else torch.float32
     nodes, dn = batch * n_nodes, layers * batch * n_nodes * n_kv_heads * head_dim
     cn = (layers - 1) * cache_layer_stride + batch * n_kv_heads * max_ctx * head_dim
     _check(fn, load().qd_tree_commit(
-        _room(fn, "tokens", tokens, i32, nodes), _room(fn, "parent", parent, i32, nodes),
-        _room(fn, "chosen", chosen, i32, (nodes - 1) * chosen_stride + 1, True), chosen_stride,
-        _room(fn, "n_valid", n_valid, i32, batch), n_nodes, _room(fn, "k_draft", k_draft, kv, dn),
-        _room(fn, "v_draft", v_draft, kv, dn), _room(fn, "k_cache", k_cache, kv, cn, True),
-        _room(fn, "v_cache", v_cache, kv, cn, True), 1 if kv_f16 else 0, layers, cache_layer_stride, n_kv_heads,
-        head_dim, _room(fn, "pos", pos, i32, batch), max_ctx, batch, _room(fn, "path", path, i32, nodes),
-        _room(fn, "n_accept", n_accept, i32, batch), _room(fn, "next_token", next_token, i32, batch),
-        _room(fn, "pos_out", pos_out, i32, batch), _stream(stream)))
+        _room(fn, "tokens", tokens, i32, dev, nodes), _room(fn, "parent", parent, i32, dev, nodes),
+        _room(fn, "chosen", chosen, i32, dev, (nodes - 1) * chosen_stride + 1, True), chosen_stride,
+        _room(fn, "n_valid", n_valid, i32, dev, batch), n_nodes, _room(fn, "k_draft", k_draft, kv, dev, dn),
+        _room(fn, "v_draft", v_draft, kv, dev, dn), _room(fn, "k_cache", k_cache, kv, dev, cn, True),
+        _room(fn, "v_cache", v_cache, kv, dev, cn, True), 1 if kv_f16 else 0, layers, cache_layer_stride, n_kv_heads,
+        head_dim, _room(fn, "pos", pos, i32, dev, batch), max_ctx, batch, _room(fn, "path", path, i32, dev, nodes),
+        _room(fn, "n_accept", n_accept, i32, dev, batch), _room(fn, "next_token", next_token, i32, dev, batch),
+        _room(fn, "pos_out", pos_out, i32, dev, batch), st))
 
 
 def make_config(cfg: dict, max_ctx: int, max_batch: int, tied: bool = True, kv_f16: bool | None = None,

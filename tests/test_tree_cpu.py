@@ -116,10 +116,19 @@ def test_binding_refuses_tensors_that_do_not_hold_the_call():
     room = qd._room
     a = torch.zeros(8)
     with pytest.raises(ValueError, match="has type"):
-        room("f", "a", a, (torch.int32,), 8)
+        room("f", "a", a, torch.int32, -1, 8)
     with pytest.raises(ValueError, match="current device"):
-        room("f", "a", a, (torch.float32,), 8)
-    assert room("f", "a", None, (torch.float32,), 8) is None and room("f", "a", 64, (torch.float32,), 8) == 64
+        room("f", "a", a, torch.float32, 0, 8)
+    with pytest.raises(ValueError, match="contiguous"):
+        room("f", "a", torch.zeros(2, 8).t(), torch.float32, -1, 8)
+    with pytest.raises(ValueError, match="holds 8 elements"):
+        room("f", "a", a, torch.float32, -1, 9)
+    b = torch.zeros(4, 6)[:, 2:]  # a view with gaps: 22 elements from its pointer on
+    with pytest.raises(ValueError, match="holds 22 elements"):
+        room("f", "b", b, torch.float32, -1, 23, True)
+    assert room("f", "b", b, torch.float32, -1, 22, True) == b.data_ptr()
+    assert room("f", "a", a, torch.float32, -1, 8) == a.data_ptr()
+    assert room("f", "a", None, torch.float32, 0, 8) is None and room("f", "a", 64, torch.float32, 0, 8) == 64
 
 
 def test_references_on_hand_values():
