@@ -35,6 +35,7 @@ constexpr int kThreads = 128;  // 4 warps: WM blocks of 16 rows x WN shares of t
 constexpr float kBias = 12.f;  // log2 of the weights' scale
 constexpr int kStart = 3;      // what the start of a walk costs, in tiles
 constexpr int kMinPer = 4;     // units of a CTA at least
+constexpr int kWholeTiles = 8;  // walks of at most so many tiles are not cut
 static_assert(QD_MAX_TREE <= kTile, "the drafts fit one tile");
 
 struct TreeAttnArgs {
@@ -48,6 +49,8 @@ struct TreeAttnArgs {
   const int32_t* n_valid;
   int n_nodes, max_ctx, batch;
   float* ws;
+  int blocks;  // of rows, at most
+  int whole;   // 1: a CTA takes one whole walk
 };
 
 // Work of the sequences: nt tiles for each of n_kv * rb walks (0 when pos is out of range).
@@ -208,12 +211,32 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   if (warp == 0) make_plan(a, BM, &sm.plan);
   if (tid == 0) sm.bad = 0;
   __syncthreads();
-  const int total = sm.plan.off[QD_MAX_BATCH];
-  const int per = units_per_cta(total, gridDim.x);
-  const int64_t first = (int64_t)blockIdx.x * per;
-  if (first >= total) return;
-  const int end = min((int)first + per, total);
-  Cursor cur = cursor_at(sm.plan, (int)first), pre = cur;
+  Cursor cur;
+  int end;
+  if (a.whole) {
+    const int walk = blockIdx.x;
+    cur = Cursor{walk / (a.n_kv * a.blocks), walk / a.blocks % a.n_kv, walk % a.blocks, 0, 0};
+    if (cur.r >= sm.plan.rb[cur.b]) return;
+    end = sm.plan.nt[cur.b];
+    if (!end) {  // a position out of range: zeros
+      const int rows = sm.plan.cnt[cur.b] * a.group;
+      for (int x = tid; x < BM * (kHd / 4); x += kThreads) {
+        const int at = cur.r * BM + x / (kHd / 4), node = at / a.group, g = at % a.group;
+        if (at < rows)
+          reinterpret_cast<float4*>(a.out + (((int64_t)cur.b * a.n_nodes + node) * a.n_kv * a.group +
+                                             cur.h * a.group + g) * kHd)[x % (kHd / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      return;
+    }
+  } else {
+    const int total = sm.plan.off[QD_MAX_BATCH];
+    const int per = units_per_cta(total, gridDim.x);
+    const int64_t first = (int64_t)blockIdx.x * per;
+    if (first >= total) return;
+    end = min((int)first + per, total);
+    cur = cursor_at(sm.plan, (int)first);
+  }
+  Cursor pre = cur;
 
   const KV* kc = static_cast<const KV*>(a.kc);
   const KV* vc = static_cast<const KV*>(a.vc);
@@ -683,14 +706,14 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
 // Joins the parts of the walks that more than one CTA took (a warp to a row), and writes the
 // zeros of sequences whose position is out of range.
 template <int BM>
-__global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int ctas, int blocks) {
+__global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int ctas) {
   __shared__ Plan plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) make_plan(a, BM, &plan);
   __syncthreads();
   pdl_wait();  // in every CTA: the end of this kernel is the end of both
   const int walk = blockIdx.x;  // (sequence, kv head, block of rows)
-  const int b = walk / (a.n_kv * blocks), h = walk / blocks % a.n_kv, rb = walk % blocks;
+  const int b = walk / (a.n_kv * a.blocks), h = walk / a.blocks % a.n_kv, rb = walk % a.blocks;
   const int r = blockIdx.y * 4 + warp, at = rb * BM + r;
   if (at >= plan.cnt[b] * a.group) return;
   float2* dst = reinterpret_cast<float2*>(
@@ -745,26 +768,26 @@ inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, i
 }
 
 template <bool F16, int WM, int WN>
-qd_status launch(const TreeAttnArgs& a, int blocks, cudaStream_t st) {
+qd_status launch(const TreeAttnArgs& a, cudaStream_t st) {
   static_assert(WM * WN * 32 == kThreads, "four warps");
   auto kern = k_tree_attn<F16, WM, WN>;
   const int smem = (int)sizeof(Smem<F16>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QD_ERR_CUDA;
-  const int ctas = tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, F16 ? 3 : 2);
+  const int ctas =
+      a.whole ? a.batch * a.n_kv * a.blocks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, F16 ? 3 : 2);
   kern<<<ctas, kThreads, smem, st>>>(a);
   const qd_status s = launch_status();
-  if (s != QD_OK) return s;
-  const dim3 grid((unsigned)(a.batch * a.n_kv * blocks), (unsigned)(16 * WM / 4));
-  return launch_k(k_tree_attn_join<16 * WM>, grid, dim3(kThreads), 0, st, true, a, ctas, blocks);
+  if (s != QD_OK || a.whole) return s;
+  const dim3 grid((unsigned)(a.batch * a.n_kv * a.blocks), (unsigned)(16 * WM / 4));
+  return launch_k(k_tree_attn_join<16 * WM>, grid, dim3(kThreads), 0, st, true, a, ctas);
 }
 
 template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
-  const int blocks = blocks_of(a.n_nodes, a.group);
   switch (block_rows(a.n_nodes, a.group)) {
-    case 16: return launch<F16, 1, 4>(a, blocks, st);
-    case 32: return launch<F16, 2, 2>(a, blocks, st);
-    default: return launch<F16, 4, 1>(a, blocks, st);
+    case 16: return launch<F16, 1, 4>(a, st);
+    case 32: return launch<F16, 2, 2>(a, st);
+    default: return launch<F16, 4, 1>(a, st);
   }
 }
 
@@ -825,6 +848,8 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   a.max_ctx = max_ctx;
   a.batch = batch;
   a.ws = static_cast<float*>(workspace);
+  a.blocks = blocks_of(n_nodes, a.group);
+  a.whole = (max_ctx + kTile - 1) / kTile + 1 <= kWholeTiles;
   return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
 }
 
