@@ -33,9 +33,18 @@ constexpr int kHd = 64;
 constexpr int kTile = 64;     // positions of a tile; the drafts (at most 64) are one tile
 constexpr int kThreads = 128;  // 4 warps: WM blocks of 16 rows x WN shares of the positions
 constexpr float kBias = 12.f;  // log2 of the weights' scale
-constexpr int kStart = 3;      // what the start of a walk costs, in tiles
 constexpr int kMinPer = 4;     // units of a CTA at least
-constexpr int kWholeTiles = 8;  // walks of at most so many tiles are not cut
+#ifndef WT
+#define WT 8
+#define KS 3
+#endif
+constexpr int kWholeTiles = WT;  // walks of at most so many tiles are not cut
+constexpr int kStart = KS;      // what the start of a walk costs, in tiles
+
+// k_tree_attn_16: 8 warps, each with tiles of its own of 16 positions; what the warps do side by
+// side is one unit of work
+constexpr int kSub = 16;
+constexpr int kWarps16 = 8;
 static_assert(QD_MAX_TREE <= kTile, "the drafts fit one tile");
 
 struct TreeAttnArgs {
@@ -59,7 +68,13 @@ struct Plan {
   int nt[QD_MAX_BATCH], rb[QD_MAX_BATCH], p0[QD_MAX_BATCH], cnt[QD_MAX_BATCH];
 };
 
+// Tiles of a walk over p0 cached positions and cnt drafts.
+__host__ __device__ constexpr int walk_tiles(bool by16, int p0, int cnt) {
+  return by16 ? ((p0 + kSub - 1) / kSub + (cnt + kSub - 1) / kSub + kWarps16 - 1) / kWarps16
+              : (p0 + kTile - 1) / kTile + 1;
+}
 // Filled by one warp; `bm` rows to a block.
+template <bool BY16>
 __device__ __forceinline__ void make_plan(const TreeAttnArgs& a, int bm, Plan* p) {
   const int b = threadIdx.x & 31;
   int units = 0;
@@ -67,7 +82,7 @@ __device__ __forceinline__ void make_plan(const TreeAttnArgs& a, int bm, Plan* p
     const int cnt = a.n_valid ? min(max(a.n_valid[b], 0), a.n_nodes) : a.n_nodes;
     const int p0 = a.pos[b];
     const int rb = (cnt * a.group + bm - 1) / bm;
-    const int nt = p0 < 0 || p0 > a.max_ctx ? 0 : (p0 + kTile - 1) / kTile + 1;
+    const int nt = p0 < 0 || p0 > a.max_ctx ? 0 : walk_tiles(BY16, p0, cnt);
     p->cnt[b] = cnt;
     p->p0[b] = p0;
     p->rb[b] = rb;
@@ -85,6 +100,13 @@ __device__ __forceinline__ void make_plan(const TreeAttnArgs& a, int bm, Plan* p
 }
 __device__ __forceinline__ int units_per_cta(int total, int ctas) { return max((total + ctas - 1) / ctas, kMinPer); }
 
+// Row `at` (node, head of the group) of a walk, in q or out of sequence c.b.
+template <typename C>
+__device__ __forceinline__ float* row_of(const TreeAttnArgs& a, float* out, const C& c, int at) {
+  const int node = at / a.group, g = at % a.group;
+  return out + (((int64_t)c.b * a.n_nodes + node) * a.n_kv * a.group + c.h * a.group + g) * kHd;
+}
+
 // Floats of one partial: m and l of each row, then o.
 __host__ __device__ constexpr int part_floats(int bm) { return bm * (kHd + 2); }
 
@@ -97,6 +119,9 @@ __device__ __forceinline__ float ex2(float x) {
 // 16 bytes global -> shared, or 16 zero bytes
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -116,10 +141,17 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same from zero
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // (x, y) -> two binary16 parts, hi = rn(x), lo = rn(x - hi)
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -169,6 +201,32 @@ __device__ __forceinline__ void advance(const Plan& p, int n_kv, Cursor& c) {
   while (c.b < QD_MAX_BATCH - 1 && p.off[c.b] == p.off[c.b + 1]);
 }
 
+// This CTA's first tile and the unit at which it ends; false if it has none (and zeros written
+// for a whole walk whose position is out of range).
+template <int BM>
+__device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p, Cursor& cur, int& end) {
+  if (!a.whole) {
+    const int total = p.off[QD_MAX_BATCH];
+    const int per = units_per_cta(total, gridDim.x);
+    const int64_t first = (int64_t)blockIdx.x * per;
+    if (first >= total) return false;
+    end = min((int)first + per, total);
+    cur = cursor_at(p, (int)first);
+    return cur.u < end;
+  }
+  const int walk = blockIdx.x;
+  cur = Cursor{walk / (a.n_kv * a.blocks), walk / a.blocks % a.n_kv, walk % a.blocks, 0, 0};
+  if (cur.r >= p.rb[cur.b]) return false;
+  end = p.nt[cur.b];
+  if (end) return true;
+  const int rows = p.cnt[cur.b] * a.group;
+  for (int x = threadIdx.x; x < BM * (kHd / 4); x += blockDim.x) {
+    const int at = cur.r * BM + x / (kHd / 4);
+    if (at < rows) reinterpret_cast<float4*>(row_of(a, a.out, cur, at))[x % (kHd / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  return false;
+}
+
 // Shared memory.  Binary16 cache: a ring of K and V tiles as they are.  f32 cache: a ring of
 // raw tiles, each chunk read back by the thread that copied it, and one converted tile.
 template <bool F16>
@@ -208,34 +266,12 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   const int qr = lane >> 2, qc = lane & 3;  // row and column pair of the lane in a fragment
 
   pdl_trigger();
-  if (warp == 0) make_plan(a, BM, &sm.plan);
+  if (warp == 0) make_plan<false>(a, BM, &sm.plan);
   if (tid == 0) sm.bad = 0;
   __syncthreads();
   Cursor cur;
   int end;
-  if (a.whole) {
-    const int walk = blockIdx.x;
-    cur = Cursor{walk / (a.n_kv * a.blocks), walk / a.blocks % a.n_kv, walk % a.blocks, 0, 0};
-    if (cur.r >= sm.plan.rb[cur.b]) return;
-    end = sm.plan.nt[cur.b];
-    if (!end) {  // a position out of range: zeros
-      const int rows = sm.plan.cnt[cur.b] * a.group;
-      for (int x = tid; x < BM * (kHd / 4); x += kThreads) {
-        const int at = cur.r * BM + x / (kHd / 4), node = at / a.group, g = at % a.group;
-        if (at < rows)
-          reinterpret_cast<float4*>(a.out + (((int64_t)cur.b * a.n_nodes + node) * a.n_kv * a.group +
-                                             cur.h * a.group + g) * kHd)[x % (kHd / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      return;
-    }
-  } else {
-    const int total = sm.plan.off[QD_MAX_BATCH];
-    const int per = units_per_cta(total, gridDim.x);
-    const int64_t first = (int64_t)blockIdx.x * per;
-    if (first >= total) return;
-    end = min((int)first + per, total);
-    cur = cursor_at(sm.plan, (int)first);
-  }
+  if (!first_tile<BM>(a, sm.plan, cur, end)) return;
   Cursor pre = cur;
 
   const KV* kc = static_cast<const KV*>(a.kc);
@@ -438,10 +474,6 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
     float s[NT][4];
     {
       float sl[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = sl[j][e] = 0.f;
       const int kr = wn * NP + (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
@@ -450,10 +482,17 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
           const uint32_t off = tile_off(kr + j * 8, 2 * ks + ((lane >> 3) & 1));
           uint32_t b[4];
           ldsm4(k_hi + off, b);
-          mma(s[j], qh[ks], b[0], b[1]);
-          mma(s[j + 1], qh[ks], b[2], b[3]);
-          mma(sl[j], ql[ks], b[0], b[1]);
-          mma(sl[j + 1], ql[ks], b[2], b[3]);
+          if (ks == 0) {
+            mma0(s[j], qh[ks], b[0], b[1]);
+            mma0(s[j + 1], qh[ks], b[2], b[3]);
+            mma0(sl[j], ql[ks], b[0], b[1]);
+            mma0(sl[j + 1], ql[ks], b[2], b[3]);
+          } else {
+            mma(s[j], qh[ks], b[0], b[1]);
+            mma(s[j + 1], qh[ks], b[2], b[3]);
+            mma(sl[j], ql[ks], b[0], b[1]);
+            mma(sl[j + 1], ql[ks], b[2], b[3]);
+          }
           if constexpr (!F16) {
             ldsm4(k_lo + off, b);
             mma(sl[j], qh[ks], b[0], b[1]);
@@ -581,16 +620,21 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
     for (int d = 0; d < 8; d += 2) {
       float t[2][4], tl[2][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[0][e] = t[1][e] = tl[0][e] = tl[1][e] = 0.f;
-#pragma unroll
       for (int pk = 0; pk < NT / 2; ++pk) {
         const uint32_t off = tile_off(vr + pk * 16, d + ((lane >> 4) & 1));
         uint32_t b[4];
         ldsm4t(v_hi + off, b);
-        mma(t[0], ph[pk], b[0], b[1]);
-        mma(t[1], ph[pk], b[2], b[3]);
-        mma(tl[0], pl[pk], b[0], b[1]);
-        mma(tl[1], pl[pk], b[2], b[3]);
+        if (pk == 0) {
+          mma0(t[0], ph[pk], b[0], b[1]);
+          mma0(t[1], ph[pk], b[2], b[3]);
+          mma0(tl[0], pl[pk], b[0], b[1]);
+          mma0(tl[1], pl[pk], b[2], b[3]);
+        } else {
+          mma(t[0], ph[pk], b[0], b[1]);
+          mma(t[1], ph[pk], b[2], b[3]);
+          mma(tl[0], pl[pk], b[0], b[1]);
+          mma(tl[1], pl[pk], b[2], b[3]);
+        }
         if constexpr (!F16) {
           ldsm4t(v_lo + off, b);
           mma(tl[0], ph[pk], b[0], b[1]);
@@ -613,10 +657,7 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
       }
       const float unit[2] = {F16 ? 1.f : vunit[0], F16 ? 1.f : vunit[1]};
       float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(BM);
-      auto out_row = [&](int r) {  // row r of the block
-        const int at = cur.r * BM + r, node = at / a.group, g = at % a.group;
-        return a.out + (((int64_t)cur.b * a.n_nodes + node) * a.n_kv * a.group + cur.h * a.group + g) * kHd;
-      };
+      auto out_row = [&](int r) { return row_of(a, a.out, cur, cur.r * BM + r); };  // row r of the block
       if constexpr (WN == 1) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -703,13 +744,496 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   cp_wait<0>();
 }
 
+// ------------------------------------------------------------------ 16 rows
+// Few rows to a kv head: blocks of 16, and 8 warps that walk the positions side by side, 16 at a
+// time, each with a ring of its own (no barrier until the walk's end, where the warps' results
+// are joined).  A binary16 cache as above.  An f32 cache without a conversion in
+// shared memory: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
+// fraction bits, lo = as many of the rest: at most 2^-20 off), hi hi + lo hi + hi lo.  TF32 keeps
+// f32's exponents, so nothing is scaled; the products run at half the binary16 rate, which the
+// 16 rows leave room for (1536 of the 2800 cycles in which an SM's share of HBM brings 128
+// positions).
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xFFFFE000u;  // a NaN or infinity stays one
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
+}
+// f32 rows of 256 bytes: 16-byte chunk c of row r stands at c ^ swz(r), so that both reads hit
+// all banks: k (8 rows at one chunk of each lane's four) and v (every second row at two chunks).
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) & 1) | ((((r >> 2) ^ r) & 1) << 2); }
+
+template <bool F16>
+struct Smem16 {
+  static constexpr int kStages = 3;
+  static constexpr int kRowBytes = F16 ? 128 : 256;
+  uint4 ring[kWarps16][kStages][2][kSub * kRowBytes / 16];  // K, V
+  float join[2][36][32];                                    // o, m, l of a warp's lanes
+  Plan plan;
+};
+
+template <bool F16>
+__global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(TreeAttnArgs a) {
+  using KV = typename std::conditional<F16, __half, float>::type;
+  using S = Smem16<F16>;
+  constexpr int kRow = S::kRowBytes;
+  constexpr int kLag = S::kStages - 1;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qr = lane >> 2, qc = lane & 3;
+
+  pdl_trigger();
+  if (warp == 0) make_plan<true>(a, 16, &sm.plan);
+  __syncthreads();
+  Cursor cur;
+  int end;
+  if (!first_tile<16>(a, sm.plan, cur, end)) return;
+  Cursor pre = cur;
+
+  const KV* kc = static_cast<const KV*>(a.kc);
+  const KV* vc = static_cast<const KV*>(a.vc);
+  const KV* kd = static_cast<const KV*>(a.kd);
+  const KV* vd = static_cast<const KV*>(a.vd);
+
+  // this warp's 16 positions of the unit at `pre` into ring slot s (zeros behind their end), and
+  // on to the next unit
+  auto produce = [&](int s) {
+    if (pre.u < end) {
+      const int p0 = sm.plan.p0[pre.b], cnt = sm.plan.cnt[pre.b];
+      const int np = (p0 + kSub - 1) / kSub, sub = pre.t * kWarps16 + warp;
+      const bool draft = sub >= np;
+      const int row0 = (draft ? sub - np : sub) * kSub;
+      const int rows = (draft ? cnt : p0) - row0;
+      if (rows > 0) {
+        const int64_t head = (int64_t)pre.b * a.n_kv + pre.h;
+        const int64_t base = (head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
+        const KV* ks = (draft ? kd : kc) + base;
+        const KV* vs = (draft ? vd : vc) + base;
+        const uint32_t dk = tc::smem_u32(sm.ring[warp][s][0]), dv = tc::smem_u32(sm.ring[warp][s][1]);
+        constexpr int kPer = kRow / 16;
+        const int c = lane % kPer, r0 = lane / kPer;
+        const int first = r0 * kHd + c * (16 / (int)sizeof(KV));
+#pragma unroll
+        for (int i = 0; i < kSub * kPer / 32; ++i) {
+          const int r = r0 + i * (32 / kPer);
+          const uint32_t off = F16 ? tile_off(r, c) : (uint32_t)(r * kRow + ((c ^ swz(r)) << 4));
+          if (rows >= kSub) {
+            cp16(dk + off, ks + first + i * (32 / kPer) * kHd);
+            cp16(dv + off, vs + first + i * (32 / kPer) * kHd);
+          } else {
+            const bool live = r < rows;
+            const int src = live ? r * kHd + c * (16 / (int)sizeof(KV)) : 0;
+            cp16(dk + off, ks + src, live);
+            cp16(dv + off, vs + src, live);
+          }
+        }
+      }
+      advance(sm.plan, a.n_kv, pre);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kLag; ++s) produce(s);
+
+  constexpr int KQ = F16 ? 4 : 8;  // k steps of the scores
+  uint32_t qh[KQ][4], ql[KQ][4];
+  float o[8][4];
+  float m[2], l[2], rs[2] = {1.f, 1.f};
+  uint64_t vis[2];
+  int t_begin = -1;
+
+  for (int it = 0; cur.u < end; ++it) {
+    const int p0 = sm.plan.p0[cur.b], cnt = sm.plan.cnt[cur.b], nt = sm.plan.nt[cur.b];
+    const int rows = cnt * a.group;
+    const bool last = cur.t == nt - 1;
+    const bool more = cur.u + 1 + (last ? kStart : 0) < end;
+    if (t_begin < 0) {
+      t_begin = cur.t;
+      const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = cur.r * 16 + qr + 8 * i;
+        const bool live = at < rows;
+        const int node = at / a.group, g = at % a.group;
+        const float* src = a.q + (int64_t)cur.b * a.q_batch_stride +
+                           ((int64_t)node * a.n_kv * a.group + cur.h * a.group + g) * kHd;
+        if constexpr (F16) {
+          float2 x[8];
+          uint32_t mx = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            x[c] = live ? __ldcg(reinterpret_cast<const float2*>(src + c * 8) + qc) : make_float2(0.f, 0.f);
+            x[c].x *= scale;
+            x[c].y *= scale;
+            mx = max(mx, max(abs_bits(x[c].x), abs_bits(x[c].y)));
+          }
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int e = scale_exp(mx);
+          rs[i] = pow2(e);
+          const float f = pow2(-e);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            split2(x[c].x * f, x[c].y * f, qh[c >> 1][i + 2 * (c & 1)], ql[c >> 1][i + 2 * (c & 1)]);
+        } else {
+          // the lane's dims 4 (qc + 4 j) .. + 3: k step 2 j + e / 2 has them at k = qc and qc + 4
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 x = live ? __ldcg(reinterpret_cast<const float4*>(src) + qc + 4 * j)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            auto in = [scale](float f) { return (f + (f - f)) * scale; };  // an infinity is a NaN too
+            split_tf32(in(x.x), qh[2 * j][i], ql[2 * j][i]);
+            split_tf32(in(x.y), qh[2 * j][i + 2], ql[2 * j][i + 2]);
+            split_tf32(in(x.z), qh[2 * j + 1][i], ql[2 * j + 1][i]);
+            split_tf32(in(x.w), qh[2 * j + 1][i + 2], ql[2 * j + 1][i + 2]);
+          }
+        }
+        vis[i] = live ? a.mask[(int64_t)cur.b * a.n_nodes + node] : 0ull;
+        if (cnt < 64) vis[i] &= (1ull << cnt) - 1;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    }
+
+    // ---- this warp's 16 positions
+    const int slot = it % S::kStages;
+    cp_wait<kLag - 1>();
+    __syncwarp();  // every lane's copies have landed, and the slot before this one has been read
+    produce((it + kLag) % S::kStages);
+    const int np = (p0 + kSub - 1) / kSub, sub = cur.t * kWarps16 + warp;
+    const bool draft = sub >= np;
+    const int row0 = (draft ? sub - np : sub) * kSub;
+    const int left = (draft ? cnt : p0) - row0;
+    if (left > 0) {
+      const uint32_t kt = tc::smem_u32(sm.ring[warp][slot][0]), vt = tc::smem_u32(sm.ring[warp][slot][1]);
+      const unsigned char* kp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][0]);
+      const unsigned char* vp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][1]);
+      float s[2][4], sl[2][4];
+      if constexpr (F16) {
+        const int kr = (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          uint32_t b[4];
+          ldsm4(kt + tile_off(kr, 2 * ks + ((lane >> 3) & 1)), b);
+          if (ks == 0) {
+            mma0(s[0], qh[ks], b[0], b[1]);
+            mma0(s[1], qh[ks], b[2], b[3]);
+            mma0(sl[0], ql[ks], b[0], b[1]);
+            mma0(sl[1], ql[ks], b[2], b[3]);
+          } else {
+            mma(s[0], qh[ks], b[0], b[1]);
+            mma(s[1], qh[ks], b[2], b[3]);
+            mma(sl[0], ql[ks], b[0], b[1]);
+            mma(sl[1], ql[ks], b[2], b[3]);
+          }
+        }
+      } else {
+        float sx[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t bh[2][4], bl[2][4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int r = 8 * n + qr;
+            const float4 x = *reinterpret_cast<const float4*>(kp + r * kRow + (((qc + 4 * j) ^ swz(r)) << 4));
+            split_tf32(x.x, bh[n][0], bl[n][0]);
+            split_tf32(x.y, bh[n][1], bl[n][1]);
+            split_tf32(x.z, bh[n][2], bl[n][2]);
+            split_tf32(x.w, bh[n][3], bl[n][3]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              if (j == 0 && h == 0) {
+                mma8_0(s[n], qh[0], bh[n][0], bh[n][1]);
+                mma8_0(sl[n], ql[0], bh[n][0], bh[n][1]);
+                mma8_0(sx[n], qh[0], bl[n][0], bl[n][1]);
+              } else {
+                mma8(s[n], qh[2 * j + h], bh[n][2 * h], bh[n][2 * h + 1]);
+                mma8(sl[n], ql[2 * j + h], bh[n][2 * h], bh[n][2 * h + 1]);
+                mma8(sx[n], qh[2 * j + h], bl[n][2 * h], bl[n][2 * h + 1]);
+              }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sl[n][e] += sx[n][e];
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] += sl[n][e];
+      if (draft || left < kSub) {
+        const uint32_t in = left < kSub ? (1u << left) - 1 : 0xFFFFu;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t see = (draft ? (uint32_t)(vis[i] >> row0) & 0xFFFFu : in) >> (2 * qc);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (!(see >> (8 * n) & 1)) s[n][2 * i] = -INFINITY;
+            if (!(see >> (8 * n + 1) & 1)) s[n][2 * i + 1] = -INFINITY;
+          }
+        }
+      }
+      float corr[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx * rs[i]);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        corr[i] = ex2(m[i] - mu);
+        m[i] = mn;
+        const float bias = (F16 ? kBias : 0.f) - mu;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[n][2 * i + e] = ex2(fmaf(s[n][2 * i + e], rs[i], bias));
+            sum += s[n][2 * i + e];
+          }
+        l[i] = fmaf(l[i], corr[i], sum);
+      }
+
+      // draft rows whose values hold an infinity or NaN are taken out of the product and added
+      // where they are seen
+      uint32_t bad = 0;
+      if (draft) {
+        bool off = false;  // lanes 2 r, 2 r + 1 look at row r
+        const unsigned char* row = vp + (lane >> 1) * kRow + (lane & 1) * (kRow / 2);
+#pragma unroll
+        for (int c = 0; c < kRow / 32; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * c);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            off |= F16 ? ((u[e] & 0x7C00u) == 0x7C00u || (u[e] & 0x7C000000u) == 0x7C000000u)
+                       : (u[e] & kInfBits) == kInfBits;
+        }
+        const uint32_t any = __ballot_sync(0xffffffffu, off);
+        if (any) {
+#pragma unroll
+          for (int r = 0; r < kSub; ++r) bad |= (any >> (2 * r) & 3u ? 1u : 0u) << r;
+          if (bad >> (lane >> 1) & 1) {
+            uint4* z = reinterpret_cast<uint4*>(sm.ring[warp][slot][1]) + ((lane >> 1) * kRow + (lane & 1) * (kRow / 2)) / 16;
+#pragma unroll
+            for (int c = 0; c < kRow / 32; ++c) z[c] = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+          const KV* vrow = vd + (((int64_t)cur.b * a.n_kv + cur.h) * a.n_nodes + row0) * kHd;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if ((vis[i] >> row0) & bad) {  // the other rows keep every bit
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[d][2 * i] *= corr[i];
+                o[d][2 * i + 1] *= corr[i];
+              }
+              corr[i] = 1.f;
+            }
+#pragma unroll
+          for (int r = 0; r < kSub; ++r) {
+            if (!(bad >> r & 1)) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float p = __shfl_sync(0xffffffffu, s[r / 8][2 * i + (r & 1)], (lane & 28) | ((r & 7) >> 1));
+              if (!(vis[i] >> (row0 + r) & 1)) continue;
+#pragma unroll
+              for (int d = 0; d < 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  o[d][2 * i + e] += p * (float)vrow[r * kHd + (F16 ? 8 * d + 2 * qc + e : 16 * qc + 8 * e + d)];
+            }
+          }
+        }
+      }
+
+      if constexpr (F16) {
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2(s[e >> 1][2 * (e & 1)], s[e >> 1][2 * (e & 1) + 1], ph[e], pl[e]);
+        const int vr = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int d = 0; d < 8; d += 4) {
+          uint32_t b[2][4];
+          float t[4][4];
+          ldsm4t(vt + tile_off(vr, d + ((lane >> 4) & 1)), b[0]);
+          ldsm4t(vt + tile_off(vr, d + 2 + ((lane >> 4) & 1)), b[1]);
+          // the low parts first: what is cut off there does not count
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma0(t[x], pl, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma(t[x], ph, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d + x][e] = fmaf(o[d + x][e], corr[e >> 1], t[x][e]);
+        }
+      } else {
+        // k = qc of step t is position 8 t + 2 qc, k = qc + 4 the one after it; column n of
+        // product d is dim 8 n + d, so a lane's values are two chunks of each row
+        uint32_t ph[2][4], pl[2][4];
+        float v[2][2][8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          split_tf32(s[t][0], ph[t][0], pl[t][0]);
+          split_tf32(s[t][2], ph[t][1], pl[t][1]);
+          split_tf32(s[t][1], ph[t][2], pl[t][2]);
+          split_tf32(s[t][3], ph[t][3], pl[t][3]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * t + 2 * qc + e;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float4 x = *reinterpret_cast<const float4*>(vp + r * kRow + (((2 * qr + c) ^ swz(r)) << 4));
+              v[t][e][4 * c] = x.x;
+              v[t][e][4 * c + 1] = x.y;
+              v[t][e][4 * c + 2] = x.z;
+              v[t][e][4 * c + 3] = x.w;
+            }
+          }
+        }
+        // four products at a time, so that one's chain runs in the shadow of the others'
+#pragma unroll
+        for (int d0 = 0; d0 < 8; d0 += 4) {
+          uint32_t h[4][2][2], w[4][2][2];
+          float t0[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) split_tf32(v[t][e][d0 + x], h[x][t][e], w[x][t][e]);
+          // the low parts first: what is cut off there does not count
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma8_0(t0[x], pl[0], h[x][0][0], h[x][0][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma8(t0[x], pl[1], h[x][1][0], h[x][1][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma8(t0[x], ph[0], w[x][0][0], w[x][0][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma8(t0[x], ph[1], w[x][1][0], w[x][1][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma8(t0[x], ph[0], h[x][0][0], h[x][0][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma8(t0[x], ph[1], h[x][1][0], h[x][1][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d0 + x][e] = fmaf(o[d0 + x][e], corr[e >> 1], t0[x][e]);
+        }
+      }
+    }
+
+    // ---- the end of this CTA's part of the walk
+    if (last || !more) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      }
+      // warps 6, 7 -> 4, 5 -> 2, 3 -> 0, 1, then 1 -> 0, lane by lane
+#pragma unroll
+      for (int n = kWarps16 - 2; n >= 0; n -= 2) {
+        const int from = n ? n : 1, width = n ? 2 : 1, to = n ? n - 2 : 0;
+        __syncthreads();
+        if (warp >= from && warp < from + width) {
+          float(&mine)[36][32] = sm.join[warp - from];
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mine[4 * d + e][lane] = o[d][e];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mine[32 + i][lane] = m[i];
+            mine[34 + i][lane] = l[i];
+          }
+        }
+        __syncthreads();
+        if (warp >= to && warp < to + width) {
+          const float(&of)[36][32] = sm.join[warp - to];
+          float f[2], g[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mo = of[32 + i][lane], lo = of[34 + i][lane];
+            const float top = fmaxf(m[i], mo);
+            // a share without a maximum has l = 0 or NaN
+            f[i] = m[i] == -INFINITY ? l[i] : ex2(m[i] - top);
+            g[i] = mo == -INFINITY ? lo : ex2(mo - top);
+            m[i] = top;
+            l[i] = l[i] * f[i] + lo * g[i];
+          }
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = o[d][e] * f[e >> 1] + of[4 * d + e][lane] * g[e >> 1];
+        }
+      }
+      if (warp == 0) {
+        const bool whole = t_begin == 0 && last;
+        float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = qr + 8 * i;
+          if (whole && cur.r * 16 + r >= rows) continue;
+          const float inv = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
+          float* dst = whole ? row_of(a, a.out, cur, cur.r * 16 + r) : part + 32 + r * kHd;
+          if (!whole && qc == 0) {
+            part[r] = m[i];
+            part[16 + r] = l[i];
+          }
+          const bool none = whole && l[i] == 0.f;
+          float x[8][2];
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[d][e] = none ? 0.f : o[d][2 * i + e] * inv;
+          if constexpr (F16) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) reinterpret_cast<float2*>(dst)[4 * d + qc] = make_float2(x[d][0], x[d][1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                reinterpret_cast<float4*>(dst)[4 * qc + 2 * e + c] =
+                    make_float4(x[4 * c][e], x[4 * c + 1][e], x[4 * c + 2][e], x[4 * c + 3][e]);
+          }
+        }
+      }
+      t_begin = -1;
+    }
+    advance(sm.plan, a.n_kv, cur);
+  }
+  cp_wait<0>();
+}
+
 // Joins the parts of the walks that more than one CTA took (a warp to a row), and writes the
 // zeros of sequences whose position is out of range.
-template <int BM>
+template <int BM, bool BY16>
 __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int ctas) {
   __shared__ Plan plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) make_plan(a, BM, &plan);
+  if (warp == 0) make_plan<BY16>(a, BM, &plan);
   __syncthreads();
   pdl_wait();  // in every CTA: the end of this kernel is the end of both
   const int walk = blockIdx.x;  // (sequence, kv head, block of rows)
@@ -750,11 +1274,12 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
   *dst = lt == 0.f ? make_float2(0.f, 0.f) : make_float2(ot.x / lt, ot.y / lt);
 }
 
-// Rows to a block: all of them up to 64.
-inline int block_rows(int n_nodes, int group) {
-  const int r = n_nodes * group;
-  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
-}
+// The 16-row kernel up to so many rows to a kv head, the 64-row kernel behind them.
+#ifndef MAX16
+#define MAX16 32
+#endif
+inline bool by16(int n_nodes, int group) { return n_nodes * group <= MAX16; }
+inline int block_rows(int n_nodes, int group) { return by16(n_nodes, group) ? 16 : 64; }
 inline int blocks_of(int n_nodes, int group) {
   const int bm = block_rows(n_nodes, group);
   return (n_nodes * group + bm - 1) / bm;
@@ -762,33 +1287,29 @@ inline int blocks_of(int n_nodes, int group) {
 constexpr int kMaxCtas = 3;  // CTAs to an SM at most
 // CTAs of a call: what fits the device at once, and no more than there can be units for.
 inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, int per_sm) {
-  const int64_t units =
-      (int64_t)batch * n_kv * blocks_of(n_nodes, group) * ((max_ctx + (int64_t)kTile - 1) / kTile + 1 + kStart);
+  const int64_t units = (int64_t)batch * n_kv * blocks_of(n_nodes, group) *
+                        (walk_tiles(by16(n_nodes, group), max_ctx, n_nodes) + kStart);
   return (int)std::min<int64_t>((int64_t)attn_sm_count() * per_sm, (units + kMinPer - 1) / kMinPer);
 }
 
-template <bool F16, int WM, int WN>
-qd_status launch(const TreeAttnArgs& a, cudaStream_t st) {
-  static_assert(WM * WN * 32 == kThreads, "four warps");
-  auto kern = k_tree_attn<F16, WM, WN>;
-  const int smem = (int)sizeof(Smem<F16>);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QD_ERR_CUDA;
-  const int ctas =
-      a.whole ? a.batch * a.n_kv * a.blocks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, F16 ? 3 : 2);
-  kern<<<ctas, kThreads, smem, st>>>(a);
+template <int BM, bool BY16>
+qd_status launch(const TreeAttnArgs& a, void (*kern)(TreeAttnArgs), int threads, size_t smem, int per_sm,
+                 cudaStream_t st) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return QD_ERR_CUDA;
+  const int walks = a.batch * a.n_kv * a.blocks;
+  const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, per_sm);
+  kern<<<ctas, threads, smem, st>>>(a);
   const qd_status s = launch_status();
   if (s != QD_OK || a.whole) return s;
-  const dim3 grid((unsigned)(a.batch * a.n_kv * a.blocks), (unsigned)(16 * WM / 4));
-  return launch_k(k_tree_attn_join<16 * WM>, grid, dim3(kThreads), 0, st, true, a, ctas);
+  return launch_k(k_tree_attn_join<BM, BY16>, dim3((unsigned)walks, BM / 4), dim3(kThreads), 0, st, true, a, ctas);
 }
 
 template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
-  switch (block_rows(a.n_nodes, a.group)) {
-    case 16: return launch<F16, 1, 4>(a, st);
-    case 32: return launch<F16, 2, 2>(a, st);
-    default: return launch<F16, 4, 1>(a, st);
-  }
+  if (by16(a.n_nodes, a.group))
+    return launch<16, true>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), F16 ? 2 : 1, st);
+  return launch<64, false>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
 }
 
 // The units of a call must fit an int.
@@ -849,7 +1370,7 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   a.batch = batch;
   a.ws = static_cast<float*>(workspace);
   a.blocks = blocks_of(n_nodes, a.group);
-  a.whole = (max_ctx + kTile - 1) / kTile + 1 <= kWholeTiles;
+  a.whole = walk_tiles(by16(n_nodes, a.group), max_ctx, n_nodes) <= kWholeTiles;
   return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
 }
 
