@@ -33,18 +33,14 @@ constexpr int kHd = 64;
 constexpr int kTile = 64;     // positions of a tile; the drafts (at most 64) are one tile
 constexpr int kThreads = 128;  // 4 warps: WM blocks of 16 rows x WN shares of the positions
 constexpr float kBias = 12.f;  // log2 of the weights' scale
-constexpr int kMinPer = 4;     // units of a CTA at least
-#ifndef WT
-#define WT 8
-#define KS 3
-#endif
-constexpr int kWholeTiles = WT;  // walks of at most so many tiles are not cut
-constexpr int kStart = KS;      // what the start of a walk costs, in tiles
+constexpr int kMinPer = 2;     // units of a CTA at least
+constexpr int kWholeTiles = 8;  // walks of at most so many tiles are not cut
+constexpr int kStart = 3;      // what the start of a walk costs, in tiles
 
-// k_tree_attn_16: 8 warps, each with tiles of its own of 16 positions; what the warps do side by
-// side is one unit of work
-constexpr int kSub = 16;
+// k_tree_attn_16: 8 warps, each with tiles of its own of 16 (f32) or 32 positions; what the warps
+// do side by side is one unit of work
 constexpr int kWarps16 = 8;
+__host__ __device__ constexpr int sub_positions(bool f16) { return f16 ? 32 : 16; }
 static_assert(QD_MAX_TREE <= kTile, "the drafts fit one tile");
 
 struct TreeAttnArgs {
@@ -68,13 +64,13 @@ struct Plan {
   int nt[QD_MAX_BATCH], rb[QD_MAX_BATCH], p0[QD_MAX_BATCH], cnt[QD_MAX_BATCH];
 };
 
-// Tiles of a walk over p0 cached positions and cnt drafts.
-__host__ __device__ constexpr int walk_tiles(bool by16, int p0, int cnt) {
-  return by16 ? ((p0 + kSub - 1) / kSub + (cnt + kSub - 1) / kSub + kWarps16 - 1) / kWarps16
-              : (p0 + kTile - 1) / kTile + 1;
+// Tiles of a walk over p0 cached positions and cnt drafts; sub: sub_positions, or 0 for the
+// kernels with tiles of 64 positions.
+__host__ __device__ constexpr int walk_tiles(int sub, int p0, int cnt) {
+  return sub ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + kWarps16 - 1) / kWarps16 : (p0 + kTile - 1) / kTile + 1;
 }
 // Filled by one warp; `bm` rows to a block.
-template <bool BY16>
+template <int SUB>
 __device__ __forceinline__ void make_plan(const TreeAttnArgs& a, int bm, Plan* p) {
   const int b = threadIdx.x & 31;
   int units = 0;
@@ -82,7 +78,7 @@ __device__ __forceinline__ void make_plan(const TreeAttnArgs& a, int bm, Plan* p
     const int cnt = a.n_valid ? min(max(a.n_valid[b], 0), a.n_nodes) : a.n_nodes;
     const int p0 = a.pos[b];
     const int rb = (cnt * a.group + bm - 1) / bm;
-    const int nt = p0 < 0 || p0 > a.max_ctx ? 0 : walk_tiles(BY16, p0, cnt);
+    const int nt = p0 < 0 || p0 > a.max_ctx ? 0 : walk_tiles(SUB, p0, cnt);
     p->cnt[b] = cnt;
     p->p0[b] = p0;
     p->rb[b] = rb;
@@ -167,17 +163,34 @@ __device__ __forceinline__ int scale_exp(uint32_t abs_bits) { return min(max((in
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 constexpr uint32_t kInfBits = 0x7F800000u;
+__device__ __forceinline__ uint32_t abs_max(float4 x) {
+  return max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+}
+// The same without infinities and NaN.
+__device__ __forceinline__ uint32_t finite_max(float4 x) {
+  auto f = [](float v) { return abs_bits(v) < kInfBits ? abs_bits(v) : 0u; };
+  return max(max(f(x.x), f(x.y)), max(f(x.z), f(x.w)));
+}
 
 // Byte offset of 16-byte chunk c of row r in a tile of 64 rows of 64 binary16 values: chunks
 // permuted within a row so that 8 rows' same chunk (a matrix of ldmatrix) hits all banks.
 __device__ __forceinline__ uint32_t tile_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// A CTA's place in the units: the tile t of a walk (sequence, kv head, block of rows) and its unit.
+// A CTA's place in the units: the tile t of a walk (sequence, kv head, block of rows) and its
+// unit; with it the walk's tiles, positions and drafts, and the number of its kv head.
 struct Cursor {
   int b, h, r, t, u;
+  int nt, p0, cnt;
+  int64_t head;
+  __device__ __forceinline__ void enter(const Plan& p, int n_kv) {
+    nt = p.nt[b];
+    p0 = p.p0[b];
+    cnt = p.cnt[b];
+    head = (int64_t)b * n_kv + h;
+  }
 };
 // The first tile at or behind unit u.
-__device__ __forceinline__ Cursor cursor_at(const Plan& p, int u) {
+__device__ __forceinline__ Cursor cursor_at(const Plan& p, int n_kv, int u) {
   Cursor c;
   c.b = 0;
   while (u >= p.off[c.b + 1]) ++c.b;  // u < off[QD_MAX_BATCH]
@@ -186,19 +199,23 @@ __device__ __forceinline__ Cursor cursor_at(const Plan& p, int u) {
   c.u = p.off[c.b] + walk * len + kStart + c.t;
   c.h = walk / p.rb[c.b];
   c.r = walk % p.rb[c.b];
+  c.enter(p, n_kv);
   return c;
 }
 __device__ __forceinline__ void advance(const Plan& p, int n_kv, Cursor& c) {
   ++c.u;
-  if (++c.t < p.nt[c.b]) return;
+  if (++c.t < c.nt) return;
   c.u += kStart;
   c.t = 0;
   if (++c.r < p.rb[c.b]) return;
   c.r = 0;
-  if (++c.h < n_kv) return;
-  c.h = 0;
-  do ++c.b;
-  while (c.b < QD_MAX_BATCH - 1 && p.off[c.b] == p.off[c.b + 1]);
+  if (++c.h == n_kv) {
+    c.h = 0;
+    do ++c.b;
+    while (c.b < QD_MAX_BATCH - 1 && p.off[c.b] == p.off[c.b + 1]);
+    if (c.b == QD_MAX_BATCH) return;  // behind the last one
+  }
+  c.enter(p, n_kv);
 }
 
 // This CTA's first tile and the unit at which it ends; false if it has none (and zeros written
@@ -211,15 +228,19 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
     const int64_t first = (int64_t)blockIdx.x * per;
     if (first >= total) return false;
     end = min((int)first + per, total);
-    cur = cursor_at(p, (int)first);
+    cur = cursor_at(p, a.n_kv, (int)first);
     return cur.u < end;
   }
   const int walk = blockIdx.x;
-  cur = Cursor{walk / (a.n_kv * a.blocks), walk / a.blocks % a.n_kv, walk % a.blocks, 0, 0};
+  cur.b = walk / (a.n_kv * a.blocks);
+  cur.h = walk / a.blocks % a.n_kv;
+  cur.r = walk % a.blocks;
+  cur.t = cur.u = 0;
   if (cur.r >= p.rb[cur.b]) return false;
-  end = p.nt[cur.b];
+  cur.enter(p, a.n_kv);
+  end = cur.nt;
   if (end) return true;
-  const int rows = p.cnt[cur.b] * a.group;
+  const int rows = cur.cnt * a.group;
   for (int x = threadIdx.x; x < BM * (kHd / 4); x += blockDim.x) {
     const int at = cur.r * BM + x / (kHd / 4);
     if (at < rows) reinterpret_cast<float4*>(row_of(a, a.out, cur, at))[x % (kHd / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -266,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   const int qr = lane >> 2, qc = lane & 3;  // row and column pair of the lane in a fragment
 
   pdl_trigger();
-  if (warp == 0) make_plan<false>(a, BM, &sm.plan);
+  if (warp == 0) make_plan<0>(a, BM, &sm.plan);
   if (tid == 0) sm.bad = 0;
   __syncthreads();
   Cursor cur;
@@ -282,12 +303,10 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   // copy the tile at `pre` into ring slot s and move on; rows behind its end become zeros
   auto produce = [&](int s) {
     if (pre.u < end) {
-      const int p0 = sm.plan.p0[pre.b];
-      const bool draft = pre.t == sm.plan.nt[pre.b] - 1;
-      const int64_t head = (int64_t)pre.b * a.n_kv + pre.h;
+      const bool draft = pre.t == pre.nt - 1;
       const int row0 = draft ? 0 : pre.t * kTile;
-      const int rows = draft ? sm.plan.cnt[pre.b] : min(kTile, p0 - row0);
-      const int64_t base = draft ? head * a.n_nodes * kHd : (head * a.max_ctx + row0) * kHd;
+      const int rows = draft ? pre.cnt : min(kTile, pre.p0 - row0);
+      const int64_t base = (pre.head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
       const KV* ks = (draft ? kd : kc) + base;
       const KV* vs = (draft ? vd : vc) + base;
       constexpr int kPer = F16 ? 8 : 16;           // 16-byte chunks of a row
@@ -326,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   int t_begin = -1;   // first tile of this CTA's part of the walk; -1: a new walk begins
 
   for (int it = 0; cur.u < end; ++it) {
-    const int p0 = sm.plan.p0[cur.b], cnt = sm.plan.cnt[cur.b], nt = sm.plan.nt[cur.b];
+    const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
     const bool draft = cur.t == nt - 1;
     const bool more = cur.u + 1 + (draft ? kStart : 0) < end;  // this CTA has another tile
     const int rows = cnt * a.group;
@@ -413,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
       for (int i = 0; i < 8; ++i) {
         const int r = r0 + 8 * i;
         const float4 x = sm.raw[s][0][r * 16 + c];
-        uint32_t mx = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+        uint32_t mx = abs_max(x);
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         const int e = scale_exp(mx);
@@ -433,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float4 x = sm.raw[s][1][(r0 + 8 * i) * 16 + c];
-          const uint32_t rm = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
-          mx = max(mx, rm >= kInfBits ? 0u : rm);
+          const uint32_t rm = abs_max(x);
+          mx = max(mx, rm >= kInfBits ? finite_max(x) : rm);
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
       }
@@ -443,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
         const int r = r0 + 8 * i;
         float4 x = sm.raw[s][1][r * 16 + c];
         if (draft) {
-          mx = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+          mx = abs_max(x);
 #pragma unroll
           for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
           if (mx >= kInfBits) {  // as above: a row with an infinity or NaN is taken out
@@ -777,15 +796,16 @@ template <bool F16>
 struct Smem16 {
   static constexpr int kStages = 3;
   static constexpr int kRowBytes = F16 ? 128 : 256;
-  uint4 ring[kWarps16][kStages][2][kSub * kRowBytes / 16];  // K, V
+  uint4 ring[kWarps16][kStages][2][sub_positions(F16) * kRowBytes / 16];  // K, V
   float join[2][36][32];                                    // o, m, l of a warp's lanes
   Plan plan;
 };
 
 template <bool F16>
-__global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(TreeAttnArgs a) {
+__global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs a) {
   using KV = typename std::conditional<F16, __half, float>::type;
   using S = Smem16<F16>;
+  constexpr int kSub = sub_positions(F16), NT = kSub / 8;
   constexpr int kRow = S::kRowBytes;
   constexpr int kLag = S::kStages - 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -794,7 +814,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
   const int qr = lane >> 2, qc = lane & 3;
 
   pdl_trigger();
-  if (warp == 0) make_plan<true>(a, 16, &sm.plan);
+  if (warp == 0) make_plan<kSub>(a, 16, &sm.plan);
   __syncthreads();
   Cursor cur;
   int end;
@@ -810,14 +830,13 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
   // on to the next unit
   auto produce = [&](int s) {
     if (pre.u < end) {
-      const int p0 = sm.plan.p0[pre.b], cnt = sm.plan.cnt[pre.b];
+      const int p0 = pre.p0, cnt = pre.cnt;
       const int np = (p0 + kSub - 1) / kSub, sub = pre.t * kWarps16 + warp;
       const bool draft = sub >= np;
       const int row0 = (draft ? sub - np : sub) * kSub;
       const int rows = (draft ? cnt : p0) - row0;
       if (rows > 0) {
-        const int64_t head = (int64_t)pre.b * a.n_kv + pre.h;
-        const int64_t base = (head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
+        const int64_t base = (pre.head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
         const KV* ks = (draft ? kd : kc) + base;
         const KV* vs = (draft ? vd : vc) + base;
         const uint32_t dk = tc::smem_u32(sm.ring[warp][s][0]), dv = tc::smem_u32(sm.ring[warp][s][1]);
@@ -854,7 +873,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
   int t_begin = -1;
 
   for (int it = 0; cur.u < end; ++it) {
-    const int p0 = sm.plan.p0[cur.b], cnt = sm.plan.cnt[cur.b], nt = sm.plan.nt[cur.b];
+    const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
     const int rows = cnt * a.group;
     const bool last = cur.t == nt - 1;
     const bool more = cur.u + 1 + (last ? kStart : 0) < end;
@@ -923,25 +942,27 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
       const uint32_t kt = tc::smem_u32(sm.ring[warp][slot][0]), vt = tc::smem_u32(sm.ring[warp][slot][1]);
       const unsigned char* kp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][0]);
       const unsigned char* vp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][1]);
-      float s[2][4], sl[2][4];
+      float s[NT][4], sl[NT][4];
       if constexpr (F16) {
         const int kr = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t b[4];
-          ldsm4(kt + tile_off(kr, 2 * ks + ((lane >> 3) & 1)), b);
-          if (ks == 0) {
-            mma0(s[0], qh[ks], b[0], b[1]);
-            mma0(s[1], qh[ks], b[2], b[3]);
-            mma0(sl[0], ql[ks], b[0], b[1]);
-            mma0(sl[1], ql[ks], b[2], b[3]);
-          } else {
-            mma(s[0], qh[ks], b[0], b[1]);
-            mma(s[1], qh[ks], b[2], b[3]);
-            mma(sl[0], ql[ks], b[0], b[1]);
-            mma(sl[1], ql[ks], b[2], b[3]);
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4];
+            ldsm4(kt + tile_off(kr + 8 * n, 2 * ks + ((lane >> 3) & 1)), b);
+            if (ks == 0) {
+              mma0(s[n], qh[ks], b[0], b[1]);
+              mma0(s[n + 1], qh[ks], b[2], b[3]);
+              mma0(sl[n], ql[ks], b[0], b[1]);
+              mma0(sl[n + 1], ql[ks], b[2], b[3]);
+            } else {
+              mma(s[n], qh[ks], b[0], b[1]);
+              mma(s[n + 1], qh[ks], b[2], b[3]);
+              mma(sl[n], ql[ks], b[0], b[1]);
+              mma(sl[n + 1], ql[ks], b[2], b[3]);
+            }
           }
-        }
       } else {
         float sx[2][4];
 #pragma unroll
@@ -977,16 +998,16 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
           for (int e = 0; e < 4; ++e) sl[n][e] += sx[n][e];
       }
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] += sl[n][e];
       if (draft || left < kSub) {
-        const uint32_t in = left < kSub ? (1u << left) - 1 : 0xFFFFu;
+        const uint32_t in = left < kSub ? (1u << left) - 1 : ~0u;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t see = (draft ? (uint32_t)(vis[i] >> row0) & 0xFFFFu : in) >> (2 * qc);
+          const uint32_t see = (draft ? (uint32_t)(vis[i] >> row0) : in) >> (2 * qc);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < NT; ++n) {
             if (!(see >> (8 * n) & 1)) s[n][2 * i] = -INFINITY;
             if (!(see >> (8 * n + 1) & 1)) s[n][2 * i + 1] = -INFINITY;
           }
@@ -995,7 +1016,9 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
       float corr[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        float mx = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+        for (int n = 1; n < NT; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float mn = fmaxf(m[i], mx * rs[i]);
@@ -1005,7 +1028,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
         const float bias = (F16 ? kBias : 0.f) - mu;
         float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             s[n][2 * i + e] = ex2(fmaf(s[n][2 * i + e], rs[i], bias));
@@ -1018,11 +1041,11 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
       // where they are seen
       uint32_t bad = 0;
       if (draft) {
-        bool off = false;  // lanes 2 r, 2 r + 1 look at row r
-        const unsigned char* row = vp + (lane >> 1) * kRow + (lane & 1) * (kRow / 2);
+        bool off = false;  // half a row of f32 or a row of binary16 to a lane
+        uint4* row = reinterpret_cast<uint4*>(sm.ring[warp][slot][1]) + lane * 8;
 #pragma unroll
-        for (int c = 0; c < kRow / 32; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * c);
+        for (int c = 0; c < 8; ++c) {
+          const uint4 w = row[c];
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -1031,12 +1054,15 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
         }
         const uint32_t any = __ballot_sync(0xffffffffu, off);
         if (any) {
+          bad = any;
+          if (!F16) {
+            bad = 0;
 #pragma unroll
-          for (int r = 0; r < kSub; ++r) bad |= (any >> (2 * r) & 3u ? 1u : 0u) << r;
-          if (bad >> (lane >> 1) & 1) {
-            uint4* z = reinterpret_cast<uint4*>(sm.ring[warp][slot][1]) + ((lane >> 1) * kRow + (lane & 1) * (kRow / 2)) / 16;
+            for (int r = 0; r < kSub; ++r) bad |= (any >> (2 * r & 31) & 3u ? 1u : 0u) << r;
+          }
+          if (bad >> (F16 ? lane : lane >> 1) & 1) {
 #pragma unroll
-            for (int c = 0; c < kRow / 32; ++c) z[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
           }
           __syncwarp();
           const KV* vrow = vd + (((int64_t)cur.b * a.n_kv + cur.h) * a.n_nodes + row0) * kHd;
@@ -1068,21 +1094,34 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
       }
 
       if constexpr (F16) {
-        uint32_t ph[4], pl[4];
+        uint32_t ph[NT / 2][4], pl[NT / 2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2(s[e >> 1][2 * (e & 1)], s[e >> 1][2 * (e & 1) + 1], ph[e], pl[e]);
+        for (int k = 0; k < NT / 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            split2(s[2 * k + (e >> 1)][2 * (e & 1)], s[2 * k + (e >> 1)][2 * (e & 1) + 1], ph[k][e], pl[k][e]);
         const int vr = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
         for (int d = 0; d < 8; d += 4) {
-          uint32_t b[2][4];
+          uint32_t b[NT / 2][2][4];
           float t[4][4];
-          ldsm4t(vt + tile_off(vr, d + ((lane >> 4) & 1)), b[0]);
-          ldsm4t(vt + tile_off(vr, d + 2 + ((lane >> 4) & 1)), b[1]);
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ldsm4t(vt + tile_off(vr + 16 * k, d + 2 * x + ((lane >> 4) & 1)), b[k][x]);
           // the low parts first: what is cut off there does not count
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma0(t[x], pl, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
+          for (int k = 0; k < NT / 2; ++k)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma(t[x], ph, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
+            for (int x = 0; x < 4; ++x)
+              if (k == 0)
+                mma0(t[x], pl[k], b[k][x >> 1][2 * (x & 1)], b[k][x >> 1][2 * (x & 1) + 1]);
+              else
+                mma(t[x], pl[k], b[k][x >> 1][2 * (x & 1)], b[k][x >> 1][2 * (x & 1) + 1]);
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mma(t[x], ph[k], b[k][x >> 1][2 * (x & 1)], b[k][x >> 1][2 * (x & 1) + 1]);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -1227,32 +1266,491 @@ __global__ void __launch_bounds__(kWarps16 * 32, F16 ? 2 : 1) k_tree_attn_16(Tre
   cp_wait<0>();
 }
 
-// Joins the parts of the walks that more than one CTA took (a warp to a row), and writes the
-// zeros of sequences whose position is out of range.
-template <int BM, bool BY16>
+// ------------------------------------------------------------------ 128 rows
+// Many rows to a kv head: blocks of 128 on the 5th-generation tensor cores, two threads to a row.
+// Per tile of 64 positions one thread issues s = q k^T (tcgen05.mma, M = 128, N = 64, both
+// operands in shared memory) into tensor memory; a row's threads read 32 scores each (tcgen05.ld),
+// exchange their maxima, and write their weights' two parts over the scores as the A operand of
+// o = p v (V as it lies, [position][dim], is the transposed B operand); each adds 32 dims of the
+// tile's o to its own registers, rounded.  The operands' splits are those of the other kernels.
+// Two CTAs to an SM, one's products under the other's softmax.
+// Tiles lie as 8 x 8 core matrices of 128 bytes: row r, 16-byte chunk c at core_off(r, c), which
+// K (rows, 16 bytes of dims) and V (8 positions x 16 bytes of dims) share.
+constexpr int kThreads128 = 256;
+__device__ __forceinline__ uint32_t core_off(int r, int c) {
+  return (uint32_t)((((r >> 3) * 8 + c) * 128) + (r & 7) * 16);
+}
+constexpr uint32_t kIdescS = tc::idesc_f16(128, kTile);
+constexpr uint32_t kIdescO = tc::idesc_f16(128, kHd) | (1u << 16);  // B with N contiguous
+// One lane of the (whole) calling warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(p));
+  return p != 0;
+}
+constexpr uint32_t kColsS = 64, kCols128 = 128;                     // s, later p; then o
+
+// 16 consecutive 32-bit columns of this thread's tensor-memory lane
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <bool F16>
+struct Smem128 {
+  static constexpr int kStages = F16 ? 3 : 1;
+  uint4 q[2][128 * 8];                             // hi, lo
+  uint4 ring[kStages][2][kTile * (F16 ? 8 : 16)];  // K, V as they are
+  uint4 tile[F16 ? 1 : 4][F16 ? 1 : kTile * 8];    // f32 cache: K hi, K lo, V hi, V lo
+  float kscale[kTile], vscale[kTile];
+  float ex[2][128];                                // what a row's threads tell each other
+  unsigned long long mbar[2];                      // s, o
+  unsigned long long bad;
+  uint32_t tmem;
+  Plan plan;
+};
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a) {
+  using KV = typename std::conditional<F16, __half, float>::type;
+  using S = Smem128<F16>;
+  constexpr int BM = 128, NS = kTile / 2, ND = kHd / 2;  // scores and dims of a thread
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int lrow = tid & 127, half = tid >> 7;
+  const int uwarp = __shfl_sync(0xffffffffu, warp, 0);  // known to be the warp's: descriptors stay in uniform registers
+
+  pdl_trigger();
+  if (warp == 0) make_plan<0>(a, BM, &sm.plan);
+  __syncthreads();
+  Cursor cur;
+  int end;
+  if (!first_tile<BM>(a, sm.plan, cur, end)) return;
+  Cursor pre = cur;
+
+  const uint32_t mb_s = tc::smem_u32(&sm.mbar[0]), mb_o = tc::smem_u32(&sm.mbar[1]);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&sm.tmem)),
+                 "r"(kCols128)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    sm.bad = 0;
+    tc::mbar_init(mb_s, 1);
+    tc::mbar_init(mb_o, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+
+  const KV* kc = static_cast<const KV*>(a.kc);
+  const KV* vc = static_cast<const KV*>(a.vc);
+  const KV* kd = static_cast<const KV*>(a.kd);
+  const KV* vd = static_cast<const KV*>(a.vd);
+
+  // copy the tile at `pre` into ring slot s and move on; rows behind its end become zeros
+  auto produce = [&](int s) {
+    if (pre.u < end) {
+      const bool draft = pre.t == pre.nt - 1;
+      const int row0 = draft ? 0 : pre.t * kTile;
+      const int rows = draft ? pre.cnt : min(kTile, pre.p0 - row0);
+      const int64_t base = (pre.head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
+      const KV* ks = (draft ? kd : kc) + base;
+      const KV* vs = (draft ? vd : vc) + base;
+      const uint32_t dk = tc::smem_u32(sm.ring[s][0]), dv = tc::smem_u32(sm.ring[s][1]);
+      // binary16: 8 rows x 4 chunks to a warp, which fill four core matrices; f32: linear
+      constexpr int kIter = kTile * (F16 ? 8 : 16) / kThreads128;
+      constexpr int kRows = kThreads128 / (F16 ? 8 : 16);  // rows of an iteration
+      const int r0 = F16 ? (tid & 7) + (tid >> 6) * 8 : tid >> 4, c = F16 ? (tid >> 3) & 7 : tid & 15;
+      const uint32_t off = F16 ? core_off(r0, c) : (uint32_t)tid * 16;
+      const int first = r0 * kHd + c * (16 / (int)sizeof(KV));
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const uint32_t to = off + i * kRows * (F16 ? 128 : 256);
+        if (rows >= kTile) {
+          cp16(dk + to, ks + first + i * kRows * kHd);
+          cp16(dv + to, vs + first + i * kRows * kHd);
+        } else {
+          const bool live = r0 + i * kRows < rows;
+          const int src = live ? first + i * kRows * kHd : 0;
+          cp16(dk + to, ks + src, live);
+          cp16(dv + to, vs + src, live);
+        }
+      }
+      advance(sm.plan, a.n_kv, pre);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < (F16 ? S::kStages - 1 : 1); ++s) produce(s);
+
+  float o[ND];
+  float m = -INFINITY, l = 0.f, rs = 1.f, vunit = 1.f;
+  uint64_t vis = 0;
+  int t_begin = -1;
+  bool lost = false;  // a wait has run out: the result is NaN
+
+  for (int it = 0; cur.u < end; ++it) {
+    const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
+    const bool draft = cur.t == nt - 1;
+    const bool more = cur.u + 1 + (draft ? kStart : 0) < end;
+    const int rows = cnt * a.group;
+    const int row = cur.r * BM + lrow;
+    const bool warp_live = cur.r * BM + 32 * (warp & 3) < rows;
+    if (t_begin < 0) {
+      // the last walk's products are done (every thread has waited for its o): q may change
+      t_begin = cur.t;
+      const bool live = row < rows;
+      const float* src = row_of(a, const_cast<float*>(a.q), cur, live ? row : 0);
+      src += (int64_t)cur.b * (a.q_batch_stride - (int64_t)a.n_nodes * a.n_kv * a.group * kHd) + half * ND;
+      float4 x[8];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        x[c] = live ? __ldcg(reinterpret_cast<const float4*>(src) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
+        x[c].x *= scale;
+        x[c].y *= scale;
+        x[c].z *= scale;
+        x[c].w *= scale;
+        mx = max(mx, abs_max(x[c]));
+      }
+      sm.ex[half][lrow] = __uint_as_float(mx);
+      vis = live ? a.mask[(int64_t)cur.b * a.n_nodes + row / a.group] : 0ull;
+      if (cnt < 64) vis &= (1ull << cnt) - 1;
+      __syncthreads();
+      const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
+      rs = pow2(e);
+      const float f = pow2(-e);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint4 hi, lo;
+        split2(x[2 * c].x * f, x[2 * c].y * f, hi.x, lo.x);
+        split2(x[2 * c].z * f, x[2 * c].w * f, hi.y, lo.y);
+        split2(x[2 * c + 1].x * f, x[2 * c + 1].y * f, hi.z, lo.z);
+        split2(x[2 * c + 1].z * f, x[2 * c + 1].w * f, hi.w, lo.w);
+        sm.q[0][core_off(lrow, 4 * half + c) / 16] = hi;
+        sm.q[1][core_off(lrow, 4 * half + c) / 16] = lo;
+      }
+      m = -INFINITY;
+      l = 0.f;
+      vunit = pow2(-100);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] = 0.f;
+    }
+
+    // ---- the tile arrives
+    const int slot = it % S::kStages;
+    uint32_t k_hi, k_lo = 0, v_hi, v_lo = 0;
+    if constexpr (F16) {
+      cp_wait<S::kStages - 2>();
+      k_hi = tc::smem_u32(sm.ring[slot][0]);
+      v_hi = tc::smem_u32(sm.ring[slot][1]);
+      if (draft) {
+        // a value row with an infinity or NaN would reach every row of the product (0 times
+        // it is NaN): such rows are taken out here and added below where they are seen
+        __syncthreads();
+        const int r = tid >> 2;
+        uint32_t off = 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 w = sm.ring[slot][1][core_off(r, (tid & 3) * 2 + c) / 16];
+          off |= (((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
+                  ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u)) &
+                 0x80008000u;
+        }
+        off |= __shfl_xor_sync(0xffffffffu, off, 1);
+        off |= __shfl_xor_sync(0xffffffffu, off, 2);
+        if (off) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) sm.ring[slot][1][core_off(r, (tid & 3) * 2 + c) / 16] = make_uint4(0, 0, 0, 0);
+          if (!(tid & 3)) atomicOr(&sm.bad, 1ull << r);
+        }
+      }
+    } else {
+      cp_wait<0>();
+      __syncthreads();
+      // four threads to a position, 16 dims each; their 16-byte reads in an order without bank
+      // conflicts
+      const int r = tid >> 2, j = tid & 3, turn = (j >> 1) + 2 * (r & 1);
+      const float4* kraw = reinterpret_cast<const float4*>(sm.ring[0][0]) + r * 16 + 4 * j;
+      const float4* vraw = reinterpret_cast<const float4*>(sm.ring[0][1]) + r * 16 + 4 * j;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        float4 x[4];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = (kv ? vraw : kraw)[i ^ turn];
+          mx = max(mx, abs_max(x[i]));
+        }
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (kv && mx >= kInfBits) {
+          mx = 0;
+          if (draft) {  // as above: a row with an infinity or NaN is taken out
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j == 0) atomicOr(&sm.bad, 1ull << r);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = max(mx, finite_max(x[i]));
+            const unsigned quad = 15u << (threadIdx.x & 28);
+            mx = max(mx, __shfl_xor_sync(quad, mx, 1));
+            mx = max(mx, __shfl_xor_sync(quad, mx, 2));
+          }
+        }
+        const int e = scale_exp(mx);
+        const float f = pow2(-e);
+        uint2* th = reinterpret_cast<uint2*>(sm.tile[2 * kv]);
+        uint2* tl = reinterpret_cast<uint2*>(sm.tile[2 * kv + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint2 hi, lo;
+          split2(x[i].x * f, x[i].y * f, hi.x, lo.x);
+          split2(x[i].z * f, x[i].w * f, hi.y, lo.y);
+          const int c = 4 * j + (i ^ turn);
+          const uint32_t at = core_off(r, c >> 1) / 8 + (c & 1);
+          th[at] = hi;
+          tl[at] = lo;
+        }
+        if (j == 0) (kv ? sm.vscale : sm.kscale)[r] = pow2(e);
+      }
+      k_hi = tc::smem_u32(sm.tile[0]);
+      k_lo = tc::smem_u32(sm.tile[1]);
+      v_hi = tc::smem_u32(sm.tile[2]);
+      v_lo = tc::smem_u32(sm.tile[3]);
+    }
+    tc::fence_proxy_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+
+    // ---- scores
+    if (uwarp == 0 && elect_one()) {
+      tc::fence_after_sync();
+      const uint32_t q_hi = tc::smem_u32(sm.q[0]), q_lo = tc::smem_u32(sm.q[1]);
+      // the low parts first: what is cut off there does not count
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        tc::mma_f16_ss(tm, tc::smem_desc(q_lo + 256 * ks, 128, 1024), tc::smem_desc(k_hi + 256 * ks, 128, 1024),
+                       kIdescS, ks > 0);
+        if constexpr (!F16)
+          tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), tc::smem_desc(k_lo + 256 * ks, 128, 1024),
+                         kIdescS, 1);
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), tc::smem_desc(k_hi + 256 * ks, 128, 1024),
+                       kIdescS, 1);
+      tc::mma_commit(mb_s);
+    }
+    produce(F16 ? (it + S::kStages - 1) % S::kStages : 0);  // the last tile's slot; f32: all threads have read it
+    if (!lost && !tc::mbar_wait_sleep(mb_s, (uint32_t)it & 1u)) lost = true;
+    tc::fence_after_sync();
+
+    float s[NS];
+    float corr = 1.f, mt = -INFINITY;
+    if (warp_live) {
+      tc::tmem_ld32(mine + NS * half, s);
+      if constexpr (!F16) {
+#pragma unroll
+        for (int j = 0; j < NS; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.kscale[NS * half + j]);
+          s[j] *= f.x;
+          s[j + 1] *= f.y;
+          s[j + 2] *= f.z;
+          s[j + 3] *= f.w;
+        }
+      }
+      if (draft || p0 - cur.t * kTile < kTile) {
+        const uint32_t see = (uint32_t)((draft ? vis : (1ull << (p0 - cur.t * kTile)) - 1) >> (NS * half));
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+          if (!(see >> j & 1)) s[j] = -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int j = 4; j < NS; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+      mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs;
+      sm.ex[half][lrow] = mt;
+    }
+    tc::fence_before_sync();
+    __syncthreads();  // the row's other half is read, and its maximum known
+    tc::fence_after_sync();
+    float vinv = 1.f;
+    if (warp_live) {
+      // ---- online softmax
+      const float mn = fmaxf(m, fmaxf(mt, sm.ex[half ^ 1][lrow]));
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      corr = ex2(m - mu);
+      m = mn;
+      const float bias = kBias - mu;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        s[j] = ex2(fmaf(s[j], rs, bias));
+        sum[j & 3] += s[j];
+      }
+      l = fmaf(l, corr, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if constexpr (!F16) {  // the weights take over the scale of their v rows
+        const uint64_t see = draft ? vis : ~0ull;
+        float top = vunit;
+#pragma unroll
+        for (int j = 0; j < kTile; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.vscale[j]);
+          if (draft)
+            top = fmaxf(top, fmaxf(fmaxf(see >> j & 1 ? f.x : 0.f, see >> (j + 1) & 1 ? f.y : 0.f),
+                                   fmaxf(see >> (j + 2) & 1 ? f.z : 0.f, see >> (j + 3) & 1 ? f.w : 0.f)));
+          else
+            top = fmaxf(fmaxf(top, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
+        }
+        vinv = __uint_as_float((254u << 23) - __float_as_uint(top));  // 1 / top, a power of two
+        corr *= vunit * vinv;
+        vunit = top;
+      }
+      // ---- the weights' parts over the scores
+      uint32_t hi[NS / 2], lo[NS / 2];
+#pragma unroll
+      for (int j = 0; j < NS; j += 2) {
+        float x = s[j], y = s[j + 1];
+        if constexpr (!F16) {
+          const float2 f = *reinterpret_cast<const float2*>(&sm.vscale[NS * half + j]);
+          x = x * vinv * f.x;
+          y = y * vinv * f.y;
+        }
+        split2(x, y, hi[j / 2], lo[j / 2]);
+      }
+      tmem_st16(mine + NS / 2 * half, hi);
+      tmem_st16(mine + 32 + NS / 2 * half, lo);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    }
+    const unsigned long long bad = draft ? sm.bad : 0ull;
+    if (bad) {
+      if (vis & bad) {  // the other rows keep every bit
+        const int64_t at = ((int64_t)cur.b * a.n_kv + cur.h) * a.n_nodes * kHd;
+        const float* qrow = row_of(a, const_cast<float*>(a.q), cur, row) +
+                            (int64_t)cur.b * (a.q_batch_stride - (int64_t)a.n_nodes * a.n_kv * a.group * kHd);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] *= corr;
+        corr = 1.f;
+        for (int j = 0; j < kTile; ++j) {
+          if (!((vis & bad) >> j & 1)) continue;
+          float x = 0.f;
+          for (int d = 0; d < kHd; ++d) x = fmaf(qrow[d], (float)kd[at + j * kHd + d], x);
+          const float p = ex2(fmaf(x, 1.4426950408889634f * 0.125f, kBias - (m == -INFINITY ? 0.f : m)));
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[d] += p * ((float)vd[at + j * kHd + half * ND + d] * vinv);
+        }
+      }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+
+    // ---- weighted values
+    if (uwarp == 0 && elect_one()) {
+      tc::fence_after_sync();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {  // 16 positions: 8 columns of p, two rows of core matrices of v
+        tc::mma_f16_ts(tm + kColsS, tm + 32 + 8 * kk, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, kk > 0);
+        if constexpr (!F16)
+          tc::mma_f16_ts(tm + kColsS, tm + 8 * kk, tc::smem_desc(v_lo + 2048 * kk, 1024, 128), kIdescO, 1);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        tc::mma_f16_ts(tm + kColsS, tm + 8 * kk, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, 1);
+      tc::mma_commit(mb_o);
+    }
+    if (!lost && !tc::mbar_wait_sleep(mb_o, (uint32_t)it & 1u)) lost = true;
+    tc::fence_after_sync();
+    if (warp_live) {
+      float t[ND];
+      tc::tmem_ld32(mine + kColsS + ND * half, t);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] = fmaf(o[d], corr, t[d]);
+    }
+
+    // ---- the end of this CTA's part of the walk
+    if (draft || !more) {
+      const bool whole = t_begin == 0 && draft;
+      __syncthreads();  // every thread has read `bad` and `ex`
+      if (lost) l = NAN;
+      sm.ex[half][lrow] = l;
+      if (tid == 0) sm.bad = 0;
+      __syncthreads();
+      const float lt = l + sm.ex[half ^ 1][lrow];
+      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(BM);
+      if (!whole && half == 0) {
+        part[lrow] = m;
+        part[BM + lrow] = lt;
+      }
+      if (!whole || row < rows) {
+        const float inv = !whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt, unit = F16 ? 1.f : vunit;
+        float4* dst = reinterpret_cast<float4*>((whole ? row_of(a, a.out, cur, row) : part + 2 * BM + lrow * kHd) +
+                                                half * ND);
+        const bool none = whole && lt == 0.f;
+#pragma unroll
+        for (int d = 0; d < ND; d += 4)
+          dst[d / 4] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(o[d] * inv * unit, o[d + 1] * inv * unit, o[d + 2] * inv * unit,
+                                          o[d + 3] * inv * unit);
+      }
+      t_begin = -1;
+      __syncthreads();  // `ex` is read
+    }
+    advance(sm.plan, a.n_kv, cur);
+  }
+  cp_wait<0>();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kCols128) : "memory");
+}
+
+// Joins the parts of the walks that more than one CTA took, a warp to a row: block x the walk, if
+// any, whose first tile is CTA x's and whose last is not.  Also the zeros of the sequences whose
+// position is out of range.
+template <int BM, int SUB>
 __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int ctas) {
   __shared__ Plan plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) make_plan<BY16>(a, BM, &plan);
+  if (warp == 0) make_plan<SUB>(a, BM, &plan);
   __syncthreads();
   pdl_wait();  // in every CTA: the end of this kernel is the end of both
-  const int walk = blockIdx.x;  // (sequence, kv head, block of rows)
-  const int b = walk / (a.n_kv * a.blocks), h = walk / a.blocks % a.n_kv, rb = walk % a.blocks;
-  const int r = blockIdx.y * 4 + warp, at = rb * BM + r;
-  if (at >= plan.cnt[b] * a.group) return;
-  float2* dst = reinterpret_cast<float2*>(
-                    a.out + (((int64_t)b * a.n_nodes + at / a.group) * a.n_kv * a.group + h * a.group + at % a.group) *
-                                kHd) +
-                lane;
-  const int nt = plan.nt[b];
-  if (!nt) {
-    *dst = make_float2(0.f, 0.f);
-    return;
+  const int first = blockIdx.x;
+  if (first < a.batch && !plan.nt[first]) {
+    const int64_t n = (int64_t)plan.cnt[first] * a.n_kv * a.group * (kHd / 4);
+    float4* z = reinterpret_cast<float4*>(a.out + (int64_t)first * a.n_nodes * a.n_kv * a.group * kHd);
+    for (int64_t x = (int64_t)blockIdx.y * kThreads + threadIdx.x; x < n; x += (int64_t)gridDim.y * kThreads)
+      z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int per = units_per_cta(plan.off[QD_MAX_BATCH], ctas);
-  const int g0 = plan.off[b] + (h * plan.rb[b] + rb) * (nt + kStart) + kStart;  // the first tile's unit
+  const int total = plan.off[QD_MAX_BATCH], per = units_per_cta(total, ctas);
+  if ((int64_t)first * per >= total) return;
+  const int last_unit = min((int64_t)(first + 1) * per, (int64_t)total) - 1;
+  Cursor cur;  // the walk of this CTA's last unit
+  cur.b = 0;
+  while (last_unit >= plan.off[cur.b + 1]) ++cur.b;
+  const int nt = plan.nt[cur.b], walk = (last_unit - plan.off[cur.b]) / (nt + kStart);
+  cur.h = walk / plan.rb[cur.b];
+  cur.r = walk % plan.rb[cur.b];
+  const int g0 = plan.off[cur.b] + walk * (nt + kStart) + kStart;  // its first tile's unit
   const int c0 = g0 / per, c1 = (g0 + nt - 1) / per;
-  if (c0 == c1) return;
+  const int r = blockIdx.y * (kThreads / 32) + warp, at = cur.r * BM + r;
+  if (c0 != first || c0 == c1 || at >= plan.cnt[cur.b] * a.group) return;
+  float2* dst = reinterpret_cast<float2*>(row_of(a, a.out, cur, at)) + lane;
   // the walk begins in its first CTA (slot 1: that CTA's last part) and is the first part of the others
   auto part = [&](int c) { return a.ws + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats(BM); };
   float mt = -INFINITY;
@@ -1275,41 +1773,42 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
 }
 
 // The 16-row kernel up to so many rows to a kv head, the 64-row kernel behind them.
-#ifndef MAX16
-#define MAX16 32
-#endif
-inline bool by16(int n_nodes, int group) { return n_nodes * group <= MAX16; }
-inline int block_rows(int n_nodes, int group) { return by16(n_nodes, group) ? 16 : 64; }
+inline bool by16(int n_nodes, int group) { return n_nodes * group <= 32; }
+inline int block_rows(int n_nodes, int group) {
+  return by16(n_nodes, group) ? 16 : n_nodes * group <= 64 ? 64 : 128;
+}
 inline int blocks_of(int n_nodes, int group) {
   const int bm = block_rows(n_nodes, group);
   return (n_nodes * group + bm - 1) / bm;
 }
 constexpr int kMaxCtas = 3;  // CTAs to an SM at most
 // CTAs of a call: what fits the device at once, and no more than there can be units for.
-inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, int per_sm) {
+inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, int sub, int per_sm) {
   const int64_t units = (int64_t)batch * n_kv * blocks_of(n_nodes, group) *
-                        (walk_tiles(by16(n_nodes, group), max_ctx, n_nodes) + kStart);
+                        (walk_tiles(sub, max_ctx, n_nodes) + kStart);
   return (int)std::min<int64_t>((int64_t)attn_sm_count() * per_sm, (units + kMinPer - 1) / kMinPer);
 }
 
-template <int BM, bool BY16>
+template <int BM, int SUB>
 qd_status launch(const TreeAttnArgs& a, void (*kern)(TreeAttnArgs), int threads, size_t smem, int per_sm,
                  cudaStream_t st) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return QD_ERR_CUDA;
   const int walks = a.batch * a.n_kv * a.blocks;
-  const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, per_sm);
+  const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, SUB, per_sm);
   kern<<<ctas, threads, smem, st>>>(a);
   const qd_status s = launch_status();
   if (s != QD_OK || a.whole) return s;
-  return launch_k(k_tree_attn_join<BM, BY16>, dim3((unsigned)walks, BM / 4), dim3(kThreads), 0, st, true, a, ctas);
+  return launch_k(k_tree_attn_join<BM, SUB>, dim3((unsigned)ctas, BM / 4), dim3(kThreads), 0, st, true, a, ctas);
 }
 
 template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
   if (by16(a.n_nodes, a.group))
-    return launch<16, true>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), F16 ? 2 : 1, st);
-  return launch<64, false>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
+    return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), 1, st);
+  if (block_rows(a.n_nodes, a.group) == 128)
+    return launch<128, 0>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>), 2, st);
+  return launch<64, 0>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
 }
 
 // The units of a call must fit an int.
@@ -1331,7 +1830,9 @@ extern "C" {
 size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch) {
   if (!tree_shape_ok(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch)) return 0;
   const int group = n_heads / n_kv_heads;
-  return (size_t)tree_ctas(n_kv_heads, group, n_nodes, max_ctx, batch, kMaxCtas) * 2 *
+  // of either cache type: the finest tiles ask for the most CTAs
+  const int sub = by16(n_nodes, group) ? sub_positions(false) : 0;
+  return (size_t)tree_ctas(n_kv_heads, group, n_nodes, max_ctx, batch, sub, kMaxCtas) * 2 *
          part_floats(block_rows(n_nodes, group)) * sizeof(float);
 }
 
@@ -1370,7 +1871,7 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   a.batch = batch;
   a.ws = static_cast<float*>(workspace);
   a.blocks = blocks_of(n_nodes, a.group);
-  a.whole = walk_tiles(by16(n_nodes, a.group), max_ctx, n_nodes) <= kWholeTiles;
+  a.whole = walk_tiles(by16(n_nodes, a.group) ? sub_positions(kv_f16) : 0, max_ctx, n_nodes) <= kWholeTiles;
   return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
 }
 
