@@ -64,10 +64,10 @@ struct Plan {
   int nt[QD_MAX_BATCH], rb[QD_MAX_BATCH], p0[QD_MAX_BATCH], cnt[QD_MAX_BATCH];
 };
 
-// Tiles of a walk over p0 cached positions and cnt drafts; sub: sub_positions, or 0 for the
-// kernels with tiles of 64 positions.
+// Tiles of a walk over p0 cached positions and cnt drafts; sub: sub_positions, or minus the
+// positions of a tile that the whole CTA takes (the drafts are one such tile).
 __host__ __device__ constexpr int walk_tiles(int sub, int p0, int cnt) {
-  return sub ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + kWarps16 - 1) / kWarps16 : (p0 + kTile - 1) / kTile + 1;
+  return sub > 0 ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + kWarps16 - 1) / kWarps16 : (p0 - sub - 1) / -sub + 1;
 }
 // Filled by one warp; `bm` rows to a block.
 template <int SUB>
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArg
   const int qr = lane >> 2, qc = lane & 3;  // row and column pair of the lane in a fragment
 
   pdl_trigger();
-  if (warp == 0) make_plan<0>(a, BM, &sm.plan);
+  if (warp == 0) make_plan<-kTile>(a, BM, &sm.plan);
   if (tid == 0) sm.bad = 0;
   __syncthreads();
   Cursor cur;
@@ -1268,11 +1268,13 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
 
 // ------------------------------------------------------------------ 128 rows
 // Many rows to a kv head: blocks of 128 on the 5th-generation tensor cores, two threads to a row.
-// Per tile of 64 positions one thread issues s = q k^T (tcgen05.mma, M = 128, N = 64, both
-// operands in shared memory) into tensor memory; a row's threads read 32 scores each (tcgen05.ld),
-// exchange their maxima, and write their weights' two parts over the scores as the A operand of
-// o = p v (V as it lies, [position][dim], is the transposed B operand); each adds 32 dims of the
-// tile's o to its own registers, rounded.  The operands' splits are those of the other kernels.
+// Per tile (128 positions of a binary16 cache, 64 of an f32 one) one thread issues s = q k^T
+// (tcgen05.mma, M = 128, both operands in shared memory) into tensor memory; a row's threads read
+// half of its scores each (tcgen05.ld), exchange their maxima, read the scores again 16 at a time
+// (which leaves the registers for two CTAs to an SM without a spill: the shared memory leaves
+// spills no L1) and write the weights' two parts over them as the A operand of o = p v (V as it lies,
+// [position][dim], is the transposed B operand); each adds 32 dims of the tile's o to its own
+// registers, rounded.  The operands' splits are those of the other kernels.
 // Two CTAs to an SM, one's products under the other's softmax.
 // Tiles lie as 8 x 8 core matrices of 128 bytes: row r, 16-byte chunk c at core_off(r, c), which
 // K (rows, 16 bytes of dims) and V (8 positions x 16 bytes of dims) share.
@@ -1280,7 +1282,7 @@ constexpr int kThreads128 = 256;
 __device__ __forceinline__ uint32_t core_off(int r, int c) {
   return (uint32_t)((((r >> 3) * 8 + c) * 128) + (r & 7) * 16);
 }
-constexpr uint32_t kIdescS = tc::idesc_f16(128, kTile);
+__host__ __device__ constexpr int tile128(bool f16) { return f16 ? 128 : 64; }
 constexpr uint32_t kIdescO = tc::idesc_f16(128, kHd) | (1u << 16);  // B with N contiguous
 // One lane of the (whole) calling warp.
 __device__ __forceinline__ bool elect_one() {
@@ -1294,29 +1296,78 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
-constexpr uint32_t kColsS = 64, kCols128 = 128;                     // s, later p; then o
 
-// 16 consecutive 32-bit columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// 16 consecutive 32-bit columns of this thread's tensor-memory lane read, 8 written
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// two f32 operations at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n"
+      ".reg .b64 a, b, c, d;\n"
+      "mov.b64 a, {%2, %3};\n"
+      "mov.b64 b, {%4, %5};\n"
+      "mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\n"
+      "mov.b64 {%0, %1}, d;\n"
+      "}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n"
+      ".reg .b64 a, b, d;\n"
+      "mov.b64 a, {%2, %3};\n"
+      "mov.b64 b, {%4, %5};\n"
+      "add.rn.f32x2 d, a, b;\n"
+      "mov.b64 {%0, %1}, d;\n"
+      "}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// What a CTA does with a tile.  One thread steps through the units and leaves it here a tile
+// ahead; with a cursor in every thread's registers the kernel spilled, and the shared memory
+// leaves spills no L1 to stay in (a tile took 9600 cycles instead of NEWCYC).
+struct Tile128 {
+  int64_t base;           // its rows in the caches (drafts: in the draft buffers), in elements
+  int rows, left;         // rows that exist; cached positions from its first one on
+  int b, h, r, cnt;
+  int draft, begin, last, whole, slot, valid;  // begin / last of this CTA's part of the walk; slot of the part
+};
 
 template <bool F16>
 struct Smem128 {
-  static constexpr int kStages = F16 ? 3 : 1;
-  uint4 q[2][128 * 8];                             // hi, lo
-  uint4 ring[kStages][2][kTile * (F16 ? 8 : 16)];  // K, V as they are
+  static constexpr int kStages = F16 ? 2 : 1;
+  uint4 q[2][128 * 8];                                    // hi, lo
+  uint4 ring[kStages][2][tile128(F16) * (F16 ? 8 : 16)];  // K, V as they are
   uint4 tile[F16 ? 1 : 4][F16 ? 1 : kTile * 8];    // f32 cache: K hi, K lo, V hi, V lo
   float kscale[kTile], vscale[kTile];
   float ex[2][128];                                // what a row's threads tell each other
   unsigned long long mbar[2];                      // s, o
   unsigned long long bad;
   uint32_t tmem;
+  Tile128 next[3];  // of tile i: i % 3
+  Cursor pre;
+  int t_begin;
   Plan plan;
 };
 
@@ -1324,7 +1375,10 @@ template <bool F16>
 __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a) {
   using KV = typename std::conditional<F16, __half, float>::type;
   using S = Smem128<F16>;
-  constexpr int BM = 128, NS = kTile / 2, ND = kHd / 2;  // scores and dims of a thread
+  constexpr int BM = 128, kT = tile128(F16), NS = kT / 2, ND = kHd / 2;  // NS scores, ND dims to a thread
+  constexpr uint32_t kIdescS = tc::idesc_f16(128, kT);
+  // tensor memory: s (kT columns), for every 16 positions overlaid by p's 8 + 8 columns; then o
+  constexpr uint32_t kColsS = kT, kCols128 = F16 ? 256 : 128;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -1332,12 +1386,45 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
   const int uwarp = __shfl_sync(0xffffffffu, warp, 0);  // known to be the warp's: descriptors stay in uniform registers
 
   pdl_trigger();
-  if (warp == 0) make_plan<0>(a, BM, &sm.plan);
+  if (warp == 0) make_plan<-kT>(a, BM, &sm.plan);
   __syncthreads();
-  Cursor cur;
   int end;
-  if (!first_tile<BM>(a, sm.plan, cur, end)) return;
-  Cursor pre = cur;
+  {
+    Cursor cur;
+    if (!first_tile<BM>(a, sm.plan, cur, end)) return;
+    if (tid == 0) {
+      sm.pre = cur;
+      sm.t_begin = -1;
+    }
+  }
+  // thread 0: the tile at sm.pre, and on to the next
+  auto step = [&](int i) {
+    Tile128& n = sm.next[i % 3];
+    Cursor c = sm.pre;
+    n.valid = c.u < end;
+    if (!n.valid) return;
+    n.draft = c.t == c.nt - 1;
+    const int row0 = n.draft ? 0 : c.t * kT;
+    n.base = (c.head * (n.draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
+    n.left = c.p0 - row0;
+    n.rows = n.draft ? c.cnt : min(kT, n.left);
+    n.b = c.b;
+    n.h = c.h;
+    n.r = c.r;
+    n.cnt = c.cnt;
+    n.begin = sm.t_begin < 0;
+    const int first = n.begin ? c.t : sm.t_begin;
+    n.last = n.draft || c.u + 1 >= end;
+    n.whole = first == 0 && n.draft;
+    n.slot = first > 0 ? 0 : 1;
+    sm.t_begin = n.last ? -1 : first;
+    advance(sm.plan, a.n_kv, c);
+    sm.pre = c;
+  };
+  if (tid == 0) {
+    step(0);
+    step(1);
+  }
 
   const uint32_t mb_s = tc::smem_u32(&sm.mbar[0]), mb_o = tc::smem_u32(&sm.mbar[1]);
   if (warp == 0) {
@@ -1362,58 +1449,52 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
   const KV* kd = static_cast<const KV*>(a.kd);
   const KV* vd = static_cast<const KV*>(a.vd);
 
-  // copy the tile at `pre` into ring slot s and move on; rows behind its end become zeros
-  auto produce = [&](int s) {
-    if (pre.u < end) {
-      const bool draft = pre.t == pre.nt - 1;
-      const int row0 = draft ? 0 : pre.t * kTile;
-      const int rows = draft ? pre.cnt : min(kTile, pre.p0 - row0);
-      const int64_t base = (pre.head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
-      const KV* ks = (draft ? kd : kc) + base;
-      const KV* vs = (draft ? vd : vc) + base;
-      const uint32_t dk = tc::smem_u32(sm.ring[s][0]), dv = tc::smem_u32(sm.ring[s][1]);
-      // binary16: 8 rows x 4 chunks to a warp, which fill four core matrices; f32: linear
-      constexpr int kIter = kTile * (F16 ? 8 : 16) / kThreads128;
-      constexpr int kRows = kThreads128 / (F16 ? 8 : 16);  // rows of an iteration
-      const int r0 = F16 ? (tid & 7) + (tid >> 6) * 8 : tid >> 4, c = F16 ? (tid >> 3) & 7 : tid & 15;
-      const uint32_t off = F16 ? core_off(r0, c) : (uint32_t)tid * 16;
-      const int first = r0 * kHd + c * (16 / (int)sizeof(KV));
+  // binary16: 8 rows x 4 chunks to a warp, which fill four core matrices; f32: linear
+  constexpr int kIter = kT * (F16 ? 8 : 16) / kThreads128;
+  constexpr int kRows = kThreads128 / (F16 ? 8 : 16);  // rows of an iteration
+  const int cr = F16 ? (tid & 7) + (tid >> 6) * 8 : tid >> 4, cc = F16 ? (tid >> 3) & 7 : tid & 15;
+  const uint32_t cto = tc::smem_u32(sm.ring) + (F16 ? core_off(cr, cc) : (uint32_t)tid * 16);
+  const int cfrom = cr * kHd + cc * (16 / (int)sizeof(KV));
+  // copy tile i into its ring slot; rows behind its end become zeros
+  auto produce = [&](int i) {
+    const Tile128& n = sm.next[i % 3];
+    if (n.valid) {
+      const int rows = n.rows;
+      const KV* ks = (n.draft ? kd : kc) + n.base;
+      const KV* vs = (n.draft ? vd : vc) + n.base;
+      const uint32_t dk = cto + (i % S::kStages) * (uint32_t)sizeof(sm.ring[0]);
+      const uint32_t dv = dk + (uint32_t)sizeof(sm.ring[0][0]);
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const uint32_t to = off + i * kRows * (F16 ? 128 : 256);
-        if (rows >= kTile) {
-          cp16(dk + to, ks + first + i * kRows * kHd);
-          cp16(dv + to, vs + first + i * kRows * kHd);
+      for (int x = 0; x < kIter; ++x) {
+        const uint32_t to = x * kRows * (F16 ? 128 : 256);
+        if (rows >= kT) {
+          cp16(dk + to, ks + cfrom + x * kRows * kHd);
+          cp16(dv + to, vs + cfrom + x * kRows * kHd);
         } else {
-          const bool live = r0 + i * kRows < rows;
-          const int src = live ? first + i * kRows * kHd : 0;
+          const bool live = cr + x * kRows < rows;
+          const int src = live ? cfrom + x * kRows * kHd : 0;
           cp16(dk + to, ks + src, live);
           cp16(dv + to, vs + src, live);
         }
       }
-      advance(sm.plan, a.n_kv, pre);
     }
     cp_commit();
   };
-#pragma unroll
-  for (int s = 0; s < (F16 ? S::kStages - 1 : 1); ++s) produce(s);
+  produce(0);
 
   float o[ND];
   float m = -INFINITY, l = 0.f, rs = 1.f, vunit = 1.f;
   uint64_t vis = 0;
-  int t_begin = -1;
   bool lost = false;  // a wait has run out: the result is NaN
 
-  for (int it = 0; cur.u < end; ++it) {
-    const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
-    const bool draft = cur.t == nt - 1;
-    const bool more = cur.u + 1 + (draft ? kStart : 0) < end;
-    const int rows = cnt * a.group;
+  for (int it = 0; sm.next[it % 3].valid; ++it) {
+    const Tile128& cur = sm.next[it % 3];
+    const bool draft = cur.draft;
+    const int rows = cur.cnt * a.group;
     const int row = cur.r * BM + lrow;
     const bool warp_live = cur.r * BM + 32 * (warp & 3) < rows;
-    if (t_begin < 0) {
+    if (cur.begin) {
       // the last walk's products are done (every thread has waited for its o): q may change
-      t_begin = cur.t;
       const bool live = row < rows;
       const float* src = row_of(a, const_cast<float*>(a.q), cur, live ? row : 0);
       src += (int64_t)cur.b * (a.q_batch_stride - (int64_t)a.n_nodes * a.n_kv * a.group * kHd) + half * ND;
@@ -1431,7 +1512,7 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
       }
       sm.ex[half][lrow] = __uint_as_float(mx);
       vis = live ? a.mask[(int64_t)cur.b * a.n_nodes + row / a.group] : 0ull;
-      if (cnt < 64) vis &= (1ull << cnt) - 1;
+      if (cur.cnt < 64) vis &= (1ull << cur.cnt) - 1;
       __syncthreads();
       const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
       rs = pow2(e);
@@ -1457,7 +1538,7 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
     const int slot = it % S::kStages;
     uint32_t k_hi, k_lo = 0, v_hi, v_lo = 0;
     if constexpr (F16) {
-      cp_wait<S::kStages - 2>();
+      cp_wait<0>();
       k_hi = tc::smem_u32(sm.ring[slot][0]);
       v_hi = tc::smem_u32(sm.ring[slot][1]);
       if (draft) {
@@ -1558,84 +1639,107 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
                        kIdescS, 1);
       tc::mma_commit(mb_s);
     }
-    produce(F16 ? (it + S::kStages - 1) % S::kStages : 0);  // the last tile's slot; f32: all threads have read it
+    produce(it + 1);  // in the last tile's slot; f32: all threads have read it
     if (!lost && !tc::mbar_wait_sleep(mb_s, (uint32_t)it & 1u)) lost = true;
     tc::fence_after_sync();
 
-    float s[NS];
-    float corr = 1.f, mt = -INFINITY;
-    if (warp_live) {
-      tc::tmem_ld32(mine + NS * half, s);
+    // 16 of this thread's scores, in log2 units but for the row's scale; what the row does not
+    // see is -INFINITY
+    const bool partial = draft || cur.left < kT;
+    uint64_t see = ~0ull;
+    if (partial) {
+      const int in = min(max(cur.left - NS * half, 0), 64);
+      see = draft ? (half * NS < 64 ? vis >> (half * NS & 63) : 0ull) : in < 64 ? (1ull << in) - 1 : ~0ull;
+    }
+    auto scores = [&](int c, float (&s)[16]) {
+      tmem_ld16(mine + NS * half + 16 * c, s);
       if constexpr (!F16) {
 #pragma unroll
-        for (int j = 0; j < NS; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.kscale[NS * half + j]);
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.kscale[NS * half + 16 * c + j]);
           s[j] *= f.x;
           s[j + 1] *= f.y;
           s[j + 2] *= f.z;
           s[j + 3] *= f.w;
         }
       }
-      if (draft || p0 - cur.t * kTile < kTile) {
-        const uint32_t see = (uint32_t)((draft ? vis : (1ull << (p0 - cur.t * kTile)) - 1) >> (NS * half));
+      if (partial) {
+        const uint32_t bits = (uint32_t)(see >> (16 * c));
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-          if (!(see >> j & 1)) s[j] = -INFINITY;
+        for (int j = 0; j < 16; ++j)
+          if (!(bits >> j & 1)) s[j] = -INFINITY;
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+    };
+    float corr = 1.f;
+    if (warp_live) {
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 4; j < NS; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
-      mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs;
-      sm.ex[half][lrow] = mt;
+      for (int c = 0; c < NS / 16; ++c) {
+        float s[16];
+        scores(c, s);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+      }
+      sm.ex[half][lrow] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs;
     }
-    tc::fence_before_sync();
-    __syncthreads();  // the row's other half is read, and its maximum known
-    tc::fence_after_sync();
+    __syncthreads();  // the maximum of the row's other half
     float vinv = 1.f;
     if (warp_live) {
       // ---- online softmax
-      const float mn = fmaxf(m, fmaxf(mt, sm.ex[half ^ 1][lrow]));
+      const float mn = fmaxf(m, fmaxf(sm.ex[0][lrow], sm.ex[1][lrow]));
       const float mu = mn == -INFINITY ? 0.f : mn;
       corr = ex2(m - mu);
       m = mn;
       const float bias = kBias - mu;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        s[j] = ex2(fmaf(s[j], rs, bias));
-        sum[j & 3] += s[j];
-      }
-      l = fmaf(l, corr, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       if constexpr (!F16) {  // the weights take over the scale of their v rows
-        const uint64_t see = draft ? vis : ~0ull;
         float top = vunit;
 #pragma unroll
-        for (int j = 0; j < kTile; j += 4) {
+        for (int j = 0; j < kT; j += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&sm.vscale[j]);
           if (draft)
-            top = fmaxf(top, fmaxf(fmaxf(see >> j & 1 ? f.x : 0.f, see >> (j + 1) & 1 ? f.y : 0.f),
-                                   fmaxf(see >> (j + 2) & 1 ? f.z : 0.f, see >> (j + 3) & 1 ? f.w : 0.f)));
+            top = fmaxf(top, fmaxf(fmaxf(vis >> j & 1 ? f.x : 0.f, vis >> (j + 1) & 1 ? f.y : 0.f),
+                                   fmaxf(vis >> (j + 2) & 1 ? f.z : 0.f, vis >> (j + 3) & 1 ? f.w : 0.f)));
           else
             top = fmaxf(fmaxf(top, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
         }
         vinv = __uint_as_float((254u << 23) - __float_as_uint(top));  // 1 / top, a power of two
-        corr *= vunit * vinv;
-        vunit = top;
       }
-      // ---- the weights' parts over the scores
-      uint32_t hi[NS / 2], lo[NS / 2];
+      float2 sum = make_float2(0.f, 0.f), sum1 = sum;
 #pragma unroll
-      for (int j = 0; j < NS; j += 2) {
-        float x = s[j], y = s[j + 1];
-        if constexpr (!F16) {
-          const float2 f = *reinterpret_cast<const float2*>(&sm.vscale[NS * half + j]);
-          x = x * vinv * f.x;
-          y = y * vinv * f.y;
+      for (int c = 0; c < NS / 16; ++c) {
+        float s[16];
+        scores(c, s);
+        // ---- the weights' parts over the scores
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          float2 p = fma2(make_float2(s[j], s[j + 1]), make_float2(rs, rs), make_float2(bias, bias));
+          p.x = ex2(p.x);
+          p.y = ex2(p.y);
+          if (j & 2)
+            sum1 = add2(sum1, p);
+          else
+            sum = add2(sum, p);
+          if constexpr (!F16) {
+            const float2 f = *reinterpret_cast<const float2*>(&sm.vscale[NS * half + 16 * c + j]);
+            p.x = p.x * vinv * f.x;
+            p.y = p.y * vinv * f.y;
+          }
+          const __half2 h = __floats2half2_rn(p.x, p.y);
+          const float2 back = __half22float2(h);
+          const float2 rest = fma2(back, make_float2(-1.f, -1.f), p);
+          const __half2 w = __floats2half2_rn(rest.x, rest.y);
+          hi[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          lo[j / 2] = *reinterpret_cast<const uint32_t*>(&w);
         }
-        split2(x, y, hi[j / 2], lo[j / 2]);
+        tmem_st8(mine + NS * half + 16 * c, hi);
+        tmem_st8(mine + NS * half + 16 * c + 8, lo);
       }
-      tmem_st16(mine + NS / 2 * half, hi);
-      tmem_st16(mine + 32 + NS / 2 * half, lo);
+      l = fmaf(l, corr, (sum.x + sum.y) + (sum1.x + sum1.y));
+      if constexpr (!F16) {
+        corr *= vunit * vinv;
+        vunit = __uint_as_float((254u << 23) - __float_as_uint(vinv));
+      }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     }
     const unsigned long long bad = draft ? sm.bad : 0ull;
@@ -1664,35 +1768,45 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
     if (uwarp == 0 && elect_one()) {
       tc::fence_after_sync();
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {  // 16 positions: 8 columns of p, two rows of core matrices of v
-        tc::mma_f16_ts(tm + kColsS, tm + 32 + 8 * kk, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, kk > 0);
+      for (int kk = 0; kk < kT / 16; ++kk) {  // 16 positions: 8 columns of p, two rows of core matrices of v
+        const uint32_t ph = tm + 16 * kk, pl = ph + 8;
+        tc::mma_f16_ts(tm + kColsS, pl, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, kk > 0);
         if constexpr (!F16)
-          tc::mma_f16_ts(tm + kColsS, tm + 8 * kk, tc::smem_desc(v_lo + 2048 * kk, 1024, 128), kIdescO, 1);
+          tc::mma_f16_ts(tm + kColsS, ph, tc::smem_desc(v_lo + 2048 * kk, 1024, 128), kIdescO, 1);
       }
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        tc::mma_f16_ts(tm + kColsS, tm + 8 * kk, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, 1);
+      for (int kk = 0; kk < kT / 16; ++kk)
+        tc::mma_f16_ts(tm + kColsS, tm + 16 * kk, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, 1);
       tc::mma_commit(mb_o);
     }
+    if (tid == 0) step(it + 2);  // over tile it - 1's, which everyone is done with
     if (!lost && !tc::mbar_wait_sleep(mb_o, (uint32_t)it & 1u)) lost = true;
     tc::fence_after_sync();
     if (warp_live) {
-      float t[ND];
-      tc::tmem_ld32(mine + kColsS + ND * half, t);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) o[d] = fmaf(o[d], corr, t[d]);
+      for (int d0 = 0; d0 < ND; d0 += 16) {
+        float t[16];
+        tmem_ld16(mine + kColsS + ND * half + d0, t);
+#pragma unroll
+        for (int d = 0; d < 16; d += 2) {
+          const float2 x =
+              fma2(make_float2(o[d0 + d], o[d0 + d + 1]), make_float2(corr, corr), make_float2(t[d], t[d + 1]));
+          o[d0 + d] = x.x;
+          o[d0 + d + 1] = x.y;
+        }
+      }
     }
 
     // ---- the end of this CTA's part of the walk
-    if (draft || !more) {
-      const bool whole = t_begin == 0 && draft;
+    if (cur.last) {
+      const bool whole = cur.whole;
       __syncthreads();  // every thread has read `bad` and `ex`
       if (lost) l = NAN;
       sm.ex[half][lrow] = l;
       if (tid == 0) sm.bad = 0;
       __syncthreads();
       const float lt = l + sm.ex[half ^ 1][lrow];
-      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(BM);
+      float* part = a.ws + ((int64_t)blockIdx.x * 2 + cur.slot) * part_floats(BM);
       if (!whole && half == 0) {
         part[lrow] = m;
         part[BM + lrow] = lt;
@@ -1708,10 +1822,8 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
                             : make_float4(o[d] * inv * unit, o[d + 1] * inv * unit, o[d + 2] * inv * unit,
                                           o[d + 3] * inv * unit);
       }
-      t_begin = -1;
       __syncthreads();  // `ex` is read
     }
-    advance(sm.plan, a.n_kv, cur);
   }
   cp_wait<0>();
   tc::fence_before_sync();
@@ -1807,8 +1919,8 @@ qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
   if (by16(a.n_nodes, a.group))
     return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), 1, st);
   if (block_rows(a.n_nodes, a.group) == 128)
-    return launch<128, 0>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>), 2, st);
-  return launch<64, 0>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
+    return launch<128, -tile128(F16)>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>), 2, st);
+  return launch<64, -kTile>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
 }
 
 // The units of a call must fit an int.
@@ -1831,7 +1943,7 @@ size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_n
   if (!tree_shape_ok(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch)) return 0;
   const int group = n_heads / n_kv_heads;
   // of either cache type: the finest tiles ask for the most CTAs
-  const int sub = by16(n_nodes, group) ? sub_positions(false) : 0;
+  const int sub = by16(n_nodes, group) ? sub_positions(false) : -kTile;
   return (size_t)tree_ctas(n_kv_heads, group, n_nodes, max_ctx, batch, sub, kMaxCtas) * 2 *
          part_floats(block_rows(n_nodes, group)) * sizeof(float);
 }
@@ -1871,7 +1983,9 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   a.batch = batch;
   a.ws = static_cast<float*>(workspace);
   a.blocks = blocks_of(n_nodes, a.group);
-  a.whole = walk_tiles(by16(n_nodes, a.group) ? sub_positions(kv_f16) : 0, max_ctx, n_nodes) <= kWholeTiles;
+  const int rows = block_rows(n_nodes, a.group);
+  const int sub = rows == 16 ? sub_positions(kv_f16) : rows == 128 ? -tile128(kv_f16) : -kTile;
+  a.whole = walk_tiles(sub, max_ctx, n_nodes) <= kWholeTiles;
   return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
 }
 
