@@ -23,6 +23,8 @@
 // workspace and a second kernel joins the parts in order.
 #include <algorithm>
 
+#include <cuda.h>
+
 #include "qd_internal.cuh"
 #include "qd_tc.cuh"
 
@@ -1346,7 +1348,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // What a CTA does with a tile.  One thread steps through the units and leaves it here a tile
 // ahead; with a cursor in every thread's registers the kernel spilled, and the shared memory
-// leaves spills no L1 to stay in (a tile took 9600 cycles instead of NEWCYC).
+// leaves spills no L1 to stay in.
 struct Tile128 {
   int64_t base;           // its rows in the caches (drafts: in the draft buffers), in elements
   int rows, left;         // rows that exist; cached positions from its first one on
@@ -1354,15 +1356,33 @@ struct Tile128 {
   int draft, begin, last, whole, slot, valid;  // begin / last of this CTA's part of the walk; slot of the part
 };
 
+// K and V of a binary16 cache, and of the draft buffers, as rows of 64 values (128 bytes) that a
+// TMA load leaves in the 128-byte swizzle: chunk c of row r at c ^ (r & 7).
+struct Maps128 {
+  CUtensorMap m[4];  // k cache, v cache, k draft, v draft
+};
+constexpr int kBoxRows = 64;
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(row), "r"(mbar)
+      : "memory");
+}
+// Operand descriptor in the 128-byte swizzle: 8 rows (K-major) or 8 k steps (N contiguous) of 128
+// bytes to an atom, atoms 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
 template <bool F16>
 struct Smem128 {
   static constexpr int kStages = F16 ? 2 : 1;
+  uint4 ring[kStages][2][tile128(F16) * (F16 ? 8 : 16)];  // K, V as they are, at 1024 bytes
   uint4 q[2][128 * 8];                                    // hi, lo
-  uint4 ring[kStages][2][tile128(F16) * (F16 ? 8 : 16)];  // K, V as they are
-  uint4 tile[F16 ? 1 : 4][F16 ? 1 : kTile * 8];    // f32 cache: K hi, K lo, V hi, V lo
+  uint4 tile[F16 ? 1 : 4][F16 ? 1 : kTile * 8];           // f32 cache: K hi, K lo, V hi, V lo
   float kscale[kTile], vscale[kTile];
   float ex[2][128];                                // what a row's threads tell each other
-  unsigned long long mbar[2];                      // s, o
+  unsigned long long mbar[4];                      // s, o, a tile's copies in each stage
   unsigned long long bad;
   uint32_t tmem;
   Tile128 next[3];  // of tile i: i % 3
@@ -1372,7 +1392,8 @@ struct Smem128 {
 };
 
 template <bool F16>
-__global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a) {
+__global__ void __launch_bounds__(kThreads128, 2)
+    k_tree_attn_128(TreeAttnArgs a, const __grid_constant__ Maps128 maps) {
   using KV = typename std::conditional<F16, __half, float>::type;
   using S = Smem128<F16>;
   constexpr int BM = 128, kT = tile128(F16), NS = kT / 2, ND = kHd / 2;  // NS scores, ND dims to a thread
@@ -1380,7 +1401,7 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
   // tensor memory: s (kT columns), for every 16 positions overlaid by p's 8 + 8 columns; then o
   constexpr uint32_t kColsS = kT, kCols128 = F16 ? 256 : 128;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  S& sm = *reinterpret_cast<S*>(smem_raw);
+  S& sm = *reinterpret_cast<S*>(smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024);
   const int tid = threadIdx.x, warp = tid >> 5;
   const int lrow = tid & 127, half = tid >> 7;
   const int uwarp = __shfl_sync(0xffffffffu, warp, 0);  // known to be the warp's: descriptors stay in uniform registers
@@ -1437,6 +1458,8 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
     sm.bad = 0;
     tc::mbar_init(mb_s, 1);
     tc::mbar_init(mb_o, 1);
+    tc::mbar_init(mb_o + 8, 1);
+    tc::mbar_init(mb_o + 16, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::fence_before_sync();
@@ -1449,38 +1472,49 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
   const KV* kd = static_cast<const KV*>(a.kd);
   const KV* vd = static_cast<const KV*>(a.vd);
 
-  // binary16: 8 rows x 4 chunks to a warp, which fill four core matrices; f32: linear
-  constexpr int kIter = kT * (F16 ? 8 : 16) / kThreads128;
-  constexpr int kRows = kThreads128 / (F16 ? 8 : 16);  // rows of an iteration
-  const int cr = F16 ? (tid & 7) + (tid >> 6) * 8 : tid >> 4, cc = F16 ? (tid >> 3) & 7 : tid & 15;
-  const uint32_t cto = tc::smem_u32(sm.ring) + (F16 ? core_off(cr, cc) : (uint32_t)tid * 16);
-  const int cfrom = cr * kHd + cc * (16 / (int)sizeof(KV));
-  // copy tile i into its ring slot; rows behind its end become zeros
+  // Thread 0: copy tile i into its ring slot.  Binary16: whole boxes of 64 rows, whatever lies
+  // behind the last one (its scores are masked, its values cleared below); f32: the rows that exist.
   auto produce = [&](int i) {
     const Tile128& n = sm.next[i % 3];
-    if (n.valid) {
-      const int rows = n.rows;
-      const KV* ks = (n.draft ? kd : kc) + n.base;
-      const KV* vs = (n.draft ? vd : vc) + n.base;
-      const uint32_t dk = cto + (i % S::kStages) * (uint32_t)sizeof(sm.ring[0]);
-      const uint32_t dv = dk + (uint32_t)sizeof(sm.ring[0][0]);
-#pragma unroll
-      for (int x = 0; x < kIter; ++x) {
-        const uint32_t to = x * kRows * (F16 ? 128 : 256);
-        if (rows >= kT) {
-          cp16(dk + to, ks + cfrom + x * kRows * kHd);
-          cp16(dv + to, vs + cfrom + x * kRows * kHd);
-        } else {
-          const bool live = cr + x * kRows < rows;
-          const int src = live ? cfrom + x * kRows * kHd : 0;
-          cp16(dk + to, ks + src, live);
-          cp16(dv + to, vs + src, live);
-        }
+    if (!n.valid) return;
+    const int slot = i % S::kStages;
+    const uint32_t dk = tc::smem_u32(sm.ring[slot][0]), dv = tc::smem_u32(sm.ring[slot][1]), mb = mb_o + 8 + 8 * slot;
+    if constexpr (F16) {
+      const int boxes = n.draft ? 1 : kT / kBoxRows, row = (int)(n.base / kHd);
+      tc::mbar_arrive_expect_tx(mb, 2u * boxes * kBoxRows * 128);
+      for (int x = 0; x < boxes; ++x) {
+        tma_rows(dk + x * kBoxRows * 128, &maps.m[n.draft ? 2 : 0], row + x * kBoxRows, mb);
+        tma_rows(dv + x * kBoxRows * 128, &maps.m[n.draft ? 3 : 1], row + x * kBoxRows, mb);
       }
+    } else {
+      const uint32_t bytes = (uint32_t)n.rows * kHd * 4;
+      tc::mbar_arrive_expect_tx(mb, 2 * bytes);
+      tc::bulk_copy_g2s(dk, (n.draft ? kd : kc) + n.base, bytes, mb);
+      tc::bulk_copy_g2s(dv, (n.draft ? vd : vc) + n.base, bytes, mb);
     }
-    cp_commit();
   };
-  produce(0);
+  if (tid == 0) {
+    produce(0);
+    if (F16) produce(1);
+  }
+
+  // one thread: s = q k^T, the low parts first (what is cut off there does not count)
+  auto issue_s = [&](uint32_t k_hi, uint32_t k_lo) {
+    tc::fence_after_sync();
+    const uint32_t q_hi = tc::smem_u32(sm.q[0]), q_lo = tc::smem_u32(sm.q[1]);
+    auto k_desc = [&](uint32_t k, int ks) {
+      return F16 ? desc_sw128(k + 32 * ks) : tc::smem_desc(k + 256 * ks, 128, 1024);
+    };
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      tc::mma_f16_ss(tm, tc::smem_desc(q_lo + 256 * ks, 128, 1024), k_desc(k_hi, ks), kIdescS, ks > 0);
+      if constexpr (!F16)
+        tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), k_desc(k_lo, ks), kIdescS, 1);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), k_desc(k_hi, ks), kIdescS, 1);
+  };
 
   float o[ND];
   float m = -INFINITY, l = 0.f, rs = 1.f, vunit = 1.f;
@@ -1536,35 +1570,37 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
 
     // ---- the tile arrives
     const int slot = it % S::kStages;
+    const uint32_t mb_full = mb_o + 8 + 8 * slot, full = (uint32_t)(it / S::kStages) & 1u;
     uint32_t k_hi, k_lo = 0, v_hi, v_lo = 0;
     if constexpr (F16) {
-      cp_wait<0>();
       k_hi = tc::smem_u32(sm.ring[slot][0]);
       v_hi = tc::smem_u32(sm.ring[slot][1]);
-      if (draft) {
-        // a value row with an infinity or NaN would reach every row of the product (0 times
-        // it is NaN): such rows are taken out here and added below where they are seen
-        __syncthreads();
-        const int r = tid >> 2;
-        uint32_t off = 0;
+      if (cur.rows < kT) {
+        // Behind the last row lies what the cache happens to hold, and a draft's values may hold
+        // an infinity or NaN: either would reach every row of the product (0 times it is NaN).
+        // Such rows are cleared here; a draft's is added below where it is seen.
+        if (!lost && !tc::mbar_wait_sleep(mb_full, full)) lost = true;
+        for (int r = tid >> 2; r < kT; r += kThreads128 / 4) {
+          uint4* v = sm.ring[slot][1] + r * 8 + (tid & 3) * 2;
+          uint32_t off = 0;
+          if (draft && r < cur.rows) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 w = sm.ring[slot][1][core_off(r, (tid & 3) * 2 + c) / 16];
-          off |= (((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
-                  ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u)) &
-                 0x80008000u;
+            for (int c = 0; c < 2; ++c) {
+              const uint4 w = v[c];
+              off |= (((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
+                      ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u)) &
+                     0x80008000u;
+            }
+          }
+          off |= __shfl_xor_sync(0xffffffffu, off, 1);
+          off |= __shfl_xor_sync(0xffffffffu, off, 2);
+          if (off && !(tid & 3)) atomicOr(&sm.bad, 1ull << r);
+          if (off || r >= cur.rows) v[0] = v[1] = make_uint4(0, 0, 0, 0);
         }
-        off |= __shfl_xor_sync(0xffffffffu, off, 1);
-        off |= __shfl_xor_sync(0xffffffffu, off, 2);
-        if (off) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) sm.ring[slot][1][core_off(r, (tid & 3) * 2 + c) / 16] = make_uint4(0, 0, 0, 0);
-          if (!(tid & 3)) atomicOr(&sm.bad, 1ull << r);
-        }
+        tc::fence_proxy_async_smem();
       }
     } else {
-      cp_wait<0>();
-      __syncthreads();
+      if (!lost && !tc::mbar_wait_sleep(mb_full, full)) lost = true;
       // four threads to a position, 16 dims each; their 16-byte reads in an order without bank
       // conflicts
       const int r = tid >> 2, j = tid & 3, turn = (j >> 1) + 2 * (r & 1);
@@ -1576,14 +1612,14 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = (kv ? vraw : kraw)[i ^ turn];
+          x[i] = r < cur.rows ? (kv ? vraw : kraw)[i ^ turn] : make_float4(0.f, 0.f, 0.f, 0.f);
           mx = max(mx, abs_max(x[i]));
         }
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         if (kv && mx >= kInfBits) {
           mx = 0;
-          if (draft) {  // as above: a row with an infinity or NaN is taken out
+          if (draft) {  // a row with an infinity or NaN, cleared as above
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j == 0) atomicOr(&sm.bad, 1ull << r);
@@ -1616,30 +1652,20 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
       v_hi = tc::smem_u32(sm.tile[2]);
       v_lo = tc::smem_u32(sm.tile[3]);
     }
-    tc::fence_proxy_async_smem();
-    tc::fence_before_sync();
-    __syncthreads();
 
-    // ---- scores
-    if (uwarp == 0 && elect_one()) {
-      tc::fence_after_sync();
-      const uint32_t q_hi = tc::smem_u32(sm.q[0]), q_lo = tc::smem_u32(sm.q[1]);
-      // the low parts first: what is cut off there does not count
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        tc::mma_f16_ss(tm, tc::smem_desc(q_lo + 256 * ks, 128, 1024), tc::smem_desc(k_hi + 256 * ks, 128, 1024),
-                       kIdescS, ks > 0);
-        if constexpr (!F16)
-          tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), tc::smem_desc(k_lo + 256 * ks, 128, 1024),
-                         kIdescS, 1);
+    // ---- scores (of a binary16 tile inside a walk they were issued behind the last tile's products)
+    if (!F16 || cur.begin) {
+      tc::fence_proxy_async_smem();
+      tc::fence_before_sync();
+      __syncthreads();
+      if (F16 && uwarp == 0 && !lost && !tc::mbar_wait_sleep(mb_full, full)) lost = true;
+      __syncwarp();
+      if (uwarp == 0 && elect_one()) {
+        issue_s(k_hi, k_lo);
+        tc::mma_commit(mb_s);
       }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), tc::smem_desc(k_hi + 256 * ks, 128, 1024),
-                       kIdescS, 1);
-      tc::mma_commit(mb_s);
+      if (!F16 && tid == 0) produce(it + 1);  // all threads have read the raw tile
     }
-    produce(it + 1);  // in the last tile's slot; f32: all threads have read it
     if (!lost && !tc::mbar_wait_sleep(mb_s, (uint32_t)it & 1u)) lost = true;
     tc::fence_after_sync();
 
@@ -1767,20 +1793,37 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
     // ---- weighted values
     if (uwarp == 0 && elect_one()) {
       tc::fence_after_sync();
+      auto v_desc = [&](uint32_t v, int kk) {
+        return F16 ? desc_sw128(v + 2048 * kk) : tc::smem_desc(v + 2048 * kk, 1024, 128);
+      };
 #pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk) {  // 16 positions: 8 columns of p, two rows of core matrices of v
+      for (int kk = 0; kk < kT / 16; ++kk) {  // 16 positions: 8 columns of p, two atoms or rows of core matrices of v
         const uint32_t ph = tm + 16 * kk, pl = ph + 8;
-        tc::mma_f16_ts(tm + kColsS, pl, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, kk > 0);
-        if constexpr (!F16)
-          tc::mma_f16_ts(tm + kColsS, ph, tc::smem_desc(v_lo + 2048 * kk, 1024, 128), kIdescO, 1);
+        tc::mma_f16_ts(tm + kColsS, pl, v_desc(v_hi, kk), kIdescO, kk > 0);
+        if constexpr (!F16) tc::mma_f16_ts(tm + kColsS, ph, v_desc(v_lo, kk), kIdescO, 1);
       }
 #pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk)
-        tc::mma_f16_ts(tm + kColsS, tm + 16 * kk, tc::smem_desc(v_hi + 2048 * kk, 1024, 128), kIdescO, 1);
+      for (int kk = 0; kk < kT / 16; ++kk) tc::mma_f16_ts(tm + kColsS, tm + 16 * kk, v_desc(v_hi, kk), kIdescO, 1);
       tc::mma_commit(mb_o);
     }
     if (tid == 0) step(it + 2);  // over tile it - 1's, which everyone is done with
     if (!lost && !tc::mbar_wait_sleep(mb_o, (uint32_t)it & 1u)) lost = true;
+    if constexpr (F16) {
+      // p and this tile's slot are read: the next tile's scores, under the sums below, and the
+      // copy of the one after it
+      if (uwarp == 0) {
+        const bool ahead = sm.next[(it + 1) % 3].valid && !sm.next[(it + 1) % 3].begin;
+        const int ns = (it + 1) % S::kStages;
+        if (ahead && !lost && !tc::mbar_wait_sleep(mb_o + 8 + 8 * ns, (uint32_t)((it + 1) / S::kStages) & 1u))
+          lost = true;
+        __syncwarp();
+        if (ahead && elect_one()) {
+          issue_s(tc::smem_u32(sm.ring[ns][0]), 0);
+          tc::mma_commit(mb_s);
+        }
+        if (tid == 0) produce(it + 2);
+      }
+    }
     tc::fence_after_sync();
     if (warp_live) {
 #pragma unroll
@@ -1825,7 +1868,6 @@ __global__ void __launch_bounds__(kThreads128, 2) k_tree_attn_128(TreeAttnArgs a
       __syncthreads();  // `ex` is read
     }
   }
-  cp_wait<0>();
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0)
@@ -1901,25 +1943,52 @@ inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, i
   return (int)std::min<int64_t>((int64_t)attn_sm_count() * per_sm, (units + kMinPer - 1) / kMinPer);
 }
 
-template <int BM, int SUB>
-qd_status launch(const TreeAttnArgs& a, void (*kern)(TreeAttnArgs), int threads, size_t smem, int per_sm,
-                 cudaStream_t st) {
+template <int BM, int SUB, typename... More>
+qd_status launch(const TreeAttnArgs& a, void (*kern)(TreeAttnArgs, More...), int threads, size_t smem, int per_sm,
+                 cudaStream_t st, const std::remove_const_t<More>&... more) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return QD_ERR_CUDA;
   const int walks = a.batch * a.n_kv * a.blocks;
   const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, SUB, per_sm);
-  kern<<<ctas, threads, smem, st>>>(a);
+  kern<<<ctas, threads, smem, st>>>(a, more...);
   const qd_status s = launch_status();
   if (s != QD_OK || a.whole) return s;
   return launch_k(k_tree_attn_join<BM, SUB>, dim3((unsigned)ctas, BM / 4), dim3(kThreads), 0, st, true, a, ctas);
+}
+
+// The map of `rows` rows of 64 binary16 values, in boxes of kBoxRows.
+bool row_map(CUtensorMap* map, const void* base, int64_t rows) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {kHd, (cuuint64_t)rows}, strides[1] = {kHd * 2};
+  const cuuint32_t box[2] = {kHd, kBoxRows}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
   if (by16(a.n_nodes, a.group))
     return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), 1, st);
-  if (block_rows(a.n_nodes, a.group) == 128)
-    return launch<128, -tile128(F16)>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>), 2, st);
+  if (block_rows(a.n_nodes, a.group) == 128) {
+    Maps128 maps = {};
+    if constexpr (F16) {
+      const int64_t heads = (int64_t)a.batch * a.n_kv;
+      const void* base[4] = {a.kc, a.vc, a.kd, a.vd};
+      for (int i = 0; i < 4; ++i)
+        if (!row_map(&maps.m[i], base[i], heads * (i < 2 ? a.max_ctx : a.n_nodes))) return QD_ERR_CUDA;
+    }
+    return launch<128, -tile128(F16)>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>) + 1024, 2, st, maps);
+  }
   return launch<64, -kTile>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
 }
 
@@ -1929,6 +1998,7 @@ inline bool tree_shape_ok(int n_heads, int n_kv_heads, int head_dim, int n_nodes
       n_nodes < 1 || n_nodes > QD_MAX_TREE || max_ctx < 1 || batch < 1 || batch > QD_MAX_BATCH)
     return false;
   const int64_t walks = (int64_t)batch * n_kv_heads * blocks_of(n_nodes, n_heads / n_kv_heads);
+  if ((int64_t)batch * n_kv_heads * std::max(max_ctx, n_nodes) > (1ll << 31) - 128) return false;  // rows of a cache
   return walks <= (1 << 20) && walks * ((int64_t)max_ctx / kTile + 2 + kStart) <= (1 << 30);
 }
 
