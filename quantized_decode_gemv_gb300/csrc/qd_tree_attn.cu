@@ -1271,7 +1271,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
 // ------------------------------------------------------------------ 128 rows
 // Many rows to a kv head: blocks of 128 on the 5th-generation tensor cores, two threads to a row.
 // Per tile (128 positions of a binary16 cache, 64 of an f32 one) one thread issues s = q k^T
-// (tcgen05.mma, M = 128, both operands in shared memory) into tensor memory; a row's threads read
+// (tcgen05.mma, M = 128, q in tensor memory, K in shared memory) into tensor memory; a row's threads read
 // half of its scores each (tcgen05.ld), exchange their maxima, read the scores again 16 at a time
 // (which leaves the registers for two CTAs to an SM without a spill: the shared memory leaves
 // spills no L1) and write the weights' two parts over them as the A operand of o = p v (V as it lies,
@@ -1378,7 +1378,6 @@ template <bool F16>
 struct Smem128 {
   static constexpr int kStages = F16 ? 2 : 1;
   uint4 ring[kStages][2][tile128(F16) * (F16 ? 8 : 16)];  // K, V as they are, at 1024 bytes
-  uint4 q[2][128 * 8];                                    // hi, lo
   uint4 tile[F16 ? 1 : 4][F16 ? 1 : kTile * 8];           // f32 cache: K hi, K lo, V hi, V lo
   float kscale[kTile], vscale[kTile];
   float ex[2][128];                                // what a row's threads tell each other
@@ -1398,12 +1397,14 @@ __global__ void __launch_bounds__(kThreads128, 2)
   using S = Smem128<F16>;
   constexpr int BM = 128, kT = tile128(F16), NS = kT / 2, ND = kHd / 2;  // NS scores, ND dims to a thread
   constexpr uint32_t kIdescS = tc::idesc_f16(128, kT);
-  // tensor memory: s (kT columns), for every 16 positions overlaid by p's 8 + 8 columns; then o
-  constexpr uint32_t kColsS = kT, kCols128 = F16 ? 256 : 128;
+  // tensor memory: s (kT columns), for every 16 positions overlaid by p's 8 + 8 columns; then o;
+  // then q, 16 + 16 columns for every 32 dims
+  constexpr uint32_t kColsS = kT, kColsQ = kT + kHd, kCols128 = 256;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024);
   const int tid = threadIdx.x, warp = tid >> 5;
   const int lrow = tid & 127, half = tid >> 7;
+  constexpr int kStepper = 128;  // the thread that steps through the units and copies; warp 0 issues the products
   const int uwarp = __shfl_sync(0xffffffffu, warp, 0);  // known to be the warp's: descriptors stay in uniform registers
 
   pdl_trigger();
@@ -1413,12 +1414,12 @@ __global__ void __launch_bounds__(kThreads128, 2)
   {
     Cursor cur;
     if (!first_tile<BM>(a, sm.plan, cur, end)) return;
-    if (tid == 0) {
+    if (tid == kStepper) {
       sm.pre = cur;
       sm.t_begin = -1;
     }
   }
-  // thread 0: the tile at sm.pre, and on to the next
+  // one thread: the tile at sm.pre, and on to the next
   auto step = [&](int i) {
     Tile128& n = sm.next[i % 3];
     Cursor c = sm.pre;
@@ -1442,7 +1443,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
     advance(sm.plan, a.n_kv, c);
     sm.pre = c;
   };
-  if (tid == 0) {
+  if (tid == kStepper) {
     step(0);
     step(1);
   }
@@ -1472,7 +1473,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
   const KV* kd = static_cast<const KV*>(a.kd);
   const KV* vd = static_cast<const KV*>(a.vd);
 
-  // Thread 0: copy tile i into its ring slot.  Binary16: whole boxes of 64 rows, whatever lies
+  // One thread: copy tile i into its ring slot.  Binary16: whole boxes of 64 rows, whatever lies
   // behind the last one (its scores are masked, its values cleared below); f32: the rows that exist.
   auto produce = [&](int i) {
     const Tile128& n = sm.next[i % 3];
@@ -1493,7 +1494,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
       tc::bulk_copy_g2s(dv, (n.draft ? vd : vc) + n.base, bytes, mb);
     }
   };
-  if (tid == 0) {
+  if (tid == kStepper) {
     produce(0);
     if (F16) produce(1);
   }
@@ -1501,19 +1502,18 @@ __global__ void __launch_bounds__(kThreads128, 2)
   // one thread: s = q k^T, the low parts first (what is cut off there does not count)
   auto issue_s = [&](uint32_t k_hi, uint32_t k_lo) {
     tc::fence_after_sync();
-    const uint32_t q_hi = tc::smem_u32(sm.q[0]), q_lo = tc::smem_u32(sm.q[1]);
     auto k_desc = [&](uint32_t k, int ks) {
       return F16 ? desc_sw128(k + 32 * ks) : tc::smem_desc(k + 256 * ks, 128, 1024);
     };
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      tc::mma_f16_ss(tm, tc::smem_desc(q_lo + 256 * ks, 128, 1024), k_desc(k_hi, ks), kIdescS, ks > 0);
-      if constexpr (!F16)
-        tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), k_desc(k_lo, ks), kIdescS, 1);
+    for (int ks = 0; ks < 4; ++ks) {  // 16 dims: 8 columns of q
+      const uint32_t q_hi = tm + kColsQ + 32 * (ks / 2) + 8 * (ks & 1), q_lo = q_hi + 16;
+      tc::mma_f16_ts(tm, q_lo, k_desc(k_hi, ks), kIdescS, ks > 0);
+      if constexpr (!F16) tc::mma_f16_ts(tm, q_hi, k_desc(k_lo, ks), kIdescS, 1);
     }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
-      tc::mma_f16_ss(tm, tc::smem_desc(q_hi + 256 * ks, 128, 1024), k_desc(k_hi, ks), kIdescS, 1);
+      tc::mma_f16_ts(tm, tm + kColsQ + 32 * (ks / 2) + 8 * (ks & 1), k_desc(k_hi, ks), kIdescS, 1);
   };
 
   float o[ND];
@@ -1552,15 +1552,17 @@ __global__ void __launch_bounds__(kThreads128, 2)
       rs = pow2(e);
       const float f = pow2(-e);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint4 hi, lo;
-        split2(x[2 * c].x * f, x[2 * c].y * f, hi.x, lo.x);
-        split2(x[2 * c].z * f, x[2 * c].w * f, hi.y, lo.y);
-        split2(x[2 * c + 1].x * f, x[2 * c + 1].y * f, hi.z, lo.z);
-        split2(x[2 * c + 1].z * f, x[2 * c + 1].w * f, hi.w, lo.w);
-        sm.q[0][core_off(lrow, 4 * half + c) / 16] = hi;
-        sm.q[1][core_off(lrow, 4 * half + c) / 16] = lo;
+      for (int c = 0; c < 2; ++c) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          split2(x[4 * c + d].x * f, x[4 * c + d].y * f, hi[2 * d], lo[2 * d]);
+          split2(x[4 * c + d].z * f, x[4 * c + d].w * f, hi[2 * d + 1], lo[2 * d + 1]);
+        }
+        tmem_st8(mine + kColsQ + 32 * half + 8 * c, hi);
+        tmem_st8(mine + kColsQ + 32 * half + 16 + 8 * c, lo);
       }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       m = -INFINITY;
       l = 0.f;
       vunit = pow2(-100);
@@ -1664,12 +1666,12 @@ __global__ void __launch_bounds__(kThreads128, 2)
         issue_s(k_hi, k_lo);
         tc::mma_commit(mb_s);
       }
-      if (!F16 && tid == 0) produce(it + 1);  // all threads have read the raw tile
+      if (!F16 && tid == kStepper) produce(it + 1);  // all threads have read the raw tile
     }
     if (!lost && !tc::mbar_wait_sleep(mb_s, (uint32_t)it & 1u)) lost = true;
     tc::fence_after_sync();
 
-    // 16 of this thread's scores, in log2 units but for the row's scale; what the row does not
+    // 16 or 32 of this thread's scores, in log2 units but for the row's scale; what the row does not
     // see is -INFINITY
     const bool partial = draft || cur.left < kT;
     uint64_t see = ~0ull;
@@ -1677,11 +1679,15 @@ __global__ void __launch_bounds__(kThreads128, 2)
       const int in = min(max(cur.left - NS * half, 0), 64);
       see = draft ? (half * NS < 64 ? vis >> (half * NS & 63) : 0ull) : in < 64 ? (1ull << in) - 1 : ~0ull;
     }
-    auto scores = [&](int c, float (&s)[16]) {
-      tmem_ld16(mine + NS * half + 16 * c, s);
+    auto scores = [&](int c, auto& s) {
+      constexpr int n = sizeof(s) / 4;
+      if constexpr (n == 16)
+        tmem_ld16(mine + NS * half + 16 * c, s);
+      else
+        tc::tmem_ld32(mine + NS * half + 16 * c, s);
       if constexpr (!F16) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
+        for (int j = 0; j < n; j += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&sm.kscale[NS * half + 16 * c + j]);
           s[j] *= f.x;
           s[j + 1] *= f.y;
@@ -1692,7 +1698,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
       if (partial) {
         const uint32_t bits = (uint32_t)(see >> (16 * c));
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < n; ++j)
           if (!(bits >> j & 1)) s[j] = -INFINITY;
       }
     };
@@ -1700,11 +1706,11 @@ __global__ void __launch_bounds__(kThreads128, 2)
     if (warp_live) {
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < NS / 16; ++c) {
-        float s[16];
-        scores(c, s);
+      for (int c = 0; c < NS / 32; ++c) {
+        float s[32];
+        scores(2 * c, s);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
       }
       sm.ex[half][lrow] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs;
     }
@@ -1806,7 +1812,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
       for (int kk = 0; kk < kT / 16; ++kk) tc::mma_f16_ts(tm + kColsS, tm + 16 * kk, v_desc(v_hi, kk), kIdescO, 1);
       tc::mma_commit(mb_o);
     }
-    if (tid == 0) step(it + 2);  // over tile it - 1's, which everyone is done with
+    if (tid == kStepper) step(it + 2);  // over tile it - 1's, which everyone is done with
     if (!lost && !tc::mbar_wait_sleep(mb_o, (uint32_t)it & 1u)) lost = true;
     if constexpr (F16) {
       // p and this tile's slot are read: the next tile's scores, under the sums below, and the
@@ -1821,8 +1827,8 @@ __global__ void __launch_bounds__(kThreads128, 2)
           issue_s(tc::smem_u32(sm.ring[ns][0]), 0);
           tc::mma_commit(mb_s);
         }
-        if (tid == 0) produce(it + 2);
       }
+      if (tid == kStepper) produce(it + 2);
     }
     tc::fence_after_sync();
     if (warp_live) {
