@@ -2,25 +2,35 @@
 // cached positions and the draft slots j with bit j of its mask set,
 //   o = sum_p softmax_p(q . k_p / sqrt(head_dim)) v_p.
 //
-// The rows that share a kv head (nodes x query heads of the group) walk its positions together,
-// 64 at a time, with an online softmax: s = q k^T and o += p v as m16n8k16 binary16 matrix
-// products with f32 accumulators.  A binary16 operand alone is 2^-12 off, so what is f32 enters
-// as two binary16 parts (hi = rn(x), lo = rn(x - hi): 2^-22 of the operand's scale):
-//  - q, scaled by a power of two per row, in two parts;
-//  - the weights p = 2^(s - m + 12) in two parts (the 2^12 keeps the low part of small weights
-//    above binary16's subnormal step; it cancels in o / l);
-//  - a binary16 cache exactly; an f32 cache in two parts, k scaled by a power of two per
-//    position and v per group of positions, converted once per tile by the whole CTA.
-// So a tile costs 2 + 2 matrix products on a binary16 cache and 3 + 3 on an f32 one.  Scores,
-// running maxima, sums and o are f32.  The matrix unit cuts its f32 sums off instead of rounding
-// them, so a tile's products of the high parts start from zero, those with a low part have
-// accumulators of their own, and both are added to o with rounded f32 additions (one accumulator
-// through a whole walk of 4080 positions: 1.4e-6 relative error of o).
+// The rows that share a kv head (nodes x query heads of the group) walk its positions together
+// with an online softmax: s = q k^T and o += p v are matrix products with f32 accumulators.
+// Outputs are f32, and a binary16 operand alone is 2^-12 off, so what is f32 enters the products
+// in two parts (hi = rn(x), lo = rn(x - hi): 2^-22 of the operand's scale):
+//  - q, scaled by a power of two per row;
+//  - the weights p = 2^(s - m + 12) (the 2^12 keeps the low part of small weights above binary16's
+//    subnormal step; it cancels in o / l);
+//  - a binary16 cache is exact as it is; an f32 cache has two parts, or TF32 ones (see each kernel).
+// That is 2 + 2 products a tile on a binary16 cache and 3 + 3 on an f32 one (lo lo is dropped).
+// Scores, running maxima, sums and o are f32.  The matrix units cut their f32 sums off instead of
+// rounding them, so the low parts are summed first, a tile's products start from zero, and they
+// are added to o with rounded f32 additions (one accumulator through a walk of 4080 positions:
+// 1.4e-6 relative error of o instead of 4e-7).
 //
 // Work: the walks of all (sequence, kv head, block of rows) are laid end to end in units of a
 // tile and cut evenly over the CTAs, whatever the lengths; a walk's start (its queries, its
 // result) counts as kStart units.  A CTA that holds a part of a walk writes (m, l, o) to the
-// workspace and a second kernel joins the parts in order.
+// workspace and a second kernel joins the parts in order.  Where the cache has room for at most
+// kWholeTiles tiles a walk, no walk is cut and there is one launch.
+//
+// What bounds it: HBM for few rows on long caches, the instructions of the softmax and of the
+// splits for many rows, latency for short caches.  Measured on one GB300 (floor: the bytes at
+// 6.77 TB/s or the products at 1946 TFLOP/s, counted once):
+//   9/3 heads, 8 nodes, 100 positions, f32              6.6 us (floor 0.03)
+//   32/32 heads, 16 nodes, 4080 positions, f32         22.6 us (10.0)
+//   the same, 16 ragged sequences, binary16              64 us (40)
+//   32/8 heads, 64 nodes, 32700 positions, binary16      60 us (10)
+// The unit counts: kStart 3 against 1 / 2 / 5 at 16 ragged sequences 64 against 95 / 72 / 66 us;
+// kMinPer 2 against 4 at 9/3 heads and 1000 positions 11.2 against 12.9 us.
 #include <algorithm>
 
 #include <cuda.h>
@@ -32,8 +42,8 @@ namespace qd {
 namespace {
 
 constexpr int kHd = 64;
-constexpr int kTile = 64;     // positions of a tile; the drafts (at most 64) are one tile
-constexpr int kThreads = 128;  // 4 warps: WM blocks of 16 rows x WN shares of the positions
+constexpr int kTile = 64;      // positions of the smallest tile of a whole CTA; the drafts are one tile
+constexpr int kThreads = 128;  // of the join
 constexpr float kBias = 12.f;  // log2 of the weights' scale
 constexpr int kMinPer = 2;     // units of a CTA at least
 constexpr int kWholeTiles = 8;  // walks of at most so many tiles are not cut
@@ -250,524 +260,9 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
   return false;
 }
 
-// Shared memory.  Binary16 cache: a ring of K and V tiles as they are.  f32 cache: a ring of
-// raw tiles, each chunk read back by the thread that copied it, and one converted tile.
-template <bool F16>
-struct Smem;
-template <>
-struct Smem<true> {
-  static constexpr int kStages = 3;
-  uint4 tile[kStages][2][kTile * 8];  // K, V
-  float merge[4][part_floats(16)];
-  unsigned long long bad;
-  Plan plan;
-};
-template <>
-struct Smem<false> {
-  static constexpr int kStages = 2;
-  float4 raw[kStages][2][kTile * 16];
-  union {
-    uint4 tile[4][kTile * 8];  // K hi, K lo, V hi, V lo
-    float merge[4][part_floats(16)];
-  };
-  float kscale[kTile], vscale[kTile];
-  unsigned long long bad;
-  Plan plan;
-};
-
-template <bool F16, int WM, int WN>
-__global__ void __launch_bounds__(kThreads, F16 ? 3 : 2) k_tree_attn(TreeAttnArgs a) {
-  using KV = typename std::conditional<F16, __half, float>::type;
-  using S = Smem<F16>;
-  constexpr int BM = 16 * WM;
-  constexpr int NP = kTile / WN;  // positions of a warp's share of a tile
-  constexpr int NT = NP / 8;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  S& sm = *reinterpret_cast<S*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp % WM, wn = warp / WM;
-  const int qr = lane >> 2, qc = lane & 3;  // row and column pair of the lane in a fragment
-
-  pdl_trigger();
-  if (warp == 0) make_plan<-kTile>(a, BM, &sm.plan);
-  if (tid == 0) sm.bad = 0;
-  __syncthreads();
-  Cursor cur;
-  int end;
-  if (!first_tile<BM>(a, sm.plan, cur, end)) return;
-  Cursor pre = cur;
-
-  const KV* kc = static_cast<const KV*>(a.kc);
-  const KV* vc = static_cast<const KV*>(a.vc);
-  const KV* kd = static_cast<const KV*>(a.kd);
-  const KV* vd = static_cast<const KV*>(a.vd);
-
-  // copy the tile at `pre` into ring slot s and move on; rows behind its end become zeros
-  auto produce = [&](int s) {
-    if (pre.u < end) {
-      const bool draft = pre.t == pre.nt - 1;
-      const int row0 = draft ? 0 : pre.t * kTile;
-      const int rows = draft ? pre.cnt : min(kTile, pre.p0 - row0);
-      const int64_t base = (pre.head * (draft ? a.n_nodes : a.max_ctx) + row0) * kHd;
-      const KV* ks = (draft ? kd : kc) + base;
-      const KV* vs = (draft ? vd : vc) + base;
-      constexpr int kPer = F16 ? 8 : 16;           // 16-byte chunks of a row
-      constexpr int kIter = kTile * kPer / kThreads;
-      const int c = tid % kPer, r0 = tid / kPer;
-      uint32_t dk, dv;
-      if constexpr (F16) {
-        dk = tc::smem_u32(sm.tile[s][0]);
-        dv = tc::smem_u32(sm.tile[s][1]);
-      } else {
-        dk = tc::smem_u32(sm.raw[s][0]);
-        dv = tc::smem_u32(sm.raw[s][1]);
-      }
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int r = r0 + i * (kThreads / kPer);
-        const bool live = r < rows;
-        const int64_t src = live ? (int64_t)r * kHd + c * (16 / (int)sizeof(KV)) : 0;
-        const uint32_t off = F16 ? tile_off(r, c) : (uint32_t)(r * 256 + c * 16);
-        cp16(dk + off, ks + src, live);
-        cp16(dv + off, vs + src, live);
-      }
-      advance(sm.plan, a.n_kv, pre);
-    }
-    cp_commit();
-  };
-
-#pragma unroll
-  for (int s = 0; s < (F16 ? S::kStages - 1 : S::kStages); ++s) produce(s);
-
-  uint32_t qh[4][4], ql[4][4];
-  float o[8][4];
-  float m[2], l[2], rs[2];
-  uint64_t vis[2];
-  float vunit[2];     // o is in these units (f32 cache; powers of two)
-  int t_begin = -1;   // first tile of this CTA's part of the walk; -1: a new walk begins
-
-  for (int it = 0; cur.u < end; ++it) {
-    const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
-    const bool draft = cur.t == nt - 1;
-    const bool more = cur.u + 1 + (draft ? kStart : 0) < end;  // this CTA has another tile
-    const int rows = cnt * a.group;
-    if (t_begin < 0) {
-      t_begin = cur.t;
-      const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = cur.r * BM + wm * 16 + qr + 8 * i;
-        const int node = r / a.group, g = r % a.group;
-        const bool live = r < rows;
-        const float* src = a.q + (int64_t)cur.b * a.q_batch_stride +
-                           ((int64_t)node * a.n_kv * a.group + cur.h * a.group + g) * kHd;
-        float2 x[8];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          x[c] = live ? __ldcg(reinterpret_cast<const float2*>(src + c * 8) + qc) : make_float2(0.f, 0.f);
-          x[c].x *= scale;
-          x[c].y *= scale;
-          mx = max(mx, max(abs_bits(x[c].x), abs_bits(x[c].y)));
-        }
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e = scale_exp(mx);
-        rs[i] = pow2(e);
-        const float f = pow2(-e);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)  // columns 8c..8c+7: k step c / 2, its low or high half
-          split2(x[c].x * f, x[c].y * f, qh[c >> 1][i + 2 * (c & 1)], ql[c >> 1][i + 2 * (c & 1)]);
-        vis[i] = live ? a.mask[(int64_t)cur.b * a.n_nodes + node] : 0ull;
-        if (cnt < 64) vis[i] &= (1ull << cnt) - 1;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        vunit[i] = pow2(-100);
-      }
-#pragma unroll
-      for (int d = 0; d < 8; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
-    }
-
-    // ---- the tile arrives
-    uint32_t k_hi, k_lo = 0, v_hi, v_lo = 0;
-    if constexpr (F16) {
-      const int s = it % S::kStages;
-      cp_wait<S::kStages - 2>();
-      __syncthreads();
-      produce((it + S::kStages - 1) % S::kStages);
-      k_hi = tc::smem_u32(sm.tile[s][0]);
-      v_hi = tc::smem_u32(sm.tile[s][1]);
-      if (draft) {
-        // a value row with an infinity or NaN would reach every row of the product (0 times
-        // it is NaN): such rows are taken out here and added below where they are seen
-        __half* vt = reinterpret_cast<__half*>(sm.tile[s][1]);
-        const int r = tid >> 1;
-        uint32_t mx = 0;
-        uint4* row = reinterpret_cast<uint4*>(vt + r * 64) + (tid & 1) * 4;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 w = row[c];
-          mx |= (((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
-                 ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u)) &
-                0x80008000u;
-        }
-        mx |= __shfl_xor_sync(0xffffffffu, mx, 1);
-        if (mx) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) row[c] = make_uint4(0, 0, 0, 0);
-          if (!(tid & 1)) atomicOr(&sm.bad, 1ull << r);
-        }
-        __syncthreads();
-      }
-    } else {
-      const int s = it % S::kStages;
-      cp_wait<S::kStages - 1>();  // this thread's own chunks of tile `it`
-      if (it) __syncthreads();    // the last tile's products are done with the converted tile
-      const int c = tid & 15, r0 = tid >> 4;
-      uint2* kh = reinterpret_cast<uint2*>(sm.tile[0]);
-      uint2* kl = reinterpret_cast<uint2*>(sm.tile[1]);
-      uint2* vh = reinterpret_cast<uint2*>(sm.tile[2]);
-      uint2* vl = reinterpret_cast<uint2*>(sm.tile[3]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 8 * i;
-        const float4 x = sm.raw[s][0][r * 16 + c];
-        uint32_t mx = abs_max(x);
-#pragma unroll
-        for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const int e = scale_exp(mx);
-        const float f = pow2(-e);
-        uint2 hi, lo;
-        split2(x.x * f, x.y * f, hi.x, lo.x);
-        split2(x.z * f, x.w * f, hi.y, lo.y);
-        const uint32_t at = tile_off(r, c >> 1) / 8 + (c & 1);
-        kh[at] = hi;
-        kl[at] = lo;
-        if (c == 0) sm.kscale[r] = pow2(e);
-      }
-      // v rows: cached ones, which every row of the tile sees, with one scale for the rows of a
-      // warp; drafts, which some rows do not see, each with its own
-      uint32_t mx = 0;
-      if (!draft) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 x = sm.raw[s][1][(r0 + 8 * i) * 16 + c];
-          const uint32_t rm = abs_max(x);
-          mx = max(mx, rm >= kInfBits ? finite_max(x) : rm);
-        }
-        mx = __reduce_max_sync(0xffffffffu, mx);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 8 * i;
-        float4 x = sm.raw[s][1][r * 16 + c];
-        if (draft) {
-          mx = abs_max(x);
-#pragma unroll
-          for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          if (mx >= kInfBits) {  // as above: a row with an infinity or NaN is taken out
-            x = make_float4(0.f, 0.f, 0.f, 0.f);
-            mx = 0;
-            if (c == 0) atomicOr(&sm.bad, 1ull << r);
-          }
-        }
-        const int e = scale_exp(mx);
-        const float f = pow2(-e);
-        uint2 hi, lo;
-        split2(x.x * f, x.y * f, hi.x, lo.x);
-        split2(x.z * f, x.w * f, hi.y, lo.y);
-        const uint32_t at = tile_off(r, c >> 1) / 8 + (c & 1);
-        vh[at] = hi;
-        vl[at] = lo;
-        if (c == 0) sm.vscale[r] = pow2(e);
-      }
-      produce(s);  // the slot's chunks of this thread are read
-      __syncthreads();
-      k_hi = tc::smem_u32(sm.tile[0]);
-      k_lo = tc::smem_u32(sm.tile[1]);
-      v_hi = tc::smem_u32(sm.tile[2]);
-      v_lo = tc::smem_u32(sm.tile[3]);
-    }
-
-    // ---- scores
-    float s[NT][4];
-    {
-      float sl[NT][4];
-      const int kr = wn * NP + (lane & 7) + ((lane >> 4) & 1) * 8;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          const uint32_t off = tile_off(kr + j * 8, 2 * ks + ((lane >> 3) & 1));
-          uint32_t b[4];
-          ldsm4(k_hi + off, b);
-          if (ks == 0) {
-            mma0(s[j], qh[ks], b[0], b[1]);
-            mma0(s[j + 1], qh[ks], b[2], b[3]);
-            mma0(sl[j], ql[ks], b[0], b[1]);
-            mma0(sl[j + 1], ql[ks], b[2], b[3]);
-          } else {
-            mma(s[j], qh[ks], b[0], b[1]);
-            mma(s[j + 1], qh[ks], b[2], b[3]);
-            mma(sl[j], ql[ks], b[0], b[1]);
-            mma(sl[j + 1], ql[ks], b[2], b[3]);
-          }
-          if constexpr (!F16) {
-            ldsm4(k_lo + off, b);
-            mma(sl[j], qh[ks], b[0], b[1]);
-            mma(sl[j + 1], qh[ks], b[2], b[3]);
-          }
-        }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] += sl[j][e];
-    }
-    if constexpr (!F16) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const float2 f = *reinterpret_cast<const float2*>(&sm.kscale[wn * NP + j * 8 + 2 * qc]);
-        s[j][0] *= f.x;
-        s[j][1] *= f.y;
-        s[j][2] *= f.x;
-        s[j][3] *= f.y;
-      }
-    }
-    if (draft || p0 - cur.t * kTile < kTile) {
-      const uint64_t in = draft ? ~0ull : (1ull << (p0 - cur.t * kTile)) - 1;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint64_t see = (draft ? vis[i] : in) >> (wn * NP + 2 * qc);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (!(see >> (8 * j) & 1)) s[j][2 * i] = -INFINITY;
-          if (!(see >> (8 * j + 1) & 1)) s[j][2 * i + 1] = -INFINITY;
-        }
-      }
-    }
-
-    // ---- online softmax
-    float corr[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mx = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
-#pragma unroll
-      for (int j = 1; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[i], mx * rs[i]);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      corr[i] = ex2(m[i] - mu);
-      m[i] = mn;
-      const float bias = kBias - mu;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        s[j][2 * i] = ex2(fmaf(s[j][2 * i], rs[i], bias));
-        s[j][2 * i + 1] = ex2(fmaf(s[j][2 * i + 1], rs[i], bias));
-        sum += s[j][2 * i] + s[j][2 * i + 1];
-      }
-      l[i] = fmaf(l[i], corr[i], sum);
-    }
-    // f32 cache: the weights take over the scale of their v rows, in units of the largest that
-    // the row sees
-    float2 vs[F16 ? 1 : NT];
-    float vinv[2] = {1.f, 1.f};
-    if constexpr (!F16) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) vs[j] = *reinterpret_cast<const float2*>(&sm.vscale[wn * NP + j * 8 + 2 * qc]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint64_t see = (draft ? vis[i] : ~0ull) >> (wn * NP + 2 * qc);
-        float top = vunit[i];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          top = fmaxf(top, fmaxf(see >> (8 * j) & 1 ? vs[j].x : 0.f, see >> (8 * j + 1) & 1 ? vs[j].y : 0.f));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        vinv[i] = __uint_as_float((254u << 23) - __float_as_uint(top));  // 1 / top, a power of two
-        corr[i] *= vunit[i] * vinv[i];
-        vunit[i] = top;
-      }
-    }
-
-    // ---- weighted values
-    const unsigned long long bad = draft ? sm.bad : 0ull;
-    if (bad) {
-      const KV* vrow = vd + ((int64_t)cur.b * a.n_kv + cur.h) * a.n_nodes * kHd;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (vis[i] & bad) {  // the other rows keep every bit
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            o[d][2 * i] *= corr[i];
-            o[d][2 * i + 1] *= corr[i];
-          }
-          corr[i] = 1.f;
-        }
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const int slot = wn * NP + j;
-        if (!(bad >> slot & 1)) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float p = __shfl_sync(0xffffffffu, s[j / 8][2 * i + (j & 1)], (lane & 28) | ((j & 7) >> 1));
-          if (!(vis[i] >> slot & 1)) continue;
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              o[d][2 * i + e] += p * ((float)vrow[(int64_t)slot * kHd + d * 8 + 2 * qc + e] * vinv[i]);
-        }
-      }
-    }
-    uint32_t ph[NT / 2][4], pl[NT / 2][4];
-#pragma unroll
-    for (int pk = 0; pk < NT / 2; ++pk)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {  // (row, row + 8) of n tile 2 pk, then of 2 pk + 1
-        const int j = 2 * pk + (e >> 1);
-        float x = s[j][2 * (e & 1)], y = s[j][2 * (e & 1) + 1];
-        if constexpr (!F16) {
-          x = x * vinv[e & 1] * vs[j].x;
-          y = y * vinv[e & 1] * vs[j].y;
-        }
-        split2(x, y, ph[pk][e], pl[pk][e]);
-      }
-    const int vr = wn * NP + (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-    for (int d = 0; d < 8; d += 2) {
-      float t[2][4], tl[2][4];
-#pragma unroll
-      for (int pk = 0; pk < NT / 2; ++pk) {
-        const uint32_t off = tile_off(vr + pk * 16, d + ((lane >> 4) & 1));
-        uint32_t b[4];
-        ldsm4t(v_hi + off, b);
-        if (pk == 0) {
-          mma0(t[0], ph[pk], b[0], b[1]);
-          mma0(t[1], ph[pk], b[2], b[3]);
-          mma0(tl[0], pl[pk], b[0], b[1]);
-          mma0(tl[1], pl[pk], b[2], b[3]);
-        } else {
-          mma(t[0], ph[pk], b[0], b[1]);
-          mma(t[1], ph[pk], b[2], b[3]);
-          mma(tl[0], pl[pk], b[0], b[1]);
-          mma(tl[1], pl[pk], b[2], b[3]);
-        }
-        if constexpr (!F16) {
-          ldsm4t(v_lo + off, b);
-          mma(tl[0], ph[pk], b[0], b[1]);
-          mma(tl[1], ph[pk], b[2], b[3]);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[d + x][e] = fmaf(o[d + x][e], corr[e >> 1], t[x][e] + tl[x][e]);
-    }
-
-    // ---- the end of this CTA's part of the walk
-    if (draft || !more) {
-      const bool whole = t_begin == 0 && draft;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      }
-      const float unit[2] = {F16 ? 1.f : vunit[0], F16 ? 1.f : vunit[1]};
-      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(BM);
-      auto out_row = [&](int r) { return row_of(a, a.out, cur, cur.r * BM + r); };  // row r of the block
-      if constexpr (WN == 1) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = wm * 16 + qr + 8 * i;
-          if (whole) {
-            if (cur.r * BM + r < rows) {
-              const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-              float2* dst = reinterpret_cast<float2*>(out_row(r)) + qc;
-#pragma unroll
-              for (int d = 0; d < 8; ++d)
-                dst[4 * d] = l[i] == 0.f ? make_float2(0.f, 0.f)
-                                         : make_float2(o[d][2 * i] * inv * unit[i], o[d][2 * i + 1] * inv * unit[i]);
-            }
-          } else {
-            if (qc == 0) {
-              part[r] = m[i];
-              part[BM + r] = l[i];
-            }
-            float2* dst = reinterpret_cast<float2*>(part + 2 * BM + r * kHd) + qc;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) dst[4 * d] = make_float2(o[d][2 * i] * unit[i], o[d][2 * i + 1] * unit[i]);
-          }
-        }
-      } else {
-        // join the warps' shares of the positions
-        __syncthreads();
-        float* mine = sm.merge[warp];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = qr + 8 * i;
-          if (qc == 0) {
-            mine[r] = m[i];
-            mine[16 + r] = l[i];
-          }
-          float2* dst = reinterpret_cast<float2*>(mine + 32 + r * kHd) + qc;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) dst[4 * d] = make_float2(o[d][2 * i] * unit[i], o[d][2 * i + 1] * unit[i]);
-        }
-        __syncthreads();
-        for (int x = tid; x < BM * (kHd / 4); x += kThreads) {
-          const int r = x / (kHd / 4), c = x % (kHd / 4);
-          const int w0 = r / 16, rr = r % 16;
-          float mt = -INFINITY, lt = 0.f;
-          float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < WN; ++w) mt = fmaxf(mt, sm.merge[w0 + w * WM][rr]);
-#pragma unroll
-          for (int w = 0; w < WN; ++w) {
-            const float* src = sm.merge[w0 + w * WM];
-            const float mw = src[rr], lw = src[16 + rr];
-            const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
-            const float4 ow = *(reinterpret_cast<const float4*>(src + 32 + rr * kHd) + c);
-            lt = fmaf(lw, f, lt);
-            ot.x = fmaf(ow.x, f, ot.x);
-            ot.y = fmaf(ow.y, f, ot.y);
-            ot.z = fmaf(ow.z, f, ot.z);
-            ot.w = fmaf(ow.w, f, ot.w);
-          }
-          if (whole) {
-            if (cur.r * BM + r < rows) {
-              const float inv = lt == 0.f ? 0.f : 1.f / lt;
-              reinterpret_cast<float4*>(out_row(r))[c] =
-                  lt == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : make_float4(ot.x * inv, ot.y * inv, ot.z * inv, ot.w * inv);
-            }
-          } else {
-            if (c == 0) {
-              part[r] = mt;
-              part[BM + r] = lt;
-            }
-            reinterpret_cast<float4*>(part + 2 * BM + r * kHd)[c] = ot;
-          }
-        }
-        if (more) __syncthreads();
-      }
-      t_begin = -1;
-      if (draft && more) {
-        __syncthreads();  // every warp has read `bad`
-        if (tid == 0) sm.bad = 0;
-      }
-    }
-    advance(sm.plan, a.n_kv, cur);
-  }
-  cp_wait<0>();
-}
-
 // ------------------------------------------------------------------ 16 rows
-// Few rows to a kv head: blocks of 16, and 8 warps that walk the positions side by side, 16 at a
-// time, each with a ring of its own (no barrier until the walk's end, where the warps' results
+// Few rows to a kv head: blocks of 16, and 8 warps that walk the positions side by side, 16
+// (f32) or 32 at a time, each with a ring of its own (no barrier until the walk's end, where the warps' results
 // are joined).  A binary16 cache as above.  An f32 cache without a conversion in
 // shared memory: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
 // fraction bits, lo = as many of the rest: at most 2^-20 off), hi hi + lo hi + hi lo.  TF32 keeps
@@ -828,7 +323,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
   const KV* kd = static_cast<const KV*>(a.kd);
   const KV* vd = static_cast<const KV*>(a.vd);
 
-  // this warp's 16 positions of the unit at `pre` into ring slot s (zeros behind their end), and
+  // this warp's positions of the unit at `pre` into ring slot s (zeros behind their end), and
   // on to the next unit
   auto produce = [&](int s) {
     if (pre.u < end) {
@@ -931,7 +426,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
         for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     }
 
-    // ---- this warp's 16 positions
+    // ---- this warp's positions
     const int slot = it % S::kStages;
     cp_wait<kLag - 1>();
     __syncwarp();  // every lane's copies have landed, and the slot before this one has been read
@@ -1498,6 +993,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
     produce(0);
     if (F16) produce(1);
   }
+  __syncwarp();
 
   // one thread: s = q k^T, the low parts first (what is cut off there does not count)
   auto issue_s = [&](uint32_t k_hi, uint32_t k_lo) {
@@ -1581,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
         // Behind the last row lies what the cache happens to hold, and a draft's values may hold
         // an infinity or NaN: either would reach every row of the product (0 times it is NaN).
         // Such rows are cleared here; a draft's is added below where it is seen.
-        if (!lost && !tc::mbar_wait_sleep(mb_full, full)) lost = true;
+        if (!lost && !tc::mbar_wait(mb_full, full)) lost = true;
         for (int r = tid >> 2; r < kT; r += kThreads128 / 4) {
           uint4* v = sm.ring[slot][1] + r * 8 + (tid & 3) * 2;
           uint32_t off = 0;
@@ -1602,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
         tc::fence_proxy_async_smem();
       }
     } else {
-      if (!lost && !tc::mbar_wait_sleep(mb_full, full)) lost = true;
+      if (!lost && !tc::mbar_wait(mb_full, full)) lost = true;
       // four threads to a position, 16 dims each; their 16-byte reads in an order without bank
       // conflicts
       const int r = tid >> 2, j = tid & 3, turn = (j >> 1) + 2 * (r & 1);
@@ -1660,15 +1156,17 @@ __global__ void __launch_bounds__(kThreads128, 2)
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncthreads();
-      if (F16 && uwarp == 0 && !lost && !tc::mbar_wait_sleep(mb_full, full)) lost = true;
+      if (F16 && uwarp == 0 && !lost && !tc::mbar_wait(mb_full, full)) lost = true;
       __syncwarp();
       if (uwarp == 0 && elect_one()) {
         issue_s(k_hi, k_lo);
         tc::mma_commit(mb_s);
       }
+      __syncwarp();
       if (!F16 && tid == kStepper) produce(it + 1);  // all threads have read the raw tile
+      __syncwarp();
     }
-    if (!lost && !tc::mbar_wait_sleep(mb_s, (uint32_t)it & 1u)) lost = true;
+    if (!lost && !tc::mbar_wait(mb_s, (uint32_t)it & 1u)) lost = true;
     tc::fence_after_sync();
 
     // 16 or 32 of this thread's scores, in log2 units but for the row's scale; what the row does not
@@ -1812,15 +1310,17 @@ __global__ void __launch_bounds__(kThreads128, 2)
       for (int kk = 0; kk < kT / 16; ++kk) tc::mma_f16_ts(tm + kColsS, tm + 16 * kk, v_desc(v_hi, kk), kIdescO, 1);
       tc::mma_commit(mb_o);
     }
+    __syncwarp();  // no lane polls while another of its warp still has the products to issue
     if (tid == kStepper) step(it + 2);  // over tile it - 1's, which everyone is done with
-    if (!lost && !tc::mbar_wait_sleep(mb_o, (uint32_t)it & 1u)) lost = true;
+    __syncwarp();
+    if (!lost && !tc::mbar_wait(mb_o, (uint32_t)it & 1u)) lost = true;
     if constexpr (F16) {
       // p and this tile's slot are read: the next tile's scores, under the sums below, and the
       // copy of the one after it
       if (uwarp == 0) {
         const bool ahead = sm.next[(it + 1) % 3].valid && !sm.next[(it + 1) % 3].begin;
         const int ns = (it + 1) % S::kStages;
-        if (ahead && !lost && !tc::mbar_wait_sleep(mb_o + 8 + 8 * ns, (uint32_t)((it + 1) / S::kStages) & 1u))
+        if (ahead && !lost && !tc::mbar_wait(mb_o + 8 + 8 * ns, (uint32_t)((it + 1) / S::kStages) & 1u))
           lost = true;
         __syncwarp();
         if (ahead && elect_one()) {
@@ -1829,6 +1329,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
         }
       }
       if (tid == kStepper) produce(it + 2);
+      __syncwarp();
     }
     tc::fence_after_sync();
     if (warp_live) {
@@ -1932,16 +1433,17 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
   *dst = lt == 0.f ? make_float2(0.f, 0.f) : make_float2(ot.x / lt, ot.y / lt);
 }
 
-// The 16-row kernel up to so many rows to a kv head, the 64-row kernel behind them.
+// The 16-row kernel up to 32 rows to a kv head (two blocks; 58.7 us for 32 rows at 4000 positions of
+// 2 x 32 heads f32, where 128-row blocks take 65 us whatever they hold), 128-row blocks behind them.
 inline bool by16(int n_nodes, int group) { return n_nodes * group <= 32; }
 inline int block_rows(int n_nodes, int group) {
-  return by16(n_nodes, group) ? 16 : n_nodes * group <= 64 ? 64 : 128;
+  return by16(n_nodes, group) ? 16 : 128;
 }
 inline int blocks_of(int n_nodes, int group) {
   const int bm = block_rows(n_nodes, group);
   return (n_nodes * group + bm - 1) / bm;
 }
-constexpr int kMaxCtas = 3;  // CTAs to an SM at most
+constexpr int kMaxCtas = 2;  // CTAs to an SM at most
 // CTAs of a call: what fits the device at once, and no more than there can be units for.
 inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, int sub, int per_sm) {
   const int64_t units = (int64_t)batch * n_kv * blocks_of(n_nodes, group) *
@@ -1968,7 +1470,8 @@ bool row_map(CUtensorMap* map, const void* base, int64_t rows) {
   static const Encode encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &found) != cudaSuccess ||
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
         found != cudaDriverEntryPointSuccess)
       f = nullptr;
     return reinterpret_cast<Encode>(f);
@@ -1985,17 +1488,14 @@ template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
   if (by16(a.n_nodes, a.group))
     return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), 1, st);
-  if (block_rows(a.n_nodes, a.group) == 128) {
-    Maps128 maps = {};
-    if constexpr (F16) {
-      const int64_t heads = (int64_t)a.batch * a.n_kv;
-      const void* base[4] = {a.kc, a.vc, a.kd, a.vd};
-      for (int i = 0; i < 4; ++i)
-        if (!row_map(&maps.m[i], base[i], heads * (i < 2 ? a.max_ctx : a.n_nodes))) return QD_ERR_CUDA;
-    }
-    return launch<128, -tile128(F16)>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>) + 1024, 2, st, maps);
+  Maps128 maps = {};
+  if constexpr (F16) {
+    const int64_t heads = (int64_t)a.batch * a.n_kv;
+    const void* base[4] = {a.kc, a.vc, a.kd, a.vd};
+    for (int i = 0; i < 4; ++i)
+      if (!row_map(&maps.m[i], base[i], heads * (i < 2 ? a.max_ctx : a.n_nodes))) return QD_ERR_CUDA;
   }
-  return launch<64, -kTile>(a, k_tree_attn<F16, 4, 1>, kThreads, sizeof(Smem<F16>), F16 ? 3 : 2, st);
+  return launch<128, -tile128(F16)>(a, k_tree_attn_128<F16>, kThreads128, sizeof(Smem128<F16>) + 1024, 2, st, maps);
 }
 
 // The units of a call must fit an int.
@@ -2059,8 +1559,7 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   a.batch = batch;
   a.ws = static_cast<float*>(workspace);
   a.blocks = blocks_of(n_nodes, a.group);
-  const int rows = block_rows(n_nodes, a.group);
-  const int sub = rows == 16 ? sub_positions(kv_f16) : rows == 128 ? -tile128(kv_f16) : -kTile;
+  const int sub = by16(n_nodes, a.group) ? sub_positions(kv_f16) : -tile128(kv_f16);
   a.whole = walk_tiles(sub, max_ctx, n_nodes) <= kWholeTiles;
   return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
 }

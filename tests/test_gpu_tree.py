@@ -74,14 +74,18 @@ class Attn:
     (1, 1, 1, 1, [0]), (1, 1, 1, 1, [1]), (9, 3, 8, 256, [100]), (9, 3, 1, 70, [64, 63, 65, 1]),
     (32, 32, 16, 200, [130, 0]), (8, 1, 27, 300, [300, 0, 17, 64, 128]), (4, 2, 64, 129, [128, 129]),
     (16, 2, 64, 520, [511]), (7, 1, 33, 96, [95]), (5, 5, 3, 2100, [2049]), (6, 2, 22, 1000, [1000, 1, 999]),
-    (10, 2, 13, 64, list(range(48, 64)))])
+    (10, 2, 13, 64, list(range(48, 64))),
+    # 16, 17, 32, 33, 64 rows to a kv head, one and two blocks of 128, walks whole and cut
+    (2, 1, 8, 40, [40]), (1, 1, 17, 300, [299, 31]), (4, 1, 8, 1030, [1029, 513]), (3, 1, 11, 640, [640, 127, 129]),
+    (2, 2, 64, 1300, [1290, 640]), (4, 1, 33, 2400, [2399, 0, 897, 128]), (8, 1, 64, 1500, [1500])])
 def test_attn_matches_64_bits(qd, hq, hk, n, ctx, pos, f16):
     Attn(qd, 1, hq, hk, n, ctx, pos, f16=f16).check()
 
 
 @pytest.mark.parametrize("f16", [False, True])
-def test_attn_long_context_split(qd, f16):
-    Attn(qd, 2, 3, 1, 5, 20000, [19990], f16=f16).check()
+@pytest.mark.parametrize("hq,n", [(3, 5), (8, 30)])
+def test_attn_long_context_split(qd, hq, n, f16):
+    Attn(qd, 2, hq, 1, n, 20000, [19990], f16=f16).check()
 
 
 @pytest.mark.parametrize("f16", [False, True])
@@ -117,10 +121,12 @@ def test_attn_mask_bits_behind_the_nodes_do_not_count(qd):
 
 
 @pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("hq,hk,ctx,pos", [(6, 2, 140, [70, 128]), (3, 3, 140, [70, 128]), (6, 2, 2300, [2201, 1000]),
+                                           (2, 2, 2500, [2201, 1000])])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_attn_unseen_values_do_not_reach_a_row(qd, bad, f16):
+def test_attn_unseen_values_do_not_reach_a_row(qd, bad, hq, hk, ctx, pos, f16):
     """Slots that a node does not see, positions behind pos and slots behind n_valid hold `bad`."""
-    a = Attn(qd, 6, 6, 2, 24, 140, [70, 128], cnt=[24, 20], f16=f16)
+    a = Attn(qd, 6, hq, hk, 24, ctx, pos, cnt=[24, 20], f16=f16)
     want = a.check(a.call())
     for b in range(2):
         a.k[b, :, a.pos[b]:] = bad
@@ -138,8 +144,37 @@ def test_attn_unseen_values_do_not_reach_a_row(qd, bad, f16):
 
 
 @pytest.mark.parametrize("f16", [False, True])
-def test_attn_non_finite_query_stays_in_its_row(qd, f16):
-    a = Attn(qd, 7, 6, 2, 24, 140, [70], f16=f16)
+@pytest.mark.parametrize("hk", [2, 6])
+def test_attn_infinite_value_in_the_cache_stays_in_its_dim(qd, hk, f16):
+    a = Attn(qd, 16, 6, hk, 24, 300, [290], f16=f16)
+    a.v[0, :, 100, 3] = np.inf
+    a.v[0, :, 17, 60] = np.nan
+    got = a.call().cpu().numpy()
+    dims = [d for d in range(HD) if d not in (3, 60)]
+    assert np.all(~np.isfinite(got[..., [3, 60]]))
+    a.v[0, :, 100, 3] = a.v[0, :, 17, 60] = 0
+    want, smax, vmax = a.ref(0)
+    assert np.abs(got[0] - want)[..., dims].max() <= attn_tol(314, smax, vmax)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("hk", [2, 6])
+def test_attn_unseen_large_values_keep_the_others_digits(qd, hk, f16):
+    """A draft that a row does not see may hold the type's largest value."""
+    a = Attn(qd, 17, 6, hk, 24, 100, [90], f16=f16)
+    want = a.call().cpu().numpy()
+    big = 65504.0 if f16 else 3e38
+    a.kd[:, :, 7] = big
+    a.vd[:, :, 7] = -big
+    got = a.call().cpu().numpy()
+    sees = a.anc[0, :, 7]
+    assert np.array_equal(got[0][~sees], want[0][~sees]) and not sees.all()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("hk", [2, 6])
+def test_attn_non_finite_query_stays_in_its_row(qd, hk, f16):
+    a = Attn(qd, 7, 6, hk, 24, 140, [70], f16=f16)
     want = a.call().cpu().numpy()
     a.q.reshape(1, 24, 6, HD)[0, 4, 1, 9] = np.nan
     a.q.reshape(1, 24, 6, HD)[0, 20, 5, 0] = np.inf
@@ -150,13 +185,15 @@ def test_attn_non_finite_query_stays_in_its_row(qd, f16):
 
 
 @pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("n", [9, 20])
 @pytest.mark.parametrize("kscale,vscale", [(1e-3, 1e-4), (8.0, 300.0)])
-def test_attn_small_and_large_values(qd, f16, kscale, vscale):
-    Attn(qd, 8, 6, 2, 9, 400, [390], f16=f16, kscale=kscale, vscale=vscale).check()
+def test_attn_small_and_large_values(qd, f16, n, kscale, vscale):
+    Attn(qd, 8, 6, 2, n, 400, [390], f16=f16, kscale=kscale, vscale=vscale).check()
 
 
-def test_attn_values_beyond_binary16_in_an_f32_cache(qd):
-    a = Attn(qd, 9, 6, 2, 9, 400, [390], kscale=1e-6, vscale=1e9)
+@pytest.mark.parametrize("n", [9, 20])
+def test_attn_values_beyond_binary16_in_an_f32_cache(qd, n):
+    a = Attn(qd, 9, 6, 2, n, 400, [390], kscale=1e-6, vscale=1e9)
     a.k[0, 0, 40] *= 1e12  # one row far larger than its neighbours: 1e6
     a.q[:] *= 1e-6
     a.check()
@@ -167,6 +204,22 @@ def test_attn_peaked_rows(qd):
     a = Attn(qd, 10, 4, 1, 12, 700, [690], kscale=6.0)
     a.q *= 6.0
     a.check()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("n", [5, 40])
+def test_attn_two_calls_at_once_with_their_own_workspaces(qd, n, f16):
+    pair = [Attn(qd, 18 + i, 9, 3, n, 5000, [4990, 3000 - 900 * i], f16=f16) for i in range(2)]
+    want = [a.call().clone() for a in pair]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in pair]
+    outs = [torch.full_like(w, 7.0) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for a, st, out in zip(pair, streams, outs):
+            qd.tree_attn(*a.args[:6], out, *a.args[7:], kv_f16=f16, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
 def test_attn_same_bits_again_and_on_another_stream(qd):
@@ -184,13 +237,15 @@ def test_attn_same_bits_again_and_on_another_stream(qd):
     assert torch.equal(out, want)
 
 
-def test_attn_captured_replays_follow_the_device_positions(qd):
-    a = Attn(qd, 12, 9, 3, 8, 600, [100, 590])
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("n,ctx", [(8, 600), (8, 3000), (30, 600), (30, 3000)])
+def test_attn_captured_replays_follow_the_device_positions(qd, n, ctx, f16):
+    a = Attn(qd, 12, 9, 3, n, ctx, [100, ctx - 10], f16=f16)
     out = a.call()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        a.qd.tree_attn(*a.args)
-    for pos in ([0, 600], [599, 1], [64, 65]):
+        a.qd.tree_attn(*a.args, kv_f16=f16)
+    for pos in ([0, ctx], [ctx - 1, 1], [64, 65]):
         a.small[0].copy_(_i32(pos))
         out.fill_(7.0)
         g.replay()
@@ -199,10 +254,11 @@ def test_attn_captured_replays_follow_the_device_positions(qd):
         a.check(out)
 
 
-def test_attn_offsets_past_32_bits(qd):
+@pytest.mark.parametrize("hq", [32, 128])
+def test_attn_offsets_past_32_bits(qd, hq):
     """A binary16 cache of more than 2^32 elements: the last sequence's rows are the ones read."""
-    hq = hk = 32
-    ctx, b, n, p = 140000, 16, 2, 130
+    hk = 32
+    ctx, b, n, p = 140000, 16, 9, 130
     need = b * hk * ctx * HD
     assert need > 2**32
     if torch.cuda.mem_get_info()[0] < 5 * need:
