@@ -263,7 +263,7 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
 // ------------------------------------------------------------------ 16 rows
 // Few rows to a kv head: blocks of 16, and 8 warps that walk the positions side by side, 16
 // (f32) or 32 at a time, each with a ring of its own (no barrier until the walk's end, where the warps' results
-// are joined).  A binary16 cache as above.  An f32 cache without a conversion in
+// are joined while the next walk's queries arrive).  A binary16 cache as above.  An f32 cache without a conversion in
 // shared memory: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
 // fraction bits, lo = as many of the rest: at most 2^-20 off), hi hi + lo hi + hi lo.  TF32 keeps
 // f32's exponents, so nothing is scaled; the products run at half the binary16 rate, which the
@@ -294,7 +294,7 @@ struct Smem16 {
   static constexpr int kStages = 3;
   static constexpr int kRowBytes = F16 ? 128 : 256;
   uint4 ring[kWarps16][kStages][2][sub_positions(F16) * kRowBytes / 16];  // K, V
-  float join[2][36][32];                                    // o, m, l of a warp's lanes
+  float part[kWarps16][part_floats(16)];                    // m, l, o of a warp's share
   Plan plan;
 };
 
@@ -369,62 +369,87 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
   uint64_t vis[2];
   int t_begin = -1;
 
+  // a walk's queries and masks: asked for ...
+  float4 x[2][4];
+  auto load_q = [&](const Cursor& c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = c.r * 16 + qr + 8 * i, node = at / a.group, g = at % a.group;
+      const bool live = at < c.cnt * a.group;
+      const float4* src = reinterpret_cast<const float4*>(
+          a.q + (int64_t)c.b * a.q_batch_stride + ((int64_t)node * a.n_kv * a.group + c.h * a.group + g) * kHd);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = live ? __ldcg(src + qc + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      vis[i] = live ? a.mask[(int64_t)c.b * a.n_nodes + node] : 0ull;
+      if (c.cnt < 64) vis[i] &= (1ull << c.cnt) - 1;
+    }
+  };
+  // ... and made operands.  The lane has dims 4 (qc + 4 j) .. + 3 of its rows.  f32 cache: k step
+  // 2 j + e / 2 has them at k = qc and qc + 4.  Binary16: a fragment wants dims 2 qc, 2 qc + 1 of
+  // every 8, so lanes qc and qc ^ 1, qc ^ 2 exchange.
+  auto set_q = [&]() {
+    const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (F16) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[i][j].x *= scale;
+          x[i][j].y *= scale;
+          x[i][j].z *= scale;
+          x[i][j].w *= scale;
+          mx = max(mx, abs_max(x[i][j]));
+        }
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = scale_exp(mx);
+        rs[i] = pow2(e);
+        const float f = pow2(-e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // dims 16 j + 4 qc .. + 3 as two pairs; k step j's fragment has pairs qc and qc + 4 of its 8
+          uint32_t h0, l0, h1, l1;
+          split2(x[i][j].x * f, x[i][j].y * f, h0, l0);
+          split2(x[i][j].z * f, x[i][j].w * f, h1, l1);
+          // pair p stands in lane p / 2, first or second
+          const int from = (lane & 28) | (qc >> 1);
+          const uint32_t ha = __shfl_sync(0xffffffffu, h0, from), hb = __shfl_sync(0xffffffffu, h1, from);
+          const uint32_t la = __shfl_sync(0xffffffffu, l0, from), lb = __shfl_sync(0xffffffffu, l1, from);
+          const uint32_t hc = __shfl_sync(0xffffffffu, h0, from + 2), hd = __shfl_sync(0xffffffffu, h1, from + 2);
+          const uint32_t lc = __shfl_sync(0xffffffffu, l0, from + 2), ld = __shfl_sync(0xffffffffu, l1, from + 2);
+          qh[j][i] = qc & 1 ? hb : ha;
+          ql[j][i] = qc & 1 ? lb : la;
+          qh[j][i + 2] = qc & 1 ? hd : hc;
+          ql[j][i + 2] = qc & 1 ? ld : lc;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          auto in = [scale](float f) { return (f + (f - f)) * scale; };  // an infinity is a NaN too
+          split_tf32(in(x[i][j].x), qh[2 * j][i], ql[2 * j][i]);
+          split_tf32(in(x[i][j].y), qh[2 * j][i + 2], ql[2 * j][i + 2]);
+          split_tf32(in(x[i][j].z), qh[2 * j + 1][i], ql[2 * j + 1][i]);
+          split_tf32(in(x[i][j].w), qh[2 * j + 1][i + 2], ql[2 * j + 1][i + 2]);
+        }
+      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+  };
+  load_q(cur);
+  set_q();
+
   for (int it = 0; cur.u < end; ++it) {
     const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
     const int rows = cnt * a.group;
     const bool last = cur.t == nt - 1;
     const bool more = cur.u + 1 + (last ? kStart : 0) < end;
-    if (t_begin < 0) {
-      t_begin = cur.t;
-      const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = cur.r * 16 + qr + 8 * i;
-        const bool live = at < rows;
-        const int node = at / a.group, g = at % a.group;
-        const float* src = a.q + (int64_t)cur.b * a.q_batch_stride +
-                           ((int64_t)node * a.n_kv * a.group + cur.h * a.group + g) * kHd;
-        if constexpr (F16) {
-          float2 x[8];
-          uint32_t mx = 0;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            x[c] = live ? __ldcg(reinterpret_cast<const float2*>(src + c * 8) + qc) : make_float2(0.f, 0.f);
-            x[c].x *= scale;
-            x[c].y *= scale;
-            mx = max(mx, max(abs_bits(x[c].x), abs_bits(x[c].y)));
-          }
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int e = scale_exp(mx);
-          rs[i] = pow2(e);
-          const float f = pow2(-e);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            split2(x[c].x * f, x[c].y * f, qh[c >> 1][i + 2 * (c & 1)], ql[c >> 1][i + 2 * (c & 1)]);
-        } else {
-          // the lane's dims 4 (qc + 4 j) .. + 3: k step 2 j + e / 2 has them at k = qc and qc + 4
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 x = live ? __ldcg(reinterpret_cast<const float4*>(src) + qc + 4 * j)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-            auto in = [scale](float f) { return (f + (f - f)) * scale; };  // an infinity is a NaN too
-            split_tf32(in(x.x), qh[2 * j][i], ql[2 * j][i]);
-            split_tf32(in(x.y), qh[2 * j][i + 2], ql[2 * j][i + 2]);
-            split_tf32(in(x.z), qh[2 * j + 1][i], ql[2 * j + 1][i]);
-            split_tf32(in(x.w), qh[2 * j + 1][i + 2], ql[2 * j + 1][i + 2]);
-          }
-        }
-        vis[i] = live ? a.mask[(int64_t)cur.b * a.n_nodes + node] : 0ull;
-        if (cnt < 64) vis[i] &= (1ull << cnt) - 1;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-      }
-#pragma unroll
-      for (int d = 0; d < 8; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
-    }
+    if (t_begin < 0) t_begin = cur.t;
 
     // ---- this warp's positions
     const int slot = it % S::kStages;
@@ -687,78 +712,72 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       }
-      // warps 6, 7 -> 4, 5 -> 2, 3 -> 0, 1, then 1 -> 0, lane by lane
-#pragma unroll
-      for (int n = kWarps16 - 2; n >= 0; n -= 2) {
-        const int from = n ? n : 1, width = n ? 2 : 1, to = n ? n - 2 : 0;
-        __syncthreads();
-        if (warp >= from && warp < from + width) {
-          float(&mine)[36][32] = sm.join[warp - from];
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mine[4 * d + e][lane] = o[d][e];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mine[32 + i][lane] = m[i];
-            mine[34 + i][lane] = l[i];
-          }
-        }
-        __syncthreads();
-        if (warp >= to && warp < to + width) {
-          const float(&of)[36][32] = sm.join[warp - to];
-          float f[2], g[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float mo = of[32 + i][lane], lo = of[34 + i][lane];
-            const float top = fmaxf(m[i], mo);
-            // a share without a maximum has l = 0 or NaN
-            f[i] = m[i] == -INFINITY ? l[i] : ex2(m[i] - top);
-            g[i] = mo == -INFINITY ? lo : ex2(mo - top);
-            m[i] = top;
-            l[i] = l[i] * f[i] + lo * g[i];
-          }
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = o[d][e] * f[e >> 1] + of[4 * d + e][lane] * g[e >> 1];
-        }
-      }
-      if (warp == 0) {
-        const bool whole = t_begin == 0 && last;
-        float* part = a.ws + ((int64_t)blockIdx.x * 2 + (t_begin > 0 ? 0 : 1)) * part_floats(16);
+      const Cursor done = cur;
+      const bool whole = t_begin == 0 && last;
+      const int part_slot = t_begin > 0 ? 0 : 1;
+      __syncthreads();  // the last walk's shares have been read
+      {
+        // pair c of a row at c ^ 4 (row & 7): no bank twice
+        float* mine = sm.part[warp];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = qr + 8 * i;
-          if (whole && cur.r * 16 + r >= rows) continue;
-          const float inv = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
-          float* dst = whole ? row_of(a, a.out, cur, cur.r * 16 + r) : part + 32 + r * kHd;
-          if (!whole && qc == 0) {
-            part[r] = m[i];
-            part[16 + r] = l[i];
+          if (qc == 0) {
+            mine[r] = m[i];
+            mine[16 + r] = l[i];
           }
-          const bool none = whole && l[i] == 0.f;
-          float x[8][2];
+          float2* dst = reinterpret_cast<float2*>(mine + 32 + r * kHd);
 #pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[d][e] = none ? 0.f : o[d][2 * i + e] * inv;
-          if constexpr (F16) {
-#pragma unroll
-            for (int d = 0; d < 8; ++d) reinterpret_cast<float2*>(dst)[4 * d + qc] = make_float2(x[d][0], x[d][1]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                reinterpret_cast<float4*>(dst)[4 * qc + 2 * e + c] =
-                    make_float4(x[4 * c][e], x[4 * c + 1][e], x[4 * c + 2][e], x[4 * c + 3][e]);
+          for (int d = 0; d < 8; ++d) {
+            if constexpr (F16)
+              dst[(4 * d + qc) ^ (4 * qr)] = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+            else  // dims 16 qc + 8 e + 2 k, + 1
+              dst[(8 * qc + d) ^ (4 * qr)] = make_float2(o[2 * (d & 3)][2 * i + (d >> 2)], o[2 * (d & 3) + 1][2 * i + (d >> 2)]);
           }
         }
       }
+      advance(sm.plan, a.n_kv, cur);
+      if (more) load_q(cur);  // on its way meanwhile
+      __syncthreads();
+      // a warp to two rows
+      const int done_rows = done.cnt * a.group;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 2 * warp + x;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps16; ++w) mt = fmaxf(mt, sm.part[w][r]);
+        float lt = 0.f;
+        float2 ot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps16; ++w) {
+          const float mw = sm.part[w][r], lw = sm.part[w][16 + r];
+          const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
+          const float2 ow = reinterpret_cast<const float2*>(sm.part[w] + 32 + r * kHd)[lane ^ (4 * (r & 7))];
+          lt = fmaf(lw, f, lt);
+          ot.x = fmaf(ow.x, f, ot.x);
+          ot.y = fmaf(ow.y, f, ot.y);
+        }
+        if (whole) {
+          if (done.r * 16 + r < done_rows) {
+            const float inv = 1.f / lt;
+            reinterpret_cast<float2*>(row_of(a, a.out, done, done.r * 16 + r))[lane] =
+                lt == 0.f ? make_float2(0.f, 0.f) : make_float2(ot.x * inv, ot.y * inv);
+          }
+        } else {
+          float* part = a.ws + ((int64_t)blockIdx.x * 2 + part_slot) * part_floats(16);
+          if (lane == 0) {
+            part[r] = mt;
+            part[16 + r] = lt;
+          }
+          reinterpret_cast<float2*>(part + 32 + r * kHd)[lane] = ot;
+        }
+      }
+      if (more) set_q();
       t_begin = -1;
+    } else {
+      advance(sm.plan, a.n_kv, cur);
     }
-    advance(sm.plan, a.n_kv, cur);
   }
   cp_wait<0>();
 }
