@@ -25,9 +25,10 @@
 // What bounds it: HBM for few rows on long caches, the instructions of the softmax and of the
 // splits for many rows, latency for short caches.  Measured on one GB300 (floor: the bytes at
 // 6.77 TB/s or the products at 1946 TFLOP/s, counted once):
-//   9/3 heads, 8 nodes, 100 positions, f32              6.6 us (floor 0.03)
-//   32/32 heads, 16 nodes, 4080 positions, f32         22.6 us (10.0)
-//   the same, 16 ragged sequences, binary16              64 us (40)
+//   9/3 heads, 8 nodes, 100 positions, f32              7.6 us (floor 0.03)
+//   32/32 heads, 16 nodes, 4080 positions, f32         22.5 us (10.0)
+//   the same, 16 sequences of 4095, f32                 183 us (160)
+//   the same, 16 ragged sequences, binary16              62 us (40)
 //   32/8 heads, 64 nodes, 32700 positions, binary16      60 us (10)
 // The unit counts: kStart 3 against 1 / 2 / 5 at 16 ragged sequences 64 against 95 / 72 / 66 us;
 // kMinPer 2 against 4 at 9/3 heads and 1000 positions 11.2 against 12.9 us.
@@ -49,10 +50,10 @@ constexpr int kMinPer = 2;     // units of a CTA at least
 constexpr int kWholeTiles = 8;  // walks of at most so many tiles are not cut
 constexpr int kStart = 3;      // what the start of a walk costs, in tiles
 
-// k_tree_attn_16: 8 warps, each with tiles of its own of 16 (f32) or 32 positions; what the warps
-// do side by side is one unit of work
-constexpr int kWarps16 = 8;
+// k_tree_attn_16: warps with tiles of their own, 12 of 16 positions (f32 cache) or 8 of 32; what
+// they do side by side is one unit of work
 __host__ __device__ constexpr int sub_positions(bool f16) { return f16 ? 32 : 16; }
+__host__ __device__ constexpr int sub_warps(int sub) { return sub == 32 ? 8 : 12; }
 static_assert(QD_MAX_TREE <= kTile, "the drafts fit one tile");
 
 struct TreeAttnArgs {
@@ -79,7 +80,7 @@ struct Plan {
 // Tiles of a walk over p0 cached positions and cnt drafts; sub: sub_positions, or minus the
 // positions of a tile that the whole CTA takes (the drafts are one such tile).
 __host__ __device__ constexpr int walk_tiles(int sub, int p0, int cnt) {
-  return sub > 0 ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + kWarps16 - 1) / kWarps16 : (p0 - sub - 1) / -sub + 1;
+  return sub > 0 ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + sub_warps(sub) - 1) / sub_warps(sub) : (p0 - sub - 1) / -sub + 1;
 }
 // Filled by one warp; `bm` rows to a block.
 template <int SUB>
@@ -261,14 +262,18 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
 }
 
 // ------------------------------------------------------------------ 16 rows
-// Few rows to a kv head: blocks of 16, and 8 warps that walk the positions side by side, 16
-// (f32) or 32 at a time, each with a ring of its own (no barrier until the walk's end, where the warps' results
-// are joined while the next walk's queries arrive).  A binary16 cache as above.  An f32 cache without a conversion in
-// shared memory: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
+// Few rows to a kv head: blocks of 16, and warps that walk the positions side by side, each with
+// tiles and a ring of its own (no barrier until the walk's end, where the warps' results are
+// joined while the next walk's queries arrive).  A binary16 cache as above, 8 warps with 32
+// positions a tile.  An f32 cache without a conversion in shared memory, 12 warps with 16
+// positions: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
 // fraction bits, lo = as many of the rest: at most 2^-20 off), hi hi + lo hi + hi lo.  TF32 keeps
-// f32's exponents, so nothing is scaled; the products run at half the binary16 rate, which the
-// 16 rows leave room for (1536 of the 2800 cycles in which an SM's share of HBM brings 128
-// positions).
+// f32's exponents, so nothing is scaled; the products run at half the binary16 rate, which 16
+// rows leave room for.  What bounds it is a warp's chain of dependent instructions (about 700 a
+// tile), hidden by the other warps: 12 warps with the queries' fragments in shared memory against
+// 8 with them in registers, 16 x 32 heads of 4095 positions f32: 183 against 203 us; with a
+// binary16 cache 12 warps spill, 68 against 62 us for 16 ragged sequences.  A conversion pass
+// through shared memory and binary16 parts instead of TF32: 33 against 23 us for one sequence.
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -291,18 +296,18 @@ __device__ __forceinline__ int swz(int r) { return ((r >> 1) & 1) | ((((r >> 2) 
 
 template <bool F16>
 struct Smem16 {
-  static constexpr int kStages = 3;
+  static constexpr int kWarps = sub_warps(sub_positions(F16)), kStages = 24 / kWarps;
   static constexpr int kRowBytes = F16 ? 128 : 256;
-  uint4 ring[kWarps16][kStages][2][sub_positions(F16) * kRowBytes / 16];  // K, V
-  float part[kWarps16][part_floats(16)];                    // m, l, o of a warp's share
+  uint4 ring[kWarps][kStages][2][sub_positions(F16) * kRowBytes / 16];  // K, V; m, l, o of a share at a walk's end
+  uint4 q[F16 ? 4 : 8][2][32];  // the fragments of q's k steps, hi and lo, by lane
   Plan plan;
 };
 
 template <bool F16>
-__global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs a) {
+__global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 1) k_tree_attn_16(TreeAttnArgs a) {
   using KV = typename std::conditional<F16, __half, float>::type;
   using S = Smem16<F16>;
-  constexpr int kSub = sub_positions(F16), NT = kSub / 8;
+  constexpr int kSub = sub_positions(F16), NT = kSub / 8, kWarps16 = S::kWarps;
   constexpr int kRow = S::kRowBytes;
   constexpr int kLag = S::kStages - 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -362,8 +367,6 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
 #pragma unroll
   for (int s = 0; s < kLag; ++s) produce(s);
 
-  constexpr int KQ = F16 ? 4 : 8;  // k steps of the scores
-  uint32_t qh[KQ][4], ql[KQ][4];
   float o[8][4];
   float m[2], l[2], rs[2] = {1.f, 1.f};
   uint64_t vis[2];
@@ -384,9 +387,9 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
       if (c.cnt < 64) vis[i] &= (1ull << c.cnt) - 1;
     }
   };
-  // ... and made operands.  The lane has dims 4 (qc + 4 j) .. + 3 of its rows.  f32 cache: k step
-  // 2 j + e / 2 has them at k = qc and qc + 4.  Binary16: a fragment wants dims 2 qc, 2 qc + 1 of
-  // every 8, so lanes qc and qc ^ 1, qc ^ 2 exchange.
+  // ... and made operands in shared memory by warp 0 (in registers they leave no room for 12
+  // warps).  The lane has dims 4 (qc + 4 j) .. + 3 of its rows; f32 cache: k step 2 j + e / 2 has
+  // them at k = qc and qc + 4.
   auto set_q = [&]() {
     const float scale = 1.4426950408889634f * 0.125f;  // scores in log2 units
 #pragma unroll
@@ -406,31 +409,38 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
         const int e = scale_exp(mx);
         rs[i] = pow2(e);
         const float f = pow2(-e);
+        if (warp == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // dims 16 j + 4 qc .. + 3 as two pairs; k step j's fragment has pairs qc and qc + 4 of its 8
-          uint32_t h0, l0, h1, l1;
-          split2(x[i][j].x * f, x[i][j].y * f, h0, l0);
-          split2(x[i][j].z * f, x[i][j].w * f, h1, l1);
-          // pair p stands in lane p / 2, first or second
-          const int from = (lane & 28) | (qc >> 1);
-          const uint32_t ha = __shfl_sync(0xffffffffu, h0, from), hb = __shfl_sync(0xffffffffu, h1, from);
-          const uint32_t la = __shfl_sync(0xffffffffu, l0, from), lb = __shfl_sync(0xffffffffu, l1, from);
-          const uint32_t hc = __shfl_sync(0xffffffffu, h0, from + 2), hd = __shfl_sync(0xffffffffu, h1, from + 2);
-          const uint32_t lc = __shfl_sync(0xffffffffu, l0, from + 2), ld = __shfl_sync(0xffffffffu, l1, from + 2);
-          qh[j][i] = qc & 1 ? hb : ha;
-          ql[j][i] = qc & 1 ? lb : la;
-          qh[j][i + 2] = qc & 1 ? hd : hc;
-          ql[j][i + 2] = qc & 1 ? ld : lc;
+          for (int j = 0; j < 4; ++j) {
+            // dims 16 j + 4 qc .. + 3 as pairs 2 qc, 2 qc + 1 of k step j; pair p belongs to lane p & 3
+            uint32_t hi, lo;
+            uint32_t* to0 = reinterpret_cast<uint32_t*>(&sm.q[j][0][(lane & 28) | (2 * qc & 3)]);
+            uint32_t* to1 = reinterpret_cast<uint32_t*>(&sm.q[j][1][(lane & 28) | (2 * qc & 3)]);
+            const int at = i + 2 * (qc >> 1);
+            split2(x[i][j].x * f, x[i][j].y * f, hi, lo);
+            to0[at] = hi;
+            to1[at] = lo;
+            split2(x[i][j].z * f, x[i][j].w * f, hi, lo);
+            to0[4 + at] = hi;
+            to1[4 + at] = lo;
+          }
         }
       } else {
+        if (warp == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          auto in = [scale](float f) { return (f + (f - f)) * scale; };  // an infinity is a NaN too
-          split_tf32(in(x[i][j].x), qh[2 * j][i], ql[2 * j][i]);
-          split_tf32(in(x[i][j].y), qh[2 * j][i + 2], ql[2 * j][i + 2]);
-          split_tf32(in(x[i][j].z), qh[2 * j + 1][i], ql[2 * j + 1][i]);
-          split_tf32(in(x[i][j].w), qh[2 * j + 1][i + 2], ql[2 * j + 1][i + 2]);
+          for (int j = 0; j < 4; ++j) {
+            auto in = [scale](float f) { return (f + (f - f)) * scale; };  // an infinity is a NaN too
+            auto put = [&](int ks, int e, float f) {
+              uint32_t hi, lo;
+              split_tf32(in(f), hi, lo);
+              reinterpret_cast<uint32_t*>(&sm.q[ks][0][lane])[e] = hi;
+              reinterpret_cast<uint32_t*>(&sm.q[ks][1][lane])[e] = lo;
+            };
+            put(2 * j, i, x[i][j].x);
+            put(2 * j, i + 2, x[i][j].y);
+            put(2 * j + 1, i, x[i][j].z);
+            put(2 * j + 1, i + 2, x[i][j].w);
+          }
         }
       }
       m[i] = -INFINITY;
@@ -443,6 +453,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
   };
   load_q(cur);
   set_q();
+  __syncthreads();
 
   for (int it = 0; cur.u < end; ++it) {
     const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
@@ -468,23 +479,26 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
       if constexpr (F16) {
         const int kr = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint4 vh = sm.q[ks][0][lane], vl = sm.q[ks][1][lane];
+          const uint32_t fh[4] = {vh.x, vh.y, vh.z, vh.w}, fl[4] = {vl.x, vl.y, vl.z, vl.w};
 #pragma unroll
           for (int n = 0; n < NT; n += 2) {
             uint32_t b[4];
             ldsm4(kt + tile_off(kr + 8 * n, 2 * ks + ((lane >> 3) & 1)), b);
             if (ks == 0) {
-              mma0(s[n], qh[ks], b[0], b[1]);
-              mma0(s[n + 1], qh[ks], b[2], b[3]);
-              mma0(sl[n], ql[ks], b[0], b[1]);
-              mma0(sl[n + 1], ql[ks], b[2], b[3]);
+              mma0(s[n], fh, b[0], b[1]);
+              mma0(s[n + 1], fh, b[2], b[3]);
+              mma0(sl[n], fl, b[0], b[1]);
+              mma0(sl[n + 1], fl, b[2], b[3]);
             } else {
-              mma(s[n], qh[ks], b[0], b[1]);
-              mma(s[n + 1], qh[ks], b[2], b[3]);
-              mma(sl[n], ql[ks], b[0], b[1]);
-              mma(sl[n + 1], ql[ks], b[2], b[3]);
+              mma(s[n], fh, b[0], b[1]);
+              mma(s[n + 1], fh, b[2], b[3]);
+              mma(sl[n], fl, b[0], b[1]);
+              mma(sl[n + 1], fl, b[2], b[3]);
             }
           }
+        }
       } else {
         float sx[2][4];
 #pragma unroll
@@ -500,19 +514,22 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
             split_tf32(x.w, bh[n][3], bl[n][3]);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
+            const uint4 vh = sm.q[2 * j + h][0][lane], vl = sm.q[2 * j + h][1][lane];
+            const uint32_t fh[4] = {vh.x, vh.y, vh.z, vh.w}, fl[4] = {vl.x, vl.y, vl.z, vl.w};
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
               if (j == 0 && h == 0) {
-                mma8_0(s[n], qh[0], bh[n][0], bh[n][1]);
-                mma8_0(sl[n], ql[0], bh[n][0], bh[n][1]);
-                mma8_0(sx[n], qh[0], bl[n][0], bl[n][1]);
+                mma8_0(s[n], fh, bh[n][0], bh[n][1]);
+                mma8_0(sl[n], fl, bh[n][0], bh[n][1]);
+                mma8_0(sx[n], fh, bl[n][0], bl[n][1]);
               } else {
-                mma8(s[n], qh[2 * j + h], bh[n][2 * h], bh[n][2 * h + 1]);
-                mma8(sl[n], ql[2 * j + h], bh[n][2 * h], bh[n][2 * h + 1]);
-                mma8(sx[n], qh[2 * j + h], bl[n][2 * h], bl[n][2 * h + 1]);
+                mma8(s[n], fh, bh[n][2 * h], bh[n][2 * h + 1]);
+                mma8(sl[n], fl, bh[n][2 * h], bh[n][2 * h + 1]);
+                mma8(sx[n], fh, bl[n][2 * h], bl[n][2 * h + 1]);
               }
             }
+          }
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -715,10 +732,13 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
       const Cursor done = cur;
       const bool whole = t_begin == 0 && last;
       const int part_slot = t_begin > 0 ? 0 : 1;
-      __syncthreads();  // the last walk's shares have been read
+      // the share goes to this warp's ring slot, which it has read and the next tile but one will
+      // fill; pair c of a row at c ^ 4 (row & 7): no bank twice
+      auto share = [&](int w) { return reinterpret_cast<float*>(sm.ring[w][slot][0]); };
+      static_assert(sizeof(sm.ring[0][0]) >= part_floats(16) * 4, "a share fits a slot");
+      __syncwarp();
       {
-        // pair c of a row at c ^ 4 (row & 7): no bank twice
-        float* mine = sm.part[warp];
+        float* mine = share(warp);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = qr + 8 * i;
@@ -739,21 +759,18 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
       advance(sm.plan, a.n_kv, cur);
       if (more) load_q(cur);  // on its way meanwhile
       __syncthreads();
-      // a warp to two rows
       const int done_rows = done.cnt * a.group;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = 2 * warp + x;
+      for (int r = warp; r < 16; r += kWarps16) {
         float mt = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps16; ++w) mt = fmaxf(mt, sm.part[w][r]);
+        for (int w = 0; w < kWarps16; ++w) mt = fmaxf(mt, share(w)[r]);
         float lt = 0.f;
         float2 ot = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps16; ++w) {
-          const float mw = sm.part[w][r], lw = sm.part[w][16 + r];
+          const float mw = share(w)[r], lw = share(w)[16 + r];
           const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
-          const float2 ow = reinterpret_cast<const float2*>(sm.part[w] + 32 + r * kHd)[lane ^ (4 * (r & 7))];
+          const float2 ow = reinterpret_cast<const float2*>(share(w) + 32 + r * kHd)[lane ^ (4 * (r & 7))];
           lt = fmaf(lw, f, lt);
           ot.x = fmaf(ow.x, f, ot.x);
           ot.y = fmaf(ow.y, f, ot.y);
@@ -774,6 +791,7 @@ __global__ void __launch_bounds__(kWarps16 * 32, 1) k_tree_attn_16(TreeAttnArgs 
         }
       }
       if (more) set_q();
+      __syncthreads();  // every share has been read, and q stands
       t_begin = -1;
     } else {
       advance(sm.plan, a.n_kv, cur);
@@ -1506,7 +1524,7 @@ bool row_map(CUtensorMap* map, const void* base, int64_t rows) {
 template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
   if (by16(a.n_nodes, a.group))
-    return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, kWarps16 * 32, sizeof(Smem16<F16>), 1, st);
+    return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, Smem16<F16>::kWarps * 32, sizeof(Smem16<F16>), 1, st);
   Maps128 maps = {};
   if constexpr (F16) {
     const int64_t heads = (int64_t)a.batch * a.n_kv;
