@@ -26,8 +26,8 @@
 // splits for many rows, latency for short caches.  Measured on one GB300 (floor: the bytes at
 // 6.77 TB/s or the products at 1946 TFLOP/s, counted once):
 //   9/3 heads, 8 nodes, 100 positions, f32              7.6 us (floor 0.03)
-//   32/32 heads, 16 nodes, 4080 positions, f32         22.5 us (10.0)
-//   the same, 16 sequences of 4095, f32                 183 us (160)
+//   32/32 heads, 16 nodes, 4080 positions, f32         23.4 us (10.0)
+//   the same, 16 sequences of 4095, f32                 193 us (160)
 //   the same, 16 ragged sequences, binary16              62 us (40)
 //   32/8 heads, 64 nodes, 32700 positions, binary16      60 us (10)
 // The unit counts: kStart 3 against 1 / 2 / 5 at 16 ragged sequences 64 against 95 / 72 / 66 us;
@@ -267,11 +267,11 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
 // joined while the next walk's queries arrive).  A binary16 cache as above, 8 warps with 32
 // positions a tile.  An f32 cache without a conversion in shared memory, 12 warps with 16
 // positions: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
-// fraction bits, lo = as many of the rest: at most 2^-20 off), hi hi + lo hi + hi lo.  TF32 keeps
+// fraction bits, lo = as many of the rest: 2^-21 off), hi hi + lo hi + hi lo.  TF32 keeps
 // f32's exponents, so nothing is scaled; the products run at half the binary16 rate, which 16
 // rows leave room for.  What bounds it is a warp's chain of dependent instructions (about 700 a
 // tile), hidden by the other warps: 12 warps with the queries' fragments in shared memory against
-// 8 with them in registers, 16 x 32 heads of 4095 positions f32: 183 against 203 us; with a
+// 8 with them in registers, 16 x 32 heads of 4095 positions f32: 10 % less time; with a
 // binary16 cache 12 warps spill, 68 against 62 us for 16 ragged sequences.  A conversion pass
 // through shared memory and binary16 parts instead of TF32: 33 against 23 us for one sequence.
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -286,9 +286,16 @@ __device__ __forceinline__ void mma8_0(float (&d)[4], const uint32_t (&a)[4], ui
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// The product reads the upper 10 fraction bits of its operands and cuts the rest off.  For the
+// scores hi is rounded, so that lo is half as large; for the values lo is, which is a shorter
+// chain.  Cutting both off left k and q 7e-8 too small on average, which a score of 10 makes 1e-6
+// of its weight.  Error of o against 64 bits over the plain f32 form's, and the time for 16 x 32
+// heads of 4095 positions: as here 0.9 and 193 us, hi rounded everywhere 0.9 and 205 us, lo
+// rounded everywhere 1.2 and 194 us, both cut off 2.0 and 183 us.
+template <bool SCORES = false>
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xFFFFE000u;  // a NaN or infinity stays one
-  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
+  hi = (__float_as_uint(x) + (SCORES ? 0x1000u : 0u)) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + (SCORES ? 0u : 0x1000u);  // one of the two is NaN where x is
 }
 // f32 rows of 256 bytes: 16-byte chunk c of row r stands at c ^ swz(r), so that both reads hit
 // all banks: k (8 rows at one chunk of each lane's four) and v (every second row at two chunks).
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 1) k_tree_attn_16(Tr
             auto in = [scale](float f) { return (f + (f - f)) * scale; };  // an infinity is a NaN too
             auto put = [&](int ks, int e, float f) {
               uint32_t hi, lo;
-              split_tf32(in(f), hi, lo);
+              split_tf32<true>(in(f), hi, lo);
               reinterpret_cast<uint32_t*>(&sm.q[ks][0][lane])[e] = hi;
               reinterpret_cast<uint32_t*>(&sm.q[ks][1][lane])[e] = lo;
             };
@@ -508,10 +515,10 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 1) k_tree_attn_16(Tr
           for (int n = 0; n < 2; ++n) {
             const int r = 8 * n + qr;
             const float4 x = *reinterpret_cast<const float4*>(kp + r * kRow + (((qc + 4 * j) ^ swz(r)) << 4));
-            split_tf32(x.x, bh[n][0], bl[n][0]);
-            split_tf32(x.y, bh[n][1], bl[n][1]);
-            split_tf32(x.z, bh[n][2], bl[n][2]);
-            split_tf32(x.w, bh[n][3], bl[n][3]);
+            split_tf32<true>(x.x, bh[n][0], bl[n][0]);
+            split_tf32<true>(x.y, bh[n][1], bl[n][1]);
+            split_tf32<true>(x.z, bh[n][2], bl[n][2]);
+            split_tf32<true>(x.w, bh[n][3], bl[n][3]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

@@ -163,7 +163,7 @@ def test_attn_unseen_large_values_keep_the_others_digits(qd, hk, f16):
     """A draft that a row does not see may hold the type's largest value."""
     a = Attn(qd, 17, 6, hk, 24, 100, [90], f16=f16)
     want = a.call().cpu().numpy()
-    big = 65504.0 if f16 else 3e38
+    big = 65504.0 if f16 else np.finfo(np.float32).max
     a.kd[:, :, 7] = big
     a.vd[:, :, 7] = -big
     got = a.call().cpu().numpy()
