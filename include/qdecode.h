@@ -424,8 +424,13 @@ qd_status qd_tree_append(const float* q, const float* k, const float* v, int64_t
  * head_dim 64; n_heads % n_kv_heads == 0, group size <= 8.  A node that sees nothing gives
  * zeros, as do the nodes of a sequence with pos[b] outside [0, max_ctx].  A non-finite q
  * gives NaN in its own row alone, and what a slot holds that a node does not see, NaN and
- * infinities included, does not reach that node's row.  The result does not depend on what
- * the caches hold at or behind pos[b].  Results are the same bits on every run.
+ * infinities included, does not reach that node's row.  A key that is not finite makes the
+ * rows that see it non-finite, a value that dimension of them (values of an f32 cache count as
+ * such from 2^100 on).  The result does not depend on what the caches hold at or behind
+ * pos[b].  Results are the same bits on every run.
+ * Arithmetic: f32 operands enter the tensor cores in two parts (2^-21 or better of a value, or
+ * of the largest value beside it), sums, running maxima and outputs are f32; the error is about
+ * that of plain f32 arithmetic.
  * workspace (device): qd_tree_attn_workspace bytes (0: a shape the call does not take); two
  * calls that can run at the same time need one each. */
 size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch);

@@ -390,7 +390,7 @@ def tree_attn(q, q_batch_stride, k_cache, v_cache, k_draft, v_draft, out, n_head
     fn, f32, i32, (st, dev) = "qd_tree_attn", torch.float32, torch.int32, _here(stream)
     kv = torch.float16 if kv_f16 else f32
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     qn, kn = n_nodes * n_heads * head_dim, batch * n_nodes * n_kv_heads * head_dim
     cn = batch * n_kv_heads * max_ctx * head_dim
     _check(fn, load().qd_tree_attn(
