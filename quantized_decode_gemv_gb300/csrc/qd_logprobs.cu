@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 8) k_token_logprobs(Args a) {
 #pragma unroll
   for (int j = 0; j < QD_MAX_TREE / 32; ++j) {
     const int t = lane + 32 * j;
-    if (t < a.n_tokens) a.logprob[row * a.n_tokens + t] = id[j] >= 0 && id[j] < a.vocab ? (xt[j] - p.m) - lse : -INFINITY;
+    if (t < a.n_tokens)
+      a.logprob[row * a.n_tokens + t] = id[j] >= 0 && id[j] < a.vocab ? (xt[j] - p.m) - lse : -INFINITY;
   }
   if (lane < k) {
     a.top_idx[row * k + lane] = (int32_t)argmax_key_index(key);

@@ -25,13 +25,15 @@
 // What bounds it: HBM for few rows on long caches, the instructions of the softmax and of the
 // splits for many rows, latency for short caches.  Measured on one GB300 (floor: the bytes at
 // 6.77 TB/s or the products at 1946 TFLOP/s, counted once):
-//   9/3 heads, 8 nodes, 100 positions, f32              7.6 us (floor 0.03)
-//   32/32 heads, 16 nodes, 4080 positions, f32         23.4 us (10.0)
-//   the same, 16 sequences of 4095, f32                 193 us (160)
-//   the same, 16 ragged sequences, binary16              62 us (40)
+//   9/3 heads, 8 nodes, 100 positions, f32              8.0 us (floor 0.03)
+//   32/32 heads, 16 nodes, 4080 positions, f32           22 us (10.0)
+//   the same, 16 sequences of 4095, f32                 196 us (160)
+//   the same, 16 ragged sequences, binary16              54 us (40)
 //   32/8 heads, 64 nodes, 32700 positions, binary16      60 us (10)
-// The unit counts: kStart 3 against 1 / 2 / 5 at 16 ragged sequences 64 against 95 / 72 / 66 us;
-// kMinPer 2 against 4 at 9/3 heads and 1000 positions 11.2 against 12.9 us.
+// The unit counts: kStart 3 against 5 at 4080 positions 22.3 against 24.7 us (with one CTA to an SM
+// and 16 ragged sequences 64 us against 95 with 1); kMinPer 2 against 1 at 8/1 heads and 27 nodes
+// 22 against 31 us, against 4 at 9/3 heads and 1000 positions 11.2 against 12.9 us; kWholeTiles 4
+// against 8 at 9/3 heads and 370 positions 10.3 against 13.6 us.
 #include <algorithm>
 
 #include <cuda.h>
@@ -47,13 +49,13 @@ constexpr int kTile = 64;      // positions of the smallest tile of a whole CTA;
 constexpr int kThreads = 128;  // of the join
 constexpr float kBias = 12.f;  // log2 of the weights' scale
 constexpr int kMinPer = 2;     // units of a CTA at least
-constexpr int kWholeTiles = 8;  // walks of at most so many tiles are not cut
+constexpr int kWholeTiles = 4;  // walks of at most so many tiles are not cut
 constexpr int kStart = 3;      // what the start of a walk costs, in tiles
 
-// k_tree_attn_16: warps with tiles of their own, 12 of 16 positions (f32 cache) or 8 of 32; what
+// k_tree_attn_16: warps with tiles of their own, 6 of 16 positions (f32 cache) or 4 of 32; what
 // they do side by side is one unit of work
 __host__ __device__ constexpr int sub_positions(bool f16) { return f16 ? 32 : 16; }
-__host__ __device__ constexpr int sub_warps(int sub) { return sub == 32 ? 8 : 12; }
+__host__ __device__ constexpr int sub_warps(int sub) { return sub == 32 ? 4 : 6; }
 static_assert(QD_MAX_TREE <= kTile, "the drafts fit one tile");
 
 struct TreeAttnArgs {
@@ -80,7 +82,8 @@ struct Plan {
 // Tiles of a walk over p0 cached positions and cnt drafts; sub: sub_positions, or minus the
 // positions of a tile that the whole CTA takes (the drafts are one such tile).
 __host__ __device__ constexpr int walk_tiles(int sub, int p0, int cnt) {
-  return sub > 0 ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + sub_warps(sub) - 1) / sub_warps(sub) : (p0 - sub - 1) / -sub + 1;
+  return sub > 0 ? ((p0 + sub - 1) / sub + (cnt + sub - 1) / sub + sub_warps(sub) - 1) / sub_warps(sub)
+                 : (p0 - sub - 1) / -sub + 1;
 }
 // Filled by one warp; `bm` rows to a block.
 template <int SUB>
@@ -256,7 +259,8 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
   const int rows = cur.cnt * a.group;
   for (int x = threadIdx.x; x < BM * (kHd / 4); x += blockDim.x) {
     const int at = cur.r * BM + x / (kHd / 4);
-    if (at < rows) reinterpret_cast<float4*>(row_of(a, a.out, cur, at))[x % (kHd / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (at < rows)
+      reinterpret_cast<float4*>(row_of(a, a.out, cur, at))[x % (kHd / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   return false;
 }
@@ -264,16 +268,18 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
 // ------------------------------------------------------------------ 16 rows
 // Few rows to a kv head: blocks of 16, and warps that walk the positions side by side, each with
 // tiles and a ring of its own (no barrier until the walk's end, where the warps' results are
-// joined while the next walk's queries arrive).  A binary16 cache as above, 8 warps with 32
-// positions a tile.  An f32 cache without a conversion in shared memory, 12 warps with 16
+// joined while the next walk's queries arrive).  A binary16 cache as above, 4 warps with 32
+// positions a tile.  An f32 cache without a conversion in shared memory, 6 warps with 16
 // positions: m16n8k8 TF32 products, each f32 operand as two TF32 parts (hi = the upper 10
 // fraction bits, lo = as many of the rest: 2^-21 off), hi hi + lo hi + hi lo.  TF32 keeps
 // f32's exponents, so nothing is scaled; the products run at half the binary16 rate, which 16
 // rows leave room for.  What bounds it is a warp's chain of dependent instructions (about 700 a
-// tile), hidden by the other warps: 12 warps with the queries' fragments in shared memory against
-// 8 with them in registers, 16 x 32 heads of 4095 positions f32: 10 % less time; with a
-// binary16 cache 12 warps spill, 68 against 62 us for 16 ragged sequences.  A conversion pass
-// through shared memory and binary16 parts instead of TF32: 33 against 23 us for one sequence.
+// tile), hidden by the other warps, and the start and end of a walk, hidden by the SM's other CTA:
+// two CTAs of 4 warps against one of 8, 62 -> 54 us for 16 ragged sequences; two of 6 with the
+// queries' fragments in shared memory against one of 8 with them in registers, 203 -> 183 us for
+// 16 x 32 heads of 4095 positions f32 (before lo was rounded); 12 warps spill on a binary16 cache.
+// A conversion pass through shared memory and binary16 parts instead of TF32: 33 against 23 us for
+// one sequence.
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -303,7 +309,7 @@ __device__ __forceinline__ int swz(int r) { return ((r >> 1) & 1) | ((((r >> 2) 
 
 template <bool F16>
 struct Smem16 {
-  static constexpr int kWarps = sub_warps(sub_positions(F16)), kStages = 24 / kWarps;
+  static constexpr int kWarps = sub_warps(sub_positions(F16)), kStages = F16 ? 3 : 2;
   static constexpr int kRowBytes = F16 ? 128 : 256;
   uint4 ring[kWarps][kStages][2][sub_positions(F16) * kRowBytes / 16];  // K, V; m, l, o of a share at a walk's end
   uint4 q[F16 ? 4 : 8][2][32];  // the fragments of q's k steps, hi and lo, by lane
@@ -311,7 +317,7 @@ struct Smem16 {
 };
 
 template <bool F16>
-__global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 1) k_tree_attn_16(TreeAttnArgs a) {
+__global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 2) k_tree_attn_16(TreeAttnArgs a) {
   using KV = typename std::conditional<F16, __half, float>::type;
   using S = Smem16<F16>;
   constexpr int kSub = sub_positions(F16), NT = kSub / 8, kWarps16 = S::kWarps;
@@ -759,7 +765,8 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 1) k_tree_attn_16(Tr
             if constexpr (F16)
               dst[(4 * d + qc) ^ (4 * qr)] = make_float2(o[d][2 * i], o[d][2 * i + 1]);
             else  // dims 16 qc + 8 e + 2 k, + 1
-              dst[(8 * qc + d) ^ (4 * qr)] = make_float2(o[2 * (d & 3)][2 * i + (d >> 2)], o[2 * (d & 3) + 1][2 * i + (d >> 2)]);
+              dst[(8 * qc + d) ^ (4 * qr)] =
+                  make_float2(o[2 * (d & 3)][2 * i + (d >> 2)], o[2 * (d & 3) + 1][2 * i + (d >> 2)]);
           }
         }
       }
@@ -810,15 +817,16 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 1) k_tree_attn_16(Tr
 // ------------------------------------------------------------------ 128 rows
 // Many rows to a kv head: blocks of 128 on the 5th-generation tensor cores, two threads to a row.
 // Per tile (128 positions of a binary16 cache, 64 of an f32 one) one thread issues s = q k^T
-// (tcgen05.mma, M = 128, q in tensor memory, K in shared memory) into tensor memory; a row's threads read
-// half of its scores each (tcgen05.ld), exchange their maxima, read the scores again 16 at a time
-// (which leaves the registers for two CTAs to an SM without a spill: the shared memory leaves
-// spills no L1) and write the weights' two parts over them as the A operand of o = p v (V as it lies,
-// [position][dim], is the transposed B operand); each adds 32 dims of the tile's o to its own
-// registers, rounded.  The operands' splits are those of the other kernels.
+// (tcgen05.mma, M = 128, q in tensor memory, K in shared memory) into tensor memory; a row's
+// threads read half of its scores each (tcgen05.ld), exchange their maxima, read the scores again
+// 16 at a time (the registers have to do for two CTAs to an SM, and the shared memory leaves
+// spills no L1) and write the weights' two parts over them as the A operand of o = p v (V as it
+// lies, [position][dim], is the transposed B operand); each adds 32 dims of the tile's o to its
+// own registers, rounded.
 // Two CTAs to an SM, one's products under the other's softmax.
-// Tiles lie as 8 x 8 core matrices of 128 bytes: row r, 16-byte chunk c at core_off(r, c), which
-// K (rows, 16 bytes of dims) and V (8 positions x 16 bytes of dims) share.
+// A binary16 tile lies in the TMA's 128-byte swizzle; an f32 one is converted, k scaled by a power
+// of two for each position and v too (the weights take that over), into 8 x 8 core matrices of 128
+// bytes: row r, 16-byte chunk c at core_off(r, c).
 constexpr int kThreads128 = 256;
 __device__ __forceinline__ uint32_t core_off(int r, int c) {
   return (uint32_t)((((r >> 3) * 8 + c) * 128) + (r & 7) * 16);
@@ -903,7 +911,8 @@ struct Maps128 {
 constexpr int kBoxRows = 64;
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t mbar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
       "l"(map), "r"(0), "r"(row), "r"(mbar)
       : "memory");
 }
@@ -1469,7 +1478,7 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
     const float* p = part(c);
     const float mc = __ldcg(p + r), lc = __ldcg(p + BM + r);
     const float2 oc = __ldcg(reinterpret_cast<const float2*>(p + 2 * BM + r * kHd) + lane);
-    const float f = mc == -INFINITY ? lc : ex2(mc - mt);
+    const float f = mc == -INFINITY ? lc : ex2(mc - mt);  // a part without a maximum has l = 0 or NaN
     lt = fmaf(lc, f, lt);
     ot.x = fmaf(oc.x, f, ot.x);
     ot.y = fmaf(oc.y, f, ot.y);
@@ -1531,7 +1540,7 @@ bool row_map(CUtensorMap* map, const void* base, int64_t rows) {
 template <bool F16>
 qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
   if (by16(a.n_nodes, a.group))
-    return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, Smem16<F16>::kWarps * 32, sizeof(Smem16<F16>), 1, st);
+    return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, Smem16<F16>::kWarps * 32, sizeof(Smem16<F16>), 2, st);
   Maps128 maps = {};
   if constexpr (F16) {
     const int64_t heads = (int64_t)a.batch * a.n_kv;
