@@ -34,9 +34,10 @@
 // and 16 ragged sequences 64 us against 95 with 1); kMinPer 2 against 1 at 8/1 heads and 27 nodes
 // 22 against 31 us, against 4 at 9/3 heads and 1000 positions 11.2 against 12.9 us; kWholeTiles 4
 // against 8 at 9/3 heads and 370 positions 10.3 against 13.6 us.
-#include <algorithm>
-
 #include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "qd_internal.cuh"
 #include "qd_tc.cuh"
@@ -1507,8 +1508,14 @@ inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, i
 template <int BM, int SUB, typename... More>
 qd_status launch(const TreeAttnArgs& a, void (*kern)(TreeAttnArgs, More...), int threads, size_t smem, int per_sm,
                  cudaStream_t st, const std::remove_const_t<More>&... more) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return QD_ERR_CUDA;
+  static std::atomic<bool> done[64];  // one kernel to an instance of this function
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QD_ERR_CUDA;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return QD_ERR_CUDA;
+    done[dev] = true;
+  }
   const int walks = a.batch * a.n_kv * a.blocks;
   const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, SUB, per_sm);
   kern<<<ctas, threads, smem, st>>>(a, more...);
