@@ -1069,9 +1069,10 @@ __global__ void __launch_bounds__(kThreads128, 2)
   float o[ND];
   float m = -INFINITY, l = 0.f, rs = 1.f, vunit = 1.f;
   uint64_t vis = 0;
-  bool lost = false;  // a wait has run out: the result is NaN
+  bool lost = false;  // a wait has run out: the rows of the walk are NaN
 
-  for (int it = 0; sm.next[it % 3].valid; ++it) {
+  int it = 0;
+  for (; sm.next[it % 3].valid; ++it) {
     const Tile128& cur = sm.next[it % 3];
     const bool draft = cur.draft;
     const int rows = cur.cnt * a.group;
@@ -1404,8 +1405,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
     // ---- the end of this CTA's part of the walk
     if (cur.last) {
       const bool whole = cur.whole;
-      __syncthreads();  // every thread has read `bad` and `ex`
-      if (lost) l = NAN;
+      if (__syncthreads_or(lost)) l = NAN;  // every thread has read `bad` and `ex`
       sm.ex[half][lrow] = l;
       if (tid == 0) sm.bad = 0;
       __syncthreads();
@@ -1430,6 +1430,11 @@ __global__ void __launch_bounds__(kThreads128, 2)
     }
   }
   tc::fence_before_sync();
+  if (__syncthreads_or(lost) && tid == kStepper) {  // products and copies that nobody waited for
+    tc::mbar_wait(mb_o, (uint32_t)(it - 1) & 1u);
+    for (int x = 0; x < min(it, S::kStages); ++x)
+      tc::mbar_wait(mb_o + 8 + 8 * x, (uint32_t)((it - 1 - x) / S::kStages) & 1u);
+  }
   __syncthreads();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kCols128) : "memory");
