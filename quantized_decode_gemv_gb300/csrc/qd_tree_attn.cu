@@ -267,7 +267,7 @@ __device__ __forceinline__ bool first_tile(const TreeAttnArgs& a, const Plan& p,
 }
 
 // ------------------------------------------------------------------ 16 rows
-// Few rows to a kv head: blocks of 16, and warps that walk the positions side by side, each with
+// Few rows to a kv head, or little work: blocks of 16, and warps that walk the positions side by side, each with
 // tiles and a ring of its own (no barrier until the walk's end, where the warps' results are
 // joined while the next walk's queries arrive).  A binary16 cache as above, 4 warps with 32
 // positions a tile.  An f32 cache without a conversion in shared memory, 6 warps with 16
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 2) k_tree_attn_16(Tr
 }
 
 // ------------------------------------------------------------------ 128 rows
-// Many rows to a kv head: blocks of 128 on the 5th-generation tensor cores, two threads to a row.
+// Many rows to a kv head and much work: blocks of 128 on the 5th-generation tensor cores, two threads to a row.
 // Per tile (128 positions of a binary16 cache, 64 of an f32 one) one thread issues s = q k^T
 // (tcgen05.mma, M = 128, q in tensor memory, K in shared memory) into tensor memory; a row's
 // threads read half of its scores each (tcgen05.ld), exchange their maxima, read the scores again
@@ -1492,21 +1492,32 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
   *dst = lt == 0.f ? make_float2(0.f, 0.f) : make_float2(ot.x / lt, ot.y / lt);
 }
 
-// The 16-row kernel up to 32 rows to a kv head (two blocks; 58.7 us for 32 rows at 4000 positions of
-// 2 x 32 heads f32, where 128-row blocks take 65 us whatever they hold), 128-row blocks behind them.
-inline bool by16(int n_nodes, int group) { return n_nodes * group <= 32; }
-inline int block_rows(int n_nodes, int group) {
-  return by16(n_nodes, group) ? 16 : 128;
+// Blocks of 16 rows or of 128.  Up to 32 rows to a kv head 16 (two blocks; 58.7 us for 32 rows at
+// 4000 positions of 2 x 32 heads f32, where 128-row blocks take 65 us whatever they hold).  More
+// rows are walks by the dozen in blocks of 16, which read a head's positions once each; that fills
+// the SMs while there is little work, and a walk starts in fewer steps.  The work is counted in
+// positions of a 16-row block as the cache has room for, a start as 1000 of them.  16 against 128
+// rows, in us, one sequence:
+//   f32       8 x 64 rows, 500 positions (work 50e3)      11.5 14.6
+//             4 x 128, 2000 (98e3)                         16.5 18.0
+//             1 x 512, 8000 (290e3)                        34.0 37.4
+//             4 x 512, 2000 (392e3)                        36.0 29.4
+//             8 x 512, 8000 (2.3e6)                       191.4 69.5
+//   binary16  8 x 64, 500 (50e3)                           10.5 14.9
+//             8 x 256, 2000 (392e3)                        19.5 23.0
+//             4 x 512, 8000 (1.16e6)                       40.5 33.3
+//             1 x 512, 32000 (1.06e6)                      39.9 41.4
+//             8 x 512, 8000 (2.3e6)                        70.5 42.7
+constexpr int64_t kWork16 = 300000, kWork16F16 = 1100000;
+inline bool by16(int n_kv, int group, int n_nodes, int max_ctx, int batch, bool f16) {
+  const int blocks = (n_nodes * group + 15) / 16;
+  return blocks <= 2 || (int64_t)batch * n_kv * blocks * ((int64_t)max_ctx + 1000) <= (f16 ? kWork16F16 : kWork16);
 }
-inline int blocks_of(int n_nodes, int group) {
-  const int bm = block_rows(n_nodes, group);
-  return (n_nodes * group + bm - 1) / bm;
-}
+inline int blocks_of(int n_nodes, int group, int bm) { return (n_nodes * group + bm - 1) / bm; }
 constexpr int kMaxCtas = 2;  // CTAs to an SM at most
 // CTAs of a call: what fits the device at once, and no more than there can be units for.
-inline int tree_ctas(int n_kv, int group, int n_nodes, int max_ctx, int batch, int sub, int per_sm) {
-  const int64_t units = (int64_t)batch * n_kv * blocks_of(n_nodes, group) *
-                        (walk_tiles(sub, max_ctx, n_nodes) + kStart);
+inline int tree_ctas(int n_kv, int blocks, int n_nodes, int max_ctx, int batch, int sub, int per_sm) {
+  const int64_t units = (int64_t)batch * n_kv * blocks * (walk_tiles(sub, max_ctx, n_nodes) + kStart);
   return (int)std::min<int64_t>((int64_t)attn_sm_count() * per_sm, (units + kMinPer - 1) / kMinPer);
 }
 
@@ -1522,7 +1533,7 @@ qd_status launch(const TreeAttnArgs& a, void (*kern)(TreeAttnArgs, More...), int
     done[dev] = true;
   }
   const int walks = a.batch * a.n_kv * a.blocks;
-  const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.group, a.n_nodes, a.max_ctx, a.batch, SUB, per_sm);
+  const int ctas = a.whole ? walks : tree_ctas(a.n_kv, a.blocks, a.n_nodes, a.max_ctx, a.batch, SUB, per_sm);
   kern<<<ctas, threads, smem, st>>>(a, more...);
   const qd_status s = launch_status();
   if (s != QD_OK || a.whole) return s;
@@ -1550,8 +1561,8 @@ bool row_map(CUtensorMap* map, const void* base, int64_t rows) {
 }
 
 template <bool F16>
-qd_status launch_f(const TreeAttnArgs& a, cudaStream_t st) {
-  if (by16(a.n_nodes, a.group))
+qd_status launch_f(const TreeAttnArgs& a, bool rows16, cudaStream_t st) {
+  if (rows16)
     return launch<16, sub_positions(F16)>(a, k_tree_attn_16<F16>, Smem16<F16>::kWarps * 32, sizeof(Smem16<F16>), 2, st);
   Maps128 maps = {};
   if constexpr (F16) {
@@ -1568,7 +1579,9 @@ inline bool tree_shape_ok(int n_heads, int n_kv_heads, int head_dim, int n_nodes
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 8 || head_dim != kHd ||
       n_nodes < 1 || n_nodes > QD_MAX_TREE || max_ctx < 1 || batch < 1 || batch > QD_MAX_BATCH)
     return false;
-  const int64_t walks = (int64_t)batch * n_kv_heads * blocks_of(n_nodes, n_heads / n_kv_heads);
+  // (blocks of 16 with more than 32 rows: by16 keeps their work far below this)
+  const int rows = n_nodes * (n_heads / n_kv_heads);
+  const int64_t walks = (int64_t)batch * n_kv_heads * ((rows + 127) / 128 + (rows > 16 && rows <= 32));
   if ((int64_t)batch * n_kv_heads * std::max(max_ctx, n_nodes) > (1ll << 31) - 128) return false;  // rows of a cache
   return walks <= (1 << 20) && walks * ((int64_t)max_ctx / kTile + 2 + kStart) <= (1 << 30);
 }
@@ -1583,10 +1596,15 @@ extern "C" {
 size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch) {
   if (!tree_shape_ok(n_heads, n_kv_heads, head_dim, n_nodes, max_ctx, batch)) return 0;
   const int group = n_heads / n_kv_heads;
-  // of either cache type: the finest tiles ask for the most CTAs
-  const int sub = by16(n_nodes, group) ? sub_positions(false) : -kTile;
-  return (size_t)tree_ctas(n_kv_heads, group, n_nodes, max_ctx, batch, sub, kMaxCtas) * 2 *
-         part_floats(block_rows(n_nodes, group)) * sizeof(float);
+  size_t most = 0;  // of either cache type
+  for (const bool f16 : {false, true}) {
+    const bool rows16 = by16(n_kv_heads, group, n_nodes, max_ctx, batch, f16);
+    const int bm = rows16 ? 16 : 128;
+    const int ctas = tree_ctas(n_kv_heads, blocks_of(n_nodes, group, bm), n_nodes, max_ctx, batch,
+                               rows16 ? sub_positions(f16) : -tile128(f16), kMaxCtas);
+    most = std::max(most, (size_t)ctas * 2 * part_floats(bm) * sizeof(float));
+  }
+  return most;
 }
 
 qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cache, const void* v_cache,
@@ -1623,10 +1641,11 @@ qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cac
   a.max_ctx = max_ctx;
   a.batch = batch;
   a.ws = static_cast<float*>(workspace);
-  a.blocks = blocks_of(n_nodes, a.group);
-  const int sub = by16(n_nodes, a.group) ? sub_positions(kv_f16) : -tile128(kv_f16);
+  const bool rows16 = by16(n_kv_heads, a.group, n_nodes, max_ctx, batch, kv_f16);
+  a.blocks = blocks_of(n_nodes, a.group, rows16 ? 16 : 128);
+  const int sub = rows16 ? sub_positions(kv_f16) : -tile128(kv_f16);
   a.whole = walk_tiles(sub, max_ctx, n_nodes) <= kWholeTiles;
-  return kv_f16 ? launch_f<true>(a, (cudaStream_t)stream) : launch_f<false>(a, (cudaStream_t)stream);
+  return kv_f16 ? launch_f<true>(a, rows16, (cudaStream_t)stream) : launch_f<false>(a, rows16, (cudaStream_t)stream);
 }
 
 }  // extern "C"

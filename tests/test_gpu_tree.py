@@ -278,6 +278,126 @@ def test_attn_offsets_past_32_bits(qd, hq):
         assert np.abs(out[x].cpu().numpy() - w).max() <= attn_tol(p + n, smax, vmax)
 
 
+# Blocks of 128 rows take over where a call's work (in positions of 16-row blocks) passes a bound,
+# which most sizes above stay below: a head with many rows and a cache with room for many positions
+# (16 blocks' worth more than 1100000 binary16 or 300000 f32 ones), or many short walks.
+def _wide(qd, seed, pos, f16, hq=8, n=64, **kw):
+    return Attn(qd, seed, hq, 1, n, (17600000 if f16 else 4800000) // (hq * n), pos, f16=f16, **kw)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("hq,n", [(8, 64), (7, 31)])
+def test_attn_128_lengths(qd, hq, n, f16):
+    ctx = (1100000 if f16 else 300000) // (6 * ((hq * n + 15) // 16))
+    Attn(qd, 40, hq, 1, n, ctx, [0, 1, 127, 129, 1030, ctx], f16=f16).check()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_attn_128_long_walk_cut_over_all_ctas(qd, f16):
+    _wide(qd, 41, [12000 if f16 else 6000], f16, hq=7, n=37).check()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("ctx", [128, 300])
+def test_attn_128_many_short_walks(qd, ctx, f16):
+    """16 sequences, whole walks (of at most four tiles) and cut ones."""
+    hk = 3
+    a = Attn(qd, 42, 8 * hk, hk, 64, ctx, [ctx - 7 * i for i in range(16)], f16=f16,
+             cnt=[64 - 3 * i for i in range(16)], q_gap=12)
+    a.check()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_attn_128_rows_that_see_nothing_and_bad_positions(qd, f16):
+    a = _wide(qd, 43, [0, 300, 10**6, -1], f16)
+    a.anc[0, 3] = a.anc[0, 60] = False
+    got = a.call().cpu().numpy()
+    assert np.all(got[0, [3, 60]] == 0) and np.all(got[2:] == 0)
+    for b in range(2):
+        want, smax, vmax = a.ref(b)
+        assert np.abs(got[b] - want).max() <= attn_tol(a.pos[b] + 64, smax, vmax)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_attn_128_unseen_values_do_not_reach_a_row(qd, bad, f16):
+    a = _wide(qd, 44, [70, 2000], f16, cnt=[64, 50])
+    want = a.check(a.call())
+    for b in range(2):
+        a.k[b, :, a.pos[b]:] = bad
+        a.v[b, :, a.pos[b]:] = bad
+        a.kd[b, :, a.cnt[b]:] = bad
+        a.vd[b, :, a.cnt[b]:] = bad
+    assert np.array_equal(a.call().cpu().numpy(), want)
+    a.kd[:, :, 5] = bad
+    a.vd[:, :, 5, 3] = bad
+    got = a.call().cpu().numpy()
+    for b in range(2):
+        sees = a.anc[b, :a.cnt[b], 5]
+        assert np.array_equal(got[b, :a.cnt[b]][~sees], want[b, :a.cnt[b]][~sees])
+        assert np.all(~np.isfinite(got[b, :a.cnt[b]][sees][..., 3]))
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_attn_128_infinite_values_and_queries_stay_where_they_are(qd, f16):
+    a = _wide(qd, 45, [290], f16)
+    want = a.check()
+    _, smax, vmax = a.ref(0)
+    a.v[0, :, 100, 3] = np.inf
+    a.v[0, :, 17, 60] = np.nan
+    a.q.reshape(1, 64, 8, HD)[0, 4, 1, 9] = np.nan
+    a.q.reshape(1, 64, 8, HD)[0, 20, 5, 0] = np.inf
+    got = a.call().cpu().numpy()
+    assert np.isnan(got[0, 4, 1]).all() and np.isnan(got[0, 20, 5]).all()
+    keep = np.ones((64, 8), bool)
+    keep[4, 1] = keep[20, 5] = False
+    dims = [d for d in range(HD) if d not in (3, 60)]
+    assert not np.isfinite(got[0][keep][:, [3, 60]]).any()
+    # the scale of a position's values may change with them: as exact as before, not the same bits
+    assert np.abs(got[0][keep][:, dims] - want[0][keep][:, dims]).max() <= 2 * attn_tol(354, smax, vmax)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("kscale,vscale", [(1e-3, 1e-4), (8.0, 300.0)])
+def test_attn_128_small_and_large_values(qd, f16, kscale, vscale):
+    _wide(qd, 46, [390, 1500], f16, kscale=kscale, vscale=vscale).check()
+
+
+def test_attn_128_values_beyond_binary16_in_an_f32_cache(qd):
+    a = _wide(qd, 47, [390], False, kscale=1e-6, vscale=1e9)
+    a.k[0, 0, 40] *= 1e12
+    a.q[:] *= 1e-6
+    a.check()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_attn_128_two_calls_at_once_and_captured(qd, f16):
+    pair = [_wide(qd, 48 + i, [4000 - 900 * i, 33], f16) for i in range(2)]
+    want = [a.call().clone() for a in pair]
+    torch.cuda.synchronize()
+    outs = [torch.full_like(w, 7.0) for w in want]
+    streams, graphs = [torch.cuda.Stream() for _ in pair], []
+    for a, o, s in zip(pair, outs, streams):
+        ws = torch.empty_like(a.args[16])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(4):
+                qd.tree_attn(*a.args[:6], o, *a.args[7:16], ws, kv_f16=f16)
+        graphs.append((g, ws))
+    for (g, _), s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_attn_workspace_serves_both_cache_types(qd):
+    """Between the bounds an f32 cache takes blocks of 128 rows and a binary16 one blocks of 16."""
+    for f16 in (False, True):
+        Attn(qd, 50, 16, 2, 64, 6000, [1990, 700], f16=f16).check()
+
+
 # ------------------------------------------------------------------------------ append
 def _table(ctx, hd, theta=1e4):
     a = np.arange(ctx)[:, None] * theta ** (-2.0 * np.arange(hd // 2) / hd)[None]
