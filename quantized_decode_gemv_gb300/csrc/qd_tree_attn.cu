@@ -1440,9 +1440,18 @@ __global__ void __launch_bounds__(kThreads128, 2)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kCols128) : "memory");
 }
 
-// Joins the parts of the walks that more than one CTA took, a warp to a row: block x the walk, if
-// any, whose first tile is CTA x's and whose last is not.  Also the zeros of the sequences whose
-// position is out of range.
+// Joins the parts of the walks that more than one CTA took: block x the walk, if any, whose first
+// tile is CTA x's and whose last is not, a warp to a row.  A walk of many parts has the blocks of
+// its next three CTAs as well, a block to a row and a quarter of the parts to a warp.  Also the
+// zeros of the sequences whose position is out of range.
+// Bound by the latency of the loads (L2), so those of kJoin parts are under way together.  One
+// kv head, 15 rows, 16000 / 64000 positions binary16: 8.3 / 15.6 us the whole call, 11.6 / 29.0 with a
+// warp to a row whatever the parts, 13.8 / 37.9 with 4 parts at once (16 at once: 8.0 / 16.1, but
+// 65 against 59 us for 64 x 32 rows of 32700 positions).  kFewParts 8 instead of 16: 8.5 against 9.0 us
+// for 32 rows of 4000 positions, 36.3 against 33.7 us for 8 x 512 rows of 4000, whose blocks would
+// be four times as many.
+constexpr int kRows = kThreads / 32;  // of a block
+constexpr int kFewParts = 16, kJoin = 8;
 template <int BM, int SUB>
 __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int ctas) {
   __shared__ Plan plan;
@@ -1468,28 +1477,72 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
   cur.r = walk % plan.rb[cur.b];
   const int g0 = plan.off[cur.b] + walk * (nt + kStart) + kStart;  // its first tile's unit
   const int c0 = g0 / per, c1 = (g0 + nt - 1) / per;
-  const int r = blockIdx.y * (kThreads / 32) + warp, at = cur.r * BM + r;
-  if (c0 != first || c0 == c1 || at >= plan.cnt[cur.b] * a.group) return;
-  float2* dst = reinterpret_cast<float2*>(row_of(a, a.out, cur, at)) + lane;
-  // the walk begins in its first CTA (slot 1: that CTA's last part) and is the first part of the others
-  auto part = [&](int c) { return a.ws + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats(BM); };
-  float mt = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) mt = fmaxf(mt, __ldcg(part(c) + r));
+  const bool few = c1 - c0 < kFewParts;
+  const int x = first - c0;  // -1: the last unit is of the walk's start, before its first tile
+  if (c0 == c1 || x < 0 || x >= (few ? 1 : kRows)) return;
+  const int r = blockIdx.y * kRows + (few ? warp : x), at = cur.r * BM + r;
+  if (at >= plan.cnt[cur.b] * a.group) return;
+  float m = -INFINITY, l = 0.f;
+  float2 o = make_float2(0.f, 0.f);
+  auto join = [&](const float (&mc)[kJoin], const float (&lc)[kJoin], const float2 (&oc)[kJoin]) {
+    float top = m;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-  float lt = 0.f;
-  float2 ot = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float* p = part(c);
-    const float mc = __ldcg(p + r), lc = __ldcg(p + BM + r);
-    const float2 oc = __ldcg(reinterpret_cast<const float2*>(p + 2 * BM + r * kHd) + lane);
-    const float f = mc == -INFINITY ? lc : ex2(mc - mt);  // a part without a maximum has l = 0 or NaN
-    lt = fmaf(lc, f, lt);
-    ot.x = fmaf(oc.x, f, ot.x);
-    ot.y = fmaf(oc.y, f, ot.y);
+    for (int i = 0; i < kJoin; ++i) top = fmaxf(top, mc[i]);
+    const float f = m == -INFINITY ? l : ex2(m - top);  // without a maximum l is 0 or NaN
+    m = top;
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      const float g = mc[i] == -INFINITY ? lc[i] : ex2(mc[i] - top);
+      l = fmaf(lc[i], g, l);
+      o.x = fmaf(oc[i].x, g, o.x);
+      o.y = fmaf(oc[i].y, g, o.y);
+    }
+  };
+  const int step = few ? 1 : kRows;
+  for (int c = few ? c0 : c0 + warp; c <= c1; c += step * kJoin) {
+    float mc[kJoin], lc[kJoin];
+    float2 oc[kJoin];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      const int at_c = c + i * step;
+      // the walk begins in its first CTA (slot 1: that CTA's last part) and is the first part of the others
+      const float* p = a.ws + ((int64_t)at_c * 2 + (at_c == c0 ? 1 : 0)) * part_floats(BM);
+      const bool live = at_c <= c1;
+      mc[i] = live ? __ldcg(p + r) : -INFINITY;
+      lc[i] = live ? __ldcg(p + BM + r) : 0.f;
+      oc[i] = live ? __ldcg(reinterpret_cast<const float2*>(p + 2 * BM + r * kHd) + lane) : make_float2(0.f, 0.f);
+    }
+    join(mc, lc, oc);
   }
-  *dst = lt == 0.f ? make_float2(0.f, 0.f) : make_float2(ot.x / lt, ot.y / lt);
+  if (!few) {  // the warps' quarters
+    static_assert(kJoin >= kRows, "joined at once");
+    __shared__ float ms[kRows], ls[kRows];
+    __shared__ float2 os[kRows][32];
+    os[warp][lane] = o;
+    if (lane == 0) {
+      ms[warp] = m;
+      ls[warp] = l;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float mc[kJoin], lc[kJoin];
+    float2 oc[kJoin];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      mc[i] = i < kRows ? ms[i] : -INFINITY;
+      lc[i] = i < kRows ? ls[i] : 0.f;
+      oc[i] = i < kRows ? os[i][lane] : make_float2(0.f, 0.f);
+    }
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float2(0.f, 0.f);
+    join(mc, lc, oc);
+  }
+  reinterpret_cast<float2*>(row_of(a, a.out, cur, at))[lane] =
+      l == 0.f ? make_float2(0.f, 0.f) : make_float2(o.x / l, o.y / l);
 }
 
 // Blocks of 16 rows or of 128.  Up to 32 rows to a kv head 16 (two blocks; 58.7 us for 32 rows at
