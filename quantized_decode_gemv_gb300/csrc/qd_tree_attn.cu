@@ -26,14 +26,17 @@
 // splits for many rows, latency for short caches.  Measured on one GB300 (floor: the bytes at
 // 6.77 TB/s or the products at 1946 TFLOP/s, counted once):
 //   9/3 heads, 8 nodes, 100 positions, f32              8.0 us (floor 0.03)
-//   32/32 heads, 16 nodes, 4080 positions, f32           22 us (10.0)
-//   the same, 16 sequences of 4095, f32                 196 us (160)
-//   the same, 16 ragged sequences, binary16              54 us (40)
-//   32/8 heads, 64 nodes, 32700 positions, binary16      60 us (10)
-// The unit counts: kStart 3 against 5 at 4080 positions 22.3 against 24.7 us (with one CTA to an SM
-// and 16 ragged sequences 64 us against 95 with 1); kMinPer 2 against 1 at 8/1 heads and 27 nodes
-// 22 against 31 us, against 4 at 9/3 heads and 1000 positions 11.2 against 12.9 us; kWholeTiles 4
-// against 8 at 9/3 heads and 370 positions 10.3 against 13.6 us.
+//   32/32 heads, 16 nodes, 4080 positions, f32           21 us (10.0)
+//   the same, 16 sequences of 4095, f32                 195 us (160)
+//   the same, 16 ragged sequences, binary16              53 us (40)
+//   32/8 heads, 64 nodes, 32700 positions, binary16      59 us (10)
+//   8/1 heads, 27 nodes, 5 ragged sequences, f32         18 us (0.6)
+// The unit counts, in us: kStart 3 against 5 at 4080 positions 22.3 and 24.7 (before the join of
+// today), against 2 at 32/32 heads, 64 nodes and 1000 positions f32 25 and 22.5, at 3/1 heads, 5 nodes and
+// 4000 positions binary16 7.4 and 9.0.  kMinPer 2 against 1 at 3/1 heads, 5 nodes and 16000 positions f32
+// 12.1 and 13.9, 1000 positions 9.4 and 8.4.  kWholeTiles 4 against 2 at 32 heads, 64 nodes and 100
+// positions of 260 f32 9.5 and 13.7, 200 positions 11.0 and 15.0; one head, 300 of 364 12.1 and 8.7;
+// against 8 at 9/3 heads and 370 positions 10.3 and 13.6.
 #include <cuda.h>
 
 #include <algorithm>
