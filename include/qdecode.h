@@ -431,8 +431,9 @@ qd_status qd_tree_append(const float* q, const float* k, const float* v, int64_t
  * Arithmetic: f32 operands enter the tensor cores in two parts (2^-21 or better of a value, or
  * of the largest value beside it), sums, running maxima and outputs are f32; the error is about
  * that of plain f32 arithmetic.
- * workspace (device): qd_tree_attn_workspace bytes (0: a shape the call does not take); two
- * calls that can run at the same time need one each. */
+ * workspace (device): qd_tree_attn_workspace bytes (0: a shape the call does not take; no fewer
+ * for more nodes, positions or sequences, so one of the largest serves them all); two calls
+ * that can run at the same time need one each. */
 size_t qd_tree_attn_workspace(int n_heads, int n_kv_heads, int head_dim, int n_nodes, int max_ctx, int batch);
 qd_status qd_tree_attn(const float* q, int64_t q_batch_stride, const void* k_cache, const void* v_cache,
                        const void* k_draft, const void* v_draft, int kv_f16, float* out, int n_heads, int n_kv_heads,

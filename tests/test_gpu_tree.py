@@ -398,6 +398,16 @@ def test_attn_workspace_serves_both_cache_types(qd):
         Attn(qd, 50, 16, 2, 64, 6000, [1990, 700], f16=f16).check()
 
 
+def test_attn_workspace_does_not_fall_with_the_sizes(qd):
+    rng = np.random.default_rng(51)
+    for _ in range(2000):
+        hk, g, n, b = (int(rng.integers(1, x)) for x in (40, 9, 64, 16))
+        ctx = int(np.exp(rng.uniform(0, 12)))
+        need = qd.tree_attn_workspace(g * hk, hk, HD, n, ctx, b)
+        more = (n + 1, ctx, b), (n, ctx + int(rng.integers(1, 500)), b), (n, ctx, b + 1)
+        assert need > 0 and all(qd.tree_attn_workspace(g * hk, hk, HD, *m) >= need for m in more), (hk, g, n, ctx, b)
+
+
 # ------------------------------------------------------------------------------ append
 def _table(ctx, hd, theta=1e4):
     a = np.arange(ctx)[:, None] * theta ** (-2.0 * np.arange(hd // 2) / hd)[None]
