@@ -425,12 +425,12 @@ qd_status qd_tree_append(const float* q, const float* k, const float* v, int64_t
  * zeros, as do the nodes of a sequence with pos[b] outside [0, max_ctx].  A non-finite q
  * gives NaN in its own row alone, and what a slot holds that a node does not see, NaN and
  * infinities included, does not reach that node's row.  A key that is not finite makes the
- * rows that see it non-finite, a value that dimension of them (values of an f32 cache count as
- * such from 2^100 on).  The result does not depend on what the caches hold at or behind
+ * rows that see it non-finite, a value that dimension of them (of an f32 cache, values from 2^100
+ * and keys from 2^127 on may count as such).  The result does not depend on what the caches hold at or behind
  * pos[b].  Results are the same bits on every run.
- * Arithmetic: f32 operands enter the tensor cores in two parts (2^-21 or better of a value, or
- * of the largest value beside it), sums, running maxima and outputs are f32; the error is about
- * that of plain f32 arithmetic.
+ * Arithmetic: f32 operands enter the tensor cores in parts, with an f32 cache to 2^-21 or better
+ * of each value, with a binary16 one (queries and weights) to 2^-22 of the largest of their row;
+ * sums, running maxima and outputs are f32.  The error is about that of plain f32 arithmetic.
  * workspace (device): qd_tree_attn_workspace bytes (0: a shape the call does not take; no fewer
  * for more nodes, positions or sequences, so one of the largest serves them all); two calls
  * that can run at the same time need one each. */

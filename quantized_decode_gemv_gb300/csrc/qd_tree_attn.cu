@@ -5,12 +5,13 @@
 // The rows that share a kv head (nodes x query heads of the group) walk its positions together
 // with an online softmax: s = q k^T and o += p v are matrix products with f32 accumulators.
 // Outputs are f32, and a binary16 operand alone is 2^-12 off, so what is f32 enters the products
-// in two parts (hi = rn(x), lo = rn(x - hi): 2^-22 of the operand's scale):
-//  - q, scaled by a power of two per row;
-//  - the weights p = 2^(s - m + 12) (the 2^12 keeps the low part of small weights above binary16's
-//    subnormal step; it cancels in o / l);
-//  - a binary16 cache is exact as it is; an f32 cache has two parts, or TF32 ones (see each kernel).
-// That is 2 + 2 products a tile on a binary16 cache and 3 + 3 on an f32 one (lo lo is dropped).
+// in parts, each the rounded rest of those before it.  A binary16 cache is exact as it is, and
+//  - q has two binary16 parts (2^-22 of the row's scale, a power of two),
+//  - the weights p = 2^(s - m + 12) too (the 2^12 keeps the low part of small weights above
+//    binary16's subnormal step; it cancels in o / l).
+// That is 2 + 2 products a tile.  With an f32 cache all operands have two TF32 parts (2^-21, 3 + 3
+// products, lo lo is dropped) or three bfloat16 ones (2^-26, 6 + 6), see each kernel: both types
+// have f32's exponents, so what lies beside an element, and in the other rows, costs it nothing.
 // Scores, running maxima, sums and o are f32.  The matrix units cut their f32 sums off instead of
 // rounding them, so the low parts are summed first, a tile's products start from zero, and they
 // are added to o with rounded f32 additions (one accumulator through a walk of 4080 positions:
@@ -38,6 +39,7 @@
 // positions of 260 f32 9.5 and 13.7, 200 positions 11.0 and 15.0; one head, 300 of 364 12.1 and 8.7;
 // against 8 at 9/3 heads and 370 positions 10.3 and 13.6.
 #include <cuda.h>
+#include <cuda_bf16.h>
 
 #include <algorithm>
 #include <atomic>
@@ -51,7 +53,7 @@ namespace {
 constexpr int kHd = 64;
 constexpr int kTile = 64;      // positions of the smallest tile of a whole CTA; the drafts are one tile
 constexpr int kThreads = 128;  // of the join
-constexpr float kBias = 12.f;  // log2 of the weights' scale
+constexpr float kBias = 12.f;  // log2 of the weights' scale on a binary16 cache
 constexpr int kMinPer = 2;     // units of a CTA at least
 constexpr int kWholeTiles = 4;  // walks of at most so many tiles are not cut
 constexpr int kStart = 3;      // what the start of a walk costs, in tiles
@@ -185,11 +187,6 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 constexpr uint32_t kInfBits = 0x7F800000u;
 __device__ __forceinline__ uint32_t abs_max(float4 x) {
   return max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
-}
-// The same without infinities and NaN.
-__device__ __forceinline__ uint32_t finite_max(float4 x) {
-  auto f = [](float v) { return abs_bits(v) < kInfBits ? abs_bits(v) : 0u; };
-  return max(max(f(x.x), f(x.y)), max(f(x.z), f(x.w)));
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile of 64 rows of 64 binary16 values: chunks
@@ -828,15 +825,29 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 2) k_tree_attn_16(Tr
 // lies, [position][dim], is the transposed B operand); each adds 32 dims of the tile's o to its
 // own registers, rounded.
 // Two CTAs to an SM, one's products under the other's softmax.
-// A binary16 tile lies in the TMA's 128-byte swizzle; an f32 one is converted, k scaled by a power
-// of two for each position and v too (the weights take that over), into 8 x 8 core matrices of 128
-// bytes: row r, 16-byte chunk c at core_off(r, c).
+// A binary16 tile lies in the TMA's 128-byte swizzle; an f32 one is converted into 8 x 8 core
+// matrices of 128 bytes: row r, 16-byte chunk c at core_off(r, c).
+// Operands beside an f32 cache: hi, mid and lo of bfloat16, rounded, so that the products that are
+// left out (mid lo, lo mid, lo lo) are 2^-26 of the whole and of either sign.  68.1 us for 8 x 512
+// rows of 8000 positions; two binary16 parts with a power of two for each position, half as many
+// products but maxima and scales to find, took 69.6 us, an element far below its row's largest lost
+// digits, and so did all values beside a row of 10^5 times their size, whatever its weight.
 constexpr int kThreads128 = 256;
 __device__ __forceinline__ uint32_t core_off(int r, int c) {
   return (uint32_t)((((r >> 3) * 8 + c) * 128) + (r & 7) * 16);
 }
 __host__ __device__ constexpr int tile128(bool f16) { return f16 ? 128 : 64; }
+constexpr uint32_t kIdescBf16 = (1u << 7) | (1u << 10);              // A and B of bfloat16
 constexpr uint32_t kIdescO = tc::idesc_f16(128, kHd) | (1u << 16);  // B with N contiguous
+constexpr uint32_t kFarBits = 0x7F000000u;                           // 2^127: a bfloat16 part may be an infinity
+// The next bfloat16 part of (x, y), taken off them.
+__device__ __forceinline__ uint32_t bf16_part(float2& x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+  x.x -= __uint_as_float(u << 16);
+  x.y -= __uint_as_float(u & 0xFFFF0000u);
+  return u;
+}
 // One lane of the (whole) calling warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -930,8 +941,7 @@ template <bool F16>
 struct Smem128 {
   static constexpr int kStages = F16 ? 2 : 1;
   uint4 ring[kStages][2][tile128(F16) * (F16 ? 8 : 16)];  // K, V as they are, at 1024 bytes
-  uint4 tile[F16 ? 1 : 4][F16 ? 1 : kTile * 8];           // f32 cache: K hi, K lo, V hi, V lo
-  float kscale[kTile], vscale[kTile];
+  uint4 tile[F16 ? 1 : 6][F16 ? 1 : kTile * 8];           // f32 cache: K hi, mid, lo, V hi, mid, lo
   float ex[2][128];                                // what a row's threads tell each other
   unsigned long long mbar[4];                      // s, o, a tile's copies in each stage
   unsigned long long bad;
@@ -948,10 +958,12 @@ __global__ void __launch_bounds__(kThreads128, 2)
   using KV = typename std::conditional<F16, __half, float>::type;
   using S = Smem128<F16>;
   constexpr int BM = 128, kT = tile128(F16), NS = kT / 2, ND = kHd / 2;  // NS scores, ND dims to a thread
-  constexpr uint32_t kIdescS = tc::idesc_f16(128, kT);
-  // tensor memory: s (kT columns), for every 16 positions overlaid by p's 8 + 8 columns; then o;
-  // then q, 16 + 16 columns for every 32 dims
-  constexpr uint32_t kColsS = kT, kColsQ = kT + kHd, kCols128 = 256;
+  constexpr int kParts = F16 ? 2 : 3;  // of q and p; of K and V one or three
+  constexpr uint32_t kType = F16 ? 0 : kIdescBf16, kPartBytes = kTile * 128;
+  // tensor memory: s (kT columns), for every 16 positions overlaid by 8 + 8 columns of p's first two
+  // parts; the third part, 8 columns for every 16 positions; o; q, 16 columns a part for every 32 dims
+  constexpr uint32_t kColsP = kT, kColsO = F16 ? kT : kT + kT / 2, kColsQ = kColsO + kHd, kCols128 = 256;
+  static_assert(kColsQ + 32 * kParts <= kCols128, "tensor memory of half an SM");
   extern __shared__ __align__(128) unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024);
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -1052,25 +1064,36 @@ __global__ void __launch_bounds__(kThreads128, 2)
   }
   __syncwarp();
 
-  // one thread: s = q k^T, the low parts first (what is cut off there does not count)
-  auto issue_s = [&](uint32_t k_hi, uint32_t k_lo) {
-    tc::fence_after_sync();
-    auto k_desc = [&](uint32_t k, int ks) {
-      return F16 ? desc_sw128(k + 32 * ks) : tc::smem_desc(k + 256 * ks, 128, 1024);
-    };
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {  // 16 dims: 8 columns of q
-      const uint32_t q_hi = tm + kColsQ + 32 * (ks / 2) + 8 * (ks & 1), q_lo = q_hi + 16;
-      tc::mma_f16_ts(tm, q_lo, k_desc(k_hi, ks), kIdescS, ks > 0);
-      if constexpr (!F16) tc::mma_f16_ts(tm, q_hi, k_desc(k_lo, ks), kIdescS, 1);
+  // One thread: the products of the parts, the smallest first (what is cut off there does not
+  // count): mul(part of the A operand, part of the B operand, 0 for the first one).
+  auto products = [&](auto&& mul) {
+    if constexpr (F16) {
+      mul(1, 0, 0);
+    } else {
+      mul(2, 0, 0);
+      mul(0, 2, 1);
+      mul(1, 1, 1);
+      mul(1, 0, 1);
+      mul(0, 1, 1);
     }
+    mul(0, 0, 1);
+  };
+  // s = q k^T
+  auto issue_s = [&](uint32_t k) {
+    tc::fence_after_sync();
+    products([&](int a_part, int b_part, int more) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-      tc::mma_f16_ts(tm, tm + kColsQ + 32 * (ks / 2) + 8 * (ks & 1), k_desc(k_hi, ks), kIdescS, 1);
+      for (int ks = 0; ks < 4; ++ks) {  // 16 dims: 8 columns of q
+        const uint32_t at = k + kPartBytes * b_part;
+        tc::mma_f16_ts(tm, tm + kColsQ + 16 * (kParts * (ks / 2) + a_part) + 8 * (ks & 1),
+                       F16 ? desc_sw128(at + 32 * ks) : tc::smem_desc(at + 256 * ks, 128, 1024),
+                       tc::idesc_f16(128, kT) | kType, more || ks > 0);
+      }
+    });
   };
 
   float o[ND];
-  float m = -INFINITY, l = 0.f, rs = 1.f, vunit = 1.f;
+  float m = -INFINITY, l = 0.f, rs = 1.f;
   uint64_t vis = 0;
   bool lost = false;  // a wait has run out: the rows of the walk are NaN
 
@@ -1098,28 +1121,36 @@ __global__ void __launch_bounds__(kThreads128, 2)
         x[c].w *= scale;
         mx = max(mx, abs_max(x[c]));
       }
-      sm.ex[half][lrow] = __uint_as_float(mx);
       vis = live ? a.mask[(int64_t)cur.b * a.n_nodes + row / a.group] : 0ull;
       if (cur.cnt < 64) vis &= (1ull << cur.cnt) - 1;
-      __syncthreads();
-      const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
-      rs = pow2(e);
-      const float f = pow2(-e);
+      float f = 1.f;
+      if constexpr (F16) {
+        sm.ex[half][lrow] = __uint_as_float(mx);
+        __syncthreads();
+        const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
+        rs = pow2(e);
+        f = pow2(-e);
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t hi[8], lo[8];
+        uint32_t part[kParts][8];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          split2(x[4 * c + d].x * f, x[4 * c + d].y * f, hi[2 * d], lo[2 * d]);
-          split2(x[4 * c + d].z * f, x[4 * c + d].w * f, hi[2 * d + 1], lo[2 * d + 1]);
+        for (int d = 0; d < 8; ++d) {
+          const float4 y = x[4 * c + d / 2];
+          float2 z = d & 1 ? make_float2(y.z * f, y.w * f) : make_float2(y.x * f, y.y * f);
+          if constexpr (F16) {
+            split2(z.x, z.y, part[0][d], part[1][d]);
+          } else {
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) part[p][d] = bf16_part(z);
+          }
         }
-        tmem_st8(mine + kColsQ + 32 * half + 8 * c, hi);
-        tmem_st8(mine + kColsQ + 32 * half + 16 + 8 * c, lo);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) tmem_st8(mine + kColsQ + 16 * (kParts * half + p) + 8 * c, part[p]);
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       m = -INFINITY;
       l = 0.f;
-      vunit = pow2(-100);
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[d] = 0.f;
     }
@@ -1127,10 +1158,10 @@ __global__ void __launch_bounds__(kThreads128, 2)
     // ---- the tile arrives
     const int slot = it % S::kStages;
     const uint32_t mb_full = mb_o + 8 + 8 * slot, full = (uint32_t)(it / S::kStages) & 1u;
-    uint32_t k_hi, k_lo = 0, v_hi, v_lo = 0;
+    uint32_t k_at, v_at;  // the first parts
     if constexpr (F16) {
-      k_hi = tc::smem_u32(sm.ring[slot][0]);
-      v_hi = tc::smem_u32(sm.ring[slot][1]);
+      k_at = tc::smem_u32(sm.ring[slot][0]);
+      v_at = tc::smem_u32(sm.ring[slot][1]);
       if (cur.rows < kT) {
         // Behind the last row lies what the cache happens to hold, and a draft's values may hold
         // an infinity or NaN: either would reach every row of the product (0 times it is NaN).
@@ -1165,48 +1196,30 @@ __global__ void __launch_bounds__(kThreads128, 2)
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         float4 x[4];
-        uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = r < cur.rows ? (kv ? vraw : kraw)[i ^ turn] : make_float4(0.f, 0.f, 0.f, 0.f);
-          mx = max(mx, abs_max(x[i]));
-        }
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (kv && mx >= kInfBits) {
-          mx = 0;
-          if (draft) {  // a row with an infinity or NaN, cleared as above
+        for (int i = 0; i < 4; ++i) x[i] = r < cur.rows ? (kv ? vraw : kraw)[i ^ turn] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kv && draft) {  // a row that has no bfloat16 parts, cleared as above
+          uint32_t mx = max(max(abs_max(x[0]), abs_max(x[1])), max(abs_max(x[2]), abs_max(x[3])));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          if (mx >= kFarBits) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j == 0) atomicOr(&sm.bad, 1ull << r);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx = max(mx, finite_max(x[i]));
-            const unsigned quad = 15u << (threadIdx.x & 28);
-            mx = max(mx, __shfl_xor_sync(quad, mx, 1));
-            mx = max(mx, __shfl_xor_sync(quad, mx, 2));
           }
         }
-        const int e = scale_exp(mx);
-        const float f = pow2(-e);
-        uint2* th = reinterpret_cast<uint2*>(sm.tile[2 * kv]);
-        uint2* tl = reinterpret_cast<uint2*>(sm.tile[2 * kv + 1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint2 hi, lo;
-          split2(x[i].x * f, x[i].y * f, hi.x, lo.x);
-          split2(x[i].z * f, x[i].w * f, hi.y, lo.y);
+          float2 lo = make_float2(x[i].x, x[i].y), hi = make_float2(x[i].z, x[i].w);
           const int c = 4 * j + (i ^ turn);
           const uint32_t at = core_off(r, c >> 1) / 8 + (c & 1);
-          th[at] = hi;
-          tl[at] = lo;
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            reinterpret_cast<uint2*>(sm.tile[3 * kv + p])[at] = make_uint2(bf16_part(lo), bf16_part(hi));
         }
-        if (j == 0) (kv ? sm.vscale : sm.kscale)[r] = pow2(e);
       }
-      k_hi = tc::smem_u32(sm.tile[0]);
-      k_lo = tc::smem_u32(sm.tile[1]);
-      v_hi = tc::smem_u32(sm.tile[2]);
-      v_lo = tc::smem_u32(sm.tile[3]);
+      k_at = tc::smem_u32(sm.tile[0]);
+      v_at = tc::smem_u32(sm.tile[3]);
     }
 
     // ---- scores (of a binary16 tile inside a walk they were issued behind the last tile's products)
@@ -1217,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
       if (F16 && uwarp == 0 && !lost && !tc::mbar_wait(mb_full, full)) lost = true;
       __syncwarp();
       if (uwarp == 0 && elect_one()) {
-        issue_s(k_hi, k_lo);
+        issue_s(k_at);
         tc::mma_commit(mb_s);
       }
       __syncwarp();
@@ -1241,16 +1254,6 @@ __global__ void __launch_bounds__(kThreads128, 2)
         tmem_ld16(mine + NS * half + 16 * c, s);
       else
         tc::tmem_ld32(mine + NS * half + 16 * c, s);
-      if constexpr (!F16) {
-#pragma unroll
-        for (int j = 0; j < n; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.kscale[NS * half + 16 * c + j]);
-          s[j] *= f.x;
-          s[j + 1] *= f.y;
-          s[j + 2] *= f.z;
-          s[j + 3] *= f.w;
-        }
-      }
       if (partial) {
         const uint32_t bits = (uint32_t)(see >> (16 * c));
 #pragma unroll
@@ -1271,34 +1274,20 @@ __global__ void __launch_bounds__(kThreads128, 2)
       sm.ex[half][lrow] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs;
     }
     __syncthreads();  // the maximum of the row's other half
-    float vinv = 1.f;
     if (warp_live) {
       // ---- online softmax
       const float mn = fmaxf(m, fmaxf(sm.ex[0][lrow], sm.ex[1][lrow]));
       const float mu = mn == -INFINITY ? 0.f : mn;
       corr = ex2(m - mu);
       m = mn;
-      const float bias = kBias - mu;
-      if constexpr (!F16) {  // the weights take over the scale of their v rows
-        float top = vunit;
-#pragma unroll
-        for (int j = 0; j < kT; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.vscale[j]);
-          if (draft)
-            top = fmaxf(top, fmaxf(fmaxf(vis >> j & 1 ? f.x : 0.f, vis >> (j + 1) & 1 ? f.y : 0.f),
-                                   fmaxf(vis >> (j + 2) & 1 ? f.z : 0.f, vis >> (j + 3) & 1 ? f.w : 0.f)));
-          else
-            top = fmaxf(fmaxf(top, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
-        }
-        vinv = __uint_as_float((254u << 23) - __float_as_uint(top));  // 1 / top, a power of two
-      }
+      const float bias = (F16 ? kBias : 0.f) - mu;
       float2 sum = make_float2(0.f, 0.f), sum1 = sum;
 #pragma unroll
       for (int c = 0; c < NS / 16; ++c) {
         float s[16];
         scores(c, s);
         // ---- the weights' parts over the scores
-        uint32_t hi[8], lo[8];
+        uint32_t part[kParts][8];
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           float2 p = fma2(make_float2(s[j], s[j + 1]), make_float2(rs, rs), make_float2(bias, bias));
@@ -1308,26 +1297,23 @@ __global__ void __launch_bounds__(kThreads128, 2)
             sum1 = add2(sum1, p);
           else
             sum = add2(sum, p);
-          if constexpr (!F16) {
-            const float2 f = *reinterpret_cast<const float2*>(&sm.vscale[NS * half + 16 * c + j]);
-            p.x = p.x * vinv * f.x;
-            p.y = p.y * vinv * f.y;
+          if constexpr (F16) {
+            const __half2 h = __floats2half2_rn(p.x, p.y);
+            const float2 back = __half22float2(h);
+            const float2 rest = fma2(back, make_float2(-1.f, -1.f), p);
+            const __half2 w = __floats2half2_rn(rest.x, rest.y);
+            part[0][j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            part[1][j / 2] = *reinterpret_cast<const uint32_t*>(&w);
+          } else {
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) part[x][j / 2] = bf16_part(p);
           }
-          const __half2 h = __floats2half2_rn(p.x, p.y);
-          const float2 back = __half22float2(h);
-          const float2 rest = fma2(back, make_float2(-1.f, -1.f), p);
-          const __half2 w = __floats2half2_rn(rest.x, rest.y);
-          hi[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
-          lo[j / 2] = *reinterpret_cast<const uint32_t*>(&w);
         }
-        tmem_st8(mine + NS * half + 16 * c, hi);
-        tmem_st8(mine + NS * half + 16 * c + 8, lo);
+        tmem_st8(mine + NS * half + 16 * c, part[0]);
+        tmem_st8(mine + NS * half + 16 * c + 8, part[1]);
+        if constexpr (!F16) tmem_st8(mine + kColsP + NS / 2 * half + 8 * c, part[2]);
       }
       l = fmaf(l, corr, (sum.x + sum.y) + (sum1.x + sum1.y));
-      if constexpr (!F16) {
-        corr *= vunit * vinv;
-        vunit = __uint_as_float((254u << 23) - __float_as_uint(vinv));
-      }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     }
     const unsigned long long bad = draft ? sm.bad : 0ull;
@@ -1343,9 +1329,10 @@ __global__ void __launch_bounds__(kThreads128, 2)
           if (!((vis & bad) >> j & 1)) continue;
           float x = 0.f;
           for (int d = 0; d < kHd; ++d) x = fmaf(qrow[d], (float)kd[at + j * kHd + d], x);
-          const float p = ex2(fmaf(x, 1.4426950408889634f * 0.125f, kBias - (m == -INFINITY ? 0.f : m)));
+          const float p =
+              ex2(fmaf(x, 1.4426950408889634f * 0.125f, (F16 ? kBias : 0.f) - (m == -INFINITY ? 0.f : m)));
 #pragma unroll
-          for (int d = 0; d < ND; ++d) o[d] += p * ((float)vd[at + j * kHd + half * ND + d] * vinv);
+          for (int d = 0; d < ND; ++d) o[d] += p * (float)vd[at + j * kHd + half * ND + d];
         }
       }
     }
@@ -1355,17 +1342,15 @@ __global__ void __launch_bounds__(kThreads128, 2)
     // ---- weighted values
     if (uwarp == 0 && elect_one()) {
       tc::fence_after_sync();
-      auto v_desc = [&](uint32_t v, int kk) {
-        return F16 ? desc_sw128(v + 2048 * kk) : tc::smem_desc(v + 2048 * kk, 1024, 128);
-      };
+      products([&](int a_part, int b_part, int more) {
 #pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk) {  // 16 positions: 8 columns of p, two atoms or rows of core matrices of v
-        const uint32_t ph = tm + 16 * kk, pl = ph + 8;
-        tc::mma_f16_ts(tm + kColsS, pl, v_desc(v_hi, kk), kIdescO, kk > 0);
-        if constexpr (!F16) tc::mma_f16_ts(tm + kColsS, ph, v_desc(v_lo, kk), kIdescO, 1);
-      }
-#pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk) tc::mma_f16_ts(tm + kColsS, tm + 16 * kk, v_desc(v_hi, kk), kIdescO, 1);
+        for (int kk = 0; kk < kT / 16; ++kk) {  // 16 positions: 8 columns of p, two atoms or rows of core matrices of v
+          const uint32_t p = a_part < 2 ? tm + 16 * kk + 8 * a_part : tm + kColsP + 8 * kk;
+          const uint32_t at = v_at + kPartBytes * b_part + 2048 * kk;
+          tc::mma_f16_ts(tm + kColsO, p, F16 ? desc_sw128(at) : tc::smem_desc(at, 1024, 128), kIdescO | kType,
+                         more || kk > 0);
+        }
+      });
       tc::mma_commit(mb_o);
     }
     __syncwarp();  // no lane polls while another of its warp still has the products to issue
@@ -1382,7 +1367,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
           lost = true;
         __syncwarp();
         if (ahead && elect_one()) {
-          issue_s(tc::smem_u32(sm.ring[ns][0]), 0);
+          issue_s(tc::smem_u32(sm.ring[ns][0]));
           tc::mma_commit(mb_s);
         }
       }
@@ -1394,7 +1379,7 @@ __global__ void __launch_bounds__(kThreads128, 2)
 #pragma unroll
       for (int d0 = 0; d0 < ND; d0 += 16) {
         float t[16];
-        tmem_ld16(mine + kColsS + ND * half + d0, t);
+        tmem_ld16(mine + kColsO + ND * half + d0, t);
 #pragma unroll
         for (int d = 0; d < 16; d += 2) {
           const float2 x =
@@ -1419,15 +1404,14 @@ __global__ void __launch_bounds__(kThreads128, 2)
         part[BM + lrow] = lt;
       }
       if (!whole || row < rows) {
-        const float inv = !whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt, unit = F16 ? 1.f : vunit;
+        const float inv = !whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt;
         float4* dst = reinterpret_cast<float4*>((whole ? row_of(a, a.out, cur, row) : part + 2 * BM + lrow * kHd) +
                                                 half * ND);
         const bool none = whole && lt == 0.f;
 #pragma unroll
         for (int d = 0; d < ND; d += 4)
           dst[d / 4] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : make_float4(o[d] * inv * unit, o[d + 1] * inv * unit, o[d + 2] * inv * unit,
-                                          o[d + 3] * inv * unit);
+                            : make_float4(o[d] * inv, o[d + 1] * inv, o[d + 2] * inv, o[d + 3] * inv);
       }
       __syncthreads();  // `ex` is read
     }

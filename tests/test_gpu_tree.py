@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from gpu_helpers import dev
-from tree_helpers import attn_ref, attn_tol, commit_ref, logprobs_ref, mask_bits, random_tree
+from tree_helpers import (attn_bound, attn_plain, attn_ref, attn_tol, commit_ref, logprobs_ref, mask_bits, random_tree,
+                          rms)
 
 pytestmark = pytest.mark.gpu
 HD = 64
@@ -390,6 +391,113 @@ def test_attn_128_two_calls_at_once_and_captured(qd, f16):
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+# What a value's own size asks for: each output against a bound that does not grow with the other
+# dimensions of the rows, or with rows that have no weight (attn_bound).  (hq, hk, n) below the
+# bound of the 128-row blocks and above it (_wide).
+def _close(a, b=0):
+    got = a.call()[b].cpu().numpy()
+    q = a.q[b, :a.n * a.hq * HD].reshape(a.n, a.hq, HD)
+    want, tol = attn_bound(q, a.k[b], a.v[b], a.kd[b], a.vd[b], a.pos[b], a.anc[b], a.n, a.hq, a.hk, a.f16)
+    off = np.abs(got - want) / tol
+    assert off.max() <= 1, (off.max(), np.unravel_index(off.argmax(), off.shape))
+
+
+def _either(qd, wide, seed, pos, f16):
+    return _wide(qd, seed, [pos], f16) if wide else Attn(qd, seed, 6, 2, 9, pos + 10, [pos], f16=f16)
+
+
+def _rows(a):
+    return a.q.reshape(a.b, -1, HD)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("ratio", [2.0**10, 2.0**14])
+def test_attn_large_dimension_of_the_values_leaves_the_others_their_digits(qd, ratio, wide):
+    a = _either(qd, wide, 60, 390, False)
+    a.v[..., 11] *= ratio
+    a.vd[..., 11] *= ratio
+    _close(a)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("ratio", [2.0**10, 2.0**14])
+def test_attn_large_dimension_of_the_keys_leaves_the_others_their_digits(qd, ratio, wide):
+    a = _either(qd, wide, 61, 390, False)
+    a.k[..., 11] *= ratio
+    a.kd[..., 11] *= ratio
+    _rows(a)[..., 11] /= ratio
+    _close(a)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("ratio", [2.0**10, 2.0**14])
+def test_attn_large_dimension_of_the_queries_leaves_the_others_their_digits(qd, ratio, wide):
+    a = _either(qd, wide, 62, 390, False)
+    _rows(a)[..., 11] *= np.float32(ratio)
+    a.k[..., 11] /= ratio
+    a.kd[..., 11] /= ratio
+    _close(a)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("score,big", [(-300.0, 1e9), (-300.0, 1e30), (-100.0, 1e20), (-18.0, 1e6)])
+def test_attn_large_value_row_of_little_weight_leaves_the_others_their_digits(qd, score, big, wide, f16):
+    """A cached row whose values are far larger than the others', behind a score far below theirs."""
+    a = _either(qd, wide, 63, 390, f16)
+    _rows(a)[..., 5] = 16.0
+    a.k[..., 5] = a.kd[..., 5] = 0
+    a.k[0, :, 200] = 0
+    a.k[0, :, 200, 5] = score / 2
+    a.v[0, :, 200] *= min(big, 8192.0) if f16 else big
+    _close(a)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_attn_128_unseen_large_values_keep_the_others_digits(qd, f16):
+    """A draft that a row does not see may hold the type's largest value."""
+    a = _wide(qd, 65, [90], f16)
+    want = a.call().cpu().numpy()
+    a.kd[:, :, 7] = 65504.0 if f16 else np.finfo(np.float32).max
+    a.vd[:, :, 7] = -a.kd[:, :, 7]
+    got = a.call().cpu().numpy()
+    sees = a.anc[0, :, 7]
+    assert np.array_equal(got[0][~sees], want[0][~sees]) and not sees.all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("f16", [False, True])
+def test_attn_infinite_draft_value_over_a_cache_of_zeros(qd, wide, f16):
+    """The other dimensions of such a draft count with their own size, whatever the other values are."""
+    a = _either(qd, wide, 66, 120, f16)
+    a.v[:] = 0
+    a.vd[:] = 0
+    a.vd[0, :, 2] = 100.0 if f16 else 1e9
+    a.vd[0, :, 2, 3] = np.inf
+    got = a.call()[0].cpu().numpy()
+    sees = a.anc[0, :, 2]
+    assert np.all(got[~sees] == 0) and np.all(~np.isfinite(got[sees][..., 3]))
+    a.vd[0, :, 2, 3] = 0
+    q = a.q[0, :a.n * a.hq * HD].reshape(a.n, a.hq, HD)
+    want, tol = attn_bound(q, a.k[0], a.v[0], a.kd[0], a.vd[0], 120, a.anc[0], a.n, a.hq, a.hk, f16)
+    dims = [d for d in range(HD) if d != 3]
+    assert np.all(np.abs(got - want)[sees][..., dims] <= tol[sees][..., dims])
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("wide,pos", [(False, 40), (False, 700), (False, 9000), (True, 40), (True, 700), (True, 6000)])
+def test_attn_error_is_about_that_of_f32_arithmetic(qd, wide, pos, f16):
+    """RMS error against 64 bits beside that of a plain f32 computation of the same inputs.  The
+    roundings are f32's own and operands 2^-21 off at most, so it is of f32's size; an operand that
+    lost its low part is 2^-9 to 2^-12 off, hundreds of times that (test_tree_cpu.py)."""
+    a = _either(qd, wide, 64, pos, f16)
+    got = a.call()[0].cpu().numpy()
+    args = (a.q[0, :a.n * a.hq * HD].reshape(a.n, a.hq, HD), a.k[0], a.v[0], a.kd[0], a.vd[0], pos, a.anc[0], a.n, a.hq,
+            a.hk)
+    want = attn_plain(*args, dtype=np.float64)
+    plain = rms(attn_plain(*args) - want)
+    assert rms(got - want) <= 3 * plain, (rms(got - want), plain)
 
 
 def test_attn_workspace_serves_both_cache_types(qd):

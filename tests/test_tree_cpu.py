@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import quantized_decode_gemv_gb300 as qd
-from tree_helpers import commit_ref, logprobs_ref, mask_bits, random_tree
+from tree_helpers import attn_bound, attn_plain, attn_ref, commit_ref, logprobs_ref, mask_bits, random_tree, rms
 
 
 @pytest.fixture(scope="module")
@@ -145,3 +145,42 @@ def test_references_on_hand_values():
     assert commit_ref(toks, par, [2, 0, 3, 3, 7], 2, 10, 100) == ([0], 2)
     assert commit_ref(toks, par, [1, 0, 3, 3, 7], 5, 10, 11) == ([0], 1)
     assert commit_ref(toks, par, [1, 0, 3, 3, 7], 5, 11, 11) == ([], -1)
+
+
+def _tree_rows(seed, pos, n=9, hq=6, hk=2):
+    rng = np.random.default_rng(seed)
+    mk = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    q, k, v, kd, vd = 1.5 * mk(n, hq, 64), mk(hk, pos, 64), mk(hk, pos, 64), mk(hk, n, 64), mk(hk, n, 64)
+    return q, k, v, kd, vd, pos, random_tree(rng, n)[1], n, hq, hk
+
+
+def test_attention_references_agree():
+    for pos in (0, 3, 200):
+        args = _tree_rows(pos, pos)
+        want = attn_ref(*args)[0]
+        out, tol = attn_bound(*args, False)
+        assert np.abs(out - want).max() < 1e-13 and np.abs(attn_plain(*args, dtype=np.float64) - want).max() < 1e-13
+        assert np.all(np.abs(attn_plain(*args) - want) <= tol)
+
+
+def _bits(a, n):
+    """a rounded to n significant bits."""
+    m, e = np.frexp(np.asarray(a, np.float64))
+    return np.ldexp(np.round(np.ldexp(m, n)), e - n)
+
+
+@pytest.mark.parametrize("pos", [40, 700, 6000])
+@pytest.mark.parametrize("operand", ["q", "k", "v", "p"])
+def test_an_operand_without_its_low_part_is_far_from_f32(pos, operand):
+    """What the comparison with plain f32 arithmetic on the GPU would see: operands of 22 bits pass
+    it, one of 11 (a single TF32 or binary16 part) or 16 (two of the three bfloat16 parts) does not."""
+    args = _tree_rows(pos, pos)
+    want = attn_plain(*args, dtype=np.float64)
+    plain = rms(attn_plain(*args) - want)
+
+    def error(bits, only=None):
+        cut = lambda name, a: _bits(a, bits) if only in (None, name) else a  # noqa: E731
+        return rms(attn_plain(*args, dtype=np.float64, part=cut) - want)
+
+    assert error(22) <= 3 * plain
+    assert error(11, operand) > 30 * plain and error(16, operand) > 3 * plain

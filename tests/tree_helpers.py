@@ -53,6 +53,59 @@ def attn_tol(n, smax, vmax):
     return vmax * (2 * ds + 2 * (n / 16 + 64) * 2.0**-24 + 4 * 2.0**-22)
 
 
+def attn_bound(q, k, v, kd, vd, pos, anc, cnt, hq, hk, f16):
+    """One sequence in 64 bits: out [cnt][hq][64] and the bound of each output's own error.
+    With weights w_j that sum to 1, an output sum_j w_j v_j moves by at most
+    sum_j w_j e_j (|v_j| + |o|) when every weight is off by a factor 1 + e_j: a score is off by
+    80 * 2^-24 of its own sum |q k| / 8 (64 f32 additions and two operands to 2^-21 each, as in
+    attn_tol) and exp2 and the weight's parts by 8 * 2^-24.  The sums over n positions (n / 16 + 64
+    additions one after the other, as in attn_tol) and the parts of v (8 half steps) add
+    (n / 16 + 72) * 2^-24 of sum w |v| and of |o|.  Nothing here grows with another dimension of
+    the value, or with a row that has no weight.  A binary16 cache: weights and queries in two
+    binary16 parts, which end 2^-40 below the largest of the row."""
+    q, k, v, kd, vd = (np.asarray(a, np.float64) for a in (q, k, v, kd, vd))
+    u = 2.0**-24
+    out, tol = np.zeros((cnt, hq, HD)), np.zeros((cnt, hq, HD))
+    for h in range(hq):
+        g = h // (hq // hk)
+        for i in range(cnt):
+            keep = [j for j in range(cnt) if anc[i, j]]
+            kk = np.concatenate([k[g, :pos], kd[g, keep]])
+            vv = np.concatenate([v[g, :pos], vd[g, keep]])
+            s = kk @ q[i, h] / 8.0
+            w = np.exp(s - s.max())
+            rel = 80 * u * (np.abs(kk) @ np.abs(q[i, h])) / 8.0 + 8 * u
+            w /= w.sum()
+            o = w @ vv
+            end = 0.0
+            if f16:
+                rel = rel + 2 * 2.0**-40 * np.abs(q[i, h]).max() * np.abs(kk).sum(1) / 8.0
+                end = 2 * 2.0**-40 * w.max() * (np.abs(vv).sum(0) + len(vv) * np.abs(o))
+            out[i, h] = o
+            tol[i, h] = (w * rel) @ (np.abs(vv) + np.abs(o)) + (len(vv) / 16 + 72) * u * (w @ np.abs(vv) + np.abs(o)) + end
+    return out, tol
+
+
+def attn_plain(q, k, v, kd, vd, pos, anc, cnt, hq, hk, dtype=np.float32, part=lambda name, a: a):
+    """One sequence in `dtype`, a head's rows at once: out [cnt][hq][64].  part(name, a) stands for
+    what becomes of an operand ("q", "k", "p", "v") on its way into a product."""
+    q, k, v, kd, vd = (np.asarray(a, dtype) for a in (q, k, v, kd, vd))
+    out = np.zeros((cnt, hq, HD), dtype)
+    sees = np.concatenate([np.ones((cnt, pos), bool), anc[:cnt, :cnt]], 1)
+    for h in range(hq):
+        g = h // (hq // hk)
+        kk, vv = np.concatenate([k[g, :pos], kd[g, :cnt]]), np.concatenate([v[g, :pos], vd[g, :cnt]])
+        s = part("q", q[:cnt, h] * dtype(0.125)) @ part("k", kk).T
+        s = np.where(sees, s, dtype(-np.inf))
+        p = np.exp(s - s.max(1, keepdims=True))
+        out[:, h] = (part("p", p) @ part("v", vv)) / p.sum(1, keepdims=True)
+    return out
+
+
+def rms(a):
+    return float(np.sqrt(np.mean(np.square(np.asarray(a, np.float64)))))
+
+
 def logprobs_ref(x, tokens, top_k):
     """(logprob, entropy, top_idx, top_logprob) of one row in 64 bits."""
     x = np.asarray(x, np.float64)
