@@ -429,8 +429,9 @@ qd_status qd_tree_append(const float* q, const float* k, const float* v, int64_t
  * and keys from 2^127 on may count as such).  The result does not depend on what the caches hold at or behind
  * pos[b].  Results are the same bits on every run.
  * Arithmetic: f32 operands enter the tensor cores in parts, with an f32 cache to 2^-21 or better
- * of each value, with a binary16 one (queries and weights) to 2^-22 of the largest of their row;
- * sums, running maxima and outputs are f32.  The error is about that of plain f32 arithmetic.
+ * of each value, with a binary16 one (queries and weights) to 2^-22 of each value from 2^-17 of the
+ * largest of its row on, and to 2^-40 of that below; sums, running maxima and outputs are f32.  The
+ * error is about that of plain f32 arithmetic.
  * workspace (device): qd_tree_attn_workspace bytes (0: a shape the call does not take; no fewer
  * for more nodes, positions or sequences, so one of the largest serves them all); two calls
  * that can run at the same time need one each. */

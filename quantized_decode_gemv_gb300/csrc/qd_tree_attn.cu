@@ -6,9 +6,12 @@
 // with an online softmax: s = q k^T and o += p v are matrix products with f32 accumulators.
 // Outputs are f32, and a binary16 operand alone is 2^-12 off, so what is f32 enters the products
 // in parts, each the rounded rest of those before it.  A binary16 cache is exact as it is, and
-//  - q has two binary16 parts (2^-22 of the row's scale, a power of two),
-//  - the weights p = 2^(s - m + 12) too (the 2^12 keeps the low part of small weights above
-//    binary16's subnormal step; it cancels in o / l).
+//  - q has two binary16 parts, scaled by a power of two per row,
+//  - the weights p = 2^(s - m + 15) too (the 2^15 cancels in o / l).
+// A low part ends at binary16's subnormal step 2^-24, so a row's largest operand stands at 2^14 to
+// 2^15: what is 2^-17 of it or more has 22 bits, and what is less is 2^-40 of it off.  (With q at 1
+// to 2 and p at 2^12 at most those were 2^-3 and 2^-26 for q and 2^-14 and 2^-37 for p, in the same
+// time; a dimension of q 2^14 times the others left them 12 bits.)
 // That is 2 + 2 products a tile.  With an f32 cache all operands have two TF32 parts (2^-21, 3 + 3
 // products, lo lo is dropped) or three bfloat16 ones (2^-26, 6 + 6), see each kernel: both types
 // have f32's exponents, so what lies beside an element, and in the other rows, costs it nothing.
@@ -53,7 +56,7 @@ namespace {
 constexpr int kHd = 64;
 constexpr int kTile = 64;      // positions of the smallest tile of a whole CTA; the drafts are one tile
 constexpr int kThreads = 128;  // of the join
-constexpr float kBias = 12.f;  // log2 of the weights' scale on a binary16 cache
+constexpr float kBias = 15.f;  // log2 of the weights' scale on a binary16 cache
 constexpr int kMinPer = 2;     // units of a CTA at least
 constexpr int kWholeTiles = 4;  // walks of at most so many tiles are not cut
 constexpr int kStart = 3;      // what the start of a walk costs, in tiles
@@ -179,9 +182,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
-// Exponent e of a largest magnitude (given by its bits), so that x 2^-e is below 4: finite
-// values only, an infinity or NaN keeps e = 126 and stays what it is.
-__device__ __forceinline__ int scale_exp(uint32_t abs_bits) { return min(max((int)(abs_bits >> 23) - 127, -100), 126); }
+// Exponent e of a largest magnitude (given by its bits), so that x 2^-e is in 2^14 .. 2^15 (less for
+// one under 2^-100); an infinity or NaN stays what it is.
+__device__ __forceinline__ int scale_exp(uint32_t abs_bits) {
+  return min(max((int)(abs_bits >> 23) - 127, -100), 127) - 14;
+}
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 constexpr uint32_t kInfBits = 0x7F800000u;

@@ -485,6 +485,30 @@ def test_attn_infinite_draft_value_over_a_cache_of_zeros(qd, wide, f16):
     dims = [d for d in range(HD) if d != 3]
     assert np.all(np.abs(got - want)[sees][..., dims] <= tol[sees][..., dims])
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("ratio", [2.0**10, 2.0**14])
+def test_attn_large_dimension_of_the_queries_over_a_binary16_cache(qd, ratio, wide):
+    a = _either(qd, wide, 67, 390, True)
+    _rows(a)[..., 11] *= np.float32(ratio)
+    a.k[..., 11] /= ratio
+    a.kd[..., 11] /= ratio
+    _close(a)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("score", [-18.0, -20.0, -24.0])
+def test_attn_small_weights_of_large_values_over_a_binary16_cache(qd, score, wide):
+    """A row of values near the type's largest behind a small weight, the other values small."""
+    a = _either(qd, wide, 68, 390, True)
+    _rows(a)[..., 5] = 16.0
+    a.k[..., 5] = a.kd[..., 5] = 0
+    a.k[0, :, 200] = 0
+    a.k[0, :, 200, 5] = score / 2
+    a.v *= np.float16(1e-5)
+    a.vd *= np.float16(1e-5)
+    a.v[0, :, 200] = np.where(a.v[0, :, 200] < 0, -60000.0, 60000.0)
+    _close(a)
+
 @pytest.mark.parametrize("f16", [False, True])
 @pytest.mark.parametrize("wide,pos", [(False, 40), (False, 700), (False, 9000), (True, 40), (True, 700), (True, 6000)])
 def test_attn_error_is_about_that_of_f32_arithmetic(qd, wide, pos, f16):
