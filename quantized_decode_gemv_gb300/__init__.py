@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -327,24 +328,45 @@ def _here(stream):
     return _stream(stream), dev
 
 
-def _room(fn, name, t, dtype, dev, n, stepped=False):
-    """Pointer of t after a look at what only the tensor tells: its type, its device and that
-    n elements lie behind its pointer, so that a tensor too small is an error here and not a
-    read out of bounds on the device.  Only a `stepped` argument, whose strides the call is
-    given, may be a view with gaps.  Raw pointers and None pass as they are."""
+@functools.lru_cache(maxsize=1024)  # 0.4 us instead of 1.2 for a view of four dimensions
+def _extent(shape, strides, steps):
+    """Elements from a view's first one to its last; None where a dimension leaves a gap that is
+    not one of `steps` (if there are any)."""
+    n = dense = 1
+    for size, stride in zip(reversed(shape), reversed(strides)):
+        if size != 1:
+            if stride != dense and steps and stride not in steps:
+                return None
+            n += (size - 1) * stride
+            dense = size * stride
+    return n
+
+
+def _room(fn, name, t, dtype, dev, n, stepped=False, steps=()):
+    """Pointer of t after a look at what only the tensor tells: its type, its device, that n
+    elements lie behind its pointer, so that a tensor too small is an error here and not a read
+    out of bounds on the device, and that they lie there in the order of its dimensions.  Only a
+    `stepped` argument may be a view with gaps, and those have to be the `steps`, the strides that
+    the call is given (none: any).  Raw pointers and None pass as they are."""
     if t is None or t.__class__ is int:
         return t
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
-        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} has type {t.dtype}, not {dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
-    if not stepped and not t.is_contiguous():
+    if t.is_contiguous():
+        have = t.numel()
+    elif not stepped:
         raise ValueError(f"{fn}: {name} is not contiguous")
-    have = t.numel() if not stepped else t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    else:
+        have = _extent(t.shape, t.stride(), steps)
+        if have is None:
+            raise ValueError(f"{fn}: {name} has strides {t.stride()}, the call takes {steps} and no other gaps")
     if have < n:
-        raise ValueError(f"{fn}: {name} holds {have} elements, the call takes {n}")
+        if stepped:
+            have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+        if have < n:
+            raise ValueError(f"{fn}: {name} holds {have} elements, the call takes {n}")
     return t.data_ptr()
 
 
@@ -366,10 +388,11 @@ def tree_append(q, k, v, batch_stride, node_stride, q_out, k_draft, v_draft, n_h
     fn, f32, i32, (st, dev) = "qd_tree_append", torch.float32, torch.int32, _here(stream)
     kv = torch.float16 if kv_f16 else f32
     last = (batch - 1) * batch_stride + (n_nodes - 1) * node_stride
-    qn, kn = n_heads * head_dim, n_kv_heads * head_dim
+    qn, kn, steps = n_heads * head_dim, n_kv_heads * head_dim, (batch_stride, node_stride)
     _check(fn, load().qd_tree_append(
-        _room(fn, "q", q, f32, dev, last + qn, True), _room(fn, "k", k, f32, dev, last + kn, True),
-        _room(fn, "v", v, f32, dev, last + kn, True), batch_stride, node_stride,
+        _room(fn, "q", q, f32, dev, last + qn, True, steps),
+        _room(fn, "k", k, f32, dev, last + kn, True, steps),
+        _room(fn, "v", v, f32, dev, last + kn, True, steps), batch_stride, node_stride,
         _room(fn, "q_out", q_out, f32, dev, batch * n_nodes * qn),
         _room(fn, "k_draft", k_draft, kv, dev, batch * n_nodes * kn),
         _room(fn, "v_draft", v_draft, kv, dev, batch * n_nodes * kn), 1 if kv_f16 else 0, n_heads, n_kv_heads,
@@ -394,7 +417,7 @@ def tree_attn(q, q_batch_stride, k_cache, v_cache, k_draft, v_draft, out, n_head
     qn, kn = n_nodes * n_heads * head_dim, batch * n_nodes * n_kv_heads * head_dim
     cn = batch * n_kv_heads * max_ctx * head_dim
     _check(fn, load().qd_tree_attn(
-        _room(fn, "q", q, f32, dev, (batch - 1) * q_batch_stride + qn, True), q_batch_stride,
+        _room(fn, "q", q, f32, dev, (batch - 1) * q_batch_stride + qn, True, (q_batch_stride,)), q_batch_stride,
         _room(fn, "k_cache", k_cache, kv, dev, cn), _room(fn, "v_cache", v_cache, kv, dev, cn),
         _room(fn, "k_draft", k_draft, kv, dev, kn), _room(fn, "v_draft", v_draft, kv, dev, kn), 1 if kv_f16 else 0,
         _room(fn, "out", out, f32, dev, batch * qn), n_heads, n_kv_heads, head_dim,
@@ -410,8 +433,8 @@ def token_logprobs(logits, row_stride, vocab, rows, tokens, n_tokens, logprob, e
 
     fn, f32, i32, (st, dev) = "qd_token_logprobs", torch.float32, torch.int32, _here(stream)
     _check(fn, load().qd_token_logprobs(
-        _room(fn, "logits", logits, f32, dev, (rows - 1) * row_stride + vocab, True), row_stride, vocab, rows,
-        _room(fn, "tokens", tokens, i32, dev, rows * n_tokens), n_tokens,
+        _room(fn, "logits", logits, f32, dev, (rows - 1) * row_stride + vocab, True, (row_stride,)), row_stride, vocab,
+        rows, _room(fn, "tokens", tokens, i32, dev, rows * n_tokens), n_tokens,
         _room(fn, "logprob", logprob, f32, dev, rows * n_tokens), _room(fn, "entropy", entropy, f32, dev, rows), top_k,
         _room(fn, "top_idx", top_idx, i32, dev, rows * top_k),
         _room(fn, "top_logprob", top_logprob, f32, dev, rows * top_k), st))
@@ -429,11 +452,13 @@ def tree_commit(tokens, parent, chosen, chosen_stride, n_valid, n_nodes, k_draft
     cn = (layers - 1) * cache_layer_stride + batch * n_kv_heads * max_ctx * head_dim
     _check(fn, load().qd_tree_commit(
         _room(fn, "tokens", tokens, i32, dev, nodes), _room(fn, "parent", parent, i32, dev, nodes),
-        _room(fn, "chosen", chosen, i32, dev, (nodes - 1) * chosen_stride + 1, True), chosen_stride,
+        _room(fn, "chosen", chosen, i32, dev, (nodes - 1) * chosen_stride + 1, True, (chosen_stride,)), chosen_stride,
         _room(fn, "n_valid", n_valid, i32, dev, batch), n_nodes, _room(fn, "k_draft", k_draft, kv, dev, dn),
-        _room(fn, "v_draft", v_draft, kv, dev, dn), _room(fn, "k_cache", k_cache, kv, dev, cn, True),
-        _room(fn, "v_cache", v_cache, kv, dev, cn, True), 1 if kv_f16 else 0, layers, cache_layer_stride, n_kv_heads,
-        head_dim, _room(fn, "pos", pos, i32, dev, batch), max_ctx, batch, _room(fn, "path", path, i32, dev, nodes),
+        _room(fn, "v_draft", v_draft, kv, dev, dn),
+        _room(fn, "k_cache", k_cache, kv, dev, cn, True, (cache_layer_stride,)),
+        _room(fn, "v_cache", v_cache, kv, dev, cn, True, (cache_layer_stride,)), 1 if kv_f16 else 0, layers,
+        cache_layer_stride, n_kv_heads, head_dim, _room(fn, "pos", pos, i32, dev, batch), max_ctx, batch,
+        _room(fn, "path", path, i32, dev, nodes),
         _room(fn, "n_accept", n_accept, i32, dev, batch), _room(fn, "next_token", next_token, i32, dev, batch),
         _room(fn, "pos_out", pos_out, i32, dev, batch), st))
 

@@ -800,6 +800,24 @@ def test_binding_refuses_tensors_that_are_too_small(qd):
         qd.token_logprobs(x, 101, 101, 4, None, 0, None, torch.zeros(4, device="cuda"), 0, None, None)
 
 
+def test_commit_refuses_a_cache_in_another_order(qd):
+    n, ctx, L, hk = 4, 10, 2, 3
+    one = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    d = torch.ones(L, 1, hk, n, HD, device="cuda")
+    call = lambda k, v, chosen: qd.tree_commit(  # noqa: E731
+        one(1, n), one(1, n), chosen, 1, None, n, d, d, k, v, L, hk * ctx * HD, hk, HD, one(1), ctx, 1, one(1, n), one(1),
+        one(1), one(1))
+    k, turned = torch.zeros(L, 1, hk, ctx, HD, device="cuda"), torch.zeros(L, 1, ctx, hk, HD, device="cuda").transpose(2, 3)
+    for args in ((turned, k, one(1, n)), (k, turned, one(1, n)), (k, k.clone(), one(n, 2)[:, 0])):
+        with pytest.raises(ValueError, match="strides"):
+            call(*args)
+    assert not k.any() and not turned.any()
+    a = Attn(qd, 15, 4, 2, 6, 50, [20])
+    a.call()
+    q = a.args[0].reshape(1, a.n, a.hq, HD).transpose(1, 2)
+    with pytest.raises(ValueError, match="strides"):
+        qd.tree_attn(q, *a.args[1:])
+
 # ------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("f16", [False, True])
 def test_a_tree_is_verified_as_one_token_at_a_time(qd, f16):

@@ -131,6 +131,38 @@ def test_binding_refuses_tensors_that_do_not_hold_the_call():
     assert room("f", "a", None, torch.float32, 0, 8) is None and room("f", "a", 64, torch.float32, 0, 8) == 64
 
 
+def test_binding_refuses_views_in_another_order_than_the_call_takes():
+    """Only the strides that a call is given may leave gaps; what lies inside them is dense."""
+    f = torch.float32
+    cache = torch.zeros(3, 2, 4, 10, 64)  # [layers][batch][kv head][ctx][64]
+    layer, n = cache.stride(0), cache.numel()
+    room = lambda t, *steps: qd._room("f", "t", t, f, -1, 1, True, steps)  # noqa: E731
+    for bad in (cache.transpose(2, 3), cache.transpose(1, 2), cache.transpose(3, 4), cache[:, :, :, :9], cache[:, :, :3],
+                cache[..., :32], cache[..., ::2], cache[:, :1].expand(3, 2, 4, 10, 64), cache.permute(4, 3, 2, 1, 0)):
+        with pytest.raises(ValueError, match="strides"):
+            room(bad, layer)
+    padded = torch.zeros(3, layer + 64)[:, :layer]
+    for good, step in ((cache, layer), (cache[::2], 2 * layer), (padded, layer + 64), (padded.view(3, 2, 4, 10, 64), layer + 64),
+                       (cache[:, 1:], layer), (cache[1:, :1], layer)):
+        assert room(good, step) == good.data_ptr()
+    assert qd._room("f", "t", cache[1:], f, -1, 2 * layer, True, (layer,)) == cache[1:].data_ptr()
+    with pytest.raises(ValueError, match=f"holds {n - layer} elements"):
+        qd._room("f", "t", cache[1:], f, -1, n, True, (layer,))
+    # the parts of a fused projection, whole and a head short, nodes before sequences, padded rows
+    qkv = torch.zeros(2, 5, 8, 64)
+    for good in (qkv[:, :, 4:], qkv[:, :, 4:6], qkv[:, :, 1:].transpose(0, 1), qkv.view(10, 512)[:, 128:], qkv[:, :3, 2:]):
+        assert room(good, 5 * 512, 512) == good.data_ptr()
+    for bad in (qkv[:, :, 4:].transpose(2, 3), qkv[:, :, 4:].transpose(1, 2), qkv[..., :32], qkv[:, ::2, 4:]):
+        with pytest.raises(ValueError, match="strides"):
+            room(bad, 5 * 512, 512)
+    # one column of the largest logits' indices; logits inside padded rows
+    top = torch.zeros(2, 5, 4, dtype=torch.int32)
+    assert qd._room("f", "t", top[..., 1], torch.int32, -1, 37, True, (4,)) == top[..., 1].data_ptr()
+    with pytest.raises(ValueError, match="strides"):
+        qd._room("f", "t", top[..., 0].t(), torch.int32, -1, 37, True, (4,))
+    rows = torch.zeros(6, 104)[:, :97]
+    assert room(rows, 104) == rows.data_ptr() and room(rows.view(2, 3, 97), 104) == rows.data_ptr()
+
 def test_references_on_hand_values():
     """The references themselves: a two-token softmax, ties, and a walk with a repeated child."""
     lp, h, idx, tl = logprobs_ref([0.0, np.log(3.0), -np.inf], [1, 2, 5, -1], 3)
