@@ -371,10 +371,16 @@ def _room(fn, name, t, dtype, dev, n, stepped=False, steps=()):
 
 
 def tree_plan(parent):
-    """Ancestor masks (int64 bit patterns) and depths (int32) of the tree parent[i], as CPU tensors."""
+    """Ancestor masks (int64 bit patterns) and depths (int32) of one tree, parent[i] that of node i, as
+    CPU tensors; a batch stacks those of its trees."""
     import torch
 
-    par = torch.as_tensor(parent, dtype=torch.int32, device="cpu").contiguous()
+    given = torch.as_tensor(parent, device="cpu")
+    if given.dim() != 1:
+        raise ValueError(f"qd_tree_plan: parent has {given.dim()} dimensions, one tree has one")
+    par = given.to(torch.int32).contiguous()
+    if not torch.equal(par.to(given.dtype), given):
+        raise ValueError("qd_tree_plan: the parents are not whole numbers of 32 bits")
     mask, depth = torch.empty(par.numel(), dtype=torch.int64), torch.empty(par.numel(), dtype=torch.int32)
     _check("qd_tree_plan", load().qd_tree_plan(par.data_ptr(), par.numel(), mask.data_ptr(), depth.data_ptr()))
     return mask, depth

@@ -38,6 +38,18 @@ def test_plan_refusals(lib):
     assert lib.qd_tree_plan(None, 1, 16, 16) == 1
 
 
+def test_plan_takes_one_tree(lib):
+    """Parents of several trees in rows are not one tree of all their nodes."""
+    two = [[0, 0, 1], [0, 0, 0]]
+    for bad in (two, torch.tensor(two), 0):
+        with pytest.raises(ValueError, match="one tree"):
+            qd.tree_plan(bad)
+    for bad in ([-1, 0, 0.5], [-1, 0, 2**32]):
+        with pytest.raises(ValueError, match="whole numbers"):
+            qd.tree_plan(bad)
+    mask, depth = qd.tree_plan(torch.tensor([-1, 0, 1]))
+    assert mask.tolist() == [1, 3, 7] and depth.tolist() == [0, 1, 2]
+
 def _call(fn, order, base, **change):
     return fn(*[{**base, **change}[k] for k in order])
 
