@@ -1,6 +1,9 @@
 """Tree verification on the GPU: each operator against 64-bit references, the rows and slots
 that must not matter, graphs and streams, and the four operators together against one token
 at a time."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -927,3 +930,36 @@ def test_a_tree_is_verified_as_one_token_at_a_time(qd, f16):
                 assert np.abs(k - want).max() <= 2e-3 * np.abs(want).max()
         pos = outs[3].clone()
         root = [int(t) for t in nx]
+
+
+def test_the_readme_calls_run_as_they_stand(qd):
+    """The drafted-token calls of README.md on two chains of three tokens, the second one drafted wrong."""
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        code = [c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "qd.tree_append" in c]
+    assert len(code) == 1
+    heads, kv_heads, nodes, batch, layers, vocab, max_ctx = 4, 2, 3, 2, 1, 11, 16
+    f32 = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    width = (heads + 2 * kv_heads) * HD
+    qkv = f32(batch, nodes, heads + 2 * kv_heads, HD)
+    v = dict(
+        qd=qd, torch=torch, heads=heads, kv_heads=kv_heads, nodes=nodes, batch=batch, layers=layers, vocab=vocab,
+        max_ctx=max_ctx, batch_stride=nodes * width, node_stride=width, layer_stride=batch * kv_heads * max_ctx * HD,
+        parents=[[-1, 0, 1], [-1, 0, 1]], q=qkv, k=qkv[:, :, heads:], v=qkv[:, :, heads + kv_heads:],
+        q_out=f32(batch, nodes, heads, HD), out=f32(batch, nodes, heads, HD), pos=_i32([4, 9]),
+        cos_sin=dev(_table(max_ctx, HD)), logits=f32(batch * nodes, vocab), tokens=_i32([[3, 5, 7], [3, 5, 8]]),
+        logprob=f32(batch * nodes, 1), entropy=f32(batch * nodes), top_idx=i32(batch * nodes, 4),
+        top_logprob=f32(batch * nodes, 4), path=i32(batch, nodes), accepted=i32(batch), next_token=i32(batch),
+        new_pos=i32(batch))
+    for name in ("k_drafts", "v_drafts"):
+        v[name] = f32(layers, batch, kv_heads, nodes, HD)
+        v[name[:-1]] = v[name][0]
+    for name in ("k_caches", "v_caches"):
+        v[name] = f32(layers, batch, kv_heads, max_ctx, HD)
+        v[name[:-1]] = v[name][0]
+    v["logits"][torch.arange(6), torch.tensor([5, 7, 9, 5, 7, 9])] = 20.0  # chosen after each node
+    exec(code[0], v)
+    assert v["path"].tolist() == [[0, 1, 2], [0, 1, -1]] and v["accepted"].tolist() == [3, 2]
+    assert v["next_token"].tolist() == [9, 7] and v["new_pos"].tolist() == [7, 11]
+    assert torch.equal(v["v_caches"][0, 0, :, 4:7], qkv[0, :, heads + kv_heads:].transpose(0, 1))
+    assert v["logprob"].isfinite().all() and v["out"].isfinite().all()
