@@ -393,7 +393,8 @@ qd_status qd_embed(qd_fmt fmt, const void* E, int64_t vocab, int64_t dim, const 
 /* a rejected draft leaves no trace in it.                                      */
 /* n_valid (device int32 [batch], may be NULL: n_nodes each): the number of     */
 /* nodes of each sequence; a value outside [0, n_nodes] is taken as the nearer  */
-/* of the two.  Rows of nodes behind it are not read, and not written either.   */
+/* of the two.  Rows of nodes behind it are not written, and what they hold     */
+/* does not matter (it may be read).                                            */
 /* No input may overlap an output.                                              */
 /* ------------------------------------------------------------------------- */
 #define QD_MAX_TREE 64
@@ -424,9 +425,12 @@ qd_status qd_tree_append(const float* q, const float* k, const float* v, int64_t
  * head_dim 64; n_heads % n_kv_heads == 0, group size <= 8.  A node that sees nothing gives
  * zeros, as do the nodes of a sequence with pos[b] outside [0, max_ctx].  A non-finite q
  * gives NaN in its own row alone, and what a slot holds that a node does not see, NaN and
- * infinities included, does not reach that node's row.  A key that is not finite makes the
- * rows that see it non-finite, a value that dimension of them (of an f32 cache, values from 2^100
- * and keys from 2^127 on may count as such).  The result does not depend on what the caches hold at or behind
+ * infinities included, does not reach that node's row.  A value that is not finite makes that
+ * dimension of the rows that see it non-finite, a key makes those rows NaN, or leaves them without
+ * its position where the cache is binary16 and the score -infinity (of an f32 cache, values from
+ * 2^100 and keys from 2^127 on may count as such).  Should a wait inside the kernel run out (about
+ * a second, on a GPU that is out of order), the rows that it concerns are NaN; the status, returned at
+ * the launch, is QD_OK all the same.  The result does not depend on what the caches hold at or behind
  * pos[b].  Results are the same bits on every run.
  * Arithmetic: f32 operands enter the tensor cores in parts, with an f32 cache to 2^-21 or better
  * of each value, with a binary16 one (queries and weights) to 2^-22 of each value from 2^-17 of the

@@ -512,6 +512,21 @@ def test_attn_small_weights_of_large_values_over_a_binary16_cache(qd, score, wid
     a.v[0, :, 200] = np.where(a.v[0, :, 200] < 0, -60000.0, 60000.0)
     _close(a)
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_infinite_key_of_a_binary16_cache(qd, wide):
+    """A row is NaN, or, where the score is -infinity, what it is without that position."""
+    a = _either(qd, wide, 69, 120, True)
+    a.k[0, :, 7, 9] = -np.inf
+    got = a.call()[0].cpu().numpy()
+    nan = np.isnan(got).any(-1)
+    assert np.array_equal(nan, np.isnan(got).all(-1)) and nan.any()
+    up = a.q[0, :a.n * a.hq * HD].reshape(a.n, a.hq, HD)[..., 9] < 0  # a score of +infinity
+    assert nan[up].all()
+    q = a.q[0, :a.n * a.hq * HD].reshape(a.n, a.hq, HD)
+    without = [np.delete(x, 7, axis=1) for x in (a.k[0], a.v[0])]
+    want, tol = attn_bound(q, *without, a.kd[0], a.vd[0], 119, a.anc[0], a.n, a.hq, a.hk, True)
+    assert np.all(np.abs(got - want)[~nan] <= tol[~nan])
+
 @pytest.mark.parametrize("f16", [False, True])
 @pytest.mark.parametrize("wide,pos", [(False, 40), (False, 700), (False, 9000), (True, 40), (True, 700), (True, 6000)])
 def test_attn_error_is_about_that_of_f32_arithmetic(qd, wide, pos, f16):
