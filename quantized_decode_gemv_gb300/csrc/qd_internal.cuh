@@ -18,6 +18,7 @@ constexpr uint32_t kErrPosition = 2u;  // position outside [0, max_ctx)
 constexpr uint32_t kErrTimeout = 4u;   // a bounded wait inside a kernel gave up
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 __host__ __device__ inline int64_t align16u(int64_t v) { return (v + 15) & ~(int64_t)15; }
 

@@ -490,7 +490,9 @@ qd_status qd_token_logprobs(const float* logits, int64_t row_stride, int64_t voc
   if (n_tokens && (!tokens || !logprob)) return QD_ERR_INVALID_ARG;
   if (top_k && (!top_idx || !top_logprob)) return QD_ERR_INVALID_ARG;
   if (!n_tokens && !top_k && !entropy) return QD_ERR_INVALID_ARG;  // nothing asked for
-  if (!aligned16(logits)) return QD_ERR_ALIGN;
+  if (!aligned16(logits) || (n_tokens && (!aligned4(tokens) || !aligned4(logprob))) || !aligned4(entropy) ||
+      (top_k && (!aligned4(top_idx) || !aligned4(top_logprob))))
+    return QD_ERR_ALIGN;
   // CTAs to a row: one, and more while SMs lack the four CTAs that fit and a thread would still
   // have two batches
   const int64_t chunks = (vocab + 3 + 3) / 4;  // of a row, wherever it starts

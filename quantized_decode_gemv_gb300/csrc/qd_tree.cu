@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(kCommitThreads) k_tree_commit(
 }
 
 inline bool kv_shape_ok(int head_dim) { return head_dim >= 8 && head_dim <= 1024 && head_dim % 8 == 0; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 }  // namespace qd

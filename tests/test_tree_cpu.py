@@ -107,6 +107,13 @@ def test_logprobs_refusals(lib):
         assert bad(**c) == 2, c
 
 
+def test_logprobs_refuses_small_arrays_off_their_type(lib):
+    order = "x rs v rows t nt lp h k ti tl st".split()
+    base = dict(x=G, rs=1000, v=1000, rows=3, t=G, nt=2, lp=G, h=G, k=5, ti=G, tl=G, st=None)
+    for k in "t lp h ti tl".split():
+        assert _call(lib.qd_token_logprobs, order, base, **{k: G + 2}) == 3, k
+
+
 def test_commit_refusals(lib):
     order = "t par ch cs nv n kd vd k v f16 la ls hk hd pos ctx b path na nx po st".split()
     base = dict(t=G, par=G, ch=G, cs=1, nv=None, n=8, kd=G, vd=G, k=G, v=G, f16=1, la=3, ls=2 * 2 * 32 * 64, hk=2, hd=64,
