@@ -26,18 +26,20 @@
 // workspace and a second kernel joins the parts in order.  Where the cache has room for at most
 // kWholeTiles tiles a walk, no walk is cut and there is one launch.
 //
-// What bounds it: HBM for few rows on long caches, the instructions of the softmax and of the
-// splits for many rows, latency for short caches.  Measured on one GB300 (floor: the bytes at
-// 6.77 TB/s or the products at 1946 TFLOP/s, counted once):
-//   9/3 heads, 8 nodes, 100 positions, f32              8.0 us (floor 0.03)
+// What bounds it: HBM for few rows on long caches, for many rows the latency of a tile's dependent
+// steps (1.8 of 4 instructions a cycle, the tensor pipe active 32 to 40 %), launch and a few tiles'
+// latency for short caches.  Measured on one GB300 (floor: the bytes at 6.77 TB/s or the products at
+// 1946 TFLOP/s, counted once):
+//   9/3 heads, 8 nodes, 100 positions, f32              8.2 us (floor 0.03)
 //   32/32 heads, 16 nodes, 4080 positions, f32           21 us (10.0)
 //   the same, 16 sequences of 4095, f32                 195 us (160)
 //   the same, 16 ragged sequences, binary16              53 us (40)
 //   32/8 heads, 64 nodes, 32700 positions, binary16      59 us (10)
+//   64/8 heads, 64 nodes, 8000 positions, f32            68 us (4.9)
 //   8/1 heads, 27 nodes, 5 ragged sequences, f32         18 us (0.6)
-// The unit counts, in us: kStart 3 against 5 at 4080 positions 22.3 and 24.7 (before the join of
-// today), against 2 at 32/32 heads, 64 nodes and 1000 positions f32 25 and 22.5, at 3/1 heads, 5 nodes and
-// 4000 positions binary16 7.4 and 9.0.  kMinPer 2 against 1 at 3/1 heads, 5 nodes and 16000 positions f32
+// The unit counts, in us: kStart 3 against 5 at 4080 positions 20.6 and 22.6, against 2 20.6 and 21.2, at
+// 32/32 heads, 64 nodes and 1000 positions f32 25.1 and 22.3, at 3/1 heads, 5 nodes and 4000 positions
+// binary16 7.9 and 8.9.  kMinPer 2 against 1 at 3/1 heads, 5 nodes and 16000 positions f32
 // 12.1 and 13.9, 1000 positions 9.4 and 8.4.  kWholeTiles 4 against 2 at 32 heads, 64 nodes and 100
 // positions of 260 f32 9.5 and 13.7, 200 positions 11.0 and 15.0; one head, 300 of 364 12.1 and 8.7;
 // against 8 at 9/3 heads and 370 positions 10.3 and 13.6.
@@ -826,9 +828,9 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 2) k_tree_attn_16(Tr
 // (tcgen05.mma, M = 128, q in tensor memory, K in shared memory) into tensor memory; a row's
 // threads read half of its scores each (tcgen05.ld), exchange their maxima, read the scores again
 // 16 at a time (the registers have to do for two CTAs to an SM, and the shared memory leaves
-// spills no L1) and write the weights' two parts over them as the A operand of o = p v (V as it
-// lies, [position][dim], is the transposed B operand); each adds 32 dims of the tile's o to its
-// own registers, rounded.
+// spills no L1; 36 bytes of the binary16 kernel's still spill) and write the weights' parts over
+// them as the A operand of o = p v, a third one beside them (V as it lies, [position][dim], is the
+// transposed B operand); each adds 32 dims of the tile's o to its own registers, rounded.
 // Two CTAs to an SM, one's products under the other's softmax.
 // A binary16 tile lies in the TMA's 128-byte swizzle; an f32 one is converted into 8 x 8 core
 // matrices of 128 bytes: row r, 16-byte chunk c at core_off(r, c).
@@ -1537,17 +1539,22 @@ __global__ void __launch_bounds__(kThreads) k_tree_attn_join(TreeAttnArgs a, int
       l == 0.f ? make_float2(0.f, 0.f) : make_float2(o.x / l, o.y / l);
 }
 
-// Blocks of 16 rows or of 128.  Up to 32 rows to a kv head 16 (two blocks; 58.7 us for 32 rows at
-// 4000 positions of 2 x 32 heads f32, where 128-row blocks take 65 us whatever they hold).  More
+// Blocks of 16 rows or of 128.  Up to 32 rows to a kv head 16 (two blocks; 54.9 us for 32 rows at
+// 4000 positions of 2 x 32 heads f32, where 128-row blocks take 61.7 us whatever they hold).  More
 // rows are walks by the dozen in blocks of 16, which read a head's positions once each; that fills
 // the SMs while there is little work, and a walk starts in fewer steps.  The work is counted in
 // positions of a 16-row block as the cache has room for, a start as 1000 of them.  16 against 128
 // rows, in us, one sequence:
-//   f32       8 x 64 rows, 500 positions (work 50e3)      11.5 14.6
-//             4 x 128, 2000 (98e3)                         16.5 18.0
-//             1 x 512, 8000 (290e3)                        34.0 37.4
-//             4 x 512, 2000 (392e3)                        36.0 29.4
-//             8 x 512, 8000 (2.3e6)                       191.4 69.5
+//   f32       8 x 64 rows, 500 positions (work 50e3)      12.0 13.6
+//             4 x 128, 2000 (98e3)                         15.2 15.6
+//             9 x 40, 3000, two sequences (221e3)          25.4 27.8
+//             3 x 36, 8000, three sequences (246e3)        27.3 29.9
+//             1 x 216, 3000, five ragged ones (280e3)      17.9 19.7
+//             4 x 128, 8000 (291e3)                        32.3 26.6
+//             4 x 512, 2000 (396e3)                        34.5 27.9
+//             8 x 512, 8000 (2.3e6)                       189.9 67.7
+// (on f32 caches rows that fill their blocks of 128 gain from half the bound on, those that do not
+// from above it on)
 //   binary16  8 x 64, 500 (50e3)                           10.5 14.9
 //             8 x 256, 2000 (392e3)                        19.5 23.0
 //             4 x 512, 8000 (1.16e6)                       40.5 33.3
