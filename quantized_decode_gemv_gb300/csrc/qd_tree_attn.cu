@@ -134,11 +134,6 @@ __device__ __forceinline__ float* row_of(const TreeAttnArgs& a, float* out, cons
 __host__ __device__ constexpr int part_floats(int bm) { return bm * (kHd + 2); }
 
 // ------------------------------------------------------------------ building blocks
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // 16 bytes global -> shared, or 16 zero bytes
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -478,7 +473,6 @@ __global__ void __launch_bounds__(Smem16<F16>::kWarps * 32, 2) k_tree_attn_16(Tr
 
   for (int it = 0; cur.u < end; ++it) {
     const int p0 = cur.p0, cnt = cur.cnt, nt = cur.nt;
-    const int rows = cnt * a.group;
     const bool last = cur.t == nt - 1;
     const bool more = cur.u + 1 + (last ? kStart : 0) < end;
     if (t_begin < 0) t_begin = cur.t;
