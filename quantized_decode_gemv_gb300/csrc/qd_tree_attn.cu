@@ -1198,7 +1198,8 @@ __global__ void __launch_bounds__(kThreads128, 2)
       for (int kv = 0; kv < 2; ++kv) {
         float4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = r < cur.rows ? (kv ? vraw : kraw)[i ^ turn] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 4; ++i)
+          x[i] = r < cur.rows ? (kv ? vraw : kraw)[i ^ turn] : make_float4(0.f, 0.f, 0.f, 0.f);
         if (kv && draft) {  // a row that has no bfloat16 parts, cleared as above
           uint32_t mx = max(max(abs_max(x[0]), abs_max(x[1])), max(abs_max(x[2]), abs_max(x[3])));
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
