@@ -484,6 +484,127 @@ qd_status qd_tree_commit(const int32_t* tokens, const int32_t* parent, const int
                          int32_t* next_token, int32_t* pos_out, qd_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* Paged cache in 8 bits (no counterpart on the pages: the cache of the decode   */
+/* step for many sequences that grow and end at different times).  Positions of  */
+/* a sequence live in pages of page_tokens positions, taken from a pool that all */
+/* share; keys and values are 8-bit codes, and QD_KV_BLOCK positions of a key    */
+/* head share an f32 scale: value = code * scale.  The tokens of a call are      */
+/* packed rows: sequence b has rows row_start[b] .. row_start[b + 1] - 1 (device */
+/* int32 [n_seqs + 1], ascending; rows behind row_start[n_seqs] belong to none   */
+/* and are left as they are), at positions pos[b], pos[b] + 1, ... (device int32 */
+/* [n_seqs], the positions that the sequence holds before them).  A step appends */
+/* first (qd_paged_append), then attends with the same row_start and pos         */
+/* (qd_paged_attn); qd_paged_read gives sequences back as contiguous caches, and */
+/* qd_rope_tokens rotates packed rows alone.                                     */
+/* No input may overlap an output unless stated.                                 */
+/* ------------------------------------------------------------------------- */
+#define QD_KV_BLOCK 16
+#define QD_MAX_SEQS 256
+
+/* QD_KV_I8: two's-complement codes -127..127; QD_KV_E4M3: 8-bit floats (4 exponent bits, 3 of
+ * fraction, largest 448). */
+typedef enum { QD_KV_I8 = 0, QD_KV_E4M3 = 1 } qd_kv_fmt;
+
+/* One layer's cache.  Pages: codes [n_pages][n_kv_heads][page_tokens][head_dim]; scales: f32
+ * [n_pages][n_kv_heads][page_tokens / QD_KV_BLOCK]; page_table: device int32
+ * [max_seqs][max_pages], entry (b, p / page_tokens) the page that holds position p of sequence
+ * b.  head_dim 64 or 128 (else QD_ERR_UNSUPPORTED); page_tokens a multiple of QD_KV_BLOCK, at
+ * most 1024; max_pages * page_tokens at most 2^30; 1 <= max_seqs <= QD_MAX_SEQS.  Pages and scales
+ * need no initialisation: what lies behind a sequence's end does not matter.  An entry outside
+ * [0, n_pages) is no page: nothing is stored through it, and rows that attend to or read its
+ * positions give NaN. */
+typedef struct {
+    void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    const int32_t* page_table;
+    int n_pages, page_tokens, n_kv_heads, head_dim, max_seqs, max_pages;
+    qd_kv_fmt fmt;
+} qd_paged_kv;
+
+/* Host: the rotation of pair i of the first rot_dim dimensions of a head, as the fraction of a
+ * turn per position in units of 2^-64 (turns_host[rot_dim / 2]; position times it, modulo 2^64,
+ * is exact however far the position), and what cos and sin are multiplied by.  With f_i =
+ * theta^(-2i/rot_dim) radians per position:
+ *  NONE    f_i.
+ *  LINEAR  f_i / factor (positions squeezed into the trained context).
+ *  NTK     the f_i of theta * factor^(rot_dim / (rot_dim - 2)).
+ *  TURNS   f_i (w + (1 - w) / factor), w = (r - low) / (high - low) clamped to [0, 1], r =
+ *          trained_ctx f_i / 2 pi the turns within the trained context.
+ *  PAIRS   the same with w falling from 1 to 0 over the pairs from floor(d(high)) (at least 0) to
+ *          ceil(d(low)) (at most rot_dim - 1), d(r) = rot_dim ln(trained_ctx / (2 pi r)) /
+ *          (2 ln theta); the magnitude is 0.1 ln(factor) + 1 instead of 1.
+ * rot_dim a multiple of 8, 8..1024 (QD_ERR_SHAPE); theta > 1, factor >= 1, and for TURNS and PAIRS
+ * trained_ctx >= 1 and 0 < low < high, all finite (QD_ERR_INVALID_ARG).  What a scaling does not
+ * use is not looked at. */
+typedef enum {
+    QD_ROPE_SCALE_NONE = 0,
+    QD_ROPE_SCALE_LINEAR = 1,
+    QD_ROPE_SCALE_NTK = 2,
+    QD_ROPE_SCALE_TURNS = 3,
+    QD_ROPE_SCALE_PAIRS = 4
+} qd_rope_scaling;
+qd_status qd_rope_plan(double theta, int rot_dim, qd_rope_scaling scaling, double factor, int trained_ctx, double low,
+                       double high, uint64_t* turns_host, double* magnitude_host);
+
+/* RoPE of packed rows: row t's n_heads heads (f32 [n_heads][head_dim] at x + t*x_stride) to
+ * out + t*out_stride, the first rot_dim dimensions of each rotated by position pos[t] (device
+ * int32 [n_tokens]), the others copied.  ADJACENT pairs (2i, 2i + 1), HALF (i, i + rot_dim/2).
+ * turns: device uint64 [rot_dim/2], with magnitude from qd_rope_plan (any finite magnitude).  out
+ * may be x with the same stride.  A row with pos[t] < 0 is not written.  cos and sin are the exact
+ * ones times magnitude rounded to f32, and so is each rotated value (up to 1 in 2^18 of the
+ * neighbouring f32 value).  head_dim and rot_dim multiples of 8, rot_dim <= head_dim <= 1024;
+ * strides multiples of 4, at least n_heads*head_dim; 1 <= n_tokens <= QD_MAX_GEMM_TOKENS. */
+qd_status qd_rope_tokens(const float* x, int64_t x_stride, float* out, int64_t out_stride, int n_tokens, int n_heads,
+                         int head_dim, int rot_dim, const int32_t* pos, qd_rope_pairing pairing, const uint64_t* turns,
+                         double magnitude, qd_stream_t stream);
+
+/* Append packed rows.  q, k, v: f32 rows of n_heads (n_kv_heads) heads at t*token_stride (e.g.
+ * three parts of one fused projection).  q rotated to q_out (f32 [n_tokens][n_heads][head_dim];
+ * q NULL: no queries, q_out is not looked at), k rotated, as by qd_rope_tokens, and v go to the
+ * sequence's pages.  For each block of QD_KV_BLOCK positions and head: scale = max(scale of the
+ * positions that the block held before, largest new magnitude / top), top 127 or 448; codes =
+ * value / scale to the nearest (ties away from zero for I8, to even for E4M3); where the scale
+ * grows, the codes held before become (code * old scale) / new scale to the nearest.  All of
+ * this in f32, each operation rounded once.  A block whose first position is appended starts anew,
+ * whatever its page held.  A new value that is not finite makes the scale of its block NaN,
+ * and its values with it, until the block starts anew.  A sequence with pos[b] outside [0,
+ * max_pages*page_tokens] is not touched, nor its rows of q_out; positions behind the last page are
+ * not stored (their q is rotated).  A block that is appended to may belong to one sequence only.
+ * The same call again with the same pos stores the same values.  token_stride a multiple of 4, at
+ * least the widest of the three; 1 <= n_tokens <= QD_MAX_GEMM_TOKENS, 1 <= n_seqs <= max_seqs. */
+qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k, const float* v, int64_t token_stride,
+                          float* q_out, int n_heads, int n_tokens, const int32_t* row_start, const int32_t* pos,
+                          int n_seqs, int rot_dim, qd_rope_pairing pairing, const uint64_t* turns, double magnitude,
+                          qd_stream_t stream);
+
+/* Causal attention of packed rows over the pages, the rows' own positions among them: row i of
+ * sequence b (position p = pos[b] + i) gives out = sum_j softmax_j(scale * q . k_j) v_j over
+ * j = 0 .. p, or with window > 0 over the last `window` of these.  q: f32 rows [n_heads][head_dim]
+ * at t*q_stride (a multiple of 4); out: f32 [n_tokens][n_heads][head_dim].  n_heads % n_kv_heads
+ * == 0, group size <= 16; scale finite.  The rows of a sequence with pos[b] < 0, or whose last
+ * position is behind the last page, are zeros.  The result does not depend on what pages hold behind
+ * a row's position, but for the scale of the block that holds it.  A non-finite q gives NaN in its
+ * own row and head alone; a block with a NaN scale gives NaN to the rows that see a position of it,
+ * and to no other.  Results are the same bits on every run.
+ * Arithmetic: codes enter the products exactly, queries and weights in two parts (22 bits of each
+ * value from 2^-17 of the largest of its row on, 2^-40 of that below); sums, running maxima and
+ * outputs are f32.
+ * workspace (device): qd_paged_attn_workspace bytes (0: a shape the call does not take; no fewer
+ * for more tokens or sequences); two calls that can run at the same time need one each. */
+size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs);
+qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_heads, int n_tokens,
+                        const int32_t* row_start, const int32_t* pos, int n_seqs, float scale, int window,
+                        void* workspace, size_t workspace_bytes, qd_stream_t stream);
+
+/* Positions 0 .. len[b] - 1 (device int32 [n_seqs]; at most max_ctx and what the page table holds)
+ * of each sequence as contiguous caches k_out, v_out [n_seqs][n_kv_heads][max_ctx][head_dim] of f32
+ * (code * scale, rounded once) or (out_f16 = 1) binary16 (that rounded again): the layout of
+ * qd_kv_append's caches, so that the operators over those can take a sequence over.  Behind
+ * len[b] nothing is written; positions without a page become NaN. */
+qd_status qd_paged_read(const qd_paged_kv* kv, const int32_t* len, int n_seqs, int max_ctx, void* k_out, void* v_out,
+                        int out_f16, qd_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Model and decode step ([llmoxide] 7, 11, 12; [dasLLAMA] 8.7.1.6 forward,    */
 /* 8.7.1.7; [go-llm] CPU.Forward / Reset / Pos, "Design points").             */
 /* ------------------------------------------------------------------------- */

@@ -31,7 +31,8 @@ EXPORTS = ["qd_status_str", "qd_abi_version", "qd_f16_to_f32", "qd_bf16_to_f32",
            "qd_rope_table", "qd_rope", "qd_kv_append", "qd_gqa_decode_attn_workspace", "qd_gqa_decode_attn",
            "qd_gqa_decode_attn_noalloc",
            "qd_swiglu", "qd_argmax", "qd_embed", "qd_tree_plan", "qd_tree_append", "qd_tree_attn_workspace",
-           "qd_tree_attn", "qd_token_logprobs", "qd_tree_commit", "qd_model_weight_bytes", "qd_model_state_bytes",
+           "qd_tree_attn", "qd_token_logprobs", "qd_tree_commit", "qd_rope_plan", "qd_rope_tokens", "qd_paged_append",
+           "qd_paged_attn_workspace", "qd_paged_attn", "qd_paged_read", "qd_model_weight_bytes", "qd_model_state_bytes",
            "qd_model_create", "qd_model_destroy", "qd_decode_step", "qd_prefill_workspace", "qd_prefill",
            "qd_model_reset", "qd_model_set_pos",
            "qd_model_pos", "qd_model_kv_cache", "qd_model_act_q8_buffer", "qd_model_check",
@@ -41,6 +42,10 @@ STEP_AUTO, STEP_KERNEL_CHAIN, STEP_CLUSTER = 0, 1, 2
 PREFILL_EXACT = 1
 MAX_TREE = 64
 MAX_TOP = 32
+KV_BLOCK = 16
+MAX_SEQS = 256
+KV_FMT = {"i8": 0, "e4m3": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "pairs": 4}
 
 
 class QDError(RuntimeError):
@@ -60,6 +65,13 @@ class Config(ctypes.Structure):
                 ("down_fmt", ctypes.c_int)]
 
 
+class PagedKVStruct(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("max_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("fmt", ctypes.c_int)]
+
+
 def build(force: bool = False) -> str:
     from . import builder as _b
 
@@ -75,6 +87,7 @@ def load():
         raise RuntimeError(f"libqdecode.so not built ({LIB_PATH}); run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     p, i64, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    f64 = ctypes.c_double
     sig = {
         "qd_status_str": ([i32], ctypes.c_char_p),
         "qd_abi_version": ([], i32),
@@ -113,6 +126,12 @@ def load():
         "qd_token_logprobs": ([p, i64, i64, i32, p, i32, p, p, i32, p, p, p], i32),
         "qd_tree_commit": ([p, p, p, i64, p, i32, p, p, p, p, i32, i32, i64, i32, i32, p, i32, i32, p, p, p, p, p],
                            i32),
+        "qd_rope_plan": ([f64, i32, i32, f64, i32, f64, f64, p, p], i32),
+        "qd_rope_tokens": ([p, i64, p, i64, i32, i32, i32, i32, p, i32, p, f64, p], i32),
+        "qd_paged_append": ([p, p, p, p, i64, p, i32, i32, p, p, i32, i32, i32, p, f64, p], i32),
+        "qd_paged_attn_workspace": ([p, i32, i32, i32], sz),
+        "qd_paged_attn": ([p, p, i64, p, i32, i32, p, p, i32, f32, i32, p, sz, p], i32),
+        "qd_paged_read": ([p, p, i32, i32, p, p, i32, p], i32),
         "qd_model_weight_bytes": ([ctypes.POINTER(Config)], sz),
         "qd_model_state_bytes": ([ctypes.POINTER(Config)], sz),
         "qd_model_create": ([ctypes.POINTER(Config), p, p, sz, p, sz, p, ctypes.POINTER(p)], i32),
@@ -467,6 +486,119 @@ def tree_commit(tokens, parent, chosen, chosen_stride, n_valid, n_nodes, k_draft
         _room(fn, "path", path, i32, dev, nodes),
         _room(fn, "n_accept", n_accept, i32, dev, batch), _room(fn, "next_token", next_token, i32, dev, batch),
         _room(fn, "pos_out", pos_out, i32, dev, batch), st))
+
+
+def rope_plan(theta, rot_dim, scaling="none", factor=1.0, trained_ctx=0, low=1.0, high=32.0):
+    """(turns, magnitude) of qd_rope_plan: int64 bit patterns [rot_dim / 2] as a CPU tensor, and a float."""
+    import torch
+
+    turns = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
+    magnitude = ctypes.c_double()
+    _check("qd_rope_plan", load().qd_rope_plan(theta, rot_dim, ROPE_SCALING[scaling], factor, trained_ctx, low, high,
+                                               turns.data_ptr(), ctypes.byref(magnitude)))
+    return turns, magnitude.value
+
+
+def rope_tokens(x, x_stride, out, out_stride, n_tokens, n_heads, head_dim, rot_dim, pos, pairing, turns, magnitude=1.0,
+                stream=None):
+    """RoPE of packed rows at positions pos, the first rot_dim dimensions of each head (see qdecode.h)."""
+    import torch
+
+    fn, f32, (st, dev) = "qd_rope_tokens", torch.float32, _here(stream)
+    row = n_heads * head_dim
+    _check(fn, load().qd_rope_tokens(
+        _room(fn, "x", x, f32, dev, (n_tokens - 1) * x_stride + row, True, (x_stride,)), x_stride,
+        _room(fn, "out", out, f32, dev, (n_tokens - 1) * out_stride + row, True, (out_stride,)), out_stride, n_tokens,
+        n_heads, head_dim, rot_dim, _room(fn, "pos", pos, torch.int32, dev, n_tokens), PAIRING[pairing],
+        _room(fn, "turns", turns, torch.int64, dev, rot_dim // 2), magnitude, st))
+
+
+class PagedKV:
+    """One layer's paged cache (qd_paged_kv) over the caller's tensors, which it keeps alive: codes
+    [n_pages][n_kv_heads][page_tokens][head_dim] (int8 or uint8, float8_e4m3fn too for "e4m3"), scales f32
+    [n_pages][n_kv_heads][page_tokens / 16], page_table int32 [max_seqs][max_pages]."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table, fmt="i8"):
+        import torch
+
+        kinds = (torch.int8, torch.uint8) + ((torch.float8_e4m3fn,) if fmt == "e4m3" else ())
+        if k_pages.dim() != 4 or k_scale.dim() != 3 or page_table.dim() != 2:
+            raise ValueError("PagedKV: pages have 4 dimensions, scales 3, the page table 2")
+        n, hk, tokens, hd = k_pages.shape
+        dev = k_pages.get_device()
+        for name, t, kind, shape in (("k_pages", k_pages, kinds, (n, hk, tokens, hd)),
+                                     ("v_pages", v_pages, kinds, (n, hk, tokens, hd)),
+                                     ("k_scale", k_scale, (torch.float32,), (n, hk, tokens // KV_BLOCK)),
+                                     ("v_scale", v_scale, (torch.float32,), (n, hk, tokens // KV_BLOCK)),
+                                     ("page_table", page_table, (torch.int32,), tuple(page_table.shape))):
+            if t.dtype not in kind:
+                raise ValueError(f"PagedKV: {name} has type {t.dtype}, not {' or '.join(map(str, kind))}")
+            if tuple(t.shape) != shape:
+                raise ValueError(f"PagedKV: {name} has shape {tuple(t.shape)}, not {shape}")
+            if not t.is_contiguous():
+                raise ValueError(f"PagedKV: {name} is not contiguous")
+            if t.get_device() != dev:
+                raise ValueError(f"PagedKV: {name} is on {t.device}, k_pages on {k_pages.device}")
+        self.tensors = (k_pages, v_pages, k_scale, v_scale, page_table)
+        self.device, self.n_kv_heads, self.head_dim = dev, hk, hd
+        self.max_seqs, self.max_pages = page_table.shape
+        self.struct = PagedKVStruct(*(t.data_ptr() for t in self.tensors), n, tokens, hk, hd, self.max_seqs,
+                                    self.max_pages, KV_FMT[fmt])
+        self.ptr = ctypes.addressof(self.struct)
+
+
+def _paged(fn, kv, dev):
+    if kv.device != dev:
+        raise ValueError(f"{fn}: the cache is on device {kv.device}, not on the current device")
+    return kv.ptr
+
+
+def paged_append(kv, q, k, v, token_stride, q_out, n_heads, n_tokens, row_start, pos, n_seqs, rot_dim, pairing, turns,
+                 magnitude=1.0, stream=None):
+    """Rotated queries into q_out, rotated keys and values into the pages of kv (see qdecode.h)."""
+    import torch
+
+    fn, f32, i32, (st, dev) = "qd_paged_append", torch.float32, torch.int32, _here(stream)
+    hd = kv.head_dim
+    last, qn, kn, steps = (n_tokens - 1) * token_stride, n_heads * hd, kv.n_kv_heads * hd, (token_stride,)
+    _check(fn, load().qd_paged_append(
+        _paged(fn, kv, dev), _room(fn, "q", q, f32, dev, last + qn, True, steps),
+        _room(fn, "k", k, f32, dev, last + kn, True, steps), _room(fn, "v", v, f32, dev, last + kn, True, steps),
+        token_stride, _room(fn, "q_out", q_out, f32, dev, n_tokens * qn), n_heads, n_tokens,
+        _room(fn, "row_start", row_start, i32, dev, n_seqs + 1), _room(fn, "pos", pos, i32, dev, n_seqs), n_seqs, rot_dim,
+        PAIRING[pairing], _room(fn, "turns", turns, torch.int64, dev, rot_dim // 2), magnitude, st))
+
+
+def paged_attn_workspace(kv, n_heads, n_tokens, n_seqs) -> int:
+    return int(load().qd_paged_attn_workspace(kv.ptr, n_heads, n_tokens, n_seqs))
+
+
+def paged_attn(kv, q, q_stride, out, n_heads, n_tokens, row_start, pos, n_seqs, scale, window, workspace,
+               workspace_bytes=None, stream=None):
+    """Causal attention of packed rows over the pages of kv (see qdecode.h)."""
+    import torch
+
+    fn, f32, i32, (st, dev) = "qd_paged_attn", torch.float32, torch.int32, _here(stream)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    qn = n_heads * kv.head_dim
+    _check(fn, load().qd_paged_attn(
+        _paged(fn, kv, dev), _room(fn, "q", q, f32, dev, (n_tokens - 1) * q_stride + qn, True, (q_stride,)), q_stride,
+        _room(fn, "out", out, f32, dev, n_tokens * qn), n_heads, n_tokens,
+        _room(fn, "row_start", row_start, i32, dev, n_seqs + 1), _room(fn, "pos", pos, i32, dev, n_seqs), n_seqs, scale,
+        window, _room(fn, "workspace", workspace, torch.uint8, dev, workspace_bytes), workspace_bytes, st))
+
+
+def paged_read(kv, length, n_seqs, max_ctx, k_out, v_out, out_f16=False, stream=None):
+    """Sequences of kv as contiguous f32 (binary16 with out_f16) caches (see qdecode.h)."""
+    import torch
+
+    fn, (st, dev) = "qd_paged_read", _here(stream)
+    kind = torch.float16 if out_f16 else torch.float32
+    n = n_seqs * kv.n_kv_heads * max_ctx * kv.head_dim
+    _check(fn, load().qd_paged_read(
+        _paged(fn, kv, dev), _room(fn, "len", length, torch.int32, dev, n_seqs), n_seqs, max_ctx,
+        _room(fn, "k_out", k_out, kind, dev, n), _room(fn, "v_out", v_out, kind, dev, n), 1 if out_f16 else 0, st))
 
 
 def make_config(cfg: dict, max_ctx: int, max_batch: int, tied: bool = True, kv_f16: bool | None = None,
