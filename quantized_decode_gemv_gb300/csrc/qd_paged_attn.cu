@@ -1,14 +1,31 @@
 // Causal attention of packed rows over the pages of an 8-bit cache:
 //   o = sum_j softmax_j(scale q . k_j) v_j,  k_j = code * scale of its block, over the positions
 // j = 0 .. p of a row at position p (the last `window` of them with a window).
+//
+// The rows that share a kv head (tokens x query heads of the group) walk its positions together
+// with an online softmax: s = q k^T and o += p v are matrix products with f32 accumulators.  Codes
+// of 8 bits are exact in binary16, so they enter the products as they are; a block's scale of keys
+// multiplies its scores, that of values its weights.  Outputs are f32 and meant to be as exact as f32
+// arithmetic, so queries and weights enter in two binary16 parts, hi = rn(x), lo = rn(x - hi), at a power of
+// two that puts the largest of a row (of queries; of a tile's scales for weights) at 2^14 to 2^15:
+// what is 2^-17 of that or more keeps 22 bits, what is less is 2^-40 of it off.  The matrix units
+// cut their f32 sums off instead of rounding them: a tile's products start from zero and are added
+// to o with rounded f32 additions.
 #include <algorithm>
+#include <atomic>
 
 #include "qd_paged.cuh"
+#include "qd_tc.cuh"
 
 namespace qd {
 namespace {
 
 using paged::Cache;
+
+constexpr float kBias = 14.f;  // log2 of the weights' scale
+constexpr int kStart = 3;      // what the start of a walk costs, in units
+constexpr int kMinPer = 2;     // units of a CTA at least
+constexpr int kWholeUnits = 4; // walks of at most so many units are not cut
 
 struct AttnArgs {
   Cache c;
@@ -17,58 +34,701 @@ struct AttnArgs {
   float* out;
   int n_heads, n_tokens, n_seqs, group;
   const int32_t *row_start, *pos;
-  float scale;
+  float scale;  // times log2 e: scores in log2 units
   int window;
+  int whole;     // units to a walk where no walk is cut, 0: the walks are cut evenly
+  int max_rows;  // sequences of more rows (tokens x group) are another kernel's
+  float* ws;
 };
 
+// ------------------------------------------------------------------ building blocks
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {  // 16 zero bytes if not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same from zero
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (x, y) -> two binary16 parts, hi = rn(x), lo = rn(x - hi)
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t abs_max(float4 x) {
+  return max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 .. 127
+// Exponent e of a largest magnitude (given by its bits), so that x 2^-e is in 2^14 .. 2^15 (less for
+// one under 2^-100); an infinity or NaN stays what it is.
+__device__ __forceinline__ int scale_exp(uint32_t abs_bits) {
+  return min(max((int)(abs_bits >> 23) - 127, -100), 127) - 14;
+}
+
+// Four codes -> two binary16 pairs (codes 0, 1 and 2, 3), exactly.
 template <int FMT>
-__device__ __forceinline__ float value_of(uint8_t w) {
-  if constexpr (FMT == QD_KV_I8) return (float)(int8_t)w;
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
-  return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
-}
-
-// A warp a row and head, a running maximum and sum, one position at a time.
-template <int HD, int FMT>
-__global__ void k_paged_attn(AttnArgs a) {
-  constexpr int kPer = HD / 32;
-  const int row = blockIdx.x, kvh = blockIdx.y, h = kvh * a.group + threadIdx.y, lane = threadIdx.x;
-  int before = 0;
-  for (int b = lane; b < a.n_seqs; b += 32) before += a.row_start[b] <= row;
-  before = __reduce_add_sync(0xffffffffu, before);
-  if (!before || row >= a.row_start[before]) return;
-  const int seq = before - 1;
-  int row0;
-  const int t = paged::rows_of(a.row_start, seq, a.n_tokens, row0);
-  const int p0 = a.pos[seq];
-  float o[kPer] = {}, q[kPer], m = -INFINITY, l = 0.f;
-  if (p0 >= 0 && (int64_t)p0 + t <= a.c.capacity) {
-    const int p = p0 + row - row0;
-    for (int i = 0; i < kPer; ++i) q[i] = a.q[row * a.q_stride + (int64_t)h * HD + lane * kPer + i] * a.scale;
-    for (int j = a.window > 0 ? max(p - a.window + 1, 0) : 0; j <= p; ++j) {
-      int in_page;
-      const int page = paged::page_of(a.c, seq, j / QD_KV_BLOCK, in_page);
-      const int64_t at = page < 0 ? 0 : paged::block_index(a.c, page, kvh, in_page);
-      const float nan = __uint_as_float(0x7FC00000u);
-      const float ks = page < 0 ? nan : a.c.ks[at], vs = page < 0 ? nan : a.c.vs[at];
-      const int64_t e = at * (16 * HD) + j % QD_KV_BLOCK * HD + lane * kPer;
-      float s = 0.f;
-      for (int i = 0; i < kPer; ++i) s += q[i] * value_of<FMT>(a.c.k[e + i]);
-      s = warp_sum(s) * ks;
-      const float mn = s > m || isnan(s) ? s : m, keep = expf(m - mn), w = expf(s - mn);
-      l = l * keep + w;
-      for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + w * vs * value_of<FMT>(a.c.v[e + i]);
-      m = mn;
-    }
-    for (int i = 0; i < kPer; ++i) o[i] /= l;
+__device__ __forceinline__ void to_h2x2(uint32_t w, uint32_t& h01, uint32_t& h23) {
+  if constexpr (FMT == QD_KV_I8) {
+    tc::i8x4_to_h2x2(w, h01, h23);
+  } else {
+    asm("{\n"
+        ".reg .b16 lo, hi;\n"
+        "mov.b32 {lo, hi}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n"
+        "}\n"
+        : "=r"(h01), "=r"(h23)
+        : "r"(w));
   }
-  for (int i = 0; i < kPer; ++i) a.out[((int64_t)row * a.n_heads + h) * HD + lane * kPer + i] = o[i];
 }
 
+// ------------------------------------------------------------------ plan
+// The walks of all (sequence, kv head, block of BM rows) are laid end to end in units of W tiles
+// and cut evenly over the CTAs, whatever the lengths; a walk's start counts as kStart units.
+template <int W>
+struct Plan {
+  int64_t off[QD_MAX_SEQS + 1];  // first unit of each sequence
+  int p0[QD_MAX_SEQS], t[QD_MAX_SEQS], row0[QD_MAX_SEQS];
+  int64_t sums[W];
+};
+constexpr int kNone = -2;  // p0 of a sequence whose positions are out of range: zeros
+
+struct Walk {  // of one sequence
+  int first_tile, nt, rb, len;
+};
+template <int TILE, int W, int BM>
+__device__ __forceinline__ Walk walk_of(const AttnArgs& a, int p0, int t) {
+  Walk w = {0, 0, 0, 0};
+  const int64_t rows = (int64_t)t * a.group;
+  if (t == 0 || rows > a.max_rows) return w;
+  w.rb = (int)((rows + BM - 1) / BM);
+  w.nt = 1;
+  if (p0 >= 0) {
+    w.first_tile = a.window > 0 ? max(p0 - a.window + 1, 0) / TILE : 0;
+    w.nt = ((p0 + t - 1) / TILE - w.first_tile) / W + 1;
+  }
+  w.len = a.whole ? a.whole : w.nt + kStart;
+  return w;
+}
+
+// Filled by the whole CTA of W warps.
+template <int TILE, int W, int BM>
+__device__ __forceinline__ void make_plan(const AttnArgs& a, Plan<W>* p) {
+  constexpr int kPer = QD_MAX_SEQS / (32 * W);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t mine[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = threadIdx.x * kPer + i;
+    mine[i] = 0;
+    if (b < a.n_seqs) {
+      int row0;
+      const int t = paged::rows_of(a.row_start, b, a.n_tokens, row0);
+      int p0 = a.pos[b];
+      if (p0 < 0 || (int64_t)p0 + t > a.c.capacity) p0 = kNone;
+      p->p0[b] = p0;
+      p->t[b] = t;
+      p->row0[b] = row0;
+      const Walk w = walk_of<TILE, W, BM>(a, p0, t);
+      mine[i] = (int64_t)w.len * w.rb * a.c.n_kv;
+    }
+    sum += mine[i];
+  }
+  int64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) p->sums[warp] = upto;
+  __syncthreads();
+  int64_t at = upto - sum;
+#pragma unroll
+  for (int w = 0; w < W - 1; ++w)
+    if (w < warp) at += p->sums[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    p->off[threadIdx.x * kPer + i] = at;
+    at += mine[i];
+  }
+  if (threadIdx.x == 32 * W - 1) p->off[QD_MAX_SEQS] = at;
+  __syncthreads();
+}
+
+// A CTA's place in the units: tile group t of a walk (sequence b, kv head h, block of rows r).
+template <int TILE, int W, int BM>
+struct Cursor {
+  int b, h, r, t;
+  int64_t u;
+  Walk w;
+  int p0, cnt, row0;
+  __device__ __forceinline__ void enter(const AttnArgs& a, const Plan<W>& p) {
+    p0 = p.p0[b];
+    cnt = p.t[b];
+    row0 = p.row0[b];
+    w = walk_of<TILE, W, BM>(a, p0, cnt);
+  }
+  // the first tile group at or behind unit x < off[QD_MAX_SEQS]
+  __device__ __forceinline__ void seek(const AttnArgs& a, const Plan<W>& p, int64_t x) {
+    b = 0;
+#pragma unroll
+    for (int s = QD_MAX_SEQS / 2; s > 0; s >>= 1)
+      if (p.off[b + s] <= x) b += s;
+    enter(a, p);
+    const int64_t in = x - p.off[b];
+    const int walk = (int)(in / w.len), at = (int)(in - (int64_t)walk * w.len), start = a.whole ? 0 : kStart;
+    t = max(at - start, 0);
+    u = x - at + start + t;
+    h = walk / w.rb;
+    r = walk - h * w.rb;
+  }
+  __device__ __forceinline__ void advance(const AttnArgs& a, const Plan<W>& p) {
+    ++u;
+    if (++t < w.nt) return;
+    u += a.whole ? w.len - w.nt : kStart;
+    t = 0;
+    if (++r < w.rb) return;
+    r = 0;
+    if (++h < a.c.n_kv) return;
+    h = 0;
+    do ++b;
+    while (b < QD_MAX_SEQS && p.off[b] == p.off[b + 1]);
+    if (b < QD_MAX_SEQS) enter(a, p);
+  }
+  __device__ __forceinline__ int last() const { return p0 < 0 ? -1 : p0 + cnt - 1; }  // position of the last row
+};
+
+// What a CTA leaves to the join: the walk that began in it and does not end there.
+struct Cut {
+  int parts, h, r, cnt, row0, pad[3];
+};
+__host__ __device__ constexpr int part_floats(int bm, int hd) { return bm * (hd + 2); }
+constexpr int kMaxCtas = 1024;
+constexpr size_t kCutBytes = kMaxCtas * sizeof(Cut);
+__device__ __forceinline__ float* part_of(const AttnArgs& a, int bm, int hd, int cta, int slot) {
+  return a.ws + kCutBytes / 4 + ((int64_t)cta * 2 + slot) * part_floats(bm, hd);
+}
+// Row `at` (token, head of the group) of a walk, in an array of rows with this stride.
+__device__ __forceinline__ int64_t row_of(const AttnArgs& a, int hd, int64_t stride, int row0, int h, int at) {
+  const int token = at / a.group, g = at - token * a.group;
+  return (row0 + token) * stride + (int64_t)(h * a.group + g) * hd;
+}
+
+// ------------------------------------------------------------------ few rows
+// Blocks of 8 or 16 rows, and W warps that walk the positions side by side, each with tiles and a
+// ring of its own (no barrier until the walk's end, where the warps' results are joined).  With 8
+// rows the two parts of queries and weights are rows 0-7 and 8-15 of one operand, so a product
+// serves both.  The operands' columns are free to choose as long as both sides agree: a lane's part
+// of a key row is 16 bytes as they lie (its dims of q are the same 16), that of a value row 8 or
+// 16, and its outputs are neighbouring dims; nothing is transposed through shared memory, and two
+// values of a dim are paired by byte permutations on their way to binary16.
+template <int HD, bool R16>
+struct Few {
+  static constexpr int kW = 4, kStages = 3;
+  static constexpr int kTile = HD == 64 ? 32 : 16;  // positions: 2 KB of keys, 2 KB of values
+  static constexpr int kBm = R16 ? 16 : 8, kCtas = R16 ? 2 : 3;
+  static constexpr int kRow = HD + 4;               // floats of a row of a share
+  uint4 ring[kW][kStages][2][128];
+  float scales[kW][kStages][2][kTile / 16];
+  float share[kW][kBm * kRow];
+  float ml[kW][2][kBm];
+  Plan<kW> plan;
+};
+
+template <int HD, int FMT, bool R16>
+__global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_paged_few(AttnArgs a) {
+  using S = Few<HD, R16>;
+  constexpr int W = S::kW, TILE = S::kTile, BM = S::kBm, NB = TILE / 16, NT = TILE / 8, KS = HD / 16, ND = HD / 8;
+  constexpr int NR = R16 ? 2 : 1;  // rows of a lane
+  constexpr int kLag = S::kStages - 1;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qr = lane >> 2, qc = lane & 3;
+  Cut* cut = reinterpret_cast<Cut*>(a.ws) + blockIdx.x;
+
+  pdl_trigger();
+  make_plan<TILE, W, BM>(a, &sm.plan);
+  const int64_t total = sm.plan.off[QD_MAX_SEQS];
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  per = a.whole ? (per + a.whole - 1) / a.whole * a.whole : max(per, (int64_t)kMinPer);
+  const int64_t first = (int64_t)blockIdx.x * per, end = min(first + per, total);
+  if (threadIdx.x == 0 && !a.whole) cut->parts = 0;
+  if (first >= total) return;
+  Cursor<TILE, W, BM> cur, pre;
+  cur.seek(a, sm.plan, first);
+  if (cur.u >= end) return;
+  pre = cur;
+
+  // The page of each block of this warp's tile at `pre`, asked for one step before its copies.
+  int page[NB], in_page[NB];
+  auto look = [&] {
+    if (pre.u >= end) return;
+    const int tile = pre.w.first_tile + pre.t * W + warp;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int block = tile * NB + k;
+      page[k] = -1;
+      if (block * 16 <= pre.last()) page[k] = paged::page_of(a.c, pre.b, block, in_page[k]);
+    }
+  };
+  // its copies into ring slot s, and on to the next
+  auto produce = [&](int s) {
+    if (pre.u < end) {
+      const int tile = pre.w.first_tile + pre.t * W + warp, rows = pre.last() + 1 - tile * TILE;
+      if (rows > 0) {
+        const uint32_t dst[2] = {tc::smem_u32(sm.ring[warp][s][0]), tc::smem_u32(sm.ring[warp][s][1])};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = NB == 2 ? i >> 1 : 0;
+          const int byte = 512 * i + 16 * lane, r = byte / HD, c = byte % HD / 16;  // of the tile
+          const bool live = page[k] >= 0 && r < rows;
+          const int64_t src = live ? paged::block_index(a.c, page[k], pre.h, in_page[k]) * (16 * HD) + byte - k * 16 * HD : 0;
+          // 8 rows of one chunk (keys) and every second of 8 rows (values) without a bank twice
+          const int kc = HD == 64 ? byte : r * 128 + ((c ^ (4 * (r & 1))) << 4);
+          const int vc = HD == 64 ? (r >> 1) * 128 + (((c + 4 * (r & 1)) ^ (2 * ((r >> 1) & 3))) << 4)
+                                  : r * 128 + ((c ^ (2 * ((r >> 1) & 3))) << 4);
+          cp16(dst[0] + kc, a.c.k + src, live);
+          cp16(dst[1] + vc, a.c.v + src, live);
+        }
+        if (lane < 2 * NB) {
+          const int k = lane % NB, v = lane / NB;
+          float* to = &sm.scales[warp][s][v][k];
+          int pg = page[0], ip = in_page[0];
+          if (NB == 2 && k) pg = page[NB - 1], ip = in_page[NB - 1];
+          if (k * 16 >= rows)
+            *to = 0.f;
+          else if (pg < 0)
+            *to = __uint_as_float(0x7FC00000u);
+          else
+            cp4(tc::smem_u32(to), (v ? a.c.vs : a.c.ks) + paged::block_index(a.c, pg, pre.h, ip));
+        }
+      }
+      pre.advance(a, sm.plan);
+      look();
+    }
+    cp_commit();
+  };
+  look();
+#pragma unroll
+  for (int s = 0; s < kLag; ++s) produce(s);
+
+  float o[ND][2 * NR], m[NR], l[NR], rs[NR];
+  int ev = 0, emax = -1000;  // o is in units of 2^ev
+  uint32_t qf[KS][R16 ? 8 : 4];
+  int lim[NR];               // position of the lane's row, -1: none
+  int t_begin = -1;
+  auto start_walk = [&](const Cursor<TILE, W, BM>& c) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int at = c.r * BM + qr + 8 * i;
+      const bool live = at < c.cnt * a.group;
+      lim[i] = live && c.p0 >= 0 ? c.p0 + at / a.group : -1;
+      const float4* src = reinterpret_cast<const float4*>(a.q + (live ? row_of(a, HD, a.q_stride, c.row0, c.h, at) : 0));
+      float4 x[KS];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {  // dims 64 (s / 4) + 16 qc + 4 (s % 4) ..
+        x[s] = live ? __ldcg(src + (s >> 2) * 16 + 4 * qc + (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[s].x *= a.scale;
+        x[s].y *= a.scale;
+        x[s].z *= a.scale;
+        x[s].w *= a.scale;
+        mx = max(mx, abs_max(x[s]));
+      }
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = scale_exp(mx);
+      rs[i] = pow2(e);
+      const float f = pow2(-e);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        // 8 rows: hi and lo are rows qr and qr + 8; 16: the rows of hi, then those of lo
+        split2(x[s].x * f, x[s].y * f, qf[s][R16 ? i : 0], qf[s][R16 ? 4 + i : 1]);
+        split2(x[s].z * f, x[s].w * f, qf[s][R16 ? 2 + i : 2], qf[s][R16 ? 6 + i : 3]);
+      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int e = 0; e < 2 * NR; ++e) o[d][e] = 0.f;
+    ev = 0;
+    emax = -1000;
+  };
+  start_walk(cur);
+
+  for (int it = 0; cur.u < end; ++it) {
+    const bool last = cur.t == cur.w.nt - 1;
+    if (t_begin < 0) t_begin = cur.t;
+    const int slot = it % S::kStages;
+    cp_wait<kLag - 1>();
+    __syncwarp();  // every lane's copies have landed, and the slot before this one has been read
+    produce((it + kLag) % S::kStages);
+
+    const int base = (cur.w.first_tile + cur.t * W + warp) * TILE;  // the tile's first position
+    const int top = cur.p0 + min(cur.cnt - 1, (cur.r * BM + BM - 1) / a.group);  // the block's last row's
+    const int low = cur.p0 + cur.r * BM / a.group;                               // and its first one's
+    const bool some = base <= top && cur.p0 >= 0 && !(a.window > 0 && base + TILE <= low - a.window + 1);
+    if (some) {
+      const unsigned char* kp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][0]);
+      const unsigned char* vp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][1]);
+      float ks[NB], vs[NB];
+      uint32_t vtop = 0;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        ks[k] = sm.scales[warp][slot][0][k];
+        vs[k] = sm.scales[warp][slot][1][k];
+        const uint32_t bits = abs_bits(vs[k]);
+        if (bits < 0x7F800000u) vtop = max(vtop, bits);
+      }
+      // ---- scores
+      float s[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int r = 8 * j + qr;
+        uint32_t b[KS][2];
+#pragma unroll
+        for (int x = 0; x < HD / 64; ++x) {
+          const int off = HD == 64 ? r * 64 + qc * 16 : r * 128 + (((qc + 4 * x) ^ (4 * (r & 1))) << 4);
+          const uint4 w = *reinterpret_cast<const uint4*>(kp + off);
+          to_h2x2<FMT>(w.x, b[4 * x][0], b[4 * x][1]);
+          to_h2x2<FMT>(w.y, b[4 * x + 1][0], b[4 * x + 1][1]);
+          to_h2x2<FMT>(w.z, b[4 * x + 2][0], b[4 * x + 2][1]);
+          to_h2x2<FMT>(w.w, b[4 * x + 3][0], b[4 * x + 3][1]);
+        }
+        if constexpr (R16) {
+          float lo[4];
+#pragma unroll
+          for (int x = 0; x < KS; ++x) {
+            const uint32_t fh[4] = {qf[x][0], qf[x][1], qf[x][2], qf[x][3]}, fl[4] = {qf[x][4], qf[x][5], qf[x][6], qf[x][7]};
+            if (x == 0) {
+              mma0(lo, fl, b[x][0], b[x][1]);
+              mma0(s[j], fh, b[x][0], b[x][1]);
+            } else {
+              mma(lo, fl, b[x][0], b[x][1]);
+              mma(s[j], fh, b[x][0], b[x][1]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] += lo[e];
+        } else {
+#pragma unroll
+          for (int x = 0; x < KS; ++x) {
+            const uint32_t f[4] = {qf[x][0], qf[x][1], qf[x][2], qf[x][3]};
+            if (x == 0) mma0(s[j], f, b[x][0], b[x][1]);
+            else mma(s[j], f, b[x][0], b[x][1]);
+          }
+          s[j][0] += s[j][2];
+          s[j][1] += s[j][3];
+        }
+      }
+      // ---- weights
+      const bool edge = base + TILE - 1 > low || (a.window > 0 && base <= top - a.window);
+      const int etile = min(max((int)(vtop >> 23) - 127, -100), 126);
+      emax = max(emax, etile);
+      const int en = max(etile, emax - 60);
+      const float back = pow2(max(min(ev - en, 126), -126));
+      ev = en;
+      const float down = pow2(-en);
+      float corr[NR], y[NT][2 * NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        uint32_t see = ~0u;  // bit 8 j + e: position base + 8 j + 2 qc + e
+        if (edge) {
+          const int hi = lim[i] - base, lo = a.window > 0 ? lim[i] - a.window + 1 - base : 0;  // of the tile, seen
+          see = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1;
+          if (lo > 0) see &= lo >= 32 ? 0u : ~0u << lo;
+          see >>= 2 * qc;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = s[j][2 * i + e];
+            x *= rs[i] * ks[j / 2];
+            if (edge && !(see >> (8 * j + e) & 1)) x = -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn;
+        corr[i] = ex2(m[i] - mu);
+        m[i] = mn;
+        const float bias = kBias - mu;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p = ex2(s[j][2 * i + e] + bias);
+            sum += p;
+            y[j][2 * i + e] = p * (vs[j / 2] * down);
+            if (edge && !(see >> (8 * j + e) & 1)) y[j][2 * i + e] = 0.f;  // whatever the scale
+          }
+        l[i] = fmaf(l[i], corr[i], sum);
+        corr[i] *= back;
+      }
+      // ---- products with the values
+      uint32_t ph[NB][4], pl[R16 ? NB : 1][4];
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            if constexpr (R16) split2(y[2 * k + x][2 * i], y[2 * k + x][2 * i + 1], ph[k][2 * x + i], pl[k][2 * x + i]);
+            else split2(y[2 * k + x][0], y[2 * k + x][1], ph[k][2 * x], ph[k][2 * x + 1]);
+          }
+      constexpr int kWords = HD / 32;  // of a lane's part of a value row: 4 dims each
+      uint32_t v[NB][4][kWords];
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 16 * k + 8 * (x >> 1) + 2 * qc + (x & 1);  // (r >> 1) & 3 == qc
+          if constexpr (HD == 64) {
+            const uint2 w = *reinterpret_cast<const uint2*>(
+                vp + (r >> 1) * 128 + ((((qr >> 1) + 4 * (x & 1)) ^ (2 * qc)) << 4) + 8 * (qr & 1));
+            v[k][x][0] = w.x;
+            v[k][x][1] = w.y;
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(vp + r * 128 + ((qr ^ (2 * qc)) << 4));
+            v[k][x][0] = w.x;
+            v[k][x][1] = w.y;
+            v[k][x][2] = w.z;
+            v[k][x][3] = w.w;
+          }
+        }
+#pragma unroll
+      for (int g = 0; g < kWords; ++g) {
+        uint32_t b[NB][4][2];
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t w0 = v[k][2 * x][g], w1 = v[k][2 * x + 1][g];
+            to_h2x2<FMT>(__byte_perm(w0, w1, 0x5140u), b[k][0][x], b[k][1][x]);
+            to_h2x2<FMT>(__byte_perm(w0, w1, 0x7362u), b[k][2][x], b[k][3][x]);
+          }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float t[4];
+          if constexpr (R16) {  // the low parts first: what is cut off there does not count
+            mma0(t, pl[0], b[0][x][0], b[0][x][1]);
+            if constexpr (NB == 2) mma(t, pl[NB - 1], b[NB - 1][x][0], b[NB - 1][x][1]);
+            mma(t, ph[0], b[0][x][0], b[0][x][1]);
+            if constexpr (NB == 2) mma(t, ph[NB - 1], b[NB - 1][x][0], b[NB - 1][x][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * g + x][e % (2 * NR)] = fmaf(o[4 * g + x][e % (2 * NR)], corr[(e >> 1) % NR], t[e]);
+          } else {
+            mma0(t, ph[0], b[0][x][0], b[0][x][1]);
+            if constexpr (NB == 2) mma(t, ph[NB - 1], b[NB - 1][x][0], b[NB - 1][x][1]);
+            o[4 * g + x][0] = fmaf(o[4 * g + x][0], corr[0], t[0] + t[2]);
+            o[4 * g + x][1] = fmaf(o[4 * g + x][1], corr[0], t[1] + t[3]);
+          }
+        }
+      }
+    }
+
+    // ---- the end of this CTA's part of the walk
+    const Cursor<TILE, W, BM> done = cur;
+    cur.advance(a, sm.plan);
+    if (!last && cur.u < end) continue;
+    const bool whole = t_begin == 0 && last;
+    const float unit = pow2(min(max(ev, -126), 127));
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = qr + 8 * i;
+      if (qc == 0) {
+        sm.ml[warp][0][r] = m[i];
+        sm.ml[warp][1][r] = l[i];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)  // dims HD / 4 qc + HD / 8 e ..
+#pragma unroll
+        for (int d = 0; d < ND; d += 4)
+          *reinterpret_cast<float4*>(&sm.share[warp][r * S::kRow + HD / 4 * qc + ND * e + d]) =
+              make_float4(o[d][2 * i + e] * unit, o[d + 1][2 * i + e] * unit, o[d + 2][2 * i + e] * unit,
+                          o[d + 3][2 * i + e] * unit);
+    }
+    __syncthreads();
+    const int rows = min(done.cnt * a.group - done.r * BM, BM);
+    for (int x = threadIdx.x; x < rows * (HD / 4); x += W * 32) {
+      const int r = x / (HD / 4), c = x % (HD / 4);
+      float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) mt = fmaxf(mt, sm.ml[w][0][r]);
+      float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float mw = sm.ml[w][0][r], lw = sm.ml[w][1][r];
+        const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
+        const float4 ow = *reinterpret_cast<const float4*>(&sm.share[w][r * S::kRow + 4 * c]);
+        lt = fmaf(lw, f, lt);
+        ot.x = fmaf(ow.x, f, ot.x);
+        ot.y = fmaf(ow.y, f, ot.y);
+        ot.z = fmaf(ow.z, f, ot.z);
+        ot.w = fmaf(ow.w, f, ot.w);
+      }
+      if (whole) {
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, done.row0, done.h, done.r * BM + r))[c] =
+            make_float4(ot.x * inv, ot.y * inv, ot.z * inv, ot.w * inv);
+      } else {
+        float* part = part_of(a, BM, HD, blockIdx.x, t_begin > 0 ? 0 : 1);
+        if (c == 0) {
+          part[r] = mt;
+          part[BM + r] = lt;
+        }
+        reinterpret_cast<float4*>(part + 2 * BM + r * HD)[c] = ot;
+      }
+    }
+    if (!whole && t_begin == 0 && threadIdx.x == 0) {
+      const int64_t stop = done.u - done.t + done.w.nt - 1;  // the walk's last unit
+      cut->parts = (int)(stop / per) - (int)blockIdx.x + 1;
+      cut->h = done.h;
+      cut->r = done.r;
+      cut->cnt = done.cnt;
+      cut->row0 = done.row0;
+    }
+    __syncthreads();  // every share has been read
+    t_begin = -1;
+    if (cur.u < end) start_walk(cur);
+  }
+  cp_wait<0>();
+}
+
+// The parts of a cut walk, in the CTAs' order: a block to a row of the walk that CTA blockIdx.x began.
+constexpr int kJoinThreads = 128;
+template <int HD, int BM>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
+  constexpr int kLanes = HD / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ float s_w[kMaxCtas];
+  __shared__ float s_red[kJoinThreads / 32];
+  __shared__ float4 s_o[kGroups][kLanes];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();  // in every CTA: the end of this kernel is the end of both
+  const Cut* cut = reinterpret_cast<const Cut*>(a.ws) + blockIdx.x;
+  const int n = __ldcg(&cut->parts), r = blockIdx.y;
+  if (n == 0) return;
+  const int at = __ldcg(&cut->r) * BM + r;
+  if (at >= __ldcg(&cut->cnt) * a.group) return;
+  auto part = [&](int i) { return part_of(a, BM, HD, blockIdx.x + i, i == 0 ? 1 : 0); };
+  float mx = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+    s_w[i] = __ldcg(part(i) + r);
+    mx = fmaxf(mx, s_w[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) s_red[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
+  __syncthreads();
+  float l = 0.f;
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+    const float lp = __ldcg(part(i) + BM + r);
+    s_w[i] = s_w[i] == -INFINITY ? lp : ex2(s_w[i] - mx);  // a part without a maximum has l = 0 or NaN
+    l = fmaf(lp, s_w[i], l);
+  }
+  l = warp_sum(l);
+  if (lane == 0) s_red[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[w];
+  const int g = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = g; i < n; i += kGroups) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * BM + r * HD) + c);
+    const float w = s_w[i];
+    o.x = fmaf(x.x, w, o.x);
+    o.y = fmaf(x.y, w, o.y);
+    o.z = fmaf(x.z, w, o.z);
+    o.w = fmaf(x.w, w, o.w);
+  }
+  s_o[g][c] = o;
+  __syncthreads();
+  if (g != 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) {
+    const float4 x = s_o[i][c];
+    o.x += x.x;
+    o.y += x.y;
+    o.z += x.z;
+    o.w += x.w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, __ldcg(&cut->row0), __ldcg(&cut->h), at))[c] =
+      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+// ------------------------------------------------------------------ host
 inline bool attn_shape_ok(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs) {
   return paged::cache_status(kv, n_seqs) == QD_OK && n_heads >= 1 && n_heads % kv->n_kv_heads == 0 &&
          n_heads / kv->n_kv_heads <= 16 && n_tokens >= 1 && n_tokens <= QD_MAX_GEMM_TOKENS;
+}
+inline bool rows16(int group, int n_tokens, int n_seqs) { return group > 8 || n_tokens > n_seqs; }
+
+// CTAs of a call: what fits the device at once, and no more than there can be units for.
+inline int few_ctas(const Cache& c, int tile, int w, int bm, int per_sm, int group, int n_tokens, int n_seqs) {
+  const int64_t walks = ((int64_t)n_tokens * group / bm + std::min(n_tokens, n_seqs)) * c.n_kv;
+  const int64_t most = (c.capacity + tile * w - 1) / (tile * w) + kStart;  // units of a walk
+  const int64_t ctas = std::min({(int64_t)attn_sm_count() * per_sm, (int64_t)kMaxCtas, (walks * most + kMinPer - 1) / kMinPer});
+  return (int)std::max<int64_t>(ctas, 1);
+}
+
+template <int HD, int FMT, bool R16>
+qd_status launch_few(AttnArgs a, cudaStream_t st) {
+  using S = Few<HD, R16>;
+  static std::atomic<bool> done[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QD_ERR_CUDA;
+  const auto kern = k_paged_few<HD, FMT, R16>;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S)) != cudaSuccess)
+      return QD_ERR_CUDA;
+    done[dev] = true;
+  }
+  const int most = (a.c.capacity + S::kTile * S::kW - 1) / (S::kTile * S::kW);
+  a.whole = most <= kWholeUnits ? most : 0;
+  const int ctas = few_ctas(a.c, S::kTile, S::kW, S::kBm, S::kCtas, a.group, a.n_tokens, a.n_seqs);
+  kern<<<ctas, S::kW * 32, sizeof(S), st>>>(a);
+  const qd_status s = launch_status();
+  if (s != QD_OK || a.whole) return s;
+  return launch_k(k_paged_join<HD, S::kBm>, dim3((unsigned)ctas, S::kBm), dim3(kJoinThreads), 0, st, true, a);
+}
+
+template <int HD, int FMT>
+qd_status launch_attn(const AttnArgs& a, cudaStream_t st) {
+  return rows16(a.group, a.n_tokens, a.n_seqs) ? launch_few<HD, FMT, true>(a, st) : launch_few<HD, FMT, false>(a, st);
 }
 
 }  // namespace
@@ -79,7 +739,9 @@ using namespace qd;
 extern "C" {
 
 size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs) {
-  return attn_shape_ok(kv, n_heads, n_tokens, n_seqs) ? 16 : 0;
+  if (!attn_shape_ok(kv, n_heads, n_tokens, n_seqs)) return 0;
+  const int64_t ctas = std::min(attn_sm_count() * 3, kMaxCtas);  // whatever the call: it serves them all
+  return kCutBytes + (size_t)ctas * 2 * part_floats(16, kv->head_dim) * sizeof(float);
 }
 
 qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_heads, int n_tokens,
@@ -95,18 +757,25 @@ qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride,
       (n_tokens > 1 && q_stride % 4))
     return QD_ERR_ALIGN;
   if (workspace_bytes < need) return QD_ERR_NOMEM;
-  AttnArgs a = {paged::cache_of(kv), q, q_stride, out, n_heads, n_tokens, n_seqs, n_heads / kv->n_kv_heads,
-                row_start, pos, scale, window};
-  const dim3 grid((unsigned)n_tokens, (unsigned)kv->n_kv_heads), block(32, (unsigned)a.group);
+  AttnArgs a = {};
+  a.c = paged::cache_of(kv);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.n_heads = n_heads;
+  a.n_tokens = n_tokens;
+  a.n_seqs = n_seqs;
+  a.group = n_heads / kv->n_kv_heads;
+  a.row_start = row_start;
+  a.pos = pos;
+  a.scale = scale * 1.4426950408889634f;
+  a.window = window;
+  a.max_rows = 1 << 30;
+  a.ws = static_cast<float*>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
-  if (kv->head_dim == 64) {
-    if (kv->fmt == QD_KV_I8) k_paged_attn<64, QD_KV_I8><<<grid, block, 0, st>>>(a);
-    else k_paged_attn<64, QD_KV_E4M3><<<grid, block, 0, st>>>(a);
-  } else {
-    if (kv->fmt == QD_KV_I8) k_paged_attn<128, QD_KV_I8><<<grid, block, 0, st>>>(a);
-    else k_paged_attn<128, QD_KV_E4M3><<<grid, block, 0, st>>>(a);
-  }
-  return launch_status();
+  if (kv->head_dim == 64)
+    return kv->fmt == QD_KV_I8 ? launch_attn<64, QD_KV_I8>(a, st) : launch_attn<64, QD_KV_E4M3>(a, st);
+  return kv->fmt == QD_KV_I8 ? launch_attn<128, QD_KV_I8>(a, st) : launch_attn<128, QD_KV_E4M3>(a, st);
 }
 
 }  // extern "C"
