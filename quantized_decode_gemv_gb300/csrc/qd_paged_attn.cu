@@ -45,6 +45,9 @@ struct AttnArgs {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {  // 16 zero bytes if not
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -175,11 +178,11 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, Plan<W>* p) {
   __syncthreads();
 }
 
-// A CTA's place in the units: tile group t of a walk (sequence b, kv head h, block of rows r).
+// A CTA's place in the units: tile group t of a walk (sequence b, kv head h, block of rows r), with
+// `left` units of the CTA from there on.
 template <int TILE, int W, int BM>
 struct Cursor {
-  int b, h, r, t;
-  int64_t u;
+  int b, h, r, t, left;
   Walk w;
   int p0, cnt, row0;
   __device__ __forceinline__ void enter(const AttnArgs& a, const Plan<W>& p) {
@@ -188,32 +191,30 @@ struct Cursor {
     row0 = p.row0[b];
     w = walk_of<TILE, W, BM>(a, p0, cnt);
   }
-  // the first tile group at or behind unit x < off[QD_MAX_SEQS]
-  __device__ __forceinline__ void seek(const AttnArgs& a, const Plan<W>& p, int64_t x) {
+  // the first tile group at or behind unit x < off[QD_MAX_SEQS], of n units from x on
+  __device__ __forceinline__ void seek(const AttnArgs& a, const Plan<W>& p, int64_t x, int n) {
     b = 0;
-#pragma unroll
+#pragma unroll 1
     for (int s = QD_MAX_SEQS / 2; s > 0; s >>= 1)
       if (p.off[b + s] <= x) b += s;
     enter(a, p);
     const int64_t in = x - p.off[b];
     const int walk = (int)(in / w.len), at = (int)(in - (int64_t)walk * w.len), start = a.whole ? 0 : kStart;
     t = max(at - start, 0);
-    u = x - at + start + t;
+    left = n - (start + t - at);
     h = walk / w.rb;
     r = walk - h * w.rb;
   }
-  __device__ __forceinline__ void advance(const AttnArgs& a, const Plan<W>& p) {
-    ++u;
-    if (++t < w.nt) return;
-    u += a.whole ? w.len - w.nt : kStart;
+  __device__ __forceinline__ void next_walk(const AttnArgs& a, const Plan<W>& p) {  // from its last unit
+    left -= 1 + (a.whole ? w.len - w.nt : kStart);
     t = 0;
     if (++r < w.rb) return;
     r = 0;
     if (++h < a.c.n_kv) return;
     h = 0;
     do ++b;
-    while (b < QD_MAX_SEQS && p.off[b] == p.off[b + 1]);
-    if (b < QD_MAX_SEQS) enter(a, p);
+    while (b < a.n_seqs && p.off[b] == p.off[b + 1]);
+    if (b < a.n_seqs) enter(a, p);
   }
   __device__ __forceinline__ int last() const { return p0 < 0 ? -1 : p0 + cnt - 1; }  // position of the last row
 };
@@ -276,60 +277,85 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
   if (threadIdx.x == 0 && !a.whole) cut->parts = 0;
   if (first >= total) return;
   Cursor<TILE, W, BM> cur, pre;
-  cur.seek(a, sm.plan, first);
-  if (cur.u >= end) return;
+  cur.seek(a, sm.plan, first, (int)(end - first));
+  if (cur.left <= 0) return;
   pre = cur;
 
-  // The page of each block of this warp's tile at `pre`, asked for one step before its copies.
-  int page[NB], in_page[NB];
+  // Copies of this warp's tile at `pre` into the ring, a lane 16 bytes of each 512.  The page of each
+  // of its blocks is asked for one step before.
+  const uint32_t ring = tc::smem_u32(sm.ring[warp]), scales = tc::smem_u32(sm.scales[warp]);
+  // 8 rows of one chunk (keys) and every second of 8 rows (values) without a bank twice; the pattern
+  // repeats every 8 rows
+  const uint32_t to_k = HD == 64 ? 16 * lane : (lane >> 3) * 128 + (((lane & 7) ^ (4 * (lane >> 3 & 1))) << 4);
+  const uint32_t to_v = 2048 + (HD == 64 ? (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) << 4)
+                                         : (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 4))) << 4));
+  const uint8_t *from_k = a.c.k + 16 * lane, *from_v = a.c.v + 16 * lane;
+  const float* from_s = lane < NB ? a.c.ks : a.c.vs;
+  const int per_page = a.c.page_tokens / QD_KV_BLOCK;
+  int page[NB], in_page[NB], tile, rows;  // of `pre`; rows: positions from its first one on
   auto look = [&] {
-    if (pre.u >= end) return;
-    const int tile = pre.w.first_tile + pre.t * W + warp;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const int block = tile * NB + k;
       page[k] = -1;
-      if (block * 16 <= pre.last()) page[k] = paged::page_of(a.c, pre.b, block, in_page[k]);
+      if (16 * k < rows) page[k] = paged::page_of(a.c, pre.b, tile * NB + k, in_page[k]);
     }
   };
-  // its copies into ring slot s, and on to the next
-  auto produce = [&](int s) {
-    if (pre.u < end) {
-      const int tile = pre.w.first_tile + pre.t * W + warp, rows = pre.last() + 1 - tile * TILE;
+  auto enter_pre = [&] {
+    tile = pre.w.first_tile + pre.t * W + warp;
+    rows = pre.last() + 1 - tile * TILE;
+    look();
+  };
+  auto produce = [&](uint32_t s) {  // into slot s, and on to the next
+    if (pre.left > 0) {
       if (rows > 0) {
-        const uint32_t dst[2] = {tc::smem_u32(sm.ring[warp][s][0]), tc::smem_u32(sm.ring[warp][s][1])};
+        uint32_t at[NB];
+        bool all = rows >= TILE;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = NB == 2 ? i >> 1 : 0;
-          const int byte = 512 * i + 16 * lane, r = byte / HD, c = byte % HD / 16;  // of the tile
-          const bool live = page[k] >= 0 && r < rows;
-          const int64_t src = live ? paged::block_index(a.c, page[k], pre.h, in_page[k]) * (16 * HD) + byte - k * 16 * HD : 0;
-          // 8 rows of one chunk (keys) and every second of 8 rows (values) without a bank twice
-          const int kc = HD == 64 ? byte : r * 128 + ((c ^ (4 * (r & 1))) << 4);
-          const int vc = HD == 64 ? (r >> 1) * 128 + (((c + 4 * (r & 1)) ^ (2 * ((r >> 1) & 3))) << 4)
-                                  : r * 128 + ((c ^ (2 * ((r >> 1) & 3))) << 4);
-          cp16(dst[0] + kc, a.c.k + src, live);
-          cp16(dst[1] + vc, a.c.v + src, live);
+        for (int k = 0; k < NB; ++k) {
+          at[k] = (uint32_t)((page[k] * a.c.n_kv + pre.h) * per_page + in_page[k]);
+          all &= page[k] >= 0;
         }
-        if (lane < 2 * NB) {
-          const int k = lane % NB, v = lane / NB;
-          float* to = &sm.scales[warp][s][v][k];
-          int pg = page[0], ip = in_page[0];
-          if (NB == 2 && k) pg = page[NB - 1], ip = in_page[NB - 1];
-          if (k * 16 >= rows)
-            *to = 0.f;
-          else if (pg < 0)
-            *to = __uint_as_float(0x7FC00000u);
-          else
-            cp4(tc::smem_u32(to), (v ? a.c.vs : a.c.ks) + paged::block_index(a.c, pg, pre.h, ip));
+        const uint32_t dk = ring + s * 4096 + to_k, dv = ring + s * 4096 + to_v;
+        if (all) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int64_t src = (int64_t)at[NB == 2 ? i >> 1 : 0] * (16 * HD) + 512 * (NB == 2 ? i & 1 : i);
+            cp16(dk + 512 * i, from_k + src);
+            cp16((HD == 64 ? dv : dv ^ (64 * (i & 1))) + 512 * i, from_v + src);
+          }
+          if (lane < 2 * NB) cp4(scales + (s * 2 * NB + lane) * 4, from_s + at[NB == 2 ? lane & 1 : 0]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = NB == 2 ? i >> 1 : 0;
+            const bool live = page[k] >= 0 && (512 * i + 16 * lane) / HD < rows;
+            const int64_t src = live ? (int64_t)at[k] * (16 * HD) + 512 * (NB == 2 ? i & 1 : i) : 0;
+            cp16(dk + 512 * i, from_k + src, live);
+            cp16((HD == 64 ? dv : dv ^ (64 * (i & 1))) + 512 * i, from_v + src, live);
+          }
+          if (lane < 2 * NB) {
+            const int k = NB == 2 ? lane & 1 : 0;
+            float* to = &sm.scales[warp][s][lane / NB][k];
+            if (16 * k >= rows) *to = 0.f;
+            else if (page[NB == 2 ? k : 0] < 0) *to = __uint_as_float(0x7FC00000u);
+            else cp4(tc::smem_u32(to), from_s + at[NB == 2 ? k : 0]);
+          }
         }
       }
-      pre.advance(a, sm.plan);
-      look();
+      if (pre.t + 1 < pre.w.nt) {
+        ++pre.t;
+        --pre.left;
+        tile += W;
+        rows -= W * TILE;
+        if (pre.left > 0) look();
+      } else {
+        pre.next_walk(a, sm.plan);
+        if (pre.left > 0) enter_pre();
+      }
     }
     cp_commit();
   };
-  look();
+  enter_pre();
 #pragma unroll
   for (int s = 0; s < kLag; ++s) produce(s);
 
@@ -337,8 +363,16 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
   int ev = 0, emax = -1000;  // o is in units of 2^ev
   uint32_t qf[KS][R16 ? 8 : 4];
   int lim[NR];               // position of the lane's row, -1: none
-  int t_begin = -1;
+  int t_begin, base;         // of the CTA's part of the walk; this warp's first position of the tile
+  int top, above, whole_lo, whole_hi;  // tiles with a seen position: above < base <= top; seen by every row: the others
   auto start_walk = [&](const Cursor<TILE, W, BM>& c) {
+    const int low = c.p0 + c.r * BM / a.group;  // position of the block's first row
+    top = c.p0 < 0 ? -1 : c.p0 + min(c.cnt - 1, (c.r * BM + BM - 1) / a.group);
+    above = a.window > 0 ? low - a.window + 1 - TILE : -TILE;
+    whole_lo = a.window > 0 ? top - a.window + 1 : 0;
+    whole_hi = low - TILE + 1;
+    t_begin = c.t;
+    base = (c.w.first_tile + c.t * W + warp) * TILE;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int at = c.r * BM + qr + 8 * i;
@@ -379,19 +413,12 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
   };
   start_walk(cur);
 
-  for (int it = 0; cur.u < end; ++it) {
-    const bool last = cur.t == cur.w.nt - 1;
-    if (t_begin < 0) t_begin = cur.t;
-    const int slot = it % S::kStages;
+  for (uint32_t slot = 0;; slot = slot + 1 == S::kStages ? 0 : slot + 1) {
     cp_wait<kLag - 1>();
     __syncwarp();  // every lane's copies have landed, and the slot before this one has been read
-    produce((it + kLag) % S::kStages);
+    produce(slot == 0 ? S::kStages - 1 : slot - 1);
 
-    const int base = (cur.w.first_tile + cur.t * W + warp) * TILE;  // the tile's first position
-    const int top = cur.p0 + min(cur.cnt - 1, (cur.r * BM + BM - 1) / a.group);  // the block's last row's
-    const int low = cur.p0 + cur.r * BM / a.group;                               // and its first one's
-    const bool some = base <= top && cur.p0 >= 0 && !(a.window > 0 && base + TILE <= low - a.window + 1);
-    if (some) {
+    if (base <= top && base > above) {
       const unsigned char* kp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][0]);
       const unsigned char* vp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][1]);
       float ks[NB], vs[NB];
@@ -445,7 +472,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         }
       }
       // ---- weights
-      const bool edge = base + TILE - 1 > low || (a.window > 0 && base <= top - a.window);
+      const bool edge = base > whole_hi || base < whole_lo;
       const int etile = min(max((int)(vtop >> 23) - 127, -100), 126);
       emax = max(emax, etile);
       const int en = max(etile, emax - 60);
@@ -467,11 +494,17 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float& x = s[j][2 * i + e];
-            x *= rs[i] * ks[j / 2];
-            if (edge && !(see >> (8 * j + e) & 1)) x = -INFINITY;
-            mx = fmaxf(mx, x);
+            s[j][2 * i + e] *= rs[i] * ks[j / 2];
           }
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!(see >> (8 * j + e) & 1)) s[j][2 * i + e] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn;
@@ -486,8 +519,14 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
             const float p = ex2(s[j][2 * i + e] + bias);
             sum += p;
             y[j][2 * i + e] = p * (vs[j / 2] * down);
-            if (edge && !(see >> (8 * j + e) & 1)) y[j][2 * i + e] = 0.f;  // whatever the scale
           }
+        if (edge) {  // whatever the scale
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!(see >> (8 * j + e) & 1)) y[j][2 * i + e] = 0.f;
+        }
         l[i] = fmaf(l[i], corr[i], sum);
         corr[i] *= back;
       }
@@ -554,9 +593,13 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
     }
 
     // ---- the end of this CTA's part of the walk
-    const Cursor<TILE, W, BM> done = cur;
-    cur.advance(a, sm.plan);
-    if (!last && cur.u < end) continue;
+    const bool last = cur.t + 1 == cur.w.nt;
+    if (!last && cur.left > 1) {
+      ++cur.t;
+      --cur.left;
+      base += W * TILE;
+      continue;
+    }
     const bool whole = t_begin == 0 && last;
     const float unit = pow2(min(max(ev, -126), 127));
 #pragma unroll
@@ -577,8 +620,8 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
                           o[d + 3][2 * i + e] * unit);
     }
     __syncthreads();
-    const int rows = min(done.cnt * a.group - done.r * BM, BM);
-    for (int x = threadIdx.x; x < rows * (HD / 4); x += W * 32) {
+    const int live = min(cur.cnt * a.group - cur.r * BM, BM);
+    for (int x = threadIdx.x; x < live * (HD / 4); x += W * 32) {
       const int r = x / (HD / 4), c = x % (HD / 4);
       float mt = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -597,7 +640,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       }
       if (whole) {
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, done.row0, done.h, done.r * BM + r))[c] =
+        reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, cur.row0, cur.h, cur.r * BM + r))[c] =
             make_float4(ot.x * inv, ot.y * inv, ot.z * inv, ot.w * inv);
       } else {
         float* part = part_of(a, BM, HD, blockIdx.x, t_begin > 0 ? 0 : 1);
@@ -609,16 +652,18 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       }
     }
     if (!whole && t_begin == 0 && threadIdx.x == 0) {
-      const int64_t stop = done.u - done.t + done.w.nt - 1;  // the walk's last unit
+      const int64_t stop = end - cur.left - cur.t + cur.w.nt - 1;  // the walk's last unit
       cut->parts = (int)(stop / per) - (int)blockIdx.x + 1;
-      cut->h = done.h;
-      cut->r = done.r;
-      cut->cnt = done.cnt;
-      cut->row0 = done.row0;
+      cut->h = cur.h;
+      cut->r = cur.r;
+      cut->cnt = cur.cnt;
+      cut->row0 = cur.row0;
     }
     __syncthreads();  // every share has been read
-    t_begin = -1;
-    if (cur.u < end) start_walk(cur);
+    if (!last) break;
+    cur.next_walk(a, sm.plan);
+    if (cur.left <= 0) break;
+    start_walk(cur);
   }
   cp_wait<0>();
 }
