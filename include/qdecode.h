@@ -506,7 +506,7 @@ qd_status qd_tree_commit(const int32_t* tokens, const int32_t* parent, const int
 typedef enum { QD_KV_I8 = 0, QD_KV_E4M3 = 1 } qd_kv_fmt;
 
 /* One layer's cache.  Pages: codes [n_pages][n_kv_heads][page_tokens][head_dim]; scales: f32
- * [n_pages][n_kv_heads][page_tokens / QD_KV_BLOCK]; page_table: device int32
+ * [n_pages][n_kv_heads][page_tokens / QD_KV_BLOCK], not negative; page_table: device int32
  * [max_seqs][max_pages], entry (b, p / page_tokens) the page that holds position p of sequence
  * b.  head_dim 64 or 128 (else QD_ERR_UNSUPPORTED); page_tokens a multiple of QD_KV_BLOCK, at
  * most 1024; max_pages * page_tokens at most 2^30; 1 <= max_seqs <= QD_MAX_SEQS.  Pages and scales
@@ -586,9 +586,9 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
  * a row's position, but for the scale of the block that holds it.  A non-finite q gives NaN in its
  * own row and head alone; a block with a NaN scale gives NaN to the rows that see a position of it,
  * and to no other.  Results are the same bits on every run.
- * Arithmetic: codes enter the products exactly, queries and weights in two parts (22 bits of each
- * value from 2^-17 of the largest of its row on, 2^-40 of that below); sums, running maxima and
- * outputs are f32.
+ * Arithmetic: codes enter the products exactly, queries and weights times scales in two parts (22 bits
+ * of each from 2^-15 of the largest of its row on, 2^-38 of that below; scales 2^60 times smaller than
+ * others of the row do not count); sums, running maxima and outputs are f32.
  * workspace (device): qd_paged_attn_workspace bytes (0: a shape the call does not take; no fewer
  * for more tokens or sequences); two calls that can run at the same time need one each. */
 size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs);

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(AppendArgs a) {
   const int hi = (int)min((int64_t)p0 + t - (int64_t)block * QD_KV_BLOCK, (int64_t)QD_KV_BLOCK);
   const int64_t src0 = row0 + ((int64_t)block * QD_KV_BLOCK - p0);  // row of slot 0
   int in_page;
-  const int page = paged::page_of(a.c, seq, block, in_page);
+  const int page = paged::page_of(a.c, paged::table_row(a.c, seq), block, in_page);
   if (page < 0) return;
   const int pairs = a.rows.rot.rot / 2;
   for (int i = threadIdx.x; i < (hi - lo) * pairs; i += kThreads) {
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(Cache c, const int32_t*
   const int block = unit / c.n_kv, head = unit - block * c.n_kv;
   if (block >= blocks || block * QD_KV_BLOCK >= n) return;
   int in_page;
-  const int page = paged::page_of(c, seq, block, in_page);
+  const int page = paged::page_of(c, paged::table_row(c, seq), block, in_page);
   const int64_t at = page < 0 ? 0 : paged::block_index(c, page, head, in_page);
   const bool isv = blockIdx.y;
   const float scale = page < 0 ? __uint_as_float(0x7FC00000u) : (isv ? c.vs : c.ks)[at];

@@ -13,8 +13,9 @@ struct Cache {
   uint8_t *k, *v;
   float *ks, *vs;
   const int32_t* table;
-  int n_pages, page_tokens, page_shift;  // page_shift: log2 of a power of two, -1 otherwise
-  int n_kv, max_pages, capacity;         // capacity: positions of a sequence
+  int n_pages, page_tokens, per_page;  // per_page: blocks
+  uint32_t per_magic;                  // 2^32 / per_page rounded up (0 for one block)
+  int n_kv, max_pages, capacity;       // capacity: positions of a sequence
 };
 
 inline Cache cache_of(const qd_paged_kv* kv) {
@@ -26,10 +27,8 @@ inline Cache cache_of(const qd_paged_kv* kv) {
   c.table = kv->page_table;
   c.n_pages = kv->n_pages;
   c.page_tokens = kv->page_tokens;
-  c.page_shift = -1;
-  if ((kv->page_tokens & (kv->page_tokens - 1)) == 0)
-    for (c.page_shift = 0; (1 << c.page_shift) < kv->page_tokens; ++c.page_shift) {
-    }
+  c.per_page = kv->page_tokens / QD_KV_BLOCK;
+  c.per_magic = c.per_page == 1 ? 0u : (uint32_t)(((1ull << 32) + c.per_page - 1) / c.per_page);
   c.n_kv = kv->n_kv_heads;
   c.max_pages = kv->max_pages;
   c.capacity = kv->max_pages * kv->page_tokens;
@@ -53,24 +52,19 @@ inline qd_status cache_status(const qd_paged_kv* kv, int n_seqs) {
   return QD_OK;
 }
 
-// The page of sequence b's block (of QD_KV_BLOCK positions), -1 if there is none, and the block's
-// place in it.
-__device__ __forceinline__ int page_of(const Cache& c, int b, int block, int& in_page) {
-  int at;
-  if (c.page_shift >= 0) {
-    at = block >> (c.page_shift - 4);
-    in_page = block - (at << (c.page_shift - 4));
-  } else {
-    const int per = c.page_tokens / QD_KV_BLOCK;
-    at = block / per;
-    in_page = block - at * per;
-  }
-  const int page = __ldg(c.table + (int64_t)b * c.max_pages + at);
+// The page of a block (of QD_KV_BLOCK positions) in a sequence's row of the table, -1 if there is
+// none, and the block's place in it.  block / per_page by a multiplication: with at most 2^26 blocks and
+// 64 to a page, block (ceil(2^32 / per) / 2^32 - 1 / per) < 2^-6 <= 1 / per, so the floor is the quotient.
+__device__ __forceinline__ int page_of(const Cache& c, const int32_t* row, int block, int& in_page) {
+  const int at = c.per_magic ? (int)__umulhi((uint32_t)block, c.per_magic) : block;
+  in_page = block - at * c.per_page;
+  const int page = __ldg(row + at);
   return (unsigned)page < (unsigned)c.n_pages ? page : -1;
 }
+__device__ __forceinline__ const int32_t* table_row(const Cache& c, int b) { return c.table + (int64_t)b * c.max_pages; }
 // Scale index of (page, head, block in the page); times 16 * head_dim: its first code.
 __device__ __forceinline__ int64_t block_index(const Cache& c, int page, int head, int in_page) {
-  return ((int64_t)page * c.n_kv + head) * (c.page_tokens / QD_KV_BLOCK) + in_page;
+  return ((int64_t)page * c.n_kv + head) * c.per_page + in_page;
 }
 
 // Rows of sequence b, whatever row_start holds: [first, first + count) within [0, n_tokens).

@@ -7,8 +7,8 @@
 // of 8 bits are exact in binary16, so they enter the products as they are; a block's scale of keys
 // multiplies its scores, that of values its weights.  Outputs are f32 and meant to be as exact as f32
 // arithmetic, so queries and weights enter in two binary16 parts, hi = rn(x), lo = rn(x - hi), at a power of
-// two that puts the largest of a row (of queries; of a tile's scales for weights) at 2^14 to 2^15:
-// what is 2^-17 of that or more keeps 22 bits, what is less is 2^-40 of it off.  The matrix units
+// two that puts the largest of a row of queries at 2^14 to 2^15 and the largest weight times scale at
+// 2^12 to 2^15: what is 2^-15 of that or more keeps 22 bits, what is less is 2^-38 of it off.  The matrix units
 // cut their f32 sums off instead of rounding them: a tile's products start from zero and are added
 // to o with rounded f32 additions.
 #include <algorithm>
@@ -45,11 +45,19 @@ struct AttnArgs {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {  // 16 zero bytes if not
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+template <int TO, int FROM>
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.u32 p, %2, 0;\n"
+      "@p cp.async.ca.shared.global [%0], [%1], 4;\n"
+      "}\n" ::"r"(dst),
+      "l"(src), "r"((uint32_t)live)
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -250,7 +258,7 @@ struct Few {
   static constexpr int kBm = R16 ? 16 : 8, kCtas = R16 ? 2 : 3;
   static constexpr int kRow = HD + 4;               // floats of a row of a share
   uint4 ring[kW][kStages][2][128];
-  float scales[kW][kStages][2][kTile / 16];
+  __align__(16) float scales[kW][kStages][2][kTile / 16];
   float share[kW][kBm * kRow];
   float ml[kW][2][kBm];
   Plan<kW> plan;
@@ -259,7 +267,7 @@ struct Few {
 template <int HD, int FMT, bool R16>
 __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_paged_few(AttnArgs a) {
   using S = Few<HD, R16>;
-  constexpr int W = S::kW, TILE = S::kTile, BM = S::kBm, NB = TILE / 16, NT = TILE / 8, KS = HD / 16, ND = HD / 8;
+  constexpr int W = S::kW, TILE = S::kTile, BM = S::kBm, NB = TILE / 16, NT = TILE / 8, KS = HD / 16, MT = HD / 16;
   constexpr int NR = R16 ? 2 : 1;  // rows of a lane
   constexpr int kLag = S::kStages - 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -291,76 +299,81 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
                                          : (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 4))) << 4));
   const uint8_t *from_k = a.c.k + 16 * lane, *from_v = a.c.v + 16 * lane;
   const float* from_s = lane < NB ? a.c.ks : a.c.vs;
-  const int per_page = a.c.page_tokens / QD_KV_BLOCK;
-  int page[NB], in_page[NB], tile, rows;  // of `pre`; rows: positions from its first one on
+  const bool scale_lane = lane < 2 * NB, second = NB == 2 && (lane & 1);
+  const int32_t* table;     // the row of the sequence
+  int tile, rows, clamp;    // of `pre`; positions from the tile's first one on; the sequence's last block
+  int page[NB], in_page[NB];
   auto look = [&] {
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      page[k] = -1;
-      if (16 * k < rows) page[k] = paged::page_of(a.c, pre.b, tile * NB + k, in_page[k]);
-    }
+    for (int k = 0; k < NB; ++k) page[k] = paged::page_of(a.c, table, min(tile * NB + k, clamp), in_page[k]);
   };
   auto enter_pre = [&] {
+    table = paged::table_row(a.c, pre.b);
     tile = pre.w.first_tile + pre.t * W + warp;
     rows = pre.last() + 1 - tile * TILE;
-    look();
+    clamp = max(pre.last(), 0) / QD_KV_BLOCK;
   };
   auto produce = [&](uint32_t s) {  // into slot s, and on to the next
     if (pre.left > 0) {
-      if (rows > 0) {
-        uint32_t at[NB];
-        bool all = rows >= TILE;
+      uint32_t at[NB];
+      bool all = rows >= TILE;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          at[k] = (uint32_t)((page[k] * a.c.n_kv + pre.h) * per_page + in_page[k]);
-          all &= page[k] >= 0;
+      for (int k = 0; k < NB; ++k) {
+        at[k] = (uint32_t)((page[k] * a.c.n_kv + pre.h) * a.c.per_page + in_page[k]);
+        all &= page[k] >= 0;
+      }
+      const uint32_t dk = ring + s * 4096 + to_k, dv = ring + s * 4096 + to_v, dw = HD == 64 ? dv : dv ^ 64;
+      const uint8_t *k0 = from_k + (uint64_t)at[0] * (16 * HD), *v0 = from_v + (uint64_t)at[0] * (16 * HD);
+      const uint8_t *k1 = NB == 2 ? from_k + (uint64_t)at[NB - 1] * (16 * HD) : k0;
+      const uint8_t *v1 = NB == 2 ? from_v + (uint64_t)at[NB - 1] * (16 * HD) : v0;
+      const uint32_t mine = second ? at[NB - 1] : at[0];  // the block of the lane's scale
+      const uint32_t ds = scales + (s * 2 * NB + lane) * 4;
+      constexpr int kTo = NB == 2 ? 0 : 1024;  // where the second address goes on
+      if (all) {
+        cp16<0, 0>(dk, k0);
+        cp16<512, 512>(dk, k0);
+        cp16<1024, kTo>(dk, k1);
+        cp16<1536, kTo + 512>(dk, k1);
+        cp16<0, 0>(dv, v0);
+        cp16<512, 512>(dw, v0);
+        cp16<1024, kTo>(dv, v1);
+        cp16<1536, kTo + 512>(dw, v1);
+        cp4(ds, from_s + mine, scale_lane);
+      } else if (rows > 0) {  // the sequence's last tile, or a block without a page
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = NB == 2 ? i >> 1 : 0;
+          const bool live = page[k] >= 0 && (512 * i + 16 * lane) / HD < rows;
+          const int from = NB == 2 ? 512 * (i & 1) : 512 * i;
+          cp16(dk + 512 * i, live ? (k ? k1 : k0) + from : a.c.k, live);
+          cp16((i & 1 ? dw : dv) + 512 * i, live ? (k ? v1 : v0) + from : a.c.v, live);
         }
-        const uint32_t dk = ring + s * 4096 + to_k, dv = ring + s * 4096 + to_v;
-        if (all) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int64_t src = (int64_t)at[NB == 2 ? i >> 1 : 0] * (16 * HD) + 512 * (NB == 2 ? i & 1 : i);
-            cp16(dk + 512 * i, from_k + src);
-            cp16((HD == 64 ? dv : dv ^ (64 * (i & 1))) + 512 * i, from_v + src);
-          }
-          if (lane < 2 * NB) cp4(scales + (s * 2 * NB + lane) * 4, from_s + at[NB == 2 ? lane & 1 : 0]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = NB == 2 ? i >> 1 : 0;
-            const bool live = page[k] >= 0 && (512 * i + 16 * lane) / HD < rows;
-            const int64_t src = live ? (int64_t)at[k] * (16 * HD) + 512 * (NB == 2 ? i & 1 : i) : 0;
-            cp16(dk + 512 * i, from_k + src, live);
-            cp16((HD == 64 ? dv : dv ^ (64 * (i & 1))) + 512 * i, from_v + src, live);
-          }
-          if (lane < 2 * NB) {
-            const int k = NB == 2 ? lane & 1 : 0;
-            float* to = &sm.scales[warp][s][lane / NB][k];
-            if (16 * k >= rows) *to = 0.f;
-            else if (page[NB == 2 ? k : 0] < 0) *to = __uint_as_float(0x7FC00000u);
-            else cp4(tc::smem_u32(to), from_s + at[NB == 2 ? k : 0]);
-          }
-        }
+        const bool none = (second ? 16 : 0) >= rows, lost = (second ? page[NB - 1] : page[0]) < 0;
+        cp4(ds, from_s + (none || lost ? 0 : mine), scale_lane && !none && !lost);
+        if (scale_lane && (none || lost)) (&sm.scales[warp][s][0][0])[lane] = none ? 0.f : __uint_as_float(0x7FC00000u);
       }
       if (pre.t + 1 < pre.w.nt) {
         ++pre.t;
         --pre.left;
         tile += W;
         rows -= W * TILE;
-        if (pre.left > 0) look();
       } else {
         pre.next_walk(a, sm.plan);
         if (pre.left > 0) enter_pre();
       }
+      look();
     }
     cp_commit();
   };
   enter_pre();
+  look();
 #pragma unroll
   for (int s = 0; s < kLag; ++s) produce(s);
 
-  float o[ND][2 * NR], m[NR], l[NR], rs[NR];
-  int ev = 0, emax = -1000;  // o is in units of 2^ev
+  float o[MT][NR][4];  // dims HD / 8 qr + 2 i (elements 0, 1), + 1 (2, 3) of rows 8 n + 2 qc, + 1
+  float m[NR], l[NR], rs[NR];  // of rows qr + 8 i
+  int ev = 0, emax = -1000;
+  float down = 1.f;  // 2^-ev
   uint32_t qf[KS][R16 ? 8 : 4];
   int lim[NR];               // position of the lane's row, -1: none
   int t_begin, base;         // of the CTA's part of the walk; this warp's first position of the tile
@@ -405,11 +418,14 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       l[i] = 0.f;
     }
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < MT; ++d)
 #pragma unroll
-      for (int e = 0; e < 2 * NR; ++e) o[d][e] = 0.f;
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][n][e] = 0.f;
     ev = 0;
     emax = -1000;
+    down = 1.f;
   };
   start_walk(cur);
 
@@ -422,13 +438,12 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       const unsigned char* kp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][0]);
       const unsigned char* vp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][1]);
       float ks[NB], vs[NB];
-      uint32_t vtop = 0;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        ks[k] = sm.scales[warp][slot][0][k];
-        vs[k] = sm.scales[warp][slot][1][k];
-        const uint32_t bits = abs_bits(vs[k]);
-        if (bits < 0x7F800000u) vtop = max(vtop, bits);
+      if constexpr (NB == 2) {
+        const float4 x = *reinterpret_cast<const float4*>(sm.scales[warp][slot]);
+        ks[0] = x.x, ks[NB - 1] = x.y, vs[0] = x.z, vs[NB - 1] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(sm.scales[warp][slot]);
+        ks[0] = x.x, vs[0] = x.y;
       }
       // ---- scores
       float s[NT][4];
@@ -473,12 +488,18 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       }
       // ---- weights
       const bool edge = base > whole_hi || base < whole_lo;
-      const int etile = min(max((int)(vtop >> 23) - 127, -100), 126);
-      emax = max(emax, etile);
-      const int en = max(etile, emax - 60);
-      const float back = pow2(max(min(ev - en, 126), -126));
-      ev = en;
-      const float down = pow2(-en);
+      // o is in units of 2^ev, so that the tile's scales are 2^-2 to 2 of them: another unit where they are
+      // not, at least 2^-60 of the largest (a NaN does not count: there are rows that do not see it)
+      float back = 1.f;
+      const float vtop = NB == 2 ? fmaxf(fabsf(vs[0]), fabsf(vs[NB - 1])) : fabsf(vs[0]);
+      if (!(vtop * down < 2.f && vtop * down >= 0.25f)) {
+        const int etile = vtop <= 3e38f ? max((int)(__float_as_uint(vtop) >> 23) - 127, -100) : -100;
+        emax = max(emax, etile);
+        const int en = min(max(etile, emax - 60), 126);
+        back = pow2(max(min(ev - en, 126), -126));
+        ev = en;
+        down = pow2(-en);
+      }
       float corr[NR], y[NT][2 * NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
@@ -489,22 +510,22 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
           if (lo > 0) see &= lo >= 32 ? 0u : ~0u << lo;
           see >>= 2 * qc;
         }
-        float mx = -INFINITY;
+        float f[NB];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[j][2 * i + e] *= rs[i] * ks[j / 2];
-          }
+        for (int k = 0; k < NB; ++k) f[k] = rs[i] * ks[k];
         if (edge) {
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (!(see >> (8 * j + e) & 1)) s[j][2 * i + e] = -INFINITY;
-        }
+              s[j][2 * i + e] = see >> (8 * j + e) & 1 ? s[j][2 * i + e] * f[j / 2] : -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
+          for (int k = 0; k < NB; ++k) f[k] = 1.f;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NB; ++k)  // scales are not negative
+          mx = fmaxf(mx, f[k] * fmaxf(fmaxf(s[2 * k][2 * i], s[2 * k][2 * i + 1]), fmaxf(s[2 * k + 1][2 * i], s[2 * k + 1][2 * i + 1])));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn;
@@ -516,7 +537,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float p = ex2(s[j][2 * i + e] + bias);
+            const float p = ex2(fmaf(s[j][2 * i + e], f[j / 2], bias));
             sum += p;
             y[j][2 * i + e] = p * (vs[j / 2] * down);
           }
@@ -531,16 +552,18 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         corr[i] *= back;
       }
       // ---- products with the values
-      uint32_t ph[NB][4], pl[R16 ? NB : 1][4];
+      // transposed, o^T = v^T p^T: a lane's scores are columns of p^T as they stand
+      uint32_t ph[NR][NB][2], pl[NR][NB][2];
+      float keep[NR][2];  // of rows 8 n + 2 qc, + 1
 #pragma unroll
-      for (int k = 0; k < NB; ++k)
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int k = 0; k < NB; ++k)
 #pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            if constexpr (R16) split2(y[2 * k + x][2 * i], y[2 * k + x][2 * i + 1], ph[k][2 * x + i], pl[k][2 * x + i]);
-            else split2(y[2 * k + x][0], y[2 * k + x][1], ph[k][2 * x], ph[k][2 * x + 1]);
-          }
+          for (int x = 0; x < 2; ++x) split2(y[2 * k + x][2 * n], y[2 * k + x][2 * n + 1], ph[n][k][x], pl[n][k][x]);
+        keep[n][0] = __shfl_sync(0xffffffffu, corr[n], 8 * qc);
+        keep[n][1] = __shfl_sync(0xffffffffu, corr[n], 8 * qc + 4);
+      }
       constexpr int kWords = HD / 32;  // of a lane's part of a value row: 4 dims each
       uint32_t v[NB][4][kWords];
 #pragma unroll
@@ -563,32 +586,27 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         }
 #pragma unroll
       for (int g = 0; g < kWords; ++g) {
-        uint32_t b[NB][4][2];
+        uint32_t x[2][NB][4];  // dims 4 g + 2 i, + 1
 #pragma unroll
         for (int k = 0; k < NB; ++k)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t w0 = v[k][2 * x][g], w1 = v[k][2 * x + 1][g];
-            to_h2x2<FMT>(__byte_perm(w0, w1, 0x5140u), b[k][0][x], b[k][1][x]);
-            to_h2x2<FMT>(__byte_perm(w0, w1, 0x7362u), b[k][2][x], b[k][3][x]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w0 = v[k][2 * h][g], w1 = v[k][2 * h + 1][g];
+            to_h2x2<FMT>(__byte_perm(w0, w1, 0x5140u), x[0][k][2 * h], x[0][k][2 * h + 1]);
+            to_h2x2<FMT>(__byte_perm(w0, w1, 0x7362u), x[1][k][2 * h], x[1][k][2 * h + 1]);
           }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          float t[4];
-          if constexpr (R16) {  // the low parts first: what is cut off there does not count
-            mma0(t, pl[0], b[0][x][0], b[0][x][1]);
-            if constexpr (NB == 2) mma(t, pl[NB - 1], b[NB - 1][x][0], b[NB - 1][x][1]);
-            mma(t, ph[0], b[0][x][0], b[0][x][1]);
-            if constexpr (NB == 2) mma(t, ph[NB - 1], b[NB - 1][x][0], b[NB - 1][x][1]);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[4 * g + x][e % (2 * NR)] = fmaf(o[4 * g + x][e % (2 * NR)], corr[(e >> 1) % NR], t[e]);
-          } else {
-            mma0(t, ph[0], b[0][x][0], b[0][x][1]);
-            if constexpr (NB == 2) mma(t, ph[NB - 1], b[NB - 1][x][0], b[NB - 1][x][1]);
-            o[4 * g + x][0] = fmaf(o[4 * g + x][0], corr[0], t[0] + t[2]);
-            o[4 * g + x][1] = fmaf(o[4 * g + x][1], corr[0], t[1] + t[3]);
+          for (int n = 0; n < NR; ++n) {
+            float t[4];  // the low parts first: what is cut off there does not count
+            mma0(t, x[i][0], pl[n][0][0], pl[n][0][1]);
+            if constexpr (NB == 2) mma(t, x[i][NB - 1], pl[n][NB - 1][0], pl[n][NB - 1][1]);
+            mma(t, x[i][0], ph[n][0][0], ph[n][0][1]);
+            if constexpr (NB == 2) mma(t, x[i][NB - 1], ph[n][NB - 1][0], ph[n][NB - 1][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[2 * g + i][n][e] = fmaf(o[2 * g + i][n][e], keep[n][e & 1], t[e]);
           }
-        }
       }
     }
 
@@ -612,12 +630,11 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         sm.ml[warp][1][r] = l[i];
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e)  // dims HD / 4 qc + HD / 8 e ..
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int d = 0; d < ND; d += 4)
-          *reinterpret_cast<float4*>(&sm.share[warp][r * S::kRow + HD / 4 * qc + ND * e + d]) =
-              make_float4(o[d][2 * i + e] * unit, o[d + 1][2 * i + e] * unit, o[d + 2][2 * i + e] * unit,
-                          o[d + 3][2 * i + e] * unit);
+        for (int d = 0; d < MT; d += 2)
+          *reinterpret_cast<float4*>(&sm.share[warp][(8 * i + 2 * qc + e) * S::kRow + HD / 8 * qr + 2 * d]) =
+              make_float4(o[d][i][e] * unit, o[d][i][2 + e] * unit, o[d + 1][i][e] * unit, o[d + 1][i][2 + e] * unit);
     }
     __syncthreads();
     const int live = min(cur.cnt * a.group - cur.r * BM, BM);

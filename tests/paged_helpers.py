@@ -153,7 +153,7 @@ def attn_ref(q, ck, sk, cv, sv, p, scale, window):
     row's largest, and hd + 8 f32 additions and products: (hd + 16) 2^-24 of sum |q k|; exp2 and the
     weight's parts and scales add 16 * 2^-24.  The sums over n positions (at most n / 16 + 64 additions one
     after the other) and the products' own 8 half steps add (n / 16 + 72) 2^-24 of sum w |v| and of |o|;
-    weights end 2^-40 below the largest w * scale of the row."""
+    weights end 2^-38 below the largest w * scale of the row (a unit that its scales may stay 2^-2 below)."""
     lo = max(0, p - window + 1) if window else 0
     ck, sk, cv, sv = ck[lo : p + 1], sk[lo : p + 1], cv[lo : p + 1], sv[lo : p + 1]
     q, hd = q.astype(np.float64), ck.shape[1]
@@ -166,7 +166,7 @@ def attn_ref(q, ck, sk, cv, sv, p, scale, window):
     end_q = 2.0**-39 * np.abs(q).max() * np.abs(ck).sum(1) * sk * abs(scale)
     rel = (hd + 16) * U * size + end_q + 16 * U
     tol = (w * rel) @ (np.abs(v) + np.abs(o)) + (len(w) / 16 + 72) * U * (w @ np.abs(v) + np.abs(o))
-    return o, tol + 2.0**-39 * (w * sv).max() * np.abs(cv).sum(0)
+    return o, tol + 2.0**-37 * (w * sv).max() * np.abs(cv).sum(0)
 
 
 def attn_all(cache, q, row_start, pos, group, scale, window):
