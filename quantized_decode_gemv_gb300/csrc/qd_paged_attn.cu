@@ -13,6 +13,7 @@
 // to o with rounded f32 additions.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "qd_paged.cuh"
 #include "qd_tc.cuh"
@@ -23,7 +24,7 @@ namespace {
 using paged::Cache;
 
 constexpr float kBias = 14.f;  // log2 of the weights' scale
-constexpr int kStart = 3;      // what the start of a walk costs, in units
+constexpr int kStart = 1;      // what the start of a walk costs, in units
 constexpr int kMinPer = 2;     // units of a CTA at least
 constexpr int kWholeUnits = 4; // walks of at most so many units are not cut
 
@@ -119,10 +120,15 @@ __device__ __forceinline__ void to_h2x2(uint32_t w, uint32_t& h01, uint32_t& h23
 template <int W>
 struct Plan {
   int64_t off[QD_MAX_SEQS + 1];  // first unit of each sequence
-  int p0[QD_MAX_SEQS], t[QD_MAX_SEQS], row0[QD_MAX_SEQS];
   int64_t sums[W];
 };
-constexpr int kNone = -2;  // p0 of a sequence whose positions are out of range: zeros
+// A sequence's tokens, the first one's row and position: -2 where the positions are out of range (zeros).
+__device__ __forceinline__ int tokens_of(const AttnArgs& a, int b, int& row0, int& p0) {
+  const int t = paged::rows_of(a.row_start, b, a.n_tokens, row0);
+  p0 = a.pos[b];
+  if (p0 < 0 || (int64_t)p0 + t > a.c.capacity) p0 = -2;
+  return t;
+}
 
 struct Walk {  // of one sequence
   int first_tile, nt, rb, len;
@@ -153,13 +159,8 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, Plan<W>* p) {
     const int b = threadIdx.x * kPer + i;
     mine[i] = 0;
     if (b < a.n_seqs) {
-      int row0;
-      const int t = paged::rows_of(a.row_start, b, a.n_tokens, row0);
-      int p0 = a.pos[b];
-      if (p0 < 0 || (int64_t)p0 + t > a.c.capacity) p0 = kNone;
-      p->p0[b] = p0;
-      p->t[b] = t;
-      p->row0[b] = row0;
+      int row0, p0;
+      const int t = tokens_of(a, b, row0, p0);
       const Walk w = walk_of<TILE, W, BM>(a, p0, t);
       mine[i] = (int64_t)w.len * w.rb * a.c.n_kv;
     }
@@ -193,10 +194,8 @@ struct Cursor {
   int b, h, r, t, left;
   Walk w;
   int p0, cnt, row0;
-  __device__ __forceinline__ void enter(const AttnArgs& a, const Plan<W>& p) {
-    p0 = p.p0[b];
-    cnt = p.t[b];
-    row0 = p.row0[b];
+  __device__ __forceinline__ void enter(const AttnArgs& a) {
+    cnt = tokens_of(a, b, row0, p0);
     w = walk_of<TILE, W, BM>(a, p0, cnt);
   }
   // the first tile group at or behind unit x < off[QD_MAX_SEQS], of n units from x on
@@ -205,7 +204,7 @@ struct Cursor {
 #pragma unroll 1
     for (int s = QD_MAX_SEQS / 2; s > 0; s >>= 1)
       if (p.off[b + s] <= x) b += s;
-    enter(a, p);
+    enter(a);
     const int64_t in = x - p.off[b];
     const int walk = (int)(in / w.len), at = (int)(in - (int64_t)walk * w.len), start = a.whole ? 0 : kStart;
     t = max(at - start, 0);
@@ -222,7 +221,7 @@ struct Cursor {
     h = 0;
     do ++b;
     while (b < a.n_seqs && p.off[b] == p.off[b + 1]);
-    if (b < a.n_seqs) enter(a, p);
+    if (b < a.n_seqs) enter(a);
   }
   __device__ __forceinline__ int last() const { return p0 < 0 ? -1 : p0 + cnt - 1; }  // position of the last row
 };
@@ -253,13 +252,12 @@ __device__ __forceinline__ int64_t row_of(const AttnArgs& a, int hd, int64_t str
 // values of a dim are paired by byte permutations on their way to binary16.
 template <int HD, bool R16>
 struct Few {
-  static constexpr int kW = 4, kStages = 3;
-  static constexpr int kTile = HD == 64 ? 32 : 16;  // positions: 2 KB of keys, 2 KB of values
+  static constexpr int kW = 4, kStages = HD == 64 ? 3 : 2;
+  static constexpr int kTile = 32, kHalf = kTile * HD;  // positions; bytes of keys, of values
   static constexpr int kBm = R16 ? 16 : 8, kCtas = R16 ? 2 : 3;
-  static constexpr int kRow = HD + 4;               // floats of a row of a share
-  uint4 ring[kW][kStages][2][128];
+  uint4 ring[kW][kStages][2][kHalf / 16];  // at a walk's end the slot that was read last: o of the warp's share
   __align__(16) float scales[kW][kStages][2][kTile / 16];
-  float share[kW][kBm * kRow];
+  uint4 q[HD / 16][R16 ? 2 : 1][32];  // the fragments of q's k steps, by lane (16 rows: hi, lo)
   float ml[kW][2][kBm];
   Plan<kW> plan;
 };
@@ -295,18 +293,15 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
   // 8 rows of one chunk (keys) and every second of 8 rows (values) without a bank twice; the pattern
   // repeats every 8 rows
   const uint32_t to_k = HD == 64 ? 16 * lane : (lane >> 3) * 128 + (((lane & 7) ^ (4 * (lane >> 3 & 1))) << 4);
-  const uint32_t to_v = 2048 + (HD == 64 ? (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) << 4)
+  const uint32_t to_v = S::kHalf + (HD == 64 ? (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) << 4)
                                          : (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 4))) << 4));
   const uint8_t *from_k = a.c.k + 16 * lane, *from_v = a.c.v + 16 * lane;
+  const int own = lane & (NB - 1);  // the block of the tile that the lane looks up, for all, and whose scale it copies
   const float* from_s = lane < NB ? a.c.ks : a.c.vs;
-  const bool scale_lane = lane < 2 * NB, second = NB == 2 && (lane & 1);
-  const int32_t* table;     // the row of the sequence
-  int tile, rows, clamp;    // of `pre`; positions from the tile's first one on; the sequence's last block
-  int page[NB], in_page[NB];
-  auto look = [&] {
-#pragma unroll
-    for (int k = 0; k < NB; ++k) page[k] = paged::page_of(a.c, table, min(tile * NB + k, clamp), in_page[k]);
-  };
+  const int32_t* table;             // the row of the sequence
+  int tile, rows, clamp;            // of `pre`; positions from the tile's first one on; the sequence's last block
+  int page, in_page;
+  auto look = [&] { page = paged::page_of(a.c, table, min(tile * NB + own, clamp), in_page); };
   auto enter_pre = [&] {
     table = paged::table_row(a.c, pre.b);
     tile = pre.w.first_tile + pre.t * W + warp;
@@ -315,42 +310,43 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
   };
   auto produce = [&](uint32_t s) {  // into slot s, and on to the next
     if (pre.left > 0) {
-      uint32_t at[NB];
-      bool all = rows >= TILE;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        at[k] = (uint32_t)((page[k] * a.c.n_kv + pre.h) * a.c.per_page + in_page[k]);
-        all &= page[k] >= 0;
-      }
-      const uint32_t dk = ring + s * 4096 + to_k, dv = ring + s * 4096 + to_v, dw = HD == 64 ? dv : dv ^ 64;
-      const uint8_t *k0 = from_k + (uint64_t)at[0] * (16 * HD), *v0 = from_v + (uint64_t)at[0] * (16 * HD);
-      const uint8_t *k1 = NB == 2 ? from_k + (uint64_t)at[NB - 1] * (16 * HD) : k0;
-      const uint8_t *v1 = NB == 2 ? from_v + (uint64_t)at[NB - 1] * (16 * HD) : v0;
-      const uint32_t mine = second ? at[NB - 1] : at[0];  // the block of the lane's scale
+      const uint32_t mine = page < 0 ? ~0u : (uint32_t)((page * a.c.n_kv + pre.h) * a.c.per_page + in_page);
+      const bool all = __all_sync(0xffffffffu, rows >= TILE && mine != ~0u);
+      const uint32_t dk = ring + s * (2 * S::kHalf) + to_k, dv = ring + s * (2 * S::kHalf) + to_v, dw = HD == 64 ? dv : dv ^ 64;
       const uint32_t ds = scales + (s * 2 * NB + lane) * 4;
-      constexpr int kTo = NB == 2 ? 0 : 1024;  // where the second address goes on
+      constexpr int kStep = 16 * HD;  // bytes of a block of keys
       if (all) {
-        cp16<0, 0>(dk, k0);
-        cp16<512, 512>(dk, k0);
-        cp16<1024, kTo>(dk, k1);
-        cp16<1536, kTo + 512>(dk, k1);
-        cp16<0, 0>(dv, v0);
-        cp16<512, 512>(dw, v0);
-        cp16<1024, kTo>(dv, v1);
-        cp16<1536, kTo + 512>(dw, v1);
-        cp4(ds, from_s + mine, scale_lane);
+        auto block = [&](auto c) {
+          constexpr int k = decltype(c)::value;
+          const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, mine, k) * kStep;
+          const uint8_t *fk = from_k + at, *fv = from_v + at;
+          cp16<k * kStep, 0>(dk, fk);
+          cp16<k * kStep + 512, 512>(dk, fk);
+          cp16<k * kStep, 0>(dv, fv);
+          cp16<k * kStep + 512, 512>(dw, fv);
+          if constexpr (HD == 128) {
+            cp16<k * kStep + 1024, 1024>(dk, fk);
+            cp16<k * kStep + 1536, 1536>(dk, fk);
+            cp16<k * kStep + 1024, 1024>(dv, fv);
+            cp16<k * kStep + 1536, 1536>(dw, fv);
+          }
+        };
+        block(std::integral_constant<int, 0>());
+        block(std::integral_constant<int, 1>());
+        cp4(ds, from_s + mine, lane < 2 * NB);
       } else if (rows > 0) {  // the sequence's last tile, or a block without a page
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = NB == 2 ? i >> 1 : 0;
-          const bool live = page[k] >= 0 && (512 * i + 16 * lane) / HD < rows;
-          const int from = NB == 2 ? 512 * (i & 1) : 512 * i;
-          cp16(dk + 512 * i, live ? (k ? k1 : k0) + from : a.c.k, live);
-          cp16((i & 1 ? dw : dv) + 512 * i, live ? (k ? v1 : v0) + from : a.c.v, live);
+#pragma unroll 1
+        for (int i = 0; i < S::kHalf / 512; ++i) {
+          const int byte = 512 * i + 16 * lane;
+          const uint32_t at = __shfl_sync(0xffffffffu, mine, 512 * i / kStep);
+          const bool live = at != ~0u && byte / HD < rows;
+          const uint64_t from = live ? (uint64_t)at * kStep + 512 * i % kStep : 0;
+          cp16(dk + 512 * i, from_k + from, live);
+          cp16((i & 1 ? dw : dv) + 512 * i, from_v + from, live);
         }
-        const bool none = (second ? 16 : 0) >= rows, lost = (second ? page[NB - 1] : page[0]) < 0;
-        cp4(ds, from_s + (none || lost ? 0 : mine), scale_lane && !none && !lost);
-        if (scale_lane && (none || lost)) (&sm.scales[warp][s][0][0])[lane] = none ? 0.f : __uint_as_float(0x7FC00000u);
+        const bool none = 16 * own >= rows, lost = mine == ~0u;
+        cp4(ds, from_s + (none || lost ? 0 : mine), lane < 2 * NB && !none && !lost);
+        if (lane < 2 * NB && (none || lost)) (&sm.scales[warp][s][0][0])[lane] = none ? 0.f : __uint_as_float(0x7FC00000u);
       }
       if (pre.t + 1 < pre.w.nt) {
         ++pre.t;
@@ -367,17 +363,31 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
   };
   enter_pre();
   look();
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < kLag; ++s) produce(s);
 
   float o[MT][NR][4];  // dims HD / 8 qr + 2 i (elements 0, 1), + 1 (2, 3) of rows 8 n + 2 qc, + 1
   float m[NR], l[NR], rs[NR];  // of rows qr + 8 i
   int ev = 0, emax = -1000;
   float down = 1.f;  // 2^-ev
-  uint32_t qf[KS][R16 ? 8 : 4];
   int lim[NR];               // position of the lane's row, -1: none
   int t_begin, base;         // of the CTA's part of the walk; this warp's first position of the tile
   int top, above, whole_lo, whole_hi;  // tiles with a seen position: above < base <= top; seen by every row: the others
+  // a walk's queries: asked for ...
+  float4 x[NR][KS];
+  auto load_q = [&](const Cursor<TILE, W, BM>& c) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int at = c.r * BM + qr + 8 * i;
+      const bool live = at < c.cnt * a.group;
+      lim[i] = live && c.p0 >= 0 ? c.p0 + at / a.group : -1;
+      const float4* src = reinterpret_cast<const float4*>(a.q + (live ? row_of(a, HD, a.q_stride, c.row0, c.h, at) : 0));
+#pragma unroll
+      for (int s = 0; s < KS; ++s)  // dims 64 (s / 4) + 16 qc + 4 (s % 4) ..
+        x[i][s] = live ? __ldcg(src + (s >> 2) * 16 + 4 * qc + (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  // ... and made operands
   auto start_walk = [&](const Cursor<TILE, W, BM>& c) {
     const int low = c.p0 + c.r * BM / a.group;  // position of the block's first row
     top = c.p0 < 0 ? -1 : c.p0 + min(c.cnt - 1, (c.r * BM + BM - 1) / a.group);
@@ -388,20 +398,14 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
     base = (c.w.first_tile + c.t * W + warp) * TILE;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int at = c.r * BM + qr + 8 * i;
-      const bool live = at < c.cnt * a.group;
-      lim[i] = live && c.p0 >= 0 ? c.p0 + at / a.group : -1;
-      const float4* src = reinterpret_cast<const float4*>(a.q + (live ? row_of(a, HD, a.q_stride, c.row0, c.h, at) : 0));
-      float4 x[KS];
       uint32_t mx = 0;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {  // dims 64 (s / 4) + 16 qc + 4 (s % 4) ..
-        x[s] = live ? __ldcg(src + (s >> 2) * 16 + 4 * qc + (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[s].x *= a.scale;
-        x[s].y *= a.scale;
-        x[s].z *= a.scale;
-        x[s].w *= a.scale;
-        mx = max(mx, abs_max(x[s]));
+      for (int s = 0; s < KS; ++s) {
+        x[i][s].x *= a.scale;
+        x[i][s].y *= a.scale;
+        x[i][s].z *= a.scale;
+        x[i][s].w *= a.scale;
+        mx = max(mx, abs_max(x[i][s]));
       }
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -410,9 +414,20 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       const float f = pow2(-e);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        // 8 rows: hi and lo are rows qr and qr + 8; 16: the rows of hi, then those of lo
-        split2(x[s].x * f, x[s].y * f, qf[s][R16 ? i : 0], qf[s][R16 ? 4 + i : 1]);
-        split2(x[s].z * f, x[s].w * f, qf[s][R16 ? 2 + i : 2], qf[s][R16 ? 6 + i : 3]);
+        if (s % W != warp) continue;
+        uint32_t hi[2], lo[2];
+        split2(x[i][s].x * f, x[i][s].y * f, hi[0], lo[0]);
+        split2(x[i][s].z * f, x[i][s].w * f, hi[1], lo[1]);
+        if constexpr (R16) {  // hi of rows qr and qr + 8, then lo
+          uint32_t* to = reinterpret_cast<uint32_t*>(&sm.q[s][0][lane]) + i;
+          to[0] = hi[0];
+          to[2] = hi[1];
+          to = reinterpret_cast<uint32_t*>(&sm.q[s][R16 ? 1 : 0][lane]) + i;
+          to[0] = lo[0];
+          to[2] = lo[1];
+        } else {  // hi is row qr, lo row qr + 8
+          sm.q[s][0][lane] = make_uint4(hi[0], lo[0], hi[1], lo[1]);
+        }
       }
       m[i] = -INFINITY;
       l[i] = 0.f;
@@ -427,8 +442,12 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
     emax = -1000;
     down = 1.f;
   };
+  load_q(cur);
   start_walk(cur);
+  __syncthreads();
 
+  static_assert(BM * HD * 4 <= 2 * S::kHalf, "a share fits a slot");
+  auto share = [&](int w, uint32_t slot, int r) { return reinterpret_cast<float*>(sm.ring[w][slot]) + r * HD; };
   for (uint32_t slot = 0;; slot = slot + 1 == S::kStages ? 0 : slot + 1) {
     cp_wait<kLag - 1>();
     __syncwarp();  // every lane's copies have landed, and the slot before this one has been read
@@ -438,50 +457,43 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       const unsigned char* kp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][0]);
       const unsigned char* vp = reinterpret_cast<const unsigned char*>(sm.ring[warp][slot][1]);
       float ks[NB], vs[NB];
-      if constexpr (NB == 2) {
-        const float4 x = *reinterpret_cast<const float4*>(sm.scales[warp][slot]);
-        ks[0] = x.x, ks[NB - 1] = x.y, vs[0] = x.z, vs[NB - 1] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(sm.scales[warp][slot]);
-        ks[0] = x.x, vs[0] = x.y;
-      }
+      const float4 scale = *reinterpret_cast<const float4*>(sm.scales[warp][slot]);
+      ks[0] = scale.x, ks[1] = scale.y, vs[0] = scale.z, vs[1] = scale.w;
       // ---- scores
-      float s[NT][4];
+      float s[NT][4], lo[R16 ? NT : 1][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int r = 8 * j + qr;
-        uint32_t b[KS][2];
+      for (int x = 0; x < HD / 64; ++x) {
+        uint4 w[NT];
 #pragma unroll
-        for (int x = 0; x < HD / 64; ++x) {
-          const int off = HD == 64 ? r * 64 + qc * 16 : r * 128 + (((qc + 4 * x) ^ (4 * (r & 1))) << 4);
-          const uint4 w = *reinterpret_cast<const uint4*>(kp + off);
-          to_h2x2<FMT>(w.x, b[4 * x][0], b[4 * x][1]);
-          to_h2x2<FMT>(w.y, b[4 * x + 1][0], b[4 * x + 1][1]);
-          to_h2x2<FMT>(w.z, b[4 * x + 2][0], b[4 * x + 2][1]);
-          to_h2x2<FMT>(w.w, b[4 * x + 3][0], b[4 * x + 3][1]);
+        for (int j = 0; j < NT; ++j) {
+          const int r = 8 * j + qr;
+          w[j] = *reinterpret_cast<const uint4*>(
+              kp + (HD == 64 ? r * 64 + qc * 16 : r * 128 + (((qc + 4 * x) ^ (4 * (r & 1))) << 4)));
         }
-        if constexpr (R16) {
-          float lo[4];
 #pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            const uint32_t fh[4] = {qf[x][0], qf[x][1], qf[x][2], qf[x][3]}, fl[4] = {qf[x][4], qf[x][5], qf[x][6], qf[x][7]};
-            if (x == 0) {
-              mma0(lo, fl, b[x][0], b[x][1]);
-              mma0(s[j], fh, b[x][0], b[x][1]);
+        for (int z = 0; z < 4; ++z) {
+          const uint4 h = sm.q[4 * x + z][0][lane], g = sm.q[4 * x + z][R16 ? 1 : 0][lane];
+          const uint32_t fh[4] = {h.x, h.y, h.z, h.w}, fl[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t b0, b1;
+            to_h2x2<FMT>(z == 0 ? w[j].x : z == 1 ? w[j].y : z == 2 ? w[j].z : w[j].w, b0, b1);
+            if (x == 0 && z == 0) {
+              mma0(s[j], fh, b0, b1);
+              if constexpr (R16) mma0(lo[j], fl, b0, b1);
             } else {
-              mma(lo, fl, b[x][0], b[x][1]);
-              mma(s[j], fh, b[x][0], b[x][1]);
+              mma(s[j], fh, b0, b1);
+              if constexpr (R16) mma(lo[j], fl, b0, b1);
             }
           }
+        }
+      }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] += lo[e];
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (R16) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] += lo[j][e];
         } else {
-#pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            const uint32_t f[4] = {qf[x][0], qf[x][1], qf[x][2], qf[x][3]};
-            if (x == 0) mma0(s[j], f, b[x][0], b[x][1]);
-            else mma(s[j], f, b[x][0], b[x][1]);
-          }
           s[j][0] += s[j][2];
           s[j][1] += s[j][3];
         }
@@ -491,7 +503,9 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       // o is in units of 2^ev, so that the tile's scales are 2^-2 to 2 of them: another unit where they are
       // not, at least 2^-60 of the largest (a NaN does not count: there are rows that do not see it)
       float back = 1.f;
-      const float vtop = NB == 2 ? fmaxf(fabsf(vs[0]), fabsf(vs[NB - 1])) : fabsf(vs[0]);
+      float vtop = fabsf(vs[0]);
+#pragma unroll
+      for (int k = 1; k < NB; ++k) vtop = fmaxf(vtop, fabsf(vs[k]));
       if (!(vtop * down < 2.f && vtop * down >= 0.25f)) {
         const int etile = vtop <= 3e38f ? max((int)(__float_as_uint(vtop) >> 23) - 127, -100) : -100;
         emax = max(emax, etile);
@@ -503,13 +517,9 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       float corr[NR], y[NT][2 * NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        uint32_t see = ~0u;  // bit 8 j + e: position base + 8 j + 2 qc + e
-        if (edge) {
-          const int hi = lim[i] - base, lo = a.window > 0 ? lim[i] - a.window + 1 - base : 0;  // of the tile, seen
-          see = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1;
-          if (lo > 0) see &= lo >= 32 ? 0u : ~0u << lo;
-          see >>= 2 * qc;
-        }
+        // the positions of the tile that the row sees are those from lo to hi
+        const int hi = lim[i] - base, lo = a.window > 0 ? hi - a.window + 1 : 0;
+        auto sees = [&](int j, int e) { return 8 * j + 2 * qc + e <= hi && 8 * j + 2 * qc + e >= lo; };
         float f[NB];
 #pragma unroll
         for (int k = 0; k < NB; ++k) f[k] = rs[i] * ks[k];
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              s[j][2 * i + e] = see >> (8 * j + e) & 1 ? s[j][2 * i + e] * f[j / 2] : -INFINITY;
+              s[j][2 * i + e] = sees(j, e) ? s[j][2 * i + e] * f[j / 2] : -INFINITY;
 #pragma unroll
           for (int k = 0; k < NB; ++k) f[k] = 1.f;
         }
@@ -546,7 +556,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (!(see >> (8 * j + e) & 1)) y[j][2 * i + e] = 0.f;
+              if (!sees(j, e)) y[j][2 * i + e] = 0.f;
         }
         l[i] = fmaf(l[i], corr[i], sum);
         corr[i] *= back;
@@ -564,49 +574,49 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
         keep[n][0] = __shfl_sync(0xffffffffu, corr[n], 8 * qc);
         keep[n][1] = __shfl_sync(0xffffffffu, corr[n], 8 * qc + 4);
       }
+      float t[MT][NR][4];
       constexpr int kWords = HD / 32;  // of a lane's part of a value row: 4 dims each
-      uint32_t v[NB][4][kWords];
 #pragma unroll
-      for (int k = 0; k < NB; ++k)
+      for (int k = 0; k < NB; ++k) {
+        uint32_t v[4][kWords];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int r = 16 * k + 8 * (x >> 1) + 2 * qc + (x & 1);  // (r >> 1) & 3 == qc
           if constexpr (HD == 64) {
             const uint2 w = *reinterpret_cast<const uint2*>(
                 vp + (r >> 1) * 128 + ((((qr >> 1) + 4 * (x & 1)) ^ (2 * qc)) << 4) + 8 * (qr & 1));
-            v[k][x][0] = w.x;
-            v[k][x][1] = w.y;
+            v[x][0] = w.x;
+            v[x][1] = w.y;
           } else {
             const uint4 w = *reinterpret_cast<const uint4*>(vp + r * 128 + ((qr ^ (2 * qc)) << 4));
-            v[k][x][0] = w.x;
-            v[k][x][1] = w.y;
-            v[k][x][2] = w.z;
-            v[k][x][3] = w.w;
+            v[x][0] = w.x;
+            v[x][1] = w.y;
+            v[x][2] = w.z;
+            v[x][3] = w.w;
           }
         }
 #pragma unroll
-      for (int g = 0; g < kWords; ++g) {
-        uint32_t x[2][NB][4];  // dims 4 g + 2 i, + 1
-#pragma unroll
-        for (int k = 0; k < NB; ++k)
+        for (int g = 0; g < kWords; ++g) {
+          uint32_t d[2][4];  // dims 4 g + 2 i, + 1
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t w0 = v[k][2 * h][g], w1 = v[k][2 * h + 1][g];
-            to_h2x2<FMT>(__byte_perm(w0, w1, 0x5140u), x[0][k][2 * h], x[0][k][2 * h + 1]);
-            to_h2x2<FMT>(__byte_perm(w0, w1, 0x7362u), x[1][k][2 * h], x[1][k][2 * h + 1]);
+            to_h2x2<FMT>(__byte_perm(v[2 * h][g], v[2 * h + 1][g], 0x5140u), d[0][2 * h], d[0][2 * h + 1]);
+            to_h2x2<FMT>(__byte_perm(v[2 * h][g], v[2 * h + 1][g], 0x7362u), d[1][2 * h], d[1][2 * h + 1]);
           }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int n = 0; n < NR; ++n) {
-            float t[4];  // the low parts first: what is cut off there does not count
-            mma0(t, x[i][0], pl[n][0][0], pl[n][0][1]);
-            if constexpr (NB == 2) mma(t, x[i][NB - 1], pl[n][NB - 1][0], pl[n][NB - 1][1]);
-            mma(t, x[i][0], ph[n][0][0], ph[n][0][1]);
-            if constexpr (NB == 2) mma(t, x[i][NB - 1], ph[n][NB - 1][0], ph[n][NB - 1][1]);
+            for (int n = 0; n < NR; ++n) {
+              float(&tt)[4] = t[2 * g + i][n];
+              if (k == 0) mma0(tt, d[i], pl[n][0][0], pl[n][0][1]);
+              else mma(tt, d[i], pl[n][k][0], pl[n][k][1]);
+              mma(tt, d[i], ph[n][k][0], ph[n][k][1]);
+              if (k == NB - 1) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[2 * g + i][n][e] = fmaf(o[2 * g + i][n][e], keep[n][e & 1], t[e]);
-          }
+                for (int e = 0; e < 4; ++e) o[2 * g + i][n][e] = fmaf(o[2 * g + i][n][e], keep[n][e & 1], tt[e]);
+              }
+            }
+        }
       }
     }
 
@@ -619,6 +629,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       continue;
     }
     const bool whole = t_begin == 0 && last;
+    __syncwarp();  // every lane has read the slot
     const float unit = pow2(min(max(ev, -126), 127));
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
@@ -633,11 +644,16 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int d = 0; d < MT; d += 2)
-          *reinterpret_cast<float4*>(&sm.share[warp][(8 * i + 2 * qc + e) * S::kRow + HD / 8 * qr + 2 * d]) =
+          *reinterpret_cast<float4*>(share(warp, slot, 8 * i + 2 * qc + e) + HD / 8 * qr + 2 * d) =
               make_float4(o[d][i][e] * unit, o[d][i][2 + e] * unit, o[d + 1][i][e] * unit, o[d + 1][i][2 + e] * unit);
     }
+    const int done_cnt = cur.cnt, done_r = cur.r, done_h = cur.h, done_row0 = cur.row0;
+    const int64_t stop = end - cur.left - cur.t + cur.w.nt - 1;  // the walk's last unit
+    cur.next_walk(a, sm.plan);
+    const bool more = last && cur.left > 0;
+    if (more) load_q(cur);  // on its way meanwhile
     __syncthreads();
-    const int live = min(cur.cnt * a.group - cur.r * BM, BM);
+    const int live = min(done_cnt * a.group - done_r * BM, BM);
     for (int x = threadIdx.x; x < live * (HD / 4); x += W * 32) {
       const int r = x / (HD / 4), c = x % (HD / 4);
       float mt = -INFINITY, lt = 0.f;
@@ -648,7 +664,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       for (int w = 0; w < W; ++w) {
         const float mw = sm.ml[w][0][r], lw = sm.ml[w][1][r];
         const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
-        const float4 ow = *reinterpret_cast<const float4*>(&sm.share[w][r * S::kRow + 4 * c]);
+        const float4 ow = *reinterpret_cast<const float4*>(share(w, slot, r) + 4 * c);
         lt = fmaf(lw, f, lt);
         ot.x = fmaf(ow.x, f, ot.x);
         ot.y = fmaf(ow.y, f, ot.y);
@@ -657,7 +673,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       }
       if (whole) {
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, cur.row0, cur.h, cur.r * BM + r))[c] =
+        reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, done_row0, done_h, done_r * BM + r))[c] =
             make_float4(ot.x * inv, ot.y * inv, ot.z * inv, ot.w * inv);
       } else {
         float* part = part_of(a, BM, HD, blockIdx.x, t_begin > 0 ? 0 : 1);
@@ -669,18 +685,15 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       }
     }
     if (!whole && t_begin == 0 && threadIdx.x == 0) {
-      const int64_t stop = end - cur.left - cur.t + cur.w.nt - 1;  // the walk's last unit
       cut->parts = (int)(stop / per) - (int)blockIdx.x + 1;
-      cut->h = cur.h;
-      cut->r = cur.r;
-      cut->cnt = cur.cnt;
-      cut->row0 = cur.row0;
+      cut->h = done_h;
+      cut->r = done_r;
+      cut->cnt = done_cnt;
+      cut->row0 = done_row0;
     }
-    __syncthreads();  // every share has been read
-    if (!last) break;
-    cur.next_walk(a, sm.plan);
-    if (cur.left <= 0) break;
-    start_walk(cur);
+    if (more) start_walk(cur);
+    __syncthreads();  // every share has been read, and q stands
+    if (!more) break;
   }
   cp_wait<0>();
 }
@@ -802,7 +815,7 @@ extern "C" {
 
 size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs) {
   if (!attn_shape_ok(kv, n_heads, n_tokens, n_seqs)) return 0;
-  const int64_t ctas = std::min(attn_sm_count() * 3, kMaxCtas);  // whatever the call: it serves them all
+  const int64_t ctas = std::min(attn_sm_count() * 4, kMaxCtas);  // whatever the call: it serves them all
   return kCutBytes + (size_t)ctas * 2 * part_floats(16, kv->head_dim) * sizeof(float);
 }
 

@@ -327,6 +327,20 @@ def test_attention(qd, fmt, heads, hk, hd, tokens, total, rows, window):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("heads,hk,hd,total,rows", [(12, 3, 64, [2500], [140]), (32, 8, 128, [1500] * 9, [1] * 9),
+                                                    (16, 1, 128, [3000, 500], [30, 3]), (9, 3, 64, [900] * 20, [1] * 20)])
+def test_attention_gives_the_same_bits_every_time(qd, heads, hk, hd, total, rows):
+    """Walks that are cut, and CTAs that go from one to the next: 100 runs, so that warps that run ahead show."""
+    rng = np.random.default_rng([25, heads, hd])
+    c = Cache(rng, len(total), hk, hd, 32, total, "i8")
+    kv, _ = _handle(qd, c)
+    start, pos = _starts(rows), np.array(total, np.int32) - np.array(rows, np.int32)
+    q = dev((rng.normal(size=(int(start[-1]), heads, hd)) * 1.5).astype(np.float32))
+    d_start, d_pos = dev(start), dev(pos)
+    outs = [_attn(qd, kv, q, d_start, d_pos, heads, 0.1, 0) for _ in range(100)]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 def test_attention_of_many_sequences(qd):
     rng = np.random.default_rng(12)
     total = [1 + (b * 29) % 150 for b in range(256)]
