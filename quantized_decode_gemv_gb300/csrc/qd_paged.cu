@@ -44,8 +44,9 @@ __device__ __forceinline__ FF add(FF c, FF x) {
   return quick_sum(s.h, __fadd_rn(s.l, __fadd_rn(c.l, x.l)));
 }
 
-// (cos, sin) of pos * turns, times the magnitude, each rounded to f32
-__device__ __forceinline__ float2 cos_sin(uint64_t turns, int pos, FF magnitude) {
+// (cos, sin) of pos * turns, times the magnitude, each rounded to f32.  Not inlined: its 300 instructions
+// stand once in a kernel, which runs cold in a step of small calls.
+__device__ __noinline__ float2 cos_sin(uint64_t turns, int pos, FF magnitude) {
   const uint64_t a = turns * (uint64_t)pos;
   const uint64_t quadrant = (a + (1ull << 61)) >> 62;
   const int64_t r = (int64_t)(a - (quadrant << 62));  // 2^-61 (pi / 4) each, at most 2^61 of them
@@ -91,12 +92,16 @@ __device__ __forceinline__ float det(float a, float c, float b, float s) {
   const float r = __fadd_rn(d.h, __fadd_rn(d.l, __fsub_rn(p.l, q.l)));
   return isfinite(r) ? r : d.h;  // an infinity has no rest to add
 }
+__device__ __noinline__ float2 turn_small(float x0, float x1, float2 cs) {
+  const double a = x0, b = x1;
+  return make_float2((float)(a * cs.x - b * cs.y), (float)(a * cs.y + b * cs.x));
+}
 __device__ __forceinline__ void turn(float& x0, float& x1, float2 cs) {
   const float most = fmaxf(fabsf(x0), fabsf(x1));
   if (most < 0x1p-80f && most > 0.f) {  // the second parts would end at f32's smallest step
-    const double a = x0, b = x1;
-    x0 = (float)(a * cs.x - b * cs.y);
-    x1 = (float)(a * cs.y + b * cs.x);
+    const float2 y = turn_small(x0, x1, cs);
+    x0 = y.x;
+    x1 = y.y;
     return;
   }
   const float y0 = det(x0, cs.x, x1, cs.y), y1 = det(x0, cs.y, -x1, cs.x);
@@ -165,31 +170,56 @@ struct RowsArgs {
   float* out;
   int64_t out_stride;
   int n_tokens, n_heads, hd, rows;  // rows: of a CTA
+  uint32_t heads_magic;             // 2^32 / n_heads rounded up; not looked at with one row or head
   Rotation rot;
 };
 
-// Rows first .. of this CTA; s_pos: the position of each, < 0: not written.
+// Rows first .. of this CTA; s_pos: the position of each, < 0: not written.  A thread keeps its unit of
+// a head and goes from one (row, head) to another, four at a time, whose loads are on their way while
+// the CTA makes the angles.
 __device__ __forceinline__ void rotate_rows(const RowsArgs& a, int first, const int* s_pos, float2* s_cs) {
-  const int n = min(a.rows, a.n_tokens - first), pairs = a.rot.rot / 2;
-  for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-    const int row = i / pairs, p = s_pos[row];
-    if (p >= 0) s_cs[i] = cos_sin(__ldg(a.rot.turns + (i - row * pairs)), p, a.rot.magnitude);
-  }
-  __syncthreads();
-  const int per = a.hd / 8, units = a.n_heads * per;
-  for (int i = threadIdx.x; i < n * units; i += kThreads) {
-    const int row = i / units, in = i - row * units, h = in / per;
-    if (s_pos[row] < 0) continue;
-    const Unit u = unit_of(in - h * per, a.rot.rot, a.rot.pairing);
-    const float* src = a.x + (int64_t)(first + row) * a.x_stride + h * a.hd;
-    float* dst = a.out + (int64_t)(first + row) * a.out_stride + h * a.hd;
-    if (!u.rotated && src == dst) continue;
-    float4 v0 = __ldcg(reinterpret_cast<const float4*>(src + u.da)), v1 = __ldcg(reinterpret_cast<const float4*>(src + u.db));
-    if (u.rotated) turn_unit(v0, v1, s_cs + row * pairs + 4 * (in - h * per), a.rot.pairing);
-    *reinterpret_cast<float4*>(dst + u.da) = v0;
-    *reinterpret_cast<float4*>(dst + u.db) = v1;
+  const int n = min(a.rows, a.n_tokens - first), pairs = a.rot.rot / 2, per = a.hd / 8;
+  const int groups = kThreads / per, group = threadIdx.x / per, at = threadIdx.x - group * per;
+  const int items = group < groups ? n * a.n_heads : 0;  // the last threads have no whole group
+  const Unit u = unit_of(at, a.rot.rot, a.rot.pairing);
+  const bool copies = u.rotated || a.x != a.out;  // in place, what is not rotated stays
+  constexpr int kAtOnce = 4;
+  bool angles = false;
+  for (int j0 = group; j0 < items || !angles; j0 += kAtOnce * groups) {
+    float4 v0[kAtOnce], v1[kAtOnce];
+    int row[kAtOnce], head[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = j0 + i * groups;
+      row[i] = -1;
+      if (j >= items || !copies) continue;
+      const int r = a.rows == 1 ? 0 : a.n_heads == 1 ? j : (int)__umulhi((uint32_t)j, a.heads_magic);
+      head[i] = j - r * a.n_heads;
+      if (s_pos[r] < 0) continue;
+      row[i] = r;
+      const float* src = a.x + (int64_t)(first + r) * a.x_stride + head[i] * a.hd;
+      v0[i] = __ldcg(reinterpret_cast<const float4*>(src + u.da));
+      v1[i] = __ldcg(reinterpret_cast<const float4*>(src + u.db));
+    }
+    if (!angles) {  // every thread comes here once
+      for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
+        const int r = i / pairs, p = s_pos[r];
+        if (p >= 0) s_cs[i] = cos_sin(__ldg(a.rot.turns + (i - r * pairs)), p, a.rot.magnitude);
+      }
+      __syncthreads();
+      angles = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (row[i] < 0) continue;
+      if (u.rotated) turn_unit(v0[i], v1[i], s_cs + row[i] * pairs + 4 * at, a.rot.pairing);
+      float* dst = a.out + (int64_t)(first + row[i]) * a.out_stride + head[i] * a.hd;
+      *reinterpret_cast<float4*>(dst + u.da) = v0[i];
+      *reinterpret_cast<float4*>(dst + u.db) = v1[i];
+    }
   }
 }
+inline uint32_t magic_of(int n) { return n < 2 ? 0u : (uint32_t)(((1ull << 32) + n - 1) / n); }
 
 __global__ void __launch_bounds__(kThreads) k_rope_tokens(RowsArgs a, const int32_t* __restrict__ pos) {
   __shared__ __align__(16) float2 s_cs[kAngles];
@@ -254,6 +284,32 @@ __device__ __forceinline__ float4 values_of(uint32_t w) {
     return make_float4(x.x, x.y, y.x, y.y);
   }
 }
+// The same of eight values, given 1 / scale to the nearest: x (1 / scale) is within 1.5 * 2^-23 of the
+// rounded quotient, relatively.  False where that could matter, and the quotients have to be formed.
+template <int FMT>
+__device__ __forceinline__ bool codes_by(float4 x, float4 y, float inv, uint32_t& w0, uint32_t& w1) {
+  if constexpr (FMT == QD_KV_I8) {
+    constexpr float kMagic15 = 12582912.f;  // 1.5 * 2^23: a sum's low byte is the nearest whole number
+    float far = 0.f;
+    auto one = [&](float v) {
+      const float t = v * inv, m = __fadd_rn(t, kMagic15);
+      far = fmaxf(far, fabsf(t - __fsub_rn(m, kMagic15)));
+      return __float_as_uint(m);
+    };
+    auto four = [&](float4 v) {
+      return __byte_perm(__byte_perm(one(v.x), one(v.y), 0x0040u), __byte_perm(one(v.z), one(v.w), 0x0040u), 0x5410u);
+    };
+    w0 = four(x);
+    w1 = four(y);
+    return far < 0.49996f;  // 127 * 1.5 * 2^-23 < 2.3e-5 from a tie
+  } else {
+    const float up = inv * (1.f + 0x1p-21f), down = inv * (1.f - 0x1p-21f);
+    w0 = codes_of<FMT>(x.x * up, x.y * up, x.z * up, x.w * up);
+    w1 = codes_of<FMT>(y.x * up, y.y * up, y.z * up, y.w * up);
+    return w0 == codes_of<FMT>(x.x * down, x.y * down, x.z * down, x.w * down) &&
+           w1 == codes_of<FMT>(y.x * down, y.y * down, y.z * down, y.w * down);
+  }
+}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t abs_max(float4 x) {
   return max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
@@ -269,7 +325,7 @@ __device__ __forceinline__ int blocks_of(const AppendArgs& a, int b, int& p0) {
 }
 
 template <int HD, int FMT>
-__global__ void __launch_bounds__(kThreads) k_paged_append(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_paged_append(AppendArgs a) {
   __shared__ __align__(16) float2 s_cs[kAngles];
   __shared__ int s_pos[kMaxRows];
   __shared__ int s_seq, s_block;
@@ -372,14 +428,14 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(AppendArgs a) {
     most = __reduce_max_sync(0xffffffffu, most);
     const bool broken = most >= 0x7F800000u || isnan(old);
     const float mine = __fdiv_rn(__uint_as_float(most), top_code<FMT>());
-    const float now = broken ? __uint_as_float(0x7FC00000u) : fmaxf(old, mine);
+    const float now = broken ? __uint_as_float(0x7FC00000u) : fmaxf(old, mine), inv = __frcp_rn(now);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int e = lane + 32 * i, slot = e / kPer;
       if (slot < lo || slot >= hi) continue;
       const Unit u = unit_of(e % kPer, isv ? 0 : a.rows.rot.rot, a.rows.rot.pairing);
       uint32_t w0 = 0, w1 = 0;
-      if (now > 0.f) {
+      if (now > 0.f && !(now >= 0x1p-100f && codes_by<FMT>(x[i], y[i], inv, w0, w1))) {
         w0 = codes_of<FMT>(__fdiv_rn(x[i].x, now), __fdiv_rn(x[i].y, now), __fdiv_rn(x[i].z, now), __fdiv_rn(x[i].w, now));
         w1 = codes_of<FMT>(__fdiv_rn(y[i].x, now), __fdiv_rn(y[i].y, now), __fdiv_rn(y[i].z, now), __fdiv_rn(y[i].w, now));
       }
@@ -533,7 +589,7 @@ qd_status qd_rope_tokens(const float* x, int64_t x_stride, float* out, int64_t o
   if (n_tokens > 1 && (x_stride % 4 || out_stride % 4)) return QD_ERR_ALIGN;
   if (x == out && n_tokens > 1 && x_stride != out_stride) return QD_ERR_INVALID_ARG;
   const RowsArgs a = {x, x_stride, out, out_stride, n_tokens, n_heads, head_dim,
-                      rows_per_cta(n_tokens, n_heads, head_dim, rot_dim),
+                      rows_per_cta(n_tokens, n_heads, head_dim, rot_dim), magic_of(n_heads),
                       rotation_of(turns, magnitude, rot_dim, pairing)};
   k_rope_tokens<<<(n_tokens + a.rows - 1) / a.rows, kThreads, 0, (cudaStream_t)stream>>>(a, pos);
   return launch_status();
@@ -573,7 +629,8 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
   a.kv_ctas = units * a.splits;
   const int qh = q ? n_heads : 1;
   a.rows = {q, token_stride, q_out, (int64_t)qh * kv->head_dim, n_tokens, qh, kv->head_dim,
-            rows_per_cta(n_tokens, qh, kv->head_dim, rot_dim), rotation_of(turns, magnitude, rot_dim, pairing)};
+            rows_per_cta(n_tokens, qh, kv->head_dim, rot_dim), magic_of(qh),
+            rotation_of(turns, magnitude, rot_dim, pairing)};
   const int ctas = a.kv_ctas + (q ? (n_tokens + a.rows.rows - 1) / a.rows.rows : 0);
   cudaStream_t st = (cudaStream_t)stream;
   if (kv->head_dim == 64)
