@@ -551,8 +551,8 @@ qd_status qd_rope_plan(double theta, int rot_dim, qd_rope_scaling scaling, doubl
  * int32 [n_tokens]), the others copied.  ADJACENT pairs (2i, 2i + 1), HALF (i, i + rot_dim/2).
  * turns: device uint64 [rot_dim/2], with magnitude from qd_rope_plan (any finite magnitude).  out
  * may be x with the same stride.  A row with pos[t] < 0 is not written.  cos and sin are the exact
- * ones times magnitude rounded to f32, and so is each rotated value (up to 1 in 2^18 of the
- * neighbouring f32 value).  head_dim and rot_dim multiples of 8, rot_dim <= head_dim <= 1024;
+ * ones times magnitude rounded to f32 (up to one in 2^17 the neighbouring f32 value); a rotated
+ * value x0 c - x1 s (x0 s + x1 c) is off by 2^-24 of itself and of |x1 s| (|x1 c|) at most.  head_dim and rot_dim multiples of 8, rot_dim <= head_dim <= 1024;
  * strides multiples of 4, at least n_heads*head_dim; 1 <= n_tokens <= QD_MAX_GEMM_TOKENS. */
 qd_status qd_rope_tokens(const float* x, int64_t x_stride, float* out, int64_t out_stride, int n_tokens, int n_heads,
                          int head_dim, int rot_dim, const int32_t* pos, qd_rope_pairing pairing, const uint64_t* turns,
@@ -560,8 +560,8 @@ qd_status qd_rope_tokens(const float* x, int64_t x_stride, float* out, int64_t o
 
 /* Append packed rows.  q, k, v: f32 rows of n_heads (n_kv_heads) heads at t*token_stride (e.g.
  * three parts of one fused projection).  q rotated to q_out (f32 [n_tokens][n_heads][head_dim];
- * q NULL: no queries, q_out is not looked at), k rotated, as by qd_rope_tokens, and v go to the
- * sequence's pages.  For each block of QD_KV_BLOCK positions and head: scale = max(scale of the
+ * q NULL: no queries, q_out is not looked at) as by qd_rope_tokens; k, rotated by the same cos and sin
+ * and rounded once to f32, and v go to the sequence's pages.  For each block of QD_KV_BLOCK positions and head: scale = max(scale of the
  * positions that the block held before, largest new magnitude / top), top 127 or 448; codes =
  * value / scale to the nearest (ties away from zero for I8, to even for E4M3); where the scale
  * grows, the codes held before become (code * old scale) / new scale to the nearest.  All of

@@ -86,8 +86,11 @@ __device__ __noinline__ float2 cos_sin(uint64_t turns, int pos, FF magnitude) {
   }
 }
 
-// a c - b s rounded once: both products in two parts
+// a c - b s: rounded once where EXACT (both products in two parts; what the codes of keys are decided
+// by), else to 2^-24 of |b s| and of the result.
+template <bool EXACT>
 __device__ __forceinline__ float det(float a, float c, float b, float s) {
+  if constexpr (!EXACT) return __fmaf_rn(a, c, -__fmul_rn(b, s));
   const FF p = two_prod(a, c), q = two_prod(b, s), d = two_sum(p.h, -q.h);
   const float r = __fadd_rn(d.h, __fadd_rn(d.l, __fsub_rn(p.l, q.l)));
   return isfinite(r) ? r : d.h;  // an infinity has no rest to add
@@ -96,15 +99,18 @@ __device__ __noinline__ float2 turn_small(float x0, float x1, float2 cs) {
   const double a = x0, b = x1;
   return make_float2((float)(a * cs.x - b * cs.y), (float)(a * cs.y + b * cs.x));
 }
+template <bool EXACT>
 __device__ __forceinline__ void turn(float& x0, float& x1, float2 cs) {
-  const float most = fmaxf(fabsf(x0), fabsf(x1));
-  if (most < 0x1p-80f && most > 0.f) {  // the second parts would end at f32's smallest step
-    const float2 y = turn_small(x0, x1, cs);
-    x0 = y.x;
-    x1 = y.y;
-    return;
+  if constexpr (EXACT) {
+    const float most = fmaxf(fabsf(x0), fabsf(x1));
+    if (most < 0x1p-80f && most > 0.f) {  // the second parts would end at f32's smallest step
+      const float2 y = turn_small(x0, x1, cs);
+      x0 = y.x;
+      x1 = y.y;
+      return;
+    }
   }
-  const float y0 = det(x0, cs.x, x1, cs.y), y1 = det(x0, cs.y, -x1, cs.x);
+  const float y0 = det<EXACT>(x0, cs.x, x1, cs.y), y1 = det<EXACT>(x0, cs.y, -x1, cs.x);
   x0 = y0;
   x1 = y1;
 }
@@ -124,20 +130,21 @@ __device__ __forceinline__ Unit unit_of(int u, int rot, int pairing) {
   return r;
 }
 // cs: (cos, sin) of pairs 4u .. 4u + 3
+template <bool EXACT>
 __device__ __forceinline__ void turn_unit(float4& a, float4& b, const float2* cs, int pairing) {
   const float4 t0 = *reinterpret_cast<const float4*>(cs), t1 = *reinterpret_cast<const float4*>(cs + 2);
   const float2 c0 = make_float2(t0.x, t0.y), c1 = make_float2(t0.z, t0.w), c2 = make_float2(t1.x, t1.y),
                c3 = make_float2(t1.z, t1.w);
   if (pairing == QD_ROPE_HALF) {
-    turn(a.x, b.x, c0);
-    turn(a.y, b.y, c1);
-    turn(a.z, b.z, c2);
-    turn(a.w, b.w, c3);
+    turn<EXACT>(a.x, b.x, c0);
+    turn<EXACT>(a.y, b.y, c1);
+    turn<EXACT>(a.z, b.z, c2);
+    turn<EXACT>(a.w, b.w, c3);
   } else {
-    turn(a.x, a.y, c0);
-    turn(a.z, a.w, c1);
-    turn(b.x, b.y, c2);
-    turn(b.z, b.w, c3);
+    turn<EXACT>(a.x, a.y, c0);
+    turn<EXACT>(a.z, a.w, c1);
+    turn<EXACT>(b.x, b.y, c2);
+    turn<EXACT>(b.z, b.w, c3);
   }
 }
 
@@ -212,7 +219,7 @@ __device__ __forceinline__ void rotate_rows(const RowsArgs& a, int first, const 
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       if (row[i] < 0) continue;
-      if (u.rotated) turn_unit(v0[i], v1[i], s_cs + row[i] * pairs + 4 * at, a.rot.pairing);
+      if (u.rotated) turn_unit<false>(v0[i], v1[i], s_cs + row[i] * pairs + 4 * at, a.rot.pairing);
       float* dst = a.out + (int64_t)(first + row[i]) * a.out_stride + head[i] * a.hd;
       *reinterpret_cast<float4*>(dst + u.da) = v0[i];
       *reinterpret_cast<float4*>(dst + u.db) = v1[i];
@@ -324,30 +331,43 @@ __device__ __forceinline__ int blocks_of(const AppendArgs& a, int b, int& p0) {
   return (min((int64_t)p0 + t, (int64_t)a.c.capacity) - 1) / QD_KV_BLOCK - p0 / QD_KV_BLOCK + 1;
 }
 
+// With more than this many CTAs of them to an SM, the queries have a launch of their own, whose CTAs need
+// fewer registers.
+constexpr int kQueriesApart = 2;
+// Rows first .. of the queries, rotated by their sequences' positions.
+__device__ __forceinline__ void rotate_queries(const AppendArgs& a, int first, int* s_pos, float2* s_cs) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = min(a.rows.rows, a.n_tokens - first);
+  for (int r = warp; r < n; r += kThreads / 32) {  // the last sequence that starts at or before the row
+    const int row = first + r;
+    int before = 0;
+    for (int b = lane; b < a.n_seqs; b += 32) before += a.row_start[b] <= row;
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+      int p = -1;
+      if (before && row < a.row_start[before]) {
+        const int p0 = a.pos[before - 1];
+        if (p0 >= 0 && p0 <= a.c.capacity) p = p0 + (row - a.row_start[before - 1]);
+      }
+      s_pos[r] = p;
+    }
+  }
+  __syncthreads();
+  rotate_rows(a.rows, first, s_pos, s_cs);
+}
+__global__ void __launch_bounds__(kThreads) k_paged_queries(AppendArgs a) {
+  __shared__ __align__(16) float2 s_cs[kAngles];
+  __shared__ int s_pos[kMaxRows];
+  rotate_queries(a, blockIdx.x * a.rows.rows, s_pos, s_cs);
+}
+
 template <int HD, int FMT>
 __global__ void __launch_bounds__(kThreads, 2) k_paged_append(AppendArgs a) {
   __shared__ __align__(16) float2 s_cs[kAngles];
   __shared__ int s_pos[kMaxRows];
   __shared__ int s_seq, s_block;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if ((int)blockIdx.x >= a.kv_ctas) {  // queries
-    const int first = (blockIdx.x - a.kv_ctas) * a.rows.rows, n = min(a.rows.rows, a.n_tokens - first);
-    for (int r = warp; r < n; r += kThreads / 32) {  // the last sequence that starts at or before the row
-      const int row = first + r;
-      int before = 0;
-      for (int b = lane; b < a.n_seqs; b += 32) before += a.row_start[b] <= row;
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (lane == 0) {
-        int p = -1;
-        if (before && row < a.row_start[before]) {
-          const int p0 = a.pos[before - 1];
-          if (p0 >= 0 && p0 <= a.c.capacity) p = p0 + (row - a.row_start[before - 1]);
-        }
-        s_pos[r] = p;
-      }
-    }
-    __syncthreads();
-    rotate_rows(a.rows, first, s_pos, s_cs);
+  if ((int)blockIdx.x >= a.kv_ctas) {
+    rotate_queries(a, (blockIdx.x - a.kv_ctas) * a.rows.rows, s_pos, s_cs);
     return;
   }
   const int unit = blockIdx.x / a.splits, h0 = blockIdx.x % a.splits * a.heads;
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_append(AppendArgs a) {
     for (int i = 0; i < kUnits; ++i) {
       const int e = lane + 32 * i, slot = e / kPer;
       if (!isv && 8 * (e % kPer) < a.rows.rot.rot && slot >= lo && slot < hi)
-        turn_unit(x[i], y[i], s_cs + slot * pairs + 4 * (e % kPer), a.rows.rot.pairing);
+        turn_unit<true>(x[i], y[i], s_cs + slot * pairs + 4 * (e % kPer), a.rows.rot.pairing);
       most = max(most, max(abs_max(x[i]), abs_max(y[i])));
     }
     most = __reduce_max_sync(0xffffffffu, most);
@@ -631,8 +651,15 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
   a.rows = {q, token_stride, q_out, (int64_t)qh * kv->head_dim, n_tokens, qh, kv->head_dim,
             rows_per_cta(n_tokens, qh, kv->head_dim, rot_dim), magic_of(qh),
             rotation_of(turns, magnitude, rot_dim, pairing)};
-  const int ctas = a.kv_ctas + (q ? (n_tokens + a.rows.rows - 1) / a.rows.rows : 0);
   cudaStream_t st = (cudaStream_t)stream;
+  const int q_ctas = q ? (n_tokens + a.rows.rows - 1) / a.rows.rows : 0;
+  const bool apart = q_ctas > kQueriesApart * attn_sm_count();
+  if (apart) {
+    k_paged_queries<<<q_ctas, kThreads, 0, st>>>(a);
+    r = launch_status();
+    if (r != QD_OK) return r;
+  }
+  const int ctas = a.kv_ctas + (apart ? 0 : q_ctas);
   if (kv->head_dim == 64)
     return kv->fmt == QD_KV_I8 ? launch_append<64, QD_KV_I8>(a, ctas, st) : launch_append<64, QD_KV_E4M3>(a, ctas, st);
   return kv->fmt == QD_KV_I8 ? launch_append<128, QD_KV_I8>(a, ctas, st) : launch_append<128, QD_KV_E4M3>(a, ctas, st);
