@@ -2,6 +2,7 @@
 // quantises, and the way back to contiguous caches.  The attention over the pages is
 // qd_paged_attn.cu.
 #include <algorithm>
+#include <atomic>
 
 #include "qd_paged.cuh"
 
@@ -181,10 +182,11 @@ struct RowsArgs {
   Rotation rot;
 };
 
-// Rows first .. of this CTA; s_pos: the position of each, < 0: not written.  A thread keeps its unit of
-// a head and goes from one (row, head) to another, four at a time, whose loads are on their way while
-// the CTA makes the angles.
-__device__ __forceinline__ void rotate_rows(const RowsArgs& a, int first, const int* s_pos, float2* s_cs) {
+// Rows first .. of this CTA; find() puts the position of each into s_pos, < 0: not written.  A thread keeps
+// its unit of a head and goes from one (row, head) to another, four at a time, whose loads are on their way
+// while the CTA finds the positions and makes the angles.
+template <typename Find>
+__device__ __forceinline__ void rotate_rows(const RowsArgs& a, int first, int* s_pos, float2* s_cs, Find find) {
   const int n = min(a.rows, a.n_tokens - first), pairs = a.rot.rot / 2, per = a.hd / 8;
   const int groups = kThreads / per, group = threadIdx.x / per, at = threadIdx.x - group * per;
   const int items = group < groups ? n * a.n_heads : 0;  // the last threads have no whole group
@@ -202,13 +204,14 @@ __device__ __forceinline__ void rotate_rows(const RowsArgs& a, int first, const 
       if (j >= items || !copies) continue;
       const int r = a.rows == 1 ? 0 : a.n_heads == 1 ? j : (int)__umulhi((uint32_t)j, a.heads_magic);
       head[i] = j - r * a.n_heads;
-      if (s_pos[r] < 0) continue;
       row[i] = r;
       const float* src = a.x + (int64_t)(first + r) * a.x_stride + head[i] * a.hd;
       v0[i] = __ldcg(reinterpret_cast<const float4*>(src + u.da));
       v1[i] = __ldcg(reinterpret_cast<const float4*>(src + u.db));
     }
     if (!angles) {  // every thread comes here once
+      find(n);
+      __syncthreads();
       for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
         const int r = i / pairs, p = s_pos[r];
         if (p >= 0) s_cs[i] = cos_sin(__ldg(a.rot.turns + (i - r * pairs)), p, a.rot.magnitude);
@@ -218,7 +221,7 @@ __device__ __forceinline__ void rotate_rows(const RowsArgs& a, int first, const 
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      if (row[i] < 0) continue;
+      if (row[i] < 0 || s_pos[row[i]] < 0) continue;
       if (u.rotated) turn_unit<false>(v0[i], v1[i], s_cs + row[i] * pairs + 4 * at, a.rot.pairing);
       float* dst = a.out + (int64_t)(first + row[i]) * a.out_stride + head[i] * a.hd;
       *reinterpret_cast<float4*>(dst + u.da) = v0[i];
@@ -232,9 +235,9 @@ __global__ void __launch_bounds__(kThreads) k_rope_tokens(RowsArgs a, const int3
   __shared__ __align__(16) float2 s_cs[kAngles];
   __shared__ int s_pos[kMaxRows];
   const int first = blockIdx.x * a.rows;
-  if (threadIdx.x < a.rows && first + threadIdx.x < a.n_tokens) s_pos[threadIdx.x] = pos[first + threadIdx.x];
-  __syncthreads();
-  rotate_rows(a, first, s_pos, s_cs);
+  rotate_rows(a, first, s_pos, s_cs, [&](int n) {
+    if (threadIdx.x < n) s_pos[threadIdx.x] = pos[first + threadIdx.x];
+  });
 }
 
 // Rows of a CTA: about 1280 units (5 a thread), one row while there are SMs without one.
@@ -336,23 +339,23 @@ __device__ __forceinline__ int blocks_of(const AppendArgs& a, int b, int& p0) {
 constexpr int kQueriesApart = 2;
 // Rows first .. of the queries, rotated by their sequences' positions.
 __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int first, int* s_pos, float2* s_cs) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = min(a.rows.rows, a.n_tokens - first);
-  for (int r = warp; r < n; r += kThreads / 32) {  // the last sequence that starts at or before the row
-    const int row = first + r;
-    int before = 0;
-    for (int b = lane; b < a.n_seqs; b += 32) before += a.row_start[b] <= row;
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) {
-      int p = -1;
-      if (before && row < a.row_start[before]) {
-        const int p0 = a.pos[before - 1];
-        if (p0 >= 0 && p0 <= a.c.capacity) p = p0 + (row - a.row_start[before - 1]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  rotate_rows(a.rows, first, s_pos, s_cs, [&](int n) {
+    for (int r = warp; r < n; r += kThreads / 32) {  // the last sequence that starts at or before the row
+      const int row = first + r;
+      int before = 0;
+      for (int b = lane; b < a.n_seqs; b += 32) before += a.row_start[b] <= row;
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (lane == 0) {
+        int p = -1;
+        if (before && row < a.row_start[before]) {
+          const int p0 = a.pos[before - 1];
+          if (p0 >= 0 && p0 <= a.c.capacity) p = p0 + (row - a.row_start[before - 1]);
+        }
+        s_pos[r] = p;
       }
-      s_pos[r] = p;
     }
-  }
-  __syncthreads();
-  rotate_rows(a.rows, first, s_pos, s_cs);
+  });
 }
 __global__ void __launch_bounds__(kThreads) k_paged_queries(AppendArgs a) {
   __shared__ __align__(16) float2 s_cs[kAngles];
@@ -360,8 +363,13 @@ __global__ void __launch_bounds__(kThreads) k_paged_queries(AppendArgs a) {
   rotate_queries(a, blockIdx.x * a.rows.rows, s_pos, s_cs);
 }
 
+// f32 values of a warp's block on their way: rows of HD + 4, so that neighbouring slots meet other banks.
+template <int HD>
+constexpr int kBlockFloats = 16 * (HD + 4);
+
 template <int HD, int FMT>
-__global__ void __launch_bounds__(kThreads, 2) k_paged_append(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) k_paged_append(AppendArgs a) {
+  extern __shared__ __align__(16) float s_values[];
   __shared__ __align__(16) float2 s_cs[kAngles];
   __shared__ int s_pos[kMaxRows];
   __shared__ int s_seq, s_block;
@@ -405,63 +413,82 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_append(AppendArgs a) {
   const int lo = max(block * QD_KV_BLOCK, p0) - block * QD_KV_BLOCK;  // slots of new rows
   const int hi = (int)min((int64_t)p0 + t - (int64_t)block * QD_KV_BLOCK, (int64_t)QD_KV_BLOCK);
   const int64_t src0 = row0 + ((int64_t)block * QD_KV_BLOCK - p0);  // row of slot 0
+  const int heads = min(a.heads, a.c.n_kv - h0);
+  float* mine = s_values + warp * kBlockFloats<HD>;
+  auto fetch = [&](int task) {  // the new rows of (head, K or V) into this warp's block
+    const float* src = (task & 1 ? a.v : a.k) + (int64_t)(h0 + (task >> 1)) * HD;
+#pragma unroll 4
+    for (int i = lane; i < 16 * HD / 4; i += 32) {
+      const int slot = i / (HD / 4), c = i % (HD / 4);
+      if (slot >= lo && slot < hi) {
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine + slot * (HD + 4) + 4 * c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + (src0 + slot) * a.stride + 4 * c)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (warp < 2 * heads) fetch(warp);  // under the angles
   int in_page;
   const int page = paged::page_of(a.c, paged::table_row(a.c, seq), block, in_page);
-  if (page < 0) return;
+  if (page < 0) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    return;
+  }
   const int pairs = a.rows.rot.rot / 2;
   for (int i = threadIdx.x; i < (hi - lo) * pairs; i += kThreads) {
     const int r = i / pairs, j = i - r * pairs;
-    s_cs[(lo + r) * pairs + j] = cos_sin(__ldg(a.rows.rot.turns + j), block * QD_KV_BLOCK + lo + r, a.rows.rot.magnitude);
+    s_cs[(lo + r) * (pairs + 2) + j] = cos_sin(__ldg(a.rows.rot.turns + j), block * QD_KV_BLOCK + lo + r, a.rows.rot.magnitude);
   }
   __syncthreads();
 
-  constexpr int kPer = HD / 8, kUnits = 16 * kPer / 32;  // units of a row, of a lane
-  const int heads = min(a.heads, a.c.n_kv - h0);
+  // A lane has units 2 i + (lane & 1) of slot lane / 2, so that a warp's lanes rotate together or not at
+  // all.  The loops are not unrolled: a block's rotation unrolled is 30 KB of code, whose fetching took
+  // longer than its running (40 us for 6000 rows of 8 heads of 128, and 28 so).
+  const int slot = lane >> 1;
+  const bool live = slot >= lo && slot < hi;
   for (int task = warp; task < 2 * heads; task += kThreads / 32) {
     const bool isv = task & 1;
-    const int head = h0 + (task >> 1);
-    const int64_t at = paged::block_index(a.c, page, head, in_page);
+    const int rot = isv ? 0 : a.rows.rot.rot;
+    const int64_t at = paged::block_index(a.c, page, h0 + (task >> 1), in_page);
     float* scale = (isv ? a.c.vs : a.c.ks) + at;
     uint8_t* codes = (isv ? a.c.v : a.c.k) + at * (16 * HD);
-    const float* src = (isv ? a.v : a.k) + (int64_t)head * HD;
-    float4 x[kUnits], y[kUnits];
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int e = lane + 32 * i, slot = e / kPer;
-      const Unit u = unit_of(e % kPer, isv ? 0 : a.rows.rot.rot, a.rows.rot.pairing);
-      x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (slot >= lo && slot < hi) {
-        const float* p = src + (src0 + slot) * a.stride;
-        x[i] = __ldcg(reinterpret_cast<const float4*>(p + u.da));
-        y[i] = __ldcg(reinterpret_cast<const float4*>(p + u.db));
-      }
-    }
+    if (task != warp) fetch(task);
     const float old = lo > 0 ? *scale : 0.f;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int e = lane + 32 * i, slot = e / kPer;
-      if (!isv && 8 * (e % kPer) < a.rows.rot.rot && slot >= lo && slot < hi)
-        turn_unit<true>(x[i], y[i], s_cs + slot * pairs + 4 * (e % kPer), a.rows.rot.pairing);
-      most = max(most, max(abs_max(x[i]), abs_max(y[i])));
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    float* row = mine + slot * (HD + 4);
+    uint32_t most = 0;
+    if (live) {
+#pragma unroll 1
+      for (int u = lane & 1; u < HD / 8; u += 2) {
+        const Unit w = unit_of(u, rot, a.rows.rot.pairing);
+        float4 x = *reinterpret_cast<const float4*>(row + w.da), y = *reinterpret_cast<const float4*>(row + w.db);
+        if (w.rotated) {
+          turn_unit<true>(x, y, s_cs + slot * (pairs + 2) + 4 * u, a.rows.rot.pairing);
+          *reinterpret_cast<float4*>(row + w.da) = x;
+          *reinterpret_cast<float4*>(row + w.db) = y;
+        }
+        most = max(most, max(abs_max(x), abs_max(y)));
+      }
     }
     most = __reduce_max_sync(0xffffffffu, most);
     const bool broken = most >= 0x7F800000u || isnan(old);
-    const float mine = __fdiv_rn(__uint_as_float(most), top_code<FMT>());
-    const float now = broken ? __uint_as_float(0x7FC00000u) : fmaxf(old, mine), inv = __frcp_rn(now);
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int e = lane + 32 * i, slot = e / kPer;
-      if (slot < lo || slot >= hi) continue;
-      const Unit u = unit_of(e % kPer, isv ? 0 : a.rows.rot.rot, a.rows.rot.pairing);
-      uint32_t w0 = 0, w1 = 0;
-      if (now > 0.f && !(now >= 0x1p-100f && codes_by<FMT>(x[i], y[i], inv, w0, w1))) {
-        w0 = codes_of<FMT>(__fdiv_rn(x[i].x, now), __fdiv_rn(x[i].y, now), __fdiv_rn(x[i].z, now), __fdiv_rn(x[i].w, now));
-        w1 = codes_of<FMT>(__fdiv_rn(y[i].x, now), __fdiv_rn(y[i].y, now), __fdiv_rn(y[i].z, now), __fdiv_rn(y[i].w, now));
+    const float top = __fdiv_rn(__uint_as_float(most), top_code<FMT>());
+    const float now = broken ? __uint_as_float(0x7FC00000u) : fmaxf(old, top), inv = __frcp_rn(now);
+    if (live) {
+#pragma unroll 1
+      for (int u = lane & 1; u < HD / 8; u += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(row + 8 * u), y = *reinterpret_cast<const float4*>(row + 8 * u + 4);
+        uint32_t w0 = 0, w1 = 0;
+        if (now > 0.f && !(now >= 0x1p-100f && codes_by<FMT>(x, y, inv, w0, w1))) {
+          w0 = codes_of<FMT>(__fdiv_rn(x.x, now), __fdiv_rn(x.y, now), __fdiv_rn(x.z, now), __fdiv_rn(x.w, now));
+          w1 = codes_of<FMT>(__fdiv_rn(y.x, now), __fdiv_rn(y.y, now), __fdiv_rn(y.z, now), __fdiv_rn(y.w, now));
+        }
+        *reinterpret_cast<uint2*>(codes + slot * HD + 8 * u) = make_uint2(w0, w1);
       }
-      *reinterpret_cast<uint32_t*>(codes + slot * HD + u.da) = w0;
-      *reinterpret_cast<uint32_t*>(codes + slot * HD + u.db) = w1;
     }
+    __syncwarp();  // the block has been read
     if (lo > 0 && now > old) {  // the codes before, in the new steps
       for (int i = lane; i < lo * HD / 4; i += 32) {
         uint32_t* w = reinterpret_cast<uint32_t*>(codes) + i;
@@ -531,7 +558,16 @@ inline qd_status rotation_status(int head_dim, int rot_dim, const uint64_t* turn
 
 template <int HD, int FMT>
 qd_status launch_append(const AppendArgs& a, int ctas, cudaStream_t st) {
-  k_paged_append<HD, FMT><<<ctas, kThreads, 0, st>>>(a);
+  constexpr int kSmem = kThreads / 32 * kBlockFloats<HD> * 4;
+  static std::atomic<bool> done[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QD_ERR_CUDA;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(k_paged_append<HD, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+      return QD_ERR_CUDA;
+    done[dev] = true;
+  }
+  k_paged_append<HD, FMT><<<ctas, kThreads, kSmem, st>>>(a);
   return launch_status();
 }
 
