@@ -240,10 +240,10 @@ __global__ void __launch_bounds__(kThreads) k_rope_tokens(RowsArgs a, const int3
   });
 }
 
-// Rows of a CTA: about 1280 units (5 a thread), one row while there are SMs without one.
+// Rows of a CTA: about 2560 units (10 a thread; 8000 rows of 40 heads of 128 53.2 us with half, 51.2 so, 56.2 with twice as many), one row while there are SMs without one.
 inline int rows_per_cta(int n_tokens, int n_heads, int hd, int rot) {
   const int units = n_heads * (hd / 8);
-  int rows = std::min({kMaxRows, kAngles / (rot / 2), std::max(1280 / units, 1)});
+  int rows = std::min({kMaxRows, kAngles / (rot / 2), std::max(2560 / units, 1)});
   while (rows > 1 && (n_tokens + rows - 1) / rows < 4 * attn_sm_count()) rows /= 2;
   return rows;
 }
