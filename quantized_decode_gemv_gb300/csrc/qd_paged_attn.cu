@@ -765,6 +765,590 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
+// ------------------------------------------------------------------ many rows
+// Sequences of more rows than kFewRows: blocks of 128 on the 5th-generation tensor cores, two threads to a
+// row.  All threads convert a tile's codes (64 positions) to binary16 operands in shared memory, 8 x 8 core
+// matrices of 128 bytes: row r, 16-byte chunk c at core_off(r, c).  One thread issues s = q k^T (tcgen05.mma,
+// M = 128, N = 64, q's parts in shared memory) into one of two score buffers in tensor memory; a row's threads
+// read half of its scores each, exchange their maxima, read the scores again and write the weights' parts over
+// them as the A operand of o = p v (V as it lies, [position][dim], is the transposed B operand); each adds half
+// of the tile's dims to its own registers, rounded.  The next tile's keys are converted and its scores issued
+// under the products with the values, its values converted and the sums made under those scores; two CTAs to an
+// SM fill what is left.  The blocks of all walks, as long as each block's last row sees, are listed by a kernel
+// of one CTA and cut evenly over the CTAs, in heads, sequences and blocks in turn.
+constexpr int kManyThreads = 256, kManyTile = 64, kManyBm = 128;
+constexpr int kFewRows = 64;
+constexpr int kManyStart = 2, kManyMinPer = 4;  // what a walk's start costs, in tiles; tiles of a CTA at least
+constexpr int kListThreads = 1024;
+
+// A block of rows that a walk stands for, with the units (tiles, and kManyStart) of those before it.
+struct Block {
+  int off, seq, r, first_tile, nt, pad[3];
+};
+struct ManyHead {
+  int blocks, units, pad[6];
+};
+// The workspace: what both kernels' cuts need, the list, the parts.
+inline int most_blocks(int group, int n_tokens, int n_seqs) {
+  return (int)((int64_t)n_tokens * group / kManyBm) + std::min(n_tokens, n_seqs);
+}
+inline size_t list_bytes(int group, int n_tokens, int n_seqs) {
+  return sizeof(ManyHead) + (size_t)most_blocks(group, n_tokens, n_seqs) * sizeof(Block);
+}
+struct ManyArgs {
+  AttnArgs a;
+  int min_rows;     // sequences of fewer are the other kernel's
+  int most;         // blocks that the list has room for: all of them where row_start ascends
+  ManyHead* head;   // the list behind it
+  Cut* cuts;
+  float* parts;
+};
+
+__global__ void __launch_bounds__(kListThreads) k_paged_list(ManyArgs m) {
+  __shared__ int s_start[QD_MAX_SEQS + 1], s_sum[kListThreads / 32];
+  __shared__ int s_base;
+  const AttnArgs& a = m.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto scan = [&](int v, int& sum) {  // exclusive over the CTA
+    int upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll 8
+    for (int w = 0; w < kListThreads / 32; ++w) {
+      if (w < warp) before += s_sum[w];
+      all += s_sum[w];
+    }
+    __syncthreads();
+    sum = all;
+    return before + upto - v;
+  };
+  int n = 0, all;
+  if (tid < a.n_seqs) {
+    int row0, p0;
+    const int64_t rows = (int64_t)tokens_of(a, tid, row0, p0) * a.group;
+    if (rows >= m.min_rows) n = (int)((rows + kManyBm - 1) / kManyBm);
+  }
+  const int at = scan(n, all);
+  if (tid <= QD_MAX_SEQS) s_start[tid] = at;  // those behind the last sequence: all of them
+  if (tid == 0) s_base = 0;
+  __syncthreads();
+  Block* list = reinterpret_cast<Block*>(m.head + 1);
+  all = min(all, m.most);
+  for (int i0 = 0; i0 < all; i0 += kListThreads) {
+    const int i = i0 + tid;
+    Block b = {};
+    int len = 0, sum;
+    if (i < all) {
+      int q = 0;
+#pragma unroll 1
+      for (int s = QD_MAX_SEQS / 2; s > 0; s >>= 1)
+        if (s_start[q + s] <= i) q += s;
+      int row0, p0;
+      const int t = tokens_of(a, q, row0, p0);
+      b.seq = q;
+      b.r = i - s_start[q];
+      b.nt = 1;
+      if (p0 >= 0) {
+        const int low = p0 + b.r * kManyBm / a.group, top = p0 + min(t - 1, (b.r * kManyBm + kManyBm - 1) / a.group);
+        b.first_tile = a.window > 0 ? max(low - a.window + 1, 0) / kManyTile : 0;
+        b.nt = top / kManyTile - b.first_tile + 1;
+      }
+      len = b.nt + kManyStart;
+    }
+    const int before = scan(len, sum);
+    b.off = s_base + before;
+    if (i < all) list[i] = b;
+    __syncthreads();
+    if (tid == 0) s_base += sum;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    m.head->blocks = all;
+    m.head->units = s_base;
+  }
+}
+
+__device__ __forceinline__ bool elect_one() {  // one lane of the (whole) calling warp
+  uint32_t p;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(p));
+  return p != 0;
+}
+// 16 consecutive 32-bit columns of this thread's tensor-memory lane read, 8 written
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int HD>
+__device__ __forceinline__ uint32_t core_off(int r, int c) {  // in bytes
+  return (uint32_t)(((r >> 3) * (HD / 8) + c) * 128 + (r & 7) * 16);
+}
+
+// A CTA's part of a walk: n tiles from t0 on.
+struct Segment {
+  int h, r, cnt, row0, p0, seq, first_tile, nt, t0, n;
+};
+template <int HD>
+struct Many {
+  uint4 q[2][kManyBm * HD / 8];    // hi, lo
+  uint4 k[kManyTile * HD / 8], v[kManyTile * HD / 8];
+  float scales[2][2][4];           // of every second tile's blocks: keys, values
+  float ex[2][kManyBm];            // what a row's threads tell each other
+  unsigned long long mbar[2];      // scores, products
+  long long unit;                  // of the next segment: its place in all units,
+  int left, in, block, head;       // the CTA's units from there on, its place in the walk, the walk
+  uint32_t tmem;
+  Segment seg;
+};
+
+template <int HD, int FMT>
+__global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
+  using S = Many<HD>;
+  constexpr int T = kManyTile, BM = kManyBm, ND = HD / 2, kCols = 256;
+  constexpr uint32_t kColsO = 2 * T;
+  constexpr uint32_t kIdescS = tc::idesc_f16(BM, T), kIdescO = tc::idesc_f16(BM, HD) | (1u << 16);  // B: N contiguous
+  static_assert(2 * T + HD <= kCols, "tensor memory of half an SM");
+  constexpr int kPer = HD / 64;  // 16-byte pieces of a tile's keys (values) to a thread
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const AttnArgs& a = ma.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lrow = tid & 127, half = tid >> 7;
+  const int uwarp = __shfl_sync(0xffffffffu, warp, 0);  // known to be the warp's: descriptors stay in uniform registers
+
+  pdl_trigger();
+  int64_t per;
+  {
+    const int n_blocks = ma.head->blocks, head_units = ma.head->units;
+    const int64_t total = (int64_t)head_units * a.c.n_kv;
+    per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kManyMinPer);
+    const int64_t first = (int64_t)blockIdx.x * per;
+    if (tid == 0) ma.cuts[blockIdx.x].parts = 0;
+    if (first >= total) return;
+    if (tid == 0) {
+      const Block* list = reinterpret_cast<const Block*>(ma.head + 1);
+      sm.unit = first;
+      sm.left = (int)min(per, total - first);
+      sm.head = (int)(first / head_units);
+      const int in = (int)(first - (int64_t)sm.head * head_units);
+      int lo = 0, hi = n_blocks;  // the last block with off <= in
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid].off <= in) lo = mid;
+        else hi = mid;
+      }
+      sm.block = lo;
+      sm.in = in - list[lo].off;
+    }
+  }
+  // One thread: the part of the walk (head, block) from unit `in` on into sm.seg, and on to the next; n = 0: none left.
+  auto next_segment = [&] {
+    const Block* list = reinterpret_cast<const Block*>(ma.head + 1);
+    Segment g = {};
+    while (g.n <= 0 && sm.left > 0) {
+      const Block b = list[sm.block];
+      const int in = sm.in, left = sm.left;
+      g.t0 = max(in - kManyStart, 0);
+      g.n = min(b.nt - g.t0, left - (g.t0 + kManyStart - in));
+      g.h = sm.head;
+      g.r = b.r;
+      g.seq = b.seq;
+      g.first_tile = b.first_tile;
+      g.nt = b.nt;
+      g.cnt = tokens_of(a, b.seq, g.row0, g.p0);
+      if (g.n > 0 && g.t0 == 0 && g.n < g.nt) {  // goes on in the next CTAs
+        Cut* cut = ma.cuts + blockIdx.x;
+        cut->parts = (int)((sm.unit - in + kManyStart + g.nt - 1) / per) - (int)blockIdx.x + 1;
+        cut->h = g.h;
+        cut->r = g.r;
+        cut->cnt = g.cnt;
+        cut->row0 = g.row0;
+      }
+      const int rest = kManyStart + b.nt - in;  // units of the walk from here on
+      sm.unit += rest;
+      sm.left = left - rest;
+      sm.in = 0;
+      if (++sm.block == ma.head->blocks) {
+        sm.block = 0;
+        ++sm.head;
+      }
+    }
+    sm.seg = g;
+  };
+
+  const uint32_t mb_s = tc::smem_u32(&sm.mbar[0]), mb_o = tc::smem_u32(&sm.mbar[1]);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&sm.tmem)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    tc::mbar_init(mb_s, 1);
+    tc::mbar_init(mb_o, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    next_segment();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+
+  // A warp takes 8 rows of a tile and 64 dims: 8 rows of one chunk of 8 dims are a core matrix.
+  const int trow = (warp >> (kPer - 1)) * 8 + (lane & 7);            // row of the first piece; the second: 32 rows on
+  const int piece = (lane >> 3) + (kPer == 2 ? 4 * (warp & 1) : 0);  // of 16 dims
+  uint4 kc[kPer], vc[kPer];
+  int page[kPer + 1], in_page[kPer + 1];  // of the tile to be loaded next; the last: of the scale that the thread loads
+  float scale = 0.f;
+  const int32_t* table = nullptr;
+  int head = 0, last = -1;  // of the walk: its kv head, the sequence's last position
+  auto look = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) {
+      const int b = tile * 4 + (i == kPer ? tid & 3 : (trow + 32 * i) >> 4);
+      page[i] = paged::page_of(a.c, table, min(b, max(last, 0) / QD_KV_BLOCK), in_page[i]);
+    }
+  };
+  auto load_codes = [&](const uint8_t* codes, int tile, uint4 (&c)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int row = trow + 32 * i;
+      c[i] = make_uint4(0, 0, 0, 0);  // zeros behind the sequence's end
+      if (page[i] >= 0 && tile * T + row <= last)
+        c[i] = ld_stream_v4(codes + paged::block_index(a.c, page[i], head, in_page[i]) * (16 * HD) + (row & 15) * HD + 16 * piece);
+    }
+  };
+  auto load_scale = [&](int tile) {
+    if (tid >= 8) return;
+    const float* from = tid < 4 ? a.c.ks : a.c.vs;
+    scale = (tile * 4 + (tid & 3)) * QD_KV_BLOCK > last ? 0.f
+            : page[kPer] < 0                            ? __uint_as_float(0x7FC00000u)
+                                                        : __ldg(from + paged::block_index(a.c, page[kPer], head, in_page[kPer]));
+  };
+  auto convert = [&](const uint4 (&c)[kPer], uint4* to) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      uint4 x, y;
+      to_h2x2<FMT>(c[i].x, x.x, x.y);
+      to_h2x2<FMT>(c[i].y, x.z, x.w);
+      to_h2x2<FMT>(c[i].z, y.x, y.y);
+      to_h2x2<FMT>(c[i].w, y.z, y.w);
+      to[core_off<HD>(trow + 32 * i, 2 * piece) / 16] = x;
+      to[core_off<HD>(trow + 32 * i, 2 * piece + 1) / 16] = y;
+    }
+  };
+  // One thread: s = q k^T into score buffer b, lo of q first (what is cut off there does not count)
+  auto issue_s = [&](int b) {
+    tc::fence_after_sync();
+#pragma unroll
+    for (int part = 1; part >= 0; --part)
+#pragma unroll
+      for (int ks = 0; ks < HD / 16; ++ks)
+        tc::mma_f16_ss(tm + T * b, tc::smem_desc(tc::smem_u32(sm.q[part]) + 256 * ks, 128, HD * 16),
+                       tc::smem_desc(tc::smem_u32(sm.k) + 256 * ks, 128, HD * 16), kIdescS, part == 0 || ks > 0);
+    tc::mma_commit(mb_s);
+  };
+  auto issue_o = [&](int b) {
+    tc::fence_after_sync();
+#pragma unroll
+    for (int part = 1; part >= 0; --part)
+#pragma unroll
+      for (int kk = 0; kk < T / 16; ++kk)  // 16 positions: 8 columns of p, two rows of core matrices of v
+        tc::mma_f16_ts(tm + kColsO, tm + T * b + 16 * kk + 8 * part,
+                       tc::smem_desc(tc::smem_u32(sm.v) + HD * 32 * kk, HD * 16, 128), kIdescO, part == 0 || kk > 0);
+    tc::mma_commit(mb_o);
+  };
+
+  bool lost = false;  // a wait has run out: the rows of the walk are NaN
+  uint32_t it = 0;    // tiles of this CTA so far
+  while (sm.seg.n > 0) {
+    float o[ND], m = -INFINITY, l = 0.f, rs, down = 1.f;
+    int ev = 0, emax = -1000, lim, tile, stop, low, top;
+    {
+      const Segment& g = sm.seg;
+      head = g.h;
+      last = g.p0 < 0 ? -1 : g.p0 + g.cnt - 1;
+      table = paged::table_row(a.c, g.seq);
+      tile = g.first_tile + g.t0;
+      stop = tile + g.n;
+      look(tile);
+      low = g.p0 + g.r * BM / a.group;
+      top = g.p0 + min(g.cnt - 1, (g.r * BM + BM - 1) / a.group);
+      // ---- queries
+      const int row = g.r * BM + lrow;
+      const bool live = row < g.cnt * a.group;
+      lim = live && g.p0 >= 0 ? g.p0 + row / a.group : -1;
+      const float4* src = reinterpret_cast<const float4*>(a.q + (live ? row_of(a, HD, a.q_stride, g.row0, g.h, row) : 0) + half * ND);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int d = 0; d < ND; d += 4) {
+        const float4 x = live ? __ldcg(src + d / 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        o[d] = x.x * a.scale;
+        o[d + 1] = x.y * a.scale;
+        o[d + 2] = x.z * a.scale;
+        o[d + 3] = x.w * a.scale;
+        mx = max(mx, abs_max(make_float4(o[d], o[d + 1], o[d + 2], o[d + 3])));
+      }
+      load_codes(a.c.k, tile, kc);
+      load_codes(a.c.v, tile, vc);
+      load_scale(tile);
+      sm.ex[half][lrow] = __uint_as_float(mx);
+      __syncthreads();
+      const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
+      rs = pow2(e);
+      const float f = pow2(-e);
+#pragma unroll
+      for (int c = 0; c < ND / 8; ++c) {
+        uint4 hi, lo;
+        split2(o[8 * c] * f, o[8 * c + 1] * f, hi.x, lo.x);
+        split2(o[8 * c + 2] * f, o[8 * c + 3] * f, hi.y, lo.y);
+        split2(o[8 * c + 4] * f, o[8 * c + 5] * f, hi.z, lo.z);
+        split2(o[8 * c + 6] * f, o[8 * c + 7] * f, hi.w, lo.w);
+        const uint32_t at = core_off<HD>(lrow, half * (ND / 8) + c) / 16;
+        sm.q[0][at] = hi;
+        sm.q[1][at] = lo;
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] = 0.f;
+    }
+    // ---- the first tile
+    convert(kc, sm.k);
+    convert(vc, sm.v);
+    if (tid < 8) sm.scales[it & 1][tid >> 2][tid & 3] = scale;
+    tc::fence_proxy_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (uwarp == 0 && elect_one()) issue_s(it & 1);
+    __syncwarp();
+    look(tile + 1);
+    load_codes(a.c.k, tile + 1, kc);
+    load_codes(a.c.v, tile + 1, vc);
+    load_scale(tile + 1);
+    look(tile + 2);
+    const bool warp_live = sm.seg.r * BM + 32 * (warp & 3) < sm.seg.cnt * a.group;
+
+    for (; tile < stop; ++tile, ++it) {
+      const bool more = tile + 1 < stop;
+      const int base = tile * T;
+      if (!lost && !tc::mbar_wait(mb_s, it & 1u)) lost = true;
+      tc::fence_after_sync();
+      const uint32_t cols = mine + T * (it & 1) + 32 * half;  // this thread's 32 scores: two blocks
+      const bool edge = base + T - 1 > low || (a.window > 0 && base <= top - a.window);
+      const int hi = lim - base - 32 * half, lo = a.window > 0 ? hi - a.window + 1 : 0;  // seen: lo <= column <= hi
+      const float f[2] = {rs * sm.scales[it & 1][0][2 * half], rs * sm.scales[it & 1][0][2 * half + 1]};
+      if (warp_live) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float s[16];
+          tmem_ld16(cols + 16 * c, s);
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (16 * c + j <= hi && 16 * c + j >= lo) mx = fmaxf(mx, s[j] * f[c]);
+          } else {
+            float mc[2] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3])};
+#pragma unroll
+            for (int j = 4; j < 16; j += 4) {
+              mc[0] = fmaxf(mc[0], fmaxf(s[j], s[j + 1]));
+              mc[1] = fmaxf(mc[1], fmaxf(s[j + 2], s[j + 3]));
+            }
+            mx = fmaxf(mx, fmaxf(mc[0], mc[1]) * f[c]);  // scales are not negative
+          }
+        }
+        sm.ex[half][lrow] = mx;
+      }
+      __syncthreads();  // the maximum of the row's other half
+      float corr = 1.f;
+      if (warp_live) {
+        const float mn = fmaxf(m, fmaxf(sm.ex[0][lrow], sm.ex[1][lrow])), mu = mn == -INFINITY ? 0.f : mn;
+        corr = ex2(m - mu);
+        m = mn;
+        const float bias = kBias - mu;
+        // o is in units of 2^ev, as in the kernel for few rows
+        float back = 1.f, vtop = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) vtop = fmaxf(vtop, fabsf(sm.scales[it & 1][1][b]));
+        if (!(vtop * down < 2.f && vtop * down >= 0.25f)) {
+          const int etile = vtop <= 3e38f ? max((int)(__float_as_uint(vtop) >> 23) - 127, -100) : -100;
+          emax = max(emax, etile);
+          const int en = min(max(etile, emax - 60), 126);
+          back = pow2(max(min(ev - en, 126), -126));
+          ev = en;
+          down = pow2(-en);
+        }
+        float sum = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float vs = sm.scales[it & 1][1][2 * half + c] * down;
+          float s[16];
+          tmem_ld16(cols + 16 * c, s);
+          uint32_t ph[8], pl[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float p0 = ex2(fmaf(s[j], f[c], bias)), p1 = ex2(fmaf(s[j + 1], f[c], bias));
+            float y0 = p0 * vs, y1 = p1 * vs;
+            if (edge) {  // whatever the scales
+              const bool in0 = 16 * c + j <= hi && 16 * c + j >= lo, in1 = 16 * c + j + 1 <= hi && 16 * c + j + 1 >= lo;
+              p0 = in0 ? p0 : 0.f;
+              y0 = in0 ? y0 : 0.f;
+              p1 = in1 ? p1 : 0.f;
+              y1 = in1 ? y1 : 0.f;
+            }
+            sum += p0;
+            sum1 += p1;
+            split2(y0, y1, ph[j / 2], pl[j / 2]);
+          }
+          tmem_st8(cols + 16 * c, ph);
+          tmem_st8(cols + 16 * c + 8, pl);
+        }
+        l = fmaf(l, corr, sum + sum1);
+        corr *= back;
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
+      tc::fence_proxy_async_smem();  // the tile's values
+      tc::fence_before_sync();
+      __syncthreads();
+      if (uwarp == 0 && elect_one()) issue_o(it & 1);
+      __syncwarp();
+      if (more) {  // the next tile's scores
+        convert(kc, sm.k);
+        if (tid < 8) sm.scales[(it + 1) & 1][tid >> 2][tid & 3] = scale;
+        load_codes(a.c.k, tile + 2, kc);
+        load_scale(tile + 2);
+        tc::fence_proxy_async_smem();
+        tc::fence_before_sync();
+        __syncthreads();
+        if (uwarp == 0 && elect_one()) issue_s((it + 1) & 1);
+        __syncwarp();
+      }
+      if (!lost && !tc::mbar_wait(mb_o, it & 1u)) lost = true;
+      tc::fence_after_sync();
+      if (more) {
+        convert(vc, sm.v);
+        load_codes(a.c.v, tile + 2, vc);
+        look(tile + 3);
+      }
+      if (warp_live) {
+#pragma unroll
+        for (int d0 = 0; d0 < ND; d0 += 16) {
+          float t[16];
+          tmem_ld16(mine + kColsO + ND * half + d0, t);
+#pragma unroll
+          for (int d = 0; d < 16; ++d) o[d0 + d] = fmaf(o[d0 + d], corr, t[d]);
+        }
+      }
+      tc::fence_before_sync();
+    }
+
+    // ---- the end of this CTA's part of the walk
+    const int t0 = sm.seg.t0, row = sm.seg.r * BM + lrow, rows = sm.seg.cnt * a.group;
+    const bool whole = t0 == 0 && sm.seg.n == sm.seg.nt;
+    const int64_t to = row < rows ? row_of(a, HD, (int64_t)a.n_heads * HD, sm.seg.row0, sm.seg.h, row) : 0;
+    if (__syncthreads_or(lost)) l = NAN;  // every thread has read `ex`
+    sm.ex[half][lrow] = l;
+    if (tid == 0) next_segment();
+    __syncthreads();
+    const float lt = l + sm.ex[half ^ 1][lrow];
+    float* part = ma.parts + ((int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * part_floats(BM, HD);
+    if (!whole && half == 0) {
+      part[lrow] = m;
+      part[BM + lrow] = lt;
+    }
+    if (!whole || row < rows) {
+      const float unit = pow2(min(max(ev, -126), 127)) * (!whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt);
+      float4* dst = reinterpret_cast<float4*>((whole ? a.out + to : part + 2 * BM + lrow * HD) + half * ND);
+#pragma unroll
+      for (int d = 0; d < ND; d += 4)
+        dst[d / 4] = make_float4(o[d] * unit, o[d + 1] * unit, o[d + 2] * unit, o[d + 3] * unit);
+    }
+    __syncthreads();  // `ex` is read
+  }
+  tc::fence_before_sync();
+  if (__syncthreads_or(lost) && tid == 0) {  // products that nobody waited for
+    tc::mbar_wait(mb_s, (it - 1) & 1u);
+    tc::mbar_wait(mb_o, (it - 1) & 1u);
+  }
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kCols) : "memory");
+}
+
+// The parts of a cut walk of k_paged_many, in the CTAs' order: a warp to a row.
+constexpr int kJoinRows = 8;  // warps of a block
+template <int HD>
+__global__ void __launch_bounds__(kJoinRows * 32) k_paged_join_many(ManyArgs ma) {
+  constexpr int BM = kManyBm, kAtOnce = 8;
+  using V = typename std::conditional<HD == 128, float4, float2>::type;
+  pdl_wait();
+  const AttnArgs& a = ma.a;
+  const Cut* cut = ma.cuts + blockIdx.x;
+  const int n = __ldcg(&cut->parts), lane = threadIdx.x & 31, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  if (n == 0) return;
+  const int at = __ldcg(&cut->r) * BM + r;
+  if (at >= __ldcg(&cut->cnt) * a.group) return;
+  float m = -INFINITY, l = 0.f;
+  float o[4] = {};
+  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+    float mc[kAtOnce], lc[kAtOnce];
+    V oc[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float* p = ma.parts + ((int64_t)(blockIdx.x + i0 + i) * 2 + (i0 + i == 0 ? 1 : 0)) * part_floats(BM, HD);
+      const bool live = i0 + i < n;
+      mc[i] = live ? __ldcg(p + r) : -INFINITY;
+      lc[i] = live ? __ldcg(p + BM + r) : 0.f;
+      oc[i] = live ? __ldcg(reinterpret_cast<const V*>(p + 2 * BM + r * HD) + lane) : V{};
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, mc[i]);
+    const float f = m == -INFINITY ? l : ex2(m - top);  // without a maximum l is 0 or NaN
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] *= f;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float g = mc[i] == -INFINITY ? lc[i] : ex2(mc[i] - top);
+      l = fmaf(lc[i], g, l);
+      const float* x = reinterpret_cast<const float*>(&oc[i]);
+#pragma unroll
+      for (int d = 0; d < (int)(sizeof(V) / 4); ++d) o[d] = fmaf(x[d], g, o[d]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  V out;
+  float* x = reinterpret_cast<float*>(&out);
+#pragma unroll
+  for (int d = 0; d < (int)(sizeof(V) / 4); ++d) x[d] = o[d] * inv;
+  reinterpret_cast<V*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, __ldcg(&cut->row0), __ldcg(&cut->h), at))[lane] = out;
+}
+
 // ------------------------------------------------------------------ host
 inline bool attn_shape_ok(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs) {
   return paged::cache_status(kv, n_seqs) == QD_OK && n_heads >= 1 && n_heads % kv->n_kv_heads == 0 &&
@@ -801,8 +1385,49 @@ qd_status launch_few(AttnArgs a, cudaStream_t st) {
   return launch_k(k_paged_join<HD, S::kBm>, dim3((unsigned)ctas, S::kBm), dim3(kJoinThreads), 0, st, true, a);
 }
 
+// Whether a call can have sequences for the kernel of many rows: their rows are at most n_tokens x group, and a
+// batch with no more tokens than sequences has one each.
+// The units of a head must fit an int.
+inline bool has_many(int group, int n_tokens, int n_seqs, int capacity) {
+  return (int64_t)n_tokens * group > kFewRows && n_tokens > n_seqs &&
+         (int64_t)most_blocks(group, n_tokens, n_seqs) * (capacity / kManyTile + 1 + kManyStart) < (1ll << 31);
+}
+inline int many_ctas() { return std::min(2 * attn_sm_count(), kMaxCtas); }
+
 template <int HD, int FMT>
-qd_status launch_attn(const AttnArgs& a, cudaStream_t st) {
+qd_status launch_many(const ManyArgs& m, cudaStream_t st) {
+  using S = Many<HD>;
+  static std::atomic<bool> done[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QD_ERR_CUDA;
+  const auto kern = k_paged_many<HD, FMT>;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S)) != cudaSuccess)
+      return QD_ERR_CUDA;
+    done[dev] = true;
+  }
+  k_paged_list<<<1, kListThreads, 0, st>>>(m);
+  kern<<<many_ctas(), kManyThreads, sizeof(S), st>>>(m);
+  const qd_status s = launch_status();
+  if (s != QD_OK) return s;
+  return launch_k(k_paged_join_many<HD>, dim3((unsigned)many_ctas(), kManyBm / kJoinRows), dim3(kJoinRows * 32), 0, st, true, m);
+}
+
+template <int HD, int FMT>
+qd_status launch_attn(AttnArgs a, cudaStream_t st) {
+  if (has_many(a.group, a.n_tokens, a.n_seqs, a.c.capacity)) {
+    ManyArgs m;
+    m.a = a;
+    m.min_rows = a.n_seqs == 1 ? 1 : kFewRows + 1;
+    m.most = most_blocks(a.group, a.n_tokens, a.n_seqs);
+    unsigned char* at = reinterpret_cast<unsigned char*>(a.ws);  // one kernel's parts are joined before the other's begin
+    m.cuts = reinterpret_cast<Cut*>(at);
+    m.head = reinterpret_cast<ManyHead*>(at + kCutBytes);
+    m.parts = reinterpret_cast<float*>(at + kCutBytes + align_up(list_bytes(a.group, a.n_tokens, a.n_seqs), 256));
+    const qd_status s = launch_many<HD, FMT>(m, st);
+    if (s != QD_OK || a.n_seqs == 1) return s;
+    a.max_rows = kFewRows;
+  }
   return rows16(a.group, a.n_tokens, a.n_seqs) ? launch_few<HD, FMT, true>(a, st) : launch_few<HD, FMT, false>(a, st);
 }
 
@@ -815,8 +1440,13 @@ extern "C" {
 
 size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs) {
   if (!attn_shape_ok(kv, n_heads, n_tokens, n_seqs)) return 0;
-  const int64_t ctas = std::min(attn_sm_count() * 4, kMaxCtas);  // whatever the call: it serves them all
-  return kCutBytes + (size_t)ctas * 2 * part_floats(16, kv->head_dim) * sizeof(float);
+  const int group = n_heads / kv->n_kv_heads;
+  const size_t ctas = (size_t)std::min(attn_sm_count() * 3, kMaxCtas);  // of few rows, whatever the call
+  const size_t few = ctas * 2 * part_floats(16, kv->head_dim) * sizeof(float);
+  if ((int64_t)n_tokens * group <= kFewRows) return kCutBytes + few;
+  const size_t many = align_up(list_bytes(group, n_tokens, n_seqs), 256) +
+                      (size_t)many_ctas() * 2 * part_floats(kManyBm, kv->head_dim) * sizeof(float);
+  return kCutBytes + std::max(few, many);
 }
 
 qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_heads, int n_tokens,
