@@ -779,6 +779,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
 constexpr int kManyThreads = 256, kManyTile = 64, kManyBm = 128;
 constexpr int kFewRows = 64;
 constexpr int kManyStart = 2, kManyMinPer = 4;  // what a walk's start costs, in tiles; tiles of a CTA at least
+constexpr int kManyJoin = 4;                     // what the join costs, in tiles
 constexpr int kListThreads = 1024;
 
 // A block of rows that a walk stands for, with the units (tiles, and kManyStart) of those before it.
@@ -786,7 +787,9 @@ struct Block {
   int off, seq, r, first_tile, nt, pad[3];
 };
 struct ManyHead {
-  int blocks, units, pad[6];
+  int blocks, units;  // of a head
+  int whole;          // 1: no walk is cut
+  int pad[5];
 };
 // The workspace: what both kernels' cuts need, the list, the parts.
 inline int most_blocks(int group, int n_tokens, int n_seqs) {
@@ -798,6 +801,7 @@ inline size_t list_bytes(int group, int n_tokens, int n_seqs) {
 struct ManyArgs {
   AttnArgs a;
   int min_rows;     // sequences of fewer are the other kernel's
+  int ctas;
   int most;         // blocks that the list has room for: all of them where row_start ascends
   ManyHead* head;   // the list behind it
   Cut* cuts;
@@ -806,7 +810,7 @@ struct ManyArgs {
 
 __global__ void __launch_bounds__(kListThreads) k_paged_list(ManyArgs m) {
   __shared__ int s_start[QD_MAX_SEQS + 1], s_sum[kListThreads / 32];
-  __shared__ int s_base;
+  __shared__ int s_base, s_longest;
   const AttnArgs& a = m.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto scan = [&](int v, int& sum) {  // exclusive over the CTA
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(kListThreads) k_paged_list(ManyArgs m) {
   }
   const int at = scan(n, all);
   if (tid <= QD_MAX_SEQS) s_start[tid] = at;  // those behind the last sequence: all of them
-  if (tid == 0) s_base = 0;
+  if (tid == 0) s_base = s_longest = 0;
   __syncthreads();
   Block* list = reinterpret_cast<Block*>(m.head + 1);
   all = min(all, m.most);
@@ -860,6 +864,7 @@ __global__ void __launch_bounds__(kListThreads) k_paged_list(ManyArgs m) {
         b.nt = top / kManyTile - b.first_tile + 1;
       }
       len = b.nt + kManyStart;
+      atomicMax(&s_longest, len);
     }
     const int before = scan(len, sum);
     b.off = s_base + before;
@@ -871,6 +876,10 @@ __global__ void __launch_bounds__(kListThreads) k_paged_list(ManyArgs m) {
   if (tid == 0) {
     m.head->blocks = all;
     m.head->units = s_base;
+    // Cut walks are even, but their parts are written, read and joined (66 KB each); whole ones cost nothing
+    // more where there are enough of them and none is much longer than a CTA's share.
+    const int64_t walks = (int64_t)all * a.c.n_kv, share = ((int64_t)s_base * a.c.n_kv + m.ctas - 1) / m.ctas;
+    m.head->whole = walks >= m.ctas / 2 && (walks + m.ctas - 1) / m.ctas * s_longest <= share * 8 / 5 + kManyJoin;
   }
 }
 
@@ -917,9 +926,11 @@ struct Many {
   uint4 q[2][kManyBm * HD / 8];    // hi, lo
   uint4 k[kManyTile * HD / 8], v[kManyTile * HD / 8];
   float scales[2][2][4];           // of every second tile's blocks: keys, values
+  uint32_t place[2][4];            // of every second tile: its blocks in the cache, kNoPage
   float ex[2][kManyBm];            // what a row's threads tell each other
   unsigned long long mbar[2];      // scores, products
-  long long unit;                  // of the next segment: its place in all units,
+  int whole;
+  long long unit;                  // of the next segment: its place in all units (of walks where they are whole),
   int left, in, block, head;       // the CTA's units from there on, its place in the walk, the walk
   uint32_t tmem;
   Segment seg;
@@ -948,8 +959,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kManyMinPer);
     const int64_t first = (int64_t)blockIdx.x * per;
     if (tid == 0) ma.cuts[blockIdx.x].parts = 0;
-    if (first >= total) return;
-    if (tid == 0) {
+    const int whole = ma.head->whole;
+    if (whole ? (int64_t)blockIdx.x >= (int64_t)n_blocks * a.c.n_kv : first >= total) return;
+    if (tid == 0) sm.whole = whole;
+    if (tid == 0 && whole) sm.unit = blockIdx.x;
+    if (tid == 0 && !whole) {
       const Block* list = reinterpret_cast<const Block*>(ma.head + 1);
       sm.unit = first;
       sm.left = (int)min(per, total - first);
@@ -969,6 +983,21 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
   auto next_segment = [&] {
     const Block* list = reinterpret_cast<const Block*>(ma.head + 1);
     Segment g = {};
+    if (sm.whole) {  // every gridDim.x-th walk, the last blocks of a sequence, which see most, first
+      const int n_blocks = ma.head->blocks;
+      if (sm.unit < (int64_t)n_blocks * a.c.n_kv) {
+        const Block b = list[n_blocks - 1 - (int)(sm.unit / a.c.n_kv)];
+        g.h = (int)(sm.unit % a.c.n_kv);
+        g.r = b.r;
+        g.seq = b.seq;
+        g.first_tile = b.first_tile;
+        g.n = g.nt = b.nt;
+        g.cnt = tokens_of(a, b.seq, g.row0, g.p0);
+        sm.unit += gridDim.x;
+      }
+      sm.seg = g;
+      return;
+    }
     while (g.n <= 0 && sm.left > 0) {
       const Block b = list[sm.block];
       const int in = sm.in, left = sm.left;
@@ -1021,33 +1050,49 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
   // A warp takes 8 rows of a tile and 64 dims: 8 rows of one chunk of 8 dims are a core matrix.
   const int trow = (warp >> (kPer - 1)) * 8 + (lane & 7);            // row of the first piece; the second: 32 rows on
   const int piece = (lane >> 3) + (kPer == 2 ? 4 * (warp & 1) : 0);  // of 16 dims
+  constexpr uint32_t kNoPage = ~0u;
+  const uint32_t in_block = (trow & 15) * HD + 16 * piece;
   uint4 kc[kPer], vc[kPer];
-  int page[kPer + 1], in_page[kPer + 1];  // of the tile to be loaded next; the last: of the scale that the thread loads
-  float scale = 0.f;
-  const int32_t* table = nullptr;
   int head = 0, last = -1;  // of the walk: its kv head, the sequence's last position
+  // Eight threads: where the blocks of a tile are, two tiles before the tile, and their scales, one before
+  // (a thread a block and K or V).
+  const int32_t* table = nullptr;
+  uint32_t my_place = kNoPage;
+  float scale = 0.f;
   auto look = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i <= kPer; ++i) {
-      const int b = tile * 4 + (i == kPer ? tid & 3 : (trow + 32 * i) >> 4);
-      page[i] = paged::page_of(a.c, table, min(b, max(last, 0) / QD_KV_BLOCK), in_page[i]);
-    }
+    if (tid >= 8) return;
+    int in_page;
+    const int page = paged::page_of(a.c, table, min(tile * 4 + (tid & 3), max(last, 0) / QD_KV_BLOCK), in_page);
+    my_place = page < 0 ? kNoPage : (uint32_t)((page * a.c.n_kv + head) * a.c.per_page + in_page);
+  };
+  auto tell = [&](int tile) {
+    if (tid < 4) sm.place[tile & 1][tid] = my_place;
+  };
+  auto load_scale = [&](int tile) {  // looked up before
+    if (tid >= 8) return;
+    scale = (tile * 4 + (tid & 3)) * QD_KV_BLOCK > last ? 0.f
+            : my_place == kNoPage                       ? __uint_as_float(0x7FC00000u)
+                                                        : __ldg((tid < 4 ? a.c.ks : a.c.vs) + my_place);
   };
   auto load_codes = [&](const uint8_t* codes, int tile, uint4 (&c)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int row = trow + 32 * i;
-      c[i] = make_uint4(0, 0, 0, 0);  // zeros behind the sequence's end
-      if (page[i] >= 0 && tile * T + row <= last)
-        c[i] = ld_stream_v4(codes + paged::block_index(a.c, page[i], head, in_page[i]) * (16 * HD) + (row & 15) * HD + 16 * piece);
+      const uint32_t at = sm.place[tile & 1][(trow >> 4) + 2 * i];
+      const bool live = at != kNoPage && tile * T + trow + 32 * i <= last;
+      const uint8_t* from = codes + ((uint64_t)at * (16 * HD) + in_block);
+      asm volatile(  // zeros behind the sequence's end
+          "{\n"
+          ".reg .pred p;\n"
+          "setp.ne.u32 p, %5, 0;\n"
+          "mov.u32 %0, 0;\n"
+          "mov.u32 %1, 0;\n"
+          "mov.u32 %2, 0;\n"
+          "mov.u32 %3, 0;\n"
+          "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+          "}\n"
+          : "=&r"(c[i].x), "=&r"(c[i].y), "=&r"(c[i].z), "=&r"(c[i].w)
+          : "l"(from), "r"((uint32_t)live));
     }
-  };
-  auto load_scale = [&](int tile) {
-    if (tid >= 8) return;
-    const float* from = tid < 4 ? a.c.ks : a.c.vs;
-    scale = (tile * 4 + (tid & 3)) * QD_KV_BLOCK > last ? 0.f
-            : page[kPer] < 0                            ? __uint_as_float(0x7FC00000u)
-                                                        : __ldg(from + paged::block_index(a.c, page[kPer], head, in_page[kPer]));
   };
   auto convert = [&](const uint4 (&c)[kPer], uint4* to) {
 #pragma unroll
@@ -1096,6 +1141,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       tile = g.first_tile + g.t0;
       stop = tile + g.n;
       look(tile);
+      tell(tile);
+      load_scale(tile);
       low = g.p0 + g.r * BM / a.group;
       top = g.p0 + min(g.cnt - 1, (g.r * BM + BM - 1) / a.group);
       // ---- queries
@@ -1113,11 +1160,12 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         o[d + 3] = x.w * a.scale;
         mx = max(mx, abs_max(make_float4(o[d], o[d + 1], o[d + 2], o[d + 3])));
       }
-      load_codes(a.c.k, tile, kc);
-      load_codes(a.c.v, tile, vc);
-      load_scale(tile);
       sm.ex[half][lrow] = __uint_as_float(mx);
       __syncthreads();
+      load_codes(a.c.k, tile, kc);
+      load_codes(a.c.v, tile, vc);
+      look(tile + 1);
+      tell(tile + 1);
       const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
       rs = pow2(e);
       const float f = pow2(-e);
@@ -1144,7 +1192,6 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     __syncthreads();
     if (uwarp == 0 && elect_one()) issue_s(it & 1);
     __syncwarp();
-    look(tile + 1);
     load_codes(a.c.k, tile + 1, kc);
     load_codes(a.c.v, tile + 1, vc);
     load_scale(tile + 1);
@@ -1154,7 +1201,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     for (; tile < stop; ++tile, ++it) {
       const bool more = tile + 1 < stop;
       const int base = tile * T;
-      if (!lost && !tc::mbar_wait(mb_s, it & 1u)) lost = true;
+      if (!lost && !tc::mbar_wait_sleep(mb_s, it & 1u)) lost = true;
       tc::fence_after_sync();
       const uint32_t cols = mine + T * (it & 1) + 32 * half;  // this thread's 32 scores: two blocks
       const bool edge = base + T - 1 > low || (a.window > 0 && base <= top - a.window);
@@ -1238,7 +1285,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       if (more) {  // the next tile's scores
         convert(kc, sm.k);
         if (tid < 8) sm.scales[(it + 1) & 1][tid >> 2][tid & 3] = scale;
-        load_codes(a.c.k, tile + 2, kc);
+        tell(tile + 2);
         load_scale(tile + 2);
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
@@ -1246,7 +1293,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         if (uwarp == 0 && elect_one()) issue_s((it + 1) & 1);
         __syncwarp();
       }
-      if (!lost && !tc::mbar_wait(mb_o, it & 1u)) lost = true;
+      if (more) load_codes(a.c.k, tile + 2, kc);
+      if (!lost && !tc::mbar_wait_sleep(mb_o, it & 1u)) lost = true;
       tc::fence_after_sync();
       if (more) {
         convert(vc, sm.v);
@@ -1385,11 +1433,19 @@ qd_status launch_few(AttnArgs a, cudaStream_t st) {
   return launch_k(k_paged_join<HD, S::kBm>, dim3((unsigned)ctas, S::kBm), dim3(kJoinThreads), 0, st, true, a);
 }
 
-// Whether a call can have sequences for the kernel of many rows: their rows are at most n_tokens x group, and a
-// batch with no more tokens than sequences has one each.
+// Whether a call takes the kernel for many rows: it can have sequences of so many (their rows are at most n_tokens
+// x group, and a batch with no more tokens than sequences is taken to have one each), and there is work for it, counted
+// in positions of a 16-row block as the cache has room for, a start as 1000 of them.  Few against many rows, in us:
+//   1 head, 7 ragged sequences of 45 x 8 rows at most, 3000 positions (work 0.3e6)    14 33
+//   8 heads, 20 x 4 rows, 20000 positions (0.8e6)                                     64 72
+//   3 heads, 4 ragged sequences of 300 x 3 rows at most, 1500 positions (1.0e6)       31 41
+//   8 heads, 64 x 4 rows, 32700 positions (4.3e6)                                    156 86
+//   8 heads of 128, 1024 x 4 rows, 2040 positions (6.2e6)                            277 138
 // The units of a head must fit an int.
-inline bool has_many(int group, int n_tokens, int n_seqs, int capacity) {
-  return (int64_t)n_tokens * group > kFewRows && n_tokens > n_seqs &&
+constexpr int64_t kManyWork = 2000000;
+inline bool has_many(int n_kv, int group, int n_tokens, int n_seqs, int capacity) {
+  const int64_t rows = (int64_t)n_tokens * group;
+  return rows > kFewRows && n_tokens > n_seqs && n_kv * ((rows + 15) / 16) * ((int64_t)capacity + 1000) > kManyWork &&
          (int64_t)most_blocks(group, n_tokens, n_seqs) * (capacity / kManyTile + 1 + kManyStart) < (1ll << 31);
 }
 inline int many_ctas() { return std::min(2 * attn_sm_count(), kMaxCtas); }
@@ -1415,11 +1471,12 @@ qd_status launch_many(const ManyArgs& m, cudaStream_t st) {
 
 template <int HD, int FMT>
 qd_status launch_attn(AttnArgs a, cudaStream_t st) {
-  if (has_many(a.group, a.n_tokens, a.n_seqs, a.c.capacity)) {
+  if (has_many(a.c.n_kv, a.group, a.n_tokens, a.n_seqs, a.c.capacity)) {
     ManyArgs m;
     m.a = a;
     m.min_rows = a.n_seqs == 1 ? 1 : kFewRows + 1;
     m.most = most_blocks(a.group, a.n_tokens, a.n_seqs);
+    m.ctas = many_ctas();
     unsigned char* at = reinterpret_cast<unsigned char*>(a.ws);  // one kernel's parts are joined before the other's begin
     m.cuts = reinterpret_cast<Cut*>(at);
     m.head = reinterpret_cast<ManyHead*>(at + kCutBytes);
