@@ -512,7 +512,8 @@ typedef enum { QD_KV_I8 = 0, QD_KV_E4M3 = 1 } qd_kv_fmt;
  * most 1024; max_pages * page_tokens at most 2^30; 1 <= max_seqs <= QD_MAX_SEQS.  Pages and scales
  * need no initialisation: what lies behind a sequence's end does not matter.  An entry outside
  * [0, n_pages) is no page: nothing is stored through it, and rows that attend to or read its
- * positions give NaN. */
+ * positions give NaN.  qd_paged_append stores numbers only (of the E4M3 codes not 0x7F and 0xFF, which are
+ * NaN); a page filled otherwise must hold none of those at a sequence's positions. */
 typedef struct {
     void *k_pages, *v_pages;
     float *k_scale, *v_scale;
@@ -583,12 +584,14 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
  * at t*q_stride (a multiple of 4); out: f32 [n_tokens][n_heads][head_dim].  n_heads % n_kv_heads
  * == 0, group size <= 16; scale finite.  The rows of a sequence with pos[b] < 0, or whose last
  * position is behind the last page, are zeros.  The result does not depend on what pages hold behind
- * a row's position, but for the scale of the block that holds it.  A non-finite q gives NaN in its
+ * the sequence's last position, but for the scale of the block that holds it, nor, but for rounding, on
+ * what they hold behind a row's.  A non-finite q gives NaN in its
  * own row and head alone; a block with a NaN scale gives NaN to the rows that see a position of it,
  * and to no other.  Results are the same bits on every run.
  * Arithmetic: codes enter the products exactly, queries and weights times scales in two parts (22 bits
  * of each from 2^-15 of the largest of its row on, 2^-38 of that below; scales 2^60 times smaller than
- * others of the row do not count); sums, running maxima and outputs are f32.
+ * others of the row do not count); sums, running maxima and outputs are f32.  Should a wait inside the
+ * kernel run out (about a second, on a GPU that is out of order), the rows that it concerns are NaN.
  * workspace (device): qd_paged_attn_workspace bytes (0: a shape the call does not take; no fewer
  * for more tokens or sequences); two calls that can run at the same time need one each. */
 size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens, int n_seqs);

@@ -43,7 +43,8 @@ inline qd_status cache_status(const qd_paged_kv* kv, int n_seqs) {
   if (kv->head_dim != 64 && kv->head_dim != 128) return QD_ERR_UNSUPPORTED;
   if (kv->n_pages < 1 || kv->page_tokens < QD_KV_BLOCK || kv->page_tokens > 1024 || kv->page_tokens % QD_KV_BLOCK ||
       kv->n_kv_heads < 1 || kv->n_kv_heads > 4096 || kv->max_pages < 1 || kv->max_seqs < 1 ||
-      kv->max_seqs > QD_MAX_SEQS || (int64_t)kv->max_pages * kv->page_tokens > (1ll << 30) || n_seqs < 1 ||
+      kv->max_seqs > QD_MAX_SEQS || (int64_t)kv->max_pages * kv->page_tokens > (1ll << 30) ||
+      (int64_t)kv->n_pages * kv->n_kv_heads > ((1ll << 31) - 1) / (kv->page_tokens / QD_KV_BLOCK) || n_seqs < 1 ||
       n_seqs > kv->max_seqs)
     return QD_ERR_SHAPE;
   if (!aligned16(kv->k_pages) || !aligned16(kv->v_pages) || !aligned4(kv->k_scale) || !aligned4(kv->v_scale) ||

@@ -249,7 +249,16 @@ __device__ __forceinline__ int64_t row_of(const AttnArgs& a, int hd, int64_t str
 // serves both.  The operands' columns are free to choose as long as both sides agree: a lane's part
 // of a key row is 16 bytes as they lie (its dims of q are the same 16), that of a value row 8 or
 // 16, and its outputs are neighbouring dims; nothing is transposed through shared memory, and two
-// values of a dim are paired by byte permutations on their way to binary16.
+// values of a dim are paired by byte permutations on their way to binary16 (2.5 instructions a pair of keys,
+// 3 of values).
+// What bounds it: instructions.  A warp needs about 420 for 4 KB of the cache (176 of them turn codes into
+// operands, 32 are products), of which an SM issues 1.8 to 2.2 a cycle, where HBM brings 4 KB in 174 cycles.  100
+// sequences of 32/8 heads of 128, 4000 positions on average: 166 us (floor 123); 131000 positions of one: 58 (40);
+// 16 of 32/32 heads of 64, 2000 on average: 40 (20, and 8 of the starts and the join).  Against: tiles of 4 KB at
+// head dimension 128 178 us instead of 166, tiles of 8 KB at 64 46 instead of 40; four CTAs of 128 registers a
+// thread 253 (they spill) and 44; CTAs of two warps 227 and 39; q's fragments in registers 171 and 38;
+// o = p v instead of its transpose, where both parts of a weight have accumulators of their own, 171 and 41;
+// kStart 3 166 and 40.5, 5 169 and 43.
 template <int HD, bool R16>
 struct Few {
   static constexpr int kW = 4, kStages = HD == 64 ? 3 : 2;
@@ -775,7 +784,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
 // of the tile's dims to its own registers, rounded.  The next tile's keys are converted and its scores issued
 // under the products with the values, its values converted and the sums made under those scores; two CTAs to an
 // SM fill what is left.  The blocks of all walks, as long as each block's last row sees, are listed by a kernel
-// of one CTA and cut evenly over the CTAs, in heads, sequences and blocks in turn.
+// of one CTA and taken whole or cut evenly over the CTAs, in heads, sequences and blocks in turn.
+// What bounds it: the latency of a tile's chain between its three barriers (1.3 of 4 instructions a cycle; a tile
+// of 128 rows takes a CTA 3.7 us alone on an SM).  8 heads of 128, 1024 x 4 rows, 2040 positions: 138 us, of which the
+// list 5 and the join that finds nothing 3 (floor 13: the products once); in copies without the loads 122 us,
+// without the products 114, without the conversions 101, without half of the sums 122.  Walks cut: 151 us, 17 of them
+// the join.  Blocks of 16 rows: 277 us.
 constexpr int kManyThreads = 256, kManyTile = 64, kManyBm = 128;
 constexpr int kFewRows = 64;
 constexpr int kManyStart = 2, kManyMinPer = 4;  // what a walk's start costs, in tiles; tiles of a CTA at least
@@ -1531,7 +1545,7 @@ qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride,
   a.row_start = row_start;
   a.pos = pos;
   a.scale = scale * 1.4426950408889634f;
-  a.window = window;
+  a.window = window < a.c.capacity ? window : 0;  // a wider one hides nothing
   a.max_rows = 1 << 30;
   a.ws = static_cast<float*>(workspace);
   cudaStream_t st = (cudaStream_t)stream;

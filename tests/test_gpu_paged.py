@@ -318,6 +318,7 @@ SHAPES = [
     (4, 1, 128, 64, [700], [257], 250),
     (12, 3, 64, 16, [2500], [140], 0),
     (2, 2, 128, 16, [3000, 2], [2, 1], 5000),
+    (4, 2, 64, 16, [300, 90], [70, 2], 2**31 - 1),
 ]
 
 

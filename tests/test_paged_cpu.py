@@ -95,7 +95,7 @@ def _cache_refusals(call, reads_scale_alignment=True):
     assert call(_kv(fmt=2)) == 4 and call(_kv(fmt=-1)) == 4
     for c in (dict(n_pages=0), dict(page_tokens=8), dict(page_tokens=24), dict(page_tokens=1040), dict(page_tokens=0),
               dict(n_kv_heads=0), dict(n_kv_heads=4097), dict(max_pages=0), dict(max_seqs=0), dict(max_seqs=257),
-              dict(max_seqs=2), dict(max_pages=2**26)):
+              dict(max_seqs=2), dict(max_pages=2**26), dict(n_pages=2**30)):
         assert call(_kv(**c)) == 2, c
 
 
