@@ -557,6 +557,30 @@ def test_prompt_then_steps(qd, fmt, hd, group):
         assert np.all(np.abs((got - want).cpu().numpy()) <= 2 * tol)
 
 
+def test_the_readme_example_runs(qd):
+    """The lines of README.md on the paged cache, over names as it uses them."""
+    import os
+
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    code = next(c for c in text.split("```python")[1:] if "qd.PagedKV(" in c).split("```")[0]
+    heads, kv_heads, head_dim, n_seqs, max_ctx = 8, 2, 64, 2, 200
+    c = Cache(np.random.default_rng(26), n_seqs, kv_heads, head_dim, 64, [150, 200], "i8")
+    _, t = _handle(qd, c)
+    names = dict(qd=qd, torch=torch, k_pages=t["k"], v_pages=t["v"], k_scale=t["ks"], v_scale=t["vs"], page_table=t["table"],
+                 heads=heads, kv_heads=kv_heads, head_dim=head_dim, n_seqs=n_seqs, max_ctx=max_ctx, n_tokens=51,
+                 qkv=torch.randn(51, heads + 2 * kv_heads, head_dim, device="cuda"),
+                 q=torch.zeros(51, heads, head_dim, device="cuda"), out=torch.full((51, heads, head_dim), 9.0, device="cuda"),
+                 row_start=dev(_starts([50, 1])), pos=dev(np.array([100, 199], np.int32)),
+                 lengths=dev(np.array([150, 200], np.int32)),
+                 k_cache=torch.zeros(n_seqs, kv_heads, max_ctx, head_dim, device="cuda"),
+                 v_cache=torch.zeros(n_seqs, kv_heads, max_ctx, head_dim, device="cuda"))
+    exec(code, names)
+    k, v, q = names["k_cache"], names["v_cache"], names["q"]
+    w = (q[50].view(2, 4, 64).double() @ k[1].double().transpose(1, 2) / 8).softmax(-1)
+    assert (names["out"][50].view(2, 4, 64) - w @ v[1].double()).abs().max() < 1e-4
+    assert names["out"].isfinite().all()
+
+
 def test_a_captured_step_replays_over_new_positions(qd):
     """Append and attention in one graph: each replay takes what pos and the rows hold then."""
     rng = np.random.default_rng(21)
