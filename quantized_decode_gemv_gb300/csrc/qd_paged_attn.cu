@@ -1291,7 +1291,6 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         corr *= back;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
-      tc::fence_proxy_async_smem();  // the tile's values
       tc::fence_before_sync();
       __syncthreads();
       if (uwarp == 0 && elect_one()) issue_o(it & 1);
@@ -1300,18 +1299,21 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         convert(kc, sm.k);
         if (tid < 8) sm.scales[(it + 1) & 1][tid >> 2][tid & 3] = scale;
         tell(tile + 2);
-        load_scale(tile + 2);
-        tc::fence_proxy_async_smem();
+        tc::fence_proxy_async_smem();  // before the next loads, which it would wait for
         tc::fence_before_sync();
         __syncthreads();
         if (uwarp == 0 && elect_one()) issue_s((it + 1) & 1);
         __syncwarp();
       }
-      if (more) load_codes(a.c.k, tile + 2, kc);
+      if (more) {
+        load_codes(a.c.k, tile + 2, kc);
+        load_scale(tile + 2);
+      }
       if (!lost && !tc::mbar_wait_sleep(mb_o, it & 1u)) lost = true;
       tc::fence_after_sync();
       if (more) {
         convert(vc, sm.v);
+        tc::fence_proxy_async_smem();
         load_codes(a.c.v, tile + 2, vc);
         look(tile + 3);
       }
