@@ -786,10 +786,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
 // SM fill what is left.  The blocks of all walks, as long as each block's last row sees, are listed by a kernel
 // of one CTA and taken whole or cut evenly over the CTAs, in heads, sequences and blocks in turn.
 // What bounds it: the latency of a tile's chain between its three barriers (1.3 of 4 instructions a cycle; a tile
-// of 128 rows takes a CTA 3.7 us alone on an SM).  8 heads of 128, 1024 x 4 rows, 2040 positions: 138 us, of which the
-// list 5 and the join that finds nothing 3 (floor 13: the products once); in copies without the loads 122 us,
-// without the products 114, without the conversions 101, without half of the sums 122.  Walks cut: 151 us, 17 of them
-// the join.  Blocks of 16 rows: 277 us.
+// of 128 rows takes a CTA 3.5 us alone on an SM).  8 heads of 128, 1024 x 4 rows, 2040 positions: 136 us, of which the
+// list 5 and the join that finds nothing 3 (floor 13: the products once); in copies without the conversions 99 us,
+// without the products too 76, with a quarter of the sums too 67.  Against: walks cut 151 us, 17 of them the join; the
+// next loads before the proxy fences 144; four threads to a row, of 64 registers, 167; the values' codes through
+// shared memory 143; blocks of 16 rows 277.
 constexpr int kManyThreads = 256, kManyTile = 64, kManyBm = 128;
 constexpr int kFewRows = 64;
 constexpr int kManyStart = 2, kManyMinPer = 4;  // what a walk's start costs, in tiles; tiles of a CTA at least
@@ -1455,8 +1456,8 @@ qd_status launch_few(AttnArgs a, cudaStream_t st) {
 //   1 head, 7 ragged sequences of 45 x 8 rows at most, 3000 positions (work 0.3e6)    14 33
 //   8 heads, 20 x 4 rows, 20000 positions (0.8e6)                                     64 72
 //   3 heads, 4 ragged sequences of 300 x 3 rows at most, 1500 positions (1.0e6)       31 41
-//   8 heads, 64 x 4 rows, 32700 positions (4.3e6)                                    156 86
-//   8 heads of 128, 1024 x 4 rows, 2040 positions (6.2e6)                            277 138
+//   8 heads, 64 x 4 rows, 32700 positions (4.3e6)                                    156 91
+//   8 heads of 128, 1024 x 4 rows, 2040 positions (6.2e6)                            277 136
 // The units of a head must fit an int.
 constexpr int64_t kManyWork = 2000000;
 inline bool has_many(int n_kv, int group, int n_tokens, int n_seqs, int capacity) {
