@@ -24,9 +24,12 @@ namespace {
 using paged::Cache;
 
 constexpr float kBias = 14.f;  // log2 of the weights' scale
-constexpr int kStart = 1;      // what the start of a walk costs, in units
-constexpr int kMinPer = 2;     // units of a CTA at least
-constexpr int kWholeUnits = 4; // walks of at most so many units are not cut
+// The kernel for few rows.  kMinPer 2 against 1, one sequence, in us: 3 heads of 2000 positions 8.6 and 8.2, one head of
+// 16000 10.7 and 11.9; against 4: 8.6 and 10.6, 10.7 and 11.4.  kWholeUnits 4 against 1: 3 heads of 500 positions 8.1
+// and 8.5, 16 x 32 heads of 500 at most 15.4 and 14.1; against 16: 3 heads of 2000 8.6 and 20.0.
+constexpr int kStart = 1;       // what the start of a walk costs, in units
+constexpr int kMinPer = 2;      // units of a CTA at least
+constexpr int kWholeUnits = 4;  // where the table has room for at most so many units, no walk is cut
 
 struct AttnArgs {
   Cache c;
@@ -792,7 +795,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
 // next loads before the proxy fences 144; four threads to a row, of 64 registers, 167; the values' codes through
 // shared memory 143; blocks of 16 rows 277.
 constexpr int kManyThreads = 256, kManyTile = 64, kManyBm = 128;
-constexpr int kFewRows = 64;
+// 8 heads of 128, 16000 positions, few against many rows: 16 sequences of 32 rows 290 and 431 us, 8 of 64 288 and
+// 246, 8 of 80 346 and 251, 8 of 120 547 and 262.
+constexpr int kFewRows = 48;
 constexpr int kManyStart = 2, kManyMinPer = 4;  // what a walk's start costs, in tiles; tiles of a CTA at least
 constexpr int kManyJoin = 4;                     // what the join costs, in tiles
 constexpr int kListThreads = 1024;
@@ -1419,6 +1424,8 @@ inline bool attn_shape_ok(const qd_paged_kv* kv, int n_heads, int n_tokens, int 
   return paged::cache_status(kv, n_seqs) == QD_OK && n_heads >= 1 && n_heads % kv->n_kv_heads == 0 &&
          n_heads / kv->n_kv_heads <= 16 && n_tokens >= 1 && n_tokens <= QD_MAX_GEMM_TOKENS;
 }
+// Blocks of 16 rows where sequences can have more than 8: against blocks of 8, 20 sequences of 3 x 4 rows, 8 heads of 128,
+// 3000 positions 50 and 62 us, 8 of 8 x 4 rows of 6000 69 and 83, 4 of 8 x 3 rows, 3 heads of 64, 3000 13.6 and 12.2.
 inline bool rows16(int group, int n_tokens, int n_seqs) { return group > 8 || n_tokens > n_seqs; }
 
 // CTAs of a call: what fits the device at once, and no more than there can be units for.
