@@ -319,6 +319,11 @@ SHAPES = [
     (12, 3, 64, 16, [2500], [140], 0),
     (2, 2, 128, 16, [3000, 2], [2, 1], 5000),
     (4, 2, 64, 16, [300, 90], [70, 2], 2**31 - 1),
+    # no more rows than sequences: blocks of 8, though a sequence has several
+    (8, 2, 64, 16, [100, 20, 50], [3, 0, 0], 0),
+    (32, 8, 128, 32, [200, 7, 90, 300], [0, 4, 0, 0], 5),
+    (24, 8, 64, 48, [1000, 31, 32, 33, 500], [1, 0, 2, 1, 1], 40),
+    (8, 1, 128, 16, [700, 64], [1, 1], 0),
 ]
 
 
@@ -347,6 +352,8 @@ def test_attention(qd, fmt, heads, hk, hd, tokens, total, rows, window, room):
     _check(got, ref, tol)
     again = _attn(qd, kv, wide, dev(start), dev(pos), heads, scale, window, stride=heads * hd + gap)
     assert torch.equal(got, again)
+    # without rows behind the last sequence: blocks of 8 where no more rows than sequences are left
+    _check(_attn(qd, kv, wide[:n], dev(start), dev(pos), heads, scale, window, stride=heads * hd + gap), ref[:n], tol[:n])
 
 
 @pytest.mark.parametrize("heads,hk,hd,total,rows", [(12, 3, 64, [2500], [140]), (32, 8, 128, [1500] * 9, [1] * 9),
