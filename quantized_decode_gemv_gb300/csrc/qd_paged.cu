@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_paged_append(AppendArgs a) {
         most = max(most, max(abs_max(x), abs_max(y)));
       }
     }
+    __syncwarp();  // half of what a lane reads below its neighbour has rotated; the reduction orders no memory
     most = __reduce_max_sync(0xffffffffu, most);
     const bool broken = most >= 0x7F800000u || isnan(old);
     const float top = __fdiv_rn(__uint_as_float(most), top_code<FMT>());

@@ -224,6 +224,24 @@ def test_append_values_at_the_edges(qd, fmt):
     assert np.isnan(c.ks).sum() == 2 and np.isnan(c.vs).sum() == 2 and (c.ks == 0).sum() == 2
 
 
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("hd,rot", [(64, 8), (64, 24), (64, 40), (64, 64), (128, 24), (128, 120), (128, 128)])
+@pytest.mark.parametrize("tiny", [0, 1])
+def test_append_where_the_lanes_of_a_row_part(qd, fmt, hd, rot, tiny):
+    """Pairs (i, i + rot / 2): the two lanes of a row read each other's rotated values for their codes.  Here one of them
+    has the tiny values, whose rotation takes longer, and the numbers of rotated units differ."""
+    def change(c, x):
+        i = np.arange(rot // 2)
+        i = i[(i // 4) % 2 == tiny]
+        x[:, 4:6, np.concatenate([i, i + rot // 2])] *= np.float32(2.0**-90)  # keys
+
+    c, t, args = _append_case(qd, 6, 4, 2, hd, 32, fmt, [0, 5, 16, 31], [40, 3, 16, 1], rot, "half", change=change)
+    _same_cache(t, c)
+    for _ in range(20):
+        qd.paged_append(*args)
+    _same_cache(t, c)
+
+
 @pytest.mark.parametrize("fmt,hd", [("i8", 64), ("e4m3", 128)])
 def test_append_one_position_at_a_time(qd, fmt, hd):
     """40 steps of one token: the codes of the step by step reference, so no growing scale loses a code."""
