@@ -1163,8 +1163,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       look(tile);
       tell(tile);
       load_scale(tile);
-      low = g.p0 + g.r * BM / a.group;
-      top = g.p0 + min(g.cnt - 1, (g.r * BM + BM - 1) / a.group);
+      low = top = -1;  // out of range: no row sees a position
+      if (g.p0 >= 0) {
+        low = g.p0 + g.r * BM / a.group;
+        top = g.p0 + min(g.cnt - 1, (g.r * BM + BM - 1) / a.group);
+      }
       // ---- queries
       const int row = g.r * BM + lrow;
       const bool live = row < g.cnt * a.group;

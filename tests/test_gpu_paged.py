@@ -496,6 +496,27 @@ def test_attention_of_sequences_out_of_range(qd):
     assert w[6:8].isfinite().all()
 
 
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("heads,hk,hd", [(2, 2, 64), (8, 2, 128)])
+def test_attention_of_many_rows_out_of_range(qd, heads, hk, hd, window):
+    """Blocks of 128 rows: rows of a sequence that is out of range are zeros whatever their queries hold (an append leaves
+    them as they were), and the sequence beside them is what it is alone."""
+    rng = np.random.default_rng([27, heads])
+    c = Cache(rng, 3, hk, hd, 16, [16, 400, 16], "i8", width=WIDE // 16)
+    kv, _ = _handle(qd, c)
+    q = rng.normal(size=(900, heads, hd)).astype(np.float32)
+    q[:300], q[600:700], q[700:] = np.nan, np.inf, -np.inf
+    start, pos = _starts([300, 300, 300]), np.array([-1, 100, WIDE - 299], np.int32)
+    got = _attn(qd, kv, dev(q), dev(start), dev(pos), heads, 0.1, window)
+    assert (got[:300] == 0).all() and (got[600:] == 0).all()
+    ref, tol = attn_all(c, q[300:600], _starts([0, 300, 0]), np.array([0, 100, 0], np.int32), heads // hk, 0.1, window)
+    _check(got[300:600], ref, tol)
+    for b in (0, 2):  # a sequence alone
+        r = slice(300 * b, 300 * b + 300)
+        one = qd.PagedKV(*kv.tensors[:4], kv.tensors[4][b : b + 1], fmt=c.fmt)
+        assert (_attn(qd, one, dev(q[r]), dev(_starts([300])), dev(pos[b : b + 1]), heads, 0.1, window) == 0).all()
+
+
 def test_attention_of_shared_pages(qd):
     """Two sequences over the same pages give the same rows."""
     rng = np.random.default_rng(16)
