@@ -587,10 +587,11 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
  * the sequence's last position, but for the scale of the block that holds it, nor, but for rounding, on
  * what they hold behind a row's.  A non-finite q gives NaN in its
  * own row and head alone; a block with a NaN scale gives NaN to the rows that see a position of it,
- * and to no other.  Results are the same bits on every run.
+ * and to no other; an infinite scale (an append stores none) reaches no other rows either.  Results are the same bits on every run.
  * Arithmetic: codes enter the products exactly, queries and weights times scales in two parts (22 bits
- * of each from 2^-15 of the largest of its row on, 2^-38 of that below; scales 2^60 times smaller than
- * others of the row do not count); sums, running maxima and outputs are f32.  Should a wait inside the
+ * of each from 2^-15 of the largest of its row on, 2^-38 of that below, whatever the scales of other
+ * blocks are; fewer where every scale that a row sees is under 2^-100; weights under 2^-126 of the row's
+ * largest are zeros); sums, running maxima and outputs are f32.  Should a wait inside the
  * kernel run out (about a second, on a GPU that is out of order), the rows that it concerns are NaN.
  * workspace (device): qd_paged_attn_workspace bytes (0: a shape the call does not take; no fewer
  * for more tokens or sequences); two calls that can run at the same time need one each. */

@@ -6,9 +6,9 @@
 // with an online softmax: s = q k^T and o += p v are matrix products with f32 accumulators.  Codes
 // of 8 bits are exact in binary16, so they enter the products as they are; a block's scale of keys
 // multiplies its scores, that of values its weights.  Outputs are f32 and meant to be as exact as f32
-// arithmetic, so queries and weights enter in two binary16 parts, hi = rn(x), lo = rn(x - hi), at a power of
-// two that puts the largest of a row of queries at 2^14 to 2^15 and the largest weight times scale at
-// 2^12 to 2^15: what is 2^-15 of that or more keeps 22 bits, what is less is 2^-38 of it off.  The matrix units
+// arithmetic, so queries and weights times scales enter in two binary16 parts, hi = rn(x), lo = rn(x - hi), at a
+// power of two that puts the largest of a row at 2^14 to 2^15 (2^15.1 for weights): what is 2^-15 of that or more
+// keeps 22 bits, what is less is 2^-38 of it off.  The matrix units
 // cut their f32 sums off instead of rounding them: a tile's products start from zero and are added
 // to o with rounded f32 additions.
 #include <algorithm>
@@ -98,6 +98,26 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // one under 2^-100); an infinity or NaN stays what it is.
 __device__ __forceinline__ int scale_exp(uint32_t abs_bits) {
   return min(max((int)(abs_bits >> 23) - 127, -100), 127) - 14;
+}
+
+// o is held in units of 2^ev of its row, ev the floor of n - m: n the running maximum of score + log2 scale over the
+// positions that the row sees, m that of the scores, so that the largest weight times scale is 2^14 to 2^15.1 times
+// the unit, whatever a block weighs that the row does not see, or that has a large scale and no weight.
+__device__ __forceinline__ float log2_scale(float s) {  // log2 or up to 0.09 less; finite for any s
+  return fmaf((float)__float_as_int(s), 0x1p-23f, -127.f);
+}
+// The next ev; back: what o in the old one is multiplied by.
+__device__ __forceinline__ void next_unit(float n, float m, int& ev, float& back, float& down) {
+  const int en = min(max(__float2int_rd(n - m), -100), 126);
+  back = pow2(max(min(ev - en, 126), -126));
+  down = pow2(-en);
+  ev = en;
+}
+// s down, not over the largest finite value: a scale that the row hardly sees may be 2^100 units; NaN stays
+__device__ __forceinline__ float in_units(float s, float down) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(s * down), "f"(3e38f));
+  return y;
 }
 
 // Four codes -> two binary16 pairs (codes 0, 1 and 2, 3), exactly.
@@ -380,8 +400,8 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
 
   float o[MT][NR][4];  // dims HD / 8 qr + 2 i (elements 0, 1), + 1 (2, 3) of rows 8 n + 2 qc, + 1
   float m[NR], l[NR], rs[NR];  // of rows qr + 8 i
-  int ev = 0, emax = -1000;
-  float down = 1.f;  // 2^-ev
+  float n[NR];
+  int ev[NR];
   int lim[NR];               // position of the lane's row, -1: none
   int t_begin, base;         // of the CTA's part of the walk; this warp's first position of the tile
   int top, above, whole_lo, whole_hi;  // tiles with a seen position: above < base <= top; seen by every row: the others
@@ -441,7 +461,8 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
           sm.q[s][0][lane] = make_uint4(hi[0], lo[0], hi[1], lo[1]);
         }
       }
-      m[i] = -INFINITY;
+      m[i] = n[i] = -INFINITY;
+      ev[i] = 0;
       l[i] = 0.f;
     }
 #pragma unroll
@@ -450,9 +471,6 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[d][n][e] = 0.f;
-    ev = 0;
-    emax = -1000;
-    down = 1.f;
   };
   load_q(cur);
   start_walk(cur);
@@ -512,20 +530,9 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
       }
       // ---- weights
       const bool edge = base > whole_hi || base < whole_lo;
-      // o is in units of 2^ev, so that the tile's scales are 2^-2 to 2 of them: another unit where they are
-      // not, at least 2^-60 of the largest (a NaN does not count: there are rows that do not see it)
-      float back = 1.f;
-      float vtop = fabsf(vs[0]);
+      float lgv[NB];
 #pragma unroll
-      for (int k = 1; k < NB; ++k) vtop = fmaxf(vtop, fabsf(vs[k]));
-      if (!(vtop * down < 2.f && vtop * down >= 0.25f)) {
-        const int etile = vtop <= 3e38f ? max((int)(__float_as_uint(vtop) >> 23) - 127, -100) : -100;
-        emax = max(emax, etile);
-        const int en = min(max(etile, emax - 60), 126);
-        back = pow2(max(min(ev - en, 126), -126));
-        ev = en;
-        down = pow2(-en);
-      }
+      for (int k = 0; k < NB; ++k) lgv[k] = log2_scale(vs[k]);
       float corr[NR], y[NT][2 * NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
@@ -544,15 +551,27 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
 #pragma unroll
           for (int k = 0; k < NB; ++k) f[k] = 1.f;
         }
-        float mx = -INFINITY;
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < NB; ++k)  // scales are not negative
-          mx = fmaxf(mx, f[k] * fmaxf(fmaxf(s[2 * k][2 * i], s[2 * k][2 * i + 1]), fmaxf(s[2 * k + 1][2 * i], s[2 * k + 1][2 * i + 1])));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        for (int k = 0; k < NB; ++k) {  // scales are not negative
+          const float mk =
+              f[k] * fmaxf(fmaxf(s[2 * k][2 * i], s[2 * k][2 * i + 1]), fmaxf(s[2 * k + 1][2 * i], s[2 * k + 1][2 * i + 1]));
+          mx = fmaxf(mx, mk);
+          my = fmaxf(my, mk + lgv[k]);
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, o));
+        }
         const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn;
         corr[i] = ex2(m[i] - mu);
         m[i] = mn;
+        n[i] = fmaxf(n[i], my);
+        float back, down, vu[NB];
+        next_unit(n[i], mu, ev[i], back, down);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) vu[k] = in_units(vs[k], down);
         const float bias = kBias - mu;
         float sum = 0.f;
 #pragma unroll
@@ -561,7 +580,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
           for (int e = 0; e < 2; ++e) {
             const float p = ex2(fmaf(s[j][2 * i + e], f[j / 2], bias));
             sum += p;
-            y[j][2 * i + e] = p * (vs[j / 2] * down);
+            y[j][2 * i + e] = p * vu[j / 2];
           }
         if (edge) {  // whatever the scale
 #pragma unroll
@@ -642,9 +661,9 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
     }
     const bool whole = t_begin == 0 && last;
     __syncwarp();  // every lane has read the slot
-    const float unit = pow2(min(max(ev, -126), 127));
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
+      const float unit = pow2(ev[i]), units[2] = {__shfl_sync(0xffffffffu, unit, 8 * qc), __shfl_sync(0xffffffffu, unit, 8 * qc + 4)};
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       const int r = qr + 8 * i;
@@ -657,7 +676,7 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
 #pragma unroll
         for (int d = 0; d < MT; d += 2)
           *reinterpret_cast<float4*>(share(warp, slot, 8 * i + 2 * qc + e) + HD / 8 * qr + 2 * d) =
-              make_float4(o[d][i][e] * unit, o[d][i][2 + e] * unit, o[d + 1][i][e] * unit, o[d + 1][i][2 + e] * unit);
+              make_float4(o[d][i][e] * units[e], o[d][i][2 + e] * units[e], o[d + 1][i][e] * units[e], o[d + 1][i][2 + e] * units[e]);
     }
     const int done_cnt = cur.cnt, done_r = cur.r, done_h = cur.h, done_row0 = cur.row0;
     const int64_t stop = end - cur.left - cur.t + cur.w.nt - 1;  // the walk's last unit
@@ -940,14 +959,15 @@ __device__ __forceinline__ uint32_t core_off(int r, int c) {  // in bytes
 // A CTA's part of a walk: n tiles from t0 on.
 struct Segment {
   int h, r, cnt, row0, p0, seq, first_tile, nt, t0, n;
+  int low, top;  // positions of the block's first and last row
 };
 template <int HD>
 struct Many {
   uint4 q[2][kManyBm * HD / 8];    // hi, lo
   uint4 k[kManyTile * HD / 8], v[kManyTile * HD / 8];
-  float scales[2][2][4];           // of every second tile's blocks: keys, values
+  float scales[2][3][4];           // of every second tile's blocks: keys, values, log2_scale of those
   uint32_t place[2][4];            // of every second tile: its blocks in the cache, kNoPage
-  float ex[2][kManyBm];            // what a row's threads tell each other
+  float2 ex[2][kManyBm];           // what a row's threads tell each other
   unsigned long long mbar[2];      // scores, products
   int whole;
   long long unit;                  // of the next segment: its place in all units (of walks where they are whole),
@@ -1000,6 +1020,14 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     }
   }
   // One thread: the part of the walk (head, block) from unit `in` on into sm.seg, and on to the next; n = 0: none left.
+  auto set_segment = [&](Segment& g) {
+    g.low = g.top = -1;  // out of range: no row sees a position
+    if (g.p0 >= 0) {
+      g.low = g.p0 + g.r * BM / a.group;
+      g.top = g.p0 + min(g.cnt - 1, (g.r * BM + BM - 1) / a.group);
+    }
+    sm.seg = g;
+  };
   auto next_segment = [&] {
     const Block* list = reinterpret_cast<const Block*>(ma.head + 1);
     Segment g = {};
@@ -1015,7 +1043,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         g.cnt = tokens_of(a, b.seq, g.row0, g.p0);
         sm.unit += gridDim.x;
       }
-      sm.seg = g;
+      set_segment(g);
       return;
     }
     while (g.n <= 0 && sm.left > 0) {
@@ -1046,7 +1074,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         ++sm.head;
       }
     }
-    sm.seg = g;
+    set_segment(g);
   };
 
   const uint32_t mb_s = tc::smem_u32(&sm.mbar[0]), mb_o = tc::smem_u32(&sm.mbar[1]);
@@ -1093,6 +1121,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     scale = (tile * 4 + (tid & 3)) * QD_KV_BLOCK > last ? 0.f
             : my_place == kNoPage                       ? __uint_as_float(0x7FC00000u)
                                                         : __ldg((tid < 4 ? a.c.ks : a.c.vs) + my_place);
+  };
+  auto put_scale = [&](int slot) {
+    sm.scales[slot][tid >> 2][tid & 3] = scale;
+    if (tid >= 4) sm.scales[slot][2][tid & 3] = log2_scale(scale);
   };
   auto load_codes = [&](const uint8_t* codes, int tile, uint4 (&c)[kPer]) {
 #pragma unroll
@@ -1151,8 +1183,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
   bool lost = false;  // a wait has run out: the rows of the walk are NaN
   uint32_t it = 0;    // tiles of this CTA so far
   while (sm.seg.n > 0) {
-    float o[ND], m = -INFINITY, l = 0.f, rs, down = 1.f;
-    int ev = 0, emax = -1000, lim, tile, stop, low, top;
+    float o[ND], m = -INFINITY, n = -INFINITY, l = 0.f, rs;
+    int ev = 0, lim, tile, stop;
     {
       const Segment& g = sm.seg;
       head = g.h;
@@ -1163,11 +1195,6 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       look(tile);
       tell(tile);
       load_scale(tile);
-      low = top = -1;  // out of range: no row sees a position
-      if (g.p0 >= 0) {
-        low = g.p0 + g.r * BM / a.group;
-        top = g.p0 + min(g.cnt - 1, (g.r * BM + BM - 1) / a.group);
-      }
       // ---- queries
       const int row = g.r * BM + lrow;
       const bool live = row < g.cnt * a.group;
@@ -1183,13 +1210,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
         o[d + 3] = x.w * a.scale;
         mx = max(mx, abs_max(make_float4(o[d], o[d + 1], o[d + 2], o[d + 3])));
       }
-      sm.ex[half][lrow] = __uint_as_float(mx);
+      sm.ex[half][lrow].x = __uint_as_float(mx);
       __syncthreads();
       load_codes(a.c.k, tile, kc);
       load_codes(a.c.v, tile, vc);
       look(tile + 1);
       tell(tile + 1);
-      const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow])));
+      const int e = scale_exp(max(mx, __float_as_uint(sm.ex[half ^ 1][lrow].x)));
       rs = pow2(e);
       const float f = pow2(-e);
 #pragma unroll
@@ -1209,7 +1236,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     // ---- the first tile
     convert(kc, sm.k);
     convert(vc, sm.v);
-    if (tid < 8) sm.scales[it & 1][tid >> 2][tid & 3] = scale;
+    if (tid < 8) put_scale(it & 1);
     tc::fence_proxy_async_smem();
     tc::fence_before_sync();
     __syncthreads();
@@ -1227,19 +1254,19 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       if (!lost && !tc::mbar_wait_sleep(mb_s, it & 1u)) lost = true;
       tc::fence_after_sync();
       const uint32_t cols = mine + T * (it & 1) + 32 * half;  // this thread's 32 scores: two blocks
-      const bool edge = base + T - 1 > low || (a.window > 0 && base <= top - a.window);
+      const bool edge = base + T - 1 > sm.seg.low || (a.window > 0 && base <= sm.seg.top - a.window);
       const int hi = lim - base - 32 * half, lo = a.window > 0 ? hi - a.window + 1 : 0;  // seen: lo <= column <= hi
       const float f[2] = {rs * sm.scales[it & 1][0][2 * half], rs * sm.scales[it & 1][0][2 * half + 1]};
       if (warp_live) {
-        float mx = -INFINITY;
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float s[16];
+          float s[16], top = -INFINITY;  // of the block
           tmem_ld16(cols + 16 * c, s);
           if (edge) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              if (16 * c + j <= hi && 16 * c + j >= lo) mx = fmaxf(mx, s[j] * f[c]);
+              if (16 * c + j <= hi && 16 * c + j >= lo) top = fmaxf(top, s[j] * f[c]);
           } else {
             float mc[2] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3])};
 #pragma unroll
@@ -1247,34 +1274,28 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
               mc[0] = fmaxf(mc[0], fmaxf(s[j], s[j + 1]));
               mc[1] = fmaxf(mc[1], fmaxf(s[j + 2], s[j + 3]));
             }
-            mx = fmaxf(mx, fmaxf(mc[0], mc[1]) * f[c]);  // scales are not negative
+            top = fmaxf(mc[0], mc[1]) * f[c];  // scales are not negative
           }
+          mx = fmaxf(mx, top);
+          my = fmaxf(my, top + sm.scales[it & 1][2][2 * half + c]);
         }
-        sm.ex[half][lrow] = mx;
+        sm.ex[half][lrow] = make_float2(mx, my);
       }
       __syncthreads();  // the maximum of the row's other half
       float corr = 1.f;
       if (warp_live) {
-        const float mn = fmaxf(m, fmaxf(sm.ex[0][lrow], sm.ex[1][lrow])), mu = mn == -INFINITY ? 0.f : mn;
+        const float2 e0 = sm.ex[0][lrow], e1 = sm.ex[1][lrow];
+        const float mn = fmaxf(m, fmaxf(e0.x, e1.x)), mu = mn == -INFINITY ? 0.f : mn;
         corr = ex2(m - mu);
         m = mn;
         const float bias = kBias - mu;
-        // o is in units of 2^ev, as in the kernel for few rows
-        float back = 1.f, vtop = 0.f;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) vtop = fmaxf(vtop, fabsf(sm.scales[it & 1][1][b]));
-        if (!(vtop * down < 2.f && vtop * down >= 0.25f)) {
-          const int etile = vtop <= 3e38f ? max((int)(__float_as_uint(vtop) >> 23) - 127, -100) : -100;
-          emax = max(emax, etile);
-          const int en = min(max(etile, emax - 60), 126);
-          back = pow2(max(min(ev - en, 126), -126));
-          ev = en;
-          down = pow2(-en);
-        }
+        n = fmaxf(n, fmaxf(e0.y, e1.y));
+        float back, down;
+        next_unit(n, mu, ev, back, down);
         float sum = 0.f, sum1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float vs = sm.scales[it & 1][1][2 * half + c] * down;
+          const float vs = in_units(sm.scales[it & 1][1][2 * half + c], down);
           float s[16];
           tmem_ld16(cols + 16 * c, s);
           uint32_t ph[8], pl[8];
@@ -1306,7 +1327,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       __syncwarp();
       if (more) {  // the next tile's scores
         convert(kc, sm.k);
-        if (tid < 8) sm.scales[(it + 1) & 1][tid >> 2][tid & 3] = scale;
+        if (tid < 8) put_scale((it + 1) & 1);
         tell(tile + 2);
         tc::fence_proxy_async_smem();  // before the next loads, which it would wait for
         tc::fence_before_sync();
@@ -1343,17 +1364,17 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
     const bool whole = t0 == 0 && sm.seg.n == sm.seg.nt;
     const int64_t to = row < rows ? row_of(a, HD, (int64_t)a.n_heads * HD, sm.seg.row0, sm.seg.h, row) : 0;
     if (__syncthreads_or(lost)) l = NAN;  // every thread has read `ex`
-    sm.ex[half][lrow] = l;
+    sm.ex[half][lrow].x = l;
     if (tid == 0) next_segment();
     __syncthreads();
-    const float lt = l + sm.ex[half ^ 1][lrow];
+    const float lt = l + sm.ex[half ^ 1][lrow].x;
     float* part = ma.parts + ((int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * part_floats(BM, HD);
     if (!whole && half == 0) {
       part[lrow] = m;
       part[BM + lrow] = lt;
     }
     if (!whole || row < rows) {
-      const float unit = pow2(min(max(ev, -126), 127)) * (!whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt);
+      const float unit = pow2(ev) * (!whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt);
       float4* dst = reinterpret_cast<float4*>((whole ? a.out + to : part + 2 * BM + lrow * HD) + half * ND);
 #pragma unroll
       for (int d = 0; d < ND; d += 4)

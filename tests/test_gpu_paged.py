@@ -421,6 +421,59 @@ def test_attention_over_a_long_walk(qd, hd, rows):
             assert np.max(np.abs(got[r, h] - o) / tol) <= 1.0
 
 
+UNEQUAL = [
+    # heads, hk, hd, tokens, total positions, rows, window, room
+    (1, 1, 64, 16, [200], [1], 0, None),
+    (9, 3, 128, 16, [300, 33, 17], [1, 1, 1], 0, None),
+    (8, 2, 64, 32, [3000], [1], 100, None),  # cut walks, whose warps see tiles of their own
+    (16, 1, 128, 48, [500], [9], 17, None),
+    (4, 2, 64, 64, [150, 90], [100, 90], 0, None),
+    (4, 2, 128, 64, [150, 90], [40, 60], 20, None),
+    (4, 2, 64, 64, [450, 290], [400, 290], 0, WIDE),
+    (4, 2, 128, 64, [450, 290], [400, 290], 20, WIDE),
+    (2, 1, 64, 32, [5000], [140], 0, WIDE),
+]
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("heads,hk,hd,tokens,total,rows,window,room", UNEQUAL)
+def test_attention_of_unequal_scales(qd, fmt, heads, hk, hd, tokens, total, rows, window, room):
+    """Scales of values from 2^-60 to 2^60 and weights that differ as much, in any order: a block that weighs nothing, or
+    that a row does not see, takes nothing from the others, however large its scale."""
+    rng = np.random.default_rng([28, heads, hd, tokens, total[0]])
+    c = Cache(rng, len(total), hk, hd, tokens, total, fmt, width=room and room // tokens)
+    c.ks *= (4.0 ** rng.integers(-3, 3, c.ks.shape) * (1 if fmt == "i8" else 0.25)).astype(np.float32)
+    c.vs[:] = (2.0 ** rng.integers(-60, 61, c.vs.shape)).astype(np.float32)
+    kv, _ = _handle(qd, c)
+    start, pos = _starts(rows), np.array(total, np.int32) - np.array(rows, np.int32)
+    q = (rng.normal(size=(int(start[-1]), heads, hd)) * 2).astype(np.float32)
+    got = _attn(qd, kv, dev(q), dev(start), dev(pos), heads, 1 / math.sqrt(hd), window)
+    _check(got, *attn_all(c, q, start, pos, heads // hk, 1 / math.sqrt(hd), window))
+
+
+@pytest.mark.parametrize("name", ["ks", "vs"])
+@pytest.mark.parametrize("hd,rows,window,room", [(64, 1, 20, None), (128, 40, 0, None), (64, 40, 20, None), (64, 300, 0, WIDE),
+                                                 (128, 300, 20, WIDE)])
+def test_attention_keeps_an_infinite_scale_apart(qd, hd, rows, window, room, name):
+    """The scale of positions 160 .. 175 of the first key head is infinite: rows that do not see them are as they would be."""
+    rng = np.random.default_rng([29, hd, rows])
+    c = Cache(rng, 1, 2, hd, 32, [500], "i8", width=room and room // 32)
+    start, pos = _starts([rows]), np.array([190 if rows == 1 else 150], np.int32)
+    q = rng.normal(size=(rows, 4, hd)).astype(np.float32)
+    ref, tol = attn_all(c, q, start, pos, 2, 0.1, window)
+    getattr(c, name)[c.table[0, 5], 0, 0] = np.inf
+    kv, _ = _handle(qd, c)
+    got = _attn(qd, kv, dev(q), dev(start), dev(pos), 4, 0.1, window)
+    at = pos[0] + np.arange(rows)
+    sees = (at >= 160) & (at - window + 1 <= 175 if window else True)
+    keep = np.repeat(~sees[:, None], 4, 1)
+    keep[:, 2:] = True
+    ref[~keep], tol[~keep] = 0, np.inf
+    if name == "vs":
+        assert not got.cpu().numpy()[~keep].any(where=np.isfinite(got.cpu().numpy()[~keep]))
+    _check(torch.where(torch.from_numpy(keep).cuda()[..., None], got, 0.0), ref, tol)
+
+
 @pytest.mark.parametrize("rows", [1, 20, 130])
 @pytest.mark.parametrize("hd", [64, 128])
 def test_attention_keeps_what_is_broken_apart(qd, hd, rows):
