@@ -113,6 +113,13 @@ __device__ __forceinline__ void next_unit(float n, float m, int& ev, float& back
   down = pow2(-en);
   ev = en;
 }
+// A share of a row, as it is joined with others: the maximum score m, the sum l of the weights, and o scaled by
+// down_of(l), so that it is no larger than the row's largest value (where these are near f32's largest, their sum has
+// no place in it).  With weights ex2(m - the largest m), o of several is sum of w up_of(l) o, times down_of(sum of w l).
+__device__ __forceinline__ float down_of(float l) { return __int_as_float((253 - (__float_as_int(l) >> 23)) << 23); }
+__device__ __forceinline__ float up_of(float l) { return __int_as_float(((__float_as_int(l) >> 23) + 1) << 23); }
+// What makes o the mean.
+__device__ __forceinline__ float inv_of(float l) { return l == 0.f ? 0.f : 1.f / (l * down_of(l)); }
 // s down, not over the largest finite value: a scale that the row hardly sees may be 2^100 units; NaN stays
 __device__ __forceinline__ float in_units(float s, float down) {
   float y;
@@ -663,20 +670,22 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
     __syncwarp();  // every lane has read the slot
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const float unit = pow2(ev[i]), units[2] = {__shfl_sync(0xffffffffu, unit, 8 * qc), __shfl_sync(0xffffffffu, unit, 8 * qc + 4)};
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const float unit = pow2(ev[i]), norm = down_of(l[i]);
       const int r = qr + 8 * i;
       if (qc == 0) {
         sm.ml[warp][0][r] = m[i];
         sm.ml[warp][1][r] = l[i];
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        const float u = __shfl_sync(0xffffffffu, unit, 8 * qc + 4 * e), f = __shfl_sync(0xffffffffu, norm, 8 * qc + 4 * e);
 #pragma unroll
         for (int d = 0; d < MT; d += 2)
           *reinterpret_cast<float4*>(share(warp, slot, 8 * i + 2 * qc + e) + HD / 8 * qr + 2 * d) =
-              make_float4(o[d][i][e] * units[e], o[d][i][2 + e] * units[e], o[d + 1][i][e] * units[e], o[d + 1][i][2 + e] * units[e]);
+              make_float4(o[d][i][e] * f * u, o[d][i][2 + e] * f * u, o[d + 1][i][e] * f * u, o[d + 1][i][2 + e] * f * u);
+      }
     }
     const int done_cnt = cur.cnt, done_r = cur.r, done_h = cur.h, done_row0 = cur.row0;
     const int64_t stop = end - cur.left - cur.t + cur.w.nt - 1;  // the walk's last unit
@@ -691,19 +700,26 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
 #pragma unroll
       for (int w = 0; w < W; ++w) mt = fmaxf(mt, sm.ml[w][0][r]);
       float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+      float f[W];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float mw = sm.ml[w][0][r], lw = sm.ml[w][1][r];
-        const float f = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
+        f[w] = mw == -INFINITY ? lw : ex2(mw - mt);  // a share without a maximum has l = 0 or NaN
+        lt = fmaf(lw, f[w], lt);
+        f[w] *= up_of(lw);
+      }
+      const float norm = down_of(lt);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
         const float4 ow = *reinterpret_cast<const float4*>(share(w, slot, r) + 4 * c);
-        lt = fmaf(lw, f, lt);
-        ot.x = fmaf(ow.x, f, ot.x);
-        ot.y = fmaf(ow.y, f, ot.y);
-        ot.z = fmaf(ow.z, f, ot.z);
-        ot.w = fmaf(ow.w, f, ot.w);
+        f[w] *= norm;
+        ot.x = fmaf(ow.x, f[w], ot.x);
+        ot.y = fmaf(ow.y, f[w], ot.y);
+        ot.z = fmaf(ow.z, f[w], ot.z);
+        ot.w = fmaf(ow.w, f[w], ot.w);
       }
       if (whole) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const float inv = inv_of(lt);
         reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, done_row0, done_h, done_r * BM + r))[c] =
             make_float4(ot.x * inv, ot.y * inv, ot.z * inv, ot.w * inv);
       } else {
@@ -760,8 +776,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
   float l = 0.f;
   for (int i = threadIdx.x; i < n; i += kJoinThreads) {
     const float lp = __ldcg(part(i) + BM + r);
-    s_w[i] = s_w[i] == -INFINITY ? lp : ex2(s_w[i] - mx);  // a part without a maximum has l = 0 or NaN
-    l = fmaf(lp, s_w[i], l);
+    const float f = s_w[i] == -INFINITY ? lp : ex2(s_w[i] - mx);  // a part without a maximum has l = 0 or NaN
+    l = fmaf(lp, f, l);
+    s_w[i] = f * up_of(lp);
   }
   l = warp_sum(l);
   if (lane == 0) s_red[warp] = l;
@@ -769,12 +786,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
   l = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[w];
+  const float norm = down_of(l);
   const int g = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int i = g; i < n; i += kGroups) {
     const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * BM + r * HD) + c);
-    const float w = s_w[i];
+    const float w = s_w[i] * norm;
     o.x = fmaf(x.x, w, o.x);
     o.y = fmaf(x.y, w, o.y);
     o.z = fmaf(x.z, w, o.z);
@@ -791,7 +809,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
     o.z += x.z;
     o.w += x.w;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = inv_of(l);
   reinterpret_cast<float4*>(a.out + row_of(a, HD, (int64_t)a.n_heads * HD, __ldcg(&cut->row0), __ldcg(&cut->h), at))[c] =
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
@@ -1374,11 +1392,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       part[BM + lrow] = lt;
     }
     if (!whole || row < rows) {
-      const float unit = pow2(ev) * (!whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt);
+      const float unit = pow2(ev), f = whole ? inv_of(lt) * down_of(lt) : down_of(lt);
       float4* dst = reinterpret_cast<float4*>((whole ? a.out + to : part + 2 * BM + lrow * HD) + half * ND);
 #pragma unroll
       for (int d = 0; d < ND; d += 4)
-        dst[d / 4] = make_float4(o[d] * unit, o[d + 1] * unit, o[d + 2] * unit, o[d + 3] * unit);
+        dst[d / 4] = make_float4(o[d] * f * unit, o[d + 1] * f * unit, o[d + 2] * f * unit, o[d + 3] * f * unit);
     }
     __syncthreads();  // `ex` is read
   }
@@ -1421,21 +1439,26 @@ __global__ void __launch_bounds__(kJoinRows * 32) k_paged_join_many(ManyArgs ma)
     float top = m;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, mc[i]);
-    const float f = m == -INFINITY ? l : ex2(m - top);  // without a maximum l is 0 or NaN
+    const float f = m == -INFINITY ? l : ex2(m - top), up = up_of(l);  // without a maximum l is 0 or NaN
     m = top;
     l *= f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] *= f;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const float g = mc[i] == -INFINITY ? lc[i] : ex2(mc[i] - top);
       l = fmaf(lc[i], g, l);
+      mc[i] = g * up_of(lc[i]);
+    }
+    const float norm = down_of(l);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] *= f * up * norm;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
       const float* x = reinterpret_cast<const float*>(&oc[i]);
 #pragma unroll
-      for (int d = 0; d < (int)(sizeof(V) / 4); ++d) o[d] = fmaf(x[d], g, o[d]);
+      for (int d = 0; d < (int)(sizeof(V) / 4); ++d) o[d] = fmaf(x[d], mc[i] * norm, o[d]);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = inv_of(l);
   V out;
   float* x = reinterpret_cast<float*>(&out);
 #pragma unroll

@@ -451,6 +451,22 @@ def test_attention_of_unequal_scales(qd, fmt, heads, hk, hd, tokens, total, rows
     _check(got, *attn_all(c, q, start, pos, heads // hk, 1 / math.sqrt(hd), window))
 
 
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("exponent", [110, 117, -95])
+@pytest.mark.parametrize("heads,hk,hd,tokens,total,rows,window,room", UNEQUAL)
+def test_attention_of_values_near_the_ends_of_f32(qd, fmt, heads, hk, hd, tokens, total, rows, window, room, exponent):
+    """Values to 2^124 (and from 2^-95 on): their sums over the positions have no place in f32, their weighted means do."""
+    rng = np.random.default_rng([30, heads, hd, tokens, total[0]])
+    c = Cache(rng, len(total), hk, hd, tokens, total, fmt, width=room and room // tokens)
+    c.vs[:] = (2.0**exponent * rng.uniform(0.1, 1 if fmt == "i8" else 0.25, c.vs.shape)).astype(np.float32)
+    kv, _ = _handle(qd, c)
+    start, pos = _starts(rows), np.array(total, np.int32) - np.array(rows, np.int32)
+    q = rng.normal(size=(int(start[-1]), heads, hd)).astype(np.float32)
+    got = _attn(qd, kv, dev(q), dev(start), dev(pos), heads, 0.1, window)
+    assert got.isfinite().all()
+    _check(got, *attn_all(c, q, start, pos, heads // hk, 0.1, window))
+
+
 @pytest.mark.parametrize("name", ["ks", "vs"])
 @pytest.mark.parametrize("hd,rows,window,room", [(64, 1, 20, None), (128, 40, 0, None), (64, 40, 20, None), (64, 300, 0, WIDE),
                                                  (128, 300, 20, WIDE)])
