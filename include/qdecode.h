@@ -582,10 +582,10 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
  * sequence b (position p = pos[b] + i) gives out = sum_j softmax_j(scale * q . k_j) v_j over
  * j = 0 .. p, or with window > 0 over the last `window` of these.  q: f32 rows [n_heads][head_dim]
  * at t*q_stride (a multiple of 4); out: f32 [n_tokens][n_heads][head_dim].  n_heads % n_kv_heads
- * == 0, group size <= 16; scale finite.  The rows of a sequence with pos[b] < 0, or whose last
+ * == 0, group size <= 16; |scale| < 2^127.  The rows of a sequence with pos[b] < 0, or whose last
  * position is behind the last page, are zeros.  The result does not depend on what pages hold behind
  * the sequence's last position, but for the scale of the block that holds it, nor, but for rounding, on
- * what they hold behind a row's.  A non-finite q gives NaN in its
+ * what they hold behind a row's.  A q that is not finite, or not as q * scale * log2 e, gives NaN in its
  * own row and head alone; a block with a NaN scale gives NaN to the rows that see a position of it,
  * and to no other; an infinite scale (an append stores none) reaches no other rows either.  Results are the same bits on every run.
  * Arithmetic: codes enter the products exactly, queries and weights times scales in two parts (22 bits

@@ -1580,7 +1580,8 @@ size_t qd_paged_attn_workspace(const qd_paged_kv* kv, int n_heads, int n_tokens,
 qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_heads, int n_tokens,
                         const int32_t* row_start, const int32_t* pos, int n_seqs, float scale, int window,
                         void* workspace, size_t workspace_bytes, qd_stream_t stream) {
-  if (!q || !out || !row_start || !pos || !workspace || window < 0 || !std::isfinite(scale)) return QD_ERR_INVALID_ARG;
+  const float scale2 = scale * 1.4426950408889634f;  // scores in powers of two
+  if (!q || !out || !row_start || !pos || !workspace || window < 0 || !std::isfinite(scale2)) return QD_ERR_INVALID_ARG;
   const qd_status r = paged::cache_status(kv, n_seqs);
   if (r != QD_OK) return r;
   const size_t need = qd_paged_attn_workspace(kv, n_heads, n_tokens, n_seqs);
@@ -1601,7 +1602,7 @@ qd_status qd_paged_attn(const qd_paged_kv* kv, const float* q, int64_t q_stride,
   a.group = n_heads / kv->n_kv_heads;
   a.row_start = row_start;
   a.pos = pos;
-  a.scale = scale * 1.4426950408889634f;
+  a.scale = scale2;
   a.window = window < a.c.capacity ? window : 0;  // a wider one hides nothing
   a.max_rows = 1 << 30;
   a.ws = static_cast<float*>(workspace);

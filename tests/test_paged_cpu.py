@@ -159,6 +159,15 @@ def test_attn_refusals(lib):
         assert bad(**c) == 2, c
 
 
+def test_attn_refuses_a_scale_beyond_f32(lib):
+    """Scores are taken in powers of two: the scale times log2 e has to be a finite f32 too."""
+    kv = _kv()
+    need = lib.qd_paged_attn_workspace(_ref(kv), 8, 7, 3)
+    call = lambda scale: lib.qd_paged_attn(_ref(kv), G, 512, G, 8, 7, G, G, 3, scale, 0, G, need, None)  # noqa: E731
+    for scale in (2.4e38, -2.4e38, 3.4e38, float("inf"), float("-inf")):
+        assert call(scale) == 1, scale
+
+
 def test_read_refusals(lib):
     order = "kv len b ctx k v f16 st".split()
     kv = _kv()
