@@ -512,8 +512,8 @@ typedef enum { QD_KV_I8 = 0, QD_KV_E4M3 = 1 } qd_kv_fmt;
  * most 1024; max_pages * page_tokens at most 2^30; 1 <= max_seqs <= QD_MAX_SEQS.  Pages and scales
  * need no initialisation: what lies behind a sequence's end does not matter.  An entry outside
  * [0, n_pages) is no page: nothing is stored through it, and rows that attend to or read its
- * positions give NaN.  qd_paged_append stores numbers only (of the E4M3 codes not 0x7F and 0xFF, which are
- * NaN); a page filled otherwise must hold none of those at a sequence's positions. */
+ * positions give NaN.  qd_paged_append stores numbers only (of the E4M3 codes not 0x7F and 0xFF, which
+ * are NaN); a page filled otherwise must hold none of those at a sequence's positions. */
 typedef struct {
     void *k_pages, *v_pages;
     float *k_scale, *v_scale;
@@ -552,27 +552,29 @@ qd_status qd_rope_plan(double theta, int rot_dim, qd_rope_scaling scaling, doubl
  * int32 [n_tokens]), the others copied.  ADJACENT pairs (2i, 2i + 1), HALF (i, i + rot_dim/2).
  * turns: device uint64 [rot_dim/2], with magnitude from qd_rope_plan (any finite magnitude).  out
  * may be x with the same stride.  A row with pos[t] < 0 is not written.  cos and sin are the exact
- * ones times magnitude rounded to f32 (up to one in 2^17 the neighbouring f32 value); a rotated
- * value x0 c - x1 s (x0 s + x1 c) is off by 2^-24 of itself and of |x1 s| (|x1 c|) at most.  head_dim and rot_dim multiples of 8, rot_dim <= head_dim <= 1024;
- * strides multiples of 4, at least n_heads*head_dim; 1 <= n_tokens <= QD_MAX_GEMM_TOKENS. */
+ * ones times magnitude rounded to f32 (about one in 2^23 the neighbouring f32 value); a rotated
+ * value x0 c - x1 s (x0 s + x1 c) is off by 2^-24 of itself and of |x1 s| (|x1 c|) at most.
+ * head_dim and rot_dim multiples of 8, rot_dim <= head_dim <= 1024; strides multiples of 4, at least
+ * n_heads*head_dim; 1 <= n_tokens <= QD_MAX_GEMM_TOKENS. */
 qd_status qd_rope_tokens(const float* x, int64_t x_stride, float* out, int64_t out_stride, int n_tokens, int n_heads,
                          int head_dim, int rot_dim, const int32_t* pos, qd_rope_pairing pairing, const uint64_t* turns,
                          double magnitude, qd_stream_t stream);
 
 /* Append packed rows.  q, k, v: f32 rows of n_heads (n_kv_heads) heads at t*token_stride (e.g.
  * three parts of one fused projection).  q rotated to q_out (f32 [n_tokens][n_heads][head_dim];
- * q NULL: no queries, q_out is not looked at) as by qd_rope_tokens; k, rotated by the same cos and sin
- * and rounded once to f32, and v go to the sequence's pages.  For each block of QD_KV_BLOCK positions and head: scale = max(scale of the
- * positions that the block held before, largest new magnitude / top), top 127 or 448; codes =
- * value / scale to the nearest (ties away from zero for I8, to even for E4M3); where the scale
- * grows, the codes held before become (code * old scale) / new scale to the nearest.  All of
- * this in f32, each operation rounded once.  A block whose first position is appended starts anew,
- * whatever its page held.  A new value that is not finite makes the scale of its block NaN,
- * and its values with it, until the block starts anew.  A sequence with pos[b] outside [0,
- * max_pages*page_tokens] is not touched, nor its rows of q_out; positions behind the last page are
- * not stored (their q is rotated).  A block that is appended to may belong to one sequence only.
- * The same call again with the same pos stores the same values.  token_stride a multiple of 4, at
- * least the widest of the three; 1 <= n_tokens <= QD_MAX_GEMM_TOKENS, 1 <= n_seqs <= max_seqs. */
+ * q NULL: no queries, q_out is not looked at) as by qd_rope_tokens; k, rotated by the same cos and
+ * sin to the nearest f32 (about one in 2^24 the neighbouring value), and v go to the sequence's pages.
+ * For each block of QD_KV_BLOCK positions and head: scale = max(scale of the positions that the block
+ * held before, largest new magnitude / top), top 127 or 448; codes = value / scale to the nearest
+ * (ties away from zero for I8, to even for E4M3); where the scale grows, the codes held before become
+ * (code * old scale) / new scale to the nearest.  All of this in f32, each operation rounded once.  A
+ * block whose first position is appended starts anew, whatever its page held.  A new value that is
+ * not finite makes the scale of its block NaN, and its values with it, until the block starts anew.
+ * A sequence with pos[b] outside [0, max_pages*page_tokens] is not touched, nor its rows of q_out;
+ * positions behind the last page are not stored (their q is rotated).  A block that is appended to may
+ * belong to one sequence only.  The same call again with the same pos stores the same values.
+ * token_stride a multiple of 4, at least the widest of the three; 1 <= n_tokens <=
+ * QD_MAX_GEMM_TOKENS, 1 <= n_seqs <= max_seqs. */
 qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k, const float* v, int64_t token_stride,
                           float* q_out, int n_heads, int n_tokens, const int32_t* row_start, const int32_t* pos,
                           int n_seqs, int rot_dim, qd_rope_pairing pairing, const uint64_t* turns, double magnitude,
@@ -587,7 +589,8 @@ qd_status qd_paged_append(const qd_paged_kv* kv, const float* q, const float* k,
  * the sequence's last position, but for the scale of the block that holds it, nor, but for rounding, on
  * what they hold behind a row's.  A q that is not finite, or not as q * scale * log2 e, gives NaN in its
  * own row and head alone; a block with a NaN scale gives NaN to the rows that see a position of it,
- * and to no other; an infinite scale (an append stores none) reaches no other rows either.  Results are the same bits on every run.
+ * and to no other; an infinite scale (an append stores none) reaches no other rows either.  Results
+ * are the same bits on every run.
  * Arithmetic: codes enter the products exactly, queries and weights times scales in two parts (22 bits
  * of each from 2^-15 of the largest of its row on, 2^-38 of that below, whatever the scales of other
  * blocks are; fewer where every scale that a row sees is under 2^-100; weights under 2^-126 of the row's

@@ -15,8 +15,8 @@ using paged::Cache;
 // The angle of a pair at a position is position * turns modulo 2^64, in units of 2^-64 turns: exact
 // at any position, in one integer product.  Quadrant and remainder come off in integers too; sine
 // and cosine of the remainder (at most pi/4) are the Taylor series in pairs of f32 (unevaluated
-// sums h + l, about 2^-45), so that after the last rounding they are the correctly rounded f32
-// values but for one in 2^20.  That costs 300 f32 operations a pair of angles; FP64 units, of
+// sums h + l; off by 2^-43.9 and 2^-46.1 of themselves at most, over 24 million angles), so that after
+// the last rounding they are the correctly rounded f32 values but for about one in 2^23.  That costs 300 f32 operations a pair of angles; FP64 units, of
 // which this GPU has few, would take longer, and f32 alone is 2^-23 off, which moves a code of the
 // cache in one of 10^5 and makes it depend on the side that computes it.
 struct FF {
@@ -87,8 +87,10 @@ __device__ __noinline__ float2 cos_sin(uint64_t turns, int pos, FF magnitude) {
   }
 }
 
-// a c - b s: rounded once where EXACT (both products in two parts; what the codes of keys are decided
-// by), else to 2^-24 of |b s| and of the result.
+// a c - b s: where EXACT (both products in two parts; what the codes of keys are decided by) the rounded value but for
+// the neighbour of about one in 2^24 (2 of 60 million, 20 of them with terms that cancel to 2^-25), else to 2^-24 of
+// |b s| and of the result.  Queries and qd_rope_tokens are not EXACT: their values enter f32 arithmetic, and one product
+// and a fused step take 8000 rows of 40 heads of 128 from 60 to 55 us (error against 64 bits 3.1e-8, rounded once 2.5e-8).
 template <bool EXACT>
 __device__ __forceinline__ float det(float a, float c, float b, float s) {
   if constexpr (!EXACT) return __fmaf_rn(a, c, -__fmul_rn(b, s));

@@ -160,6 +160,8 @@ __device__ __forceinline__ int tokens_of(const AttnArgs& a, int b, int& row0, in
   return t;
 }
 
+// Every block of rows walks what any row of its sequence sees, and leaves out the products of what its own do not (8/1
+// heads of 64, 1000 tokens, a window of 16: 21 us).
 struct Walk {  // of one sequence
   int first_tile, nt, rb, len;
 };
@@ -281,12 +283,14 @@ __device__ __forceinline__ int64_t row_of(const AttnArgs& a, int hd, int64_t str
 // 16, and its outputs are neighbouring dims; nothing is transposed through shared memory, and two
 // values of a dim are paired by byte permutations on their way to binary16 (2.5 instructions a pair of keys,
 // 3 of values).
-// What bounds it: instructions.  A warp needs about 420 for 4 KB of the cache (176 of them turn codes into
-// operands, 32 are products), of which an SM issues 1.8 to 2.2 a cycle, where HBM brings 4 KB in 174 cycles.  100
-// sequences of 32/8 heads of 128, 4000 positions on average: 166 us (floor 123); 131000 positions of one: 58 (40);
-// 16 of 32/32 heads of 64, 2000 on average: 40 (20, and 8 of the starts and the join).  Against: tiles of 4 KB at
-// head dimension 128 178 us instead of 166, tiles of 8 KB at 64 46 instead of 40; four CTAs of 128 registers a
-// thread 253 (they spill) and 44; CTAs of two warps 227 and 39; q's fragments in registers 171 and 38;
+// What bounds it: the dependent chain of a tile (copies, scores, maximum, weights, products), which the 8 or 12 warps
+// that an SM's registers hold do not hide.  A warp takes about 480 instructions for 4 KB of the cache (176 turn codes into
+// operands, 32 are products; starts and joins among them), of which an SM issues 1.5 to 2 of 4 a cycle, where HBM brings
+// 4 KB in 174 cycles.  The kernels of head dimension 128 spill (76 to 92 bytes a thread with 8 rows, 164 to 212 with 16).
+// 100 sequences of 32/8 heads of 128, 4000 positions on average: 165 us (floor 123); 131000 positions of one: 59 (40);
+// 16 of 32/32 heads of 64, 2000 on average: 40 (20, and 8 of the starts and the join).  Against, at the time: tiles of 4 KB
+// at head dimension 128 178 us instead of 166, tiles of 8 KB at 64 46 instead of 40; four CTAs of 128 registers a
+// thread 253 (more spills) and 44; CTAs of two warps 227 and 39; q's fragments in registers 171 and 38;
 // o = p v instead of its transpose, where both parts of a weight have accumulators of their own, 171 and 41;
 // kStart 3 166 and 40.5, 5 169 and 43.
 template <int HD, bool R16>
@@ -826,11 +830,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
 // SM fill what is left.  The blocks of all walks, as long as each block's last row sees, are listed by a kernel
 // of one CTA and taken whole or cut evenly over the CTAs, in heads, sequences and blocks in turn.
 // What bounds it: the latency of a tile's chain between its three barriers (1.3 of 4 instructions a cycle; a tile
-// of 128 rows takes a CTA 3.5 us alone on an SM).  8 heads of 128, 1024 x 4 rows, 2040 positions: 136 us, of which the
-// list 5 and the join that finds nothing 3 (floor 13: the products once); in copies without the conversions 99 us,
-// without the products too 76, with a quarter of the sums too 67.  Against: walks cut 151 us, 17 of them the join; the
-// next loads before the proxy fences 144; four threads to a row, of 64 registers, 167; the values' codes through
-// shared memory 143; blocks of 16 rows 277.
+// of 128 rows takes a CTA 3.5 us alone on an SM; 104 bytes a thread are spilled at head dimension 128).  8 heads of 128,
+// 1024 x 4 rows, 2040 positions: 137 to 141 us, of which the list 5 and the join that finds nothing 3 (floor 13: the
+// products once); in copies, of 136 us then, without the conversions 99 us, without the products too 76, with a quarter of
+// the sums too 67.  Against the same 136: walks cut 151 us, 17 of them the join; the next loads before the proxy fences 144;
+// four threads to a row, of 64 registers, 167; the values' codes through shared memory 143; blocks of 16 rows 277.  A
+// row's units of its own cost 5 us with the bounds of the block's rows in registers, none with them in the segment.
 constexpr int kManyThreads = 256, kManyTile = 64, kManyBm = 128;
 // 8 heads of 128, 16000 positions, few against many rows: 16 sequences of 32 rows 290 and 431 us, 8 of 64 288 and
 // 246, 8 of 80 346 and 251, 8 of 120 547 and 262.
@@ -1472,7 +1477,9 @@ inline bool attn_shape_ok(const qd_paged_kv* kv, int n_heads, int n_tokens, int 
          n_heads / kv->n_kv_heads <= 16 && n_tokens >= 1 && n_tokens <= QD_MAX_GEMM_TOKENS;
 }
 // Blocks of 16 rows where sequences can have more than 8: against blocks of 8, 20 sequences of 3 x 4 rows, 8 heads of 128,
-// 3000 positions 50 and 62 us, 8 of 8 x 4 rows of 6000 69 and 83, 4 of 8 x 3 rows, 3 heads of 64, 3000 13.6 and 12.2.
+// 3000 positions 50 and 62 us, 8 of 8 x 4 rows of 6000 69 and 83; the other way round 4 of 8 x 3 rows, 3 heads of 64, 3000
+// 13.6 and 12.2.  All sequences of a call have the same blocks, so that one of two tokens among 99 single ones of 32/8
+// heads takes the call from 83 to 109 us.
 inline bool rows16(int group, int n_tokens, int n_seqs) { return group > 8 || n_tokens > n_seqs; }
 
 // CTAs of a call: what fits the device at once, and no more than there can be units for.
@@ -1512,6 +1519,11 @@ qd_status launch_few(AttnArgs a, cudaStream_t st) {
 //   3 heads, 4 ragged sequences of 300 x 3 rows at most, 1500 positions (1.0e6)       31 41
 //   8 heads, 64 x 4 rows, 32700 positions (4.3e6)                                    156 91
 //   8 heads of 128, 1024 x 4 rows, 2040 positions (6.2e6)                            277 136
+// These tables are as wide as the longest sequence.  The host knows neither the lengths nor what one sequence has of the
+// rows, so that a wider table brings this kernel to shorter walks (20 tokens of one sequence at 1000, 32/8 heads of 128:
+// 16 us with room for 2048 positions, 31 for 131072; 7 sequences of 45 rows at most, a window of 1000: 13 for 4032, 34 for
+// 120000), and a batch without a sequence of so many rows pays for a list, a kernel and a join that find nothing (100
+// of 4 tokens 100 and 110 us; 99 single tokens and one of two 109 and 119).
 // The units of a head must fit an int.
 constexpr int64_t kManyWork = 2000000;
 inline bool has_many(int n_kv, int group, int n_tokens, int n_seqs, int capacity) {
