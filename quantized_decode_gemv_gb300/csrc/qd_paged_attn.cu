@@ -100,19 +100,24 @@ __device__ __forceinline__ int scale_exp(uint32_t abs_bits) {
   return min(max((int)(abs_bits >> 23) - 127, -100), 127) - 14;
 }
 
-// o is held in units of 2^ev of its row, ev the floor of n - m: n the running maximum of score + log2 scale over the
-// positions that the row sees, m that of the scores, so that the largest weight times scale is 2^14 to 2^15.1 times
-// the unit, whatever a block weighs that the row does not see, or that has a large scale and no weight.
+// o is held in units of 2^ev of its row, ev the floor of the running maximum of score + log2 scale over the positions
+// that the row sees, less that of the scores, so that the largest weight times scale is 2^14 to 2^15.1 times the unit,
+// whatever a block weighs that the row does not see, or that has a large scale and no weight.
 __device__ __forceinline__ float log2_scale(float s) {  // log2 or up to 0.09 less; finite for any s
   return fmaf((float)__float_as_int(s), 0x1p-23f, -127.f);
 }
-// The next ev; back: what o in the old one is multiplied by.
-__device__ __forceinline__ void next_unit(float n, float m, int& ev, float& back, float& down) {
-  const int en = min(max(__float2int_rd(n - m), -100), 126);
+// The next ev for that difference; back: what o in the old unit is multiplied by.
+__device__ __forceinline__ void next_unit(float n, int& ev, float& back, float& down) {
+  const int en = min(max(__float2int_rd(n), -100), 126);
   back = pow2(max(min(ev - en, 126), -126));
   down = pow2(-en);
   ev = en;
 }
+// Scores from here on have steps of 2^-2 and more.  A fused product and difference would leave the rounding of the maximum
+// in the largest weight, which is to end at 2^14, and so would the sum of the maximum and 14: both are rounded alike, and
+// the largest weight is 1.
+constexpr float kHuge = 0x1p22f;
+__device__ __forceinline__ float bias_of(float m, bool huge) { return huge ? -m : kBias - m; }
 // A share of a row, as it is joined with others: the maximum score m, the sum l of the weights, and o scaled by
 // down_of(l), so that it is no larger than the row's largest value (where these are near f32's largest, their sum has
 // no place in it).  With weights ex2(m - the largest m), o of several is sum of w up_of(l) o, times down_of(sum of w l).
@@ -562,28 +567,34 @@ __global__ void __launch_bounds__(Few<HD, R16>::kW * 32, Few<HD, R16>::kCtas) k_
 #pragma unroll
           for (int k = 0; k < NB; ++k) f[k] = 1.f;
         }
-        float mx = -INFINITY, my = -INFINITY;
+        float mk[NB], mn = m[i];  // the blocks' maxima
 #pragma unroll
         for (int k = 0; k < NB; ++k) {  // scales are not negative
-          const float mk =
-              f[k] * fmaxf(fmaxf(s[2 * k][2 * i], s[2 * k][2 * i + 1]), fmaxf(s[2 * k + 1][2 * i], s[2 * k + 1][2 * i + 1]));
-          mx = fmaxf(mx, mk);
-          my = fmaxf(my, mk + lgv[k]);
+          mk[k] = f[k] * fmaxf(fmaxf(s[2 * k][2 * i], s[2 * k][2 * i + 1]), fmaxf(s[2 * k + 1][2 * i], s[2 * k + 1][2 * i + 1]));
+          mk[k] = fmaxf(mk[k], __shfl_xor_sync(0xffffffffu, mk[k], 1));
+          mk[k] = fmaxf(mk[k], __shfl_xor_sync(0xffffffffu, mk[k], 2));
+          mn = fmaxf(mn, mk[k]);
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, o));
-        }
-        const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn;
+        const float mu = mn == -INFINITY ? 0.f : mn;
         corr[i] = ex2(m[i] - mu);
+        n[i] += m[i] - mu;
         m[i] = mn;
-        n[i] = fmaxf(n[i], my);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) n[i] = fmaxf(n[i], (mk[k] - mu) + lgv[k]);
         float back, down, vu[NB];
-        next_unit(n[i], mu, ev[i], back, down);
+        next_unit(n[i], ev[i], back, down);
+        const bool huge = fabsf(mu) >= kHuge;
+        if (huge) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[j][2 * i + e] *= f[j / 2];
+#pragma unroll
+          for (int k = 0; k < NB; ++k) f[k] = 1.f;
+        }
 #pragma unroll
         for (int k = 0; k < NB; ++k) vu[k] = in_units(vs[k], down);
-        const float bias = kBias - mu;
+        const float bias = bias_of(mu, huge);
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -988,7 +999,7 @@ template <int HD>
 struct Many {
   uint4 q[2][kManyBm * HD / 8];    // hi, lo
   uint4 k[kManyTile * HD / 8], v[kManyTile * HD / 8];
-  float scales[2][3][4];           // of every second tile's blocks: keys, values, log2_scale of those
+  __align__(16) float scales[2][3][4];  // of every second tile's blocks: keys, values, log2_scale of those
   uint32_t place[2][4];            // of every second tile: its blocks in the cache, kNoPage
   float2 ex[2][kManyBm];           // what a row's threads tell each other
   unsigned long long mbar[2];      // scores, products
@@ -1281,10 +1292,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
       const int hi = lim - base - 32 * half, lo = a.window > 0 ? hi - a.window + 1 : 0;  // seen: lo <= column <= hi
       const float f[2] = {rs * sm.scales[it & 1][0][2 * half], rs * sm.scales[it & 1][0][2 * half + 1]};
       if (warp_live) {
-        float mx = -INFINITY, my = -INFINITY;
+        float tops[2];  // of the blocks
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float s[16], top = -INFINITY;  // of the block
+          float s[16], top = -INFINITY;
           tmem_ld16(cols + 16 * c, s);
           if (edge) {
 #pragma unroll
@@ -1299,32 +1310,40 @@ __global__ void __launch_bounds__(kManyThreads, 2) k_paged_many(ManyArgs ma) {
             }
             top = fmaxf(mc[0], mc[1]) * f[c];  // scales are not negative
           }
-          mx = fmaxf(mx, top);
-          my = fmaxf(my, top + sm.scales[it & 1][2][2 * half + c]);
+          tops[c] = top;
         }
-        sm.ex[half][lrow] = make_float2(mx, my);
+        sm.ex[half][lrow] = make_float2(tops[0], tops[1]);
       }
       __syncthreads();  // the maximum of the row's other half
       float corr = 1.f;
       if (warp_live) {
         const float2 e0 = sm.ex[0][lrow], e1 = sm.ex[1][lrow];
-        const float mn = fmaxf(m, fmaxf(e0.x, e1.x)), mu = mn == -INFINITY ? 0.f : mn;
+        const float mn = fmaxf(m, fmaxf(fmaxf(e0.x, e0.y), fmaxf(e1.x, e1.y))), mu = mn == -INFINITY ? 0.f : mn;
         corr = ex2(m - mu);
+        n += m - mu;
         m = mn;
-        const float bias = kBias - mu;
-        n = fmaxf(n, fmaxf(e0.y, e1.y));
+        const float4 lgv = *reinterpret_cast<const float4*>(sm.scales[it & 1][2]);
+        n = fmaxf(n, fmaxf(fmaxf((e0.x - mu) + lgv.x, (e0.y - mu) + lgv.y), fmaxf((e1.x - mu) + lgv.z, (e1.y - mu) + lgv.w)));
         float back, down;
-        next_unit(n, mu, ev, back, down);
+        next_unit(n, ev, back, down);
+        const bool huge = fabsf(mu) >= kHuge;
+        const float bias = bias_of(mu, huge);
         float sum = 0.f, sum1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const float vs = in_units(sm.scales[it & 1][1][2 * half + c], down);
           float s[16];
           tmem_ld16(cols + 16 * c, s);
+          float fc = f[c];
+          if (huge) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[j] *= fc;
+            fc = 1.f;
+          }
           uint32_t ph[8], pl[8];
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            float p0 = ex2(fmaf(s[j], f[c], bias)), p1 = ex2(fmaf(s[j + 1], f[c], bias));
+            float p0 = ex2(fmaf(s[j], fc, bias)), p1 = ex2(fmaf(s[j + 1], fc, bias));
             float y0 = p0 * vs, y1 = p1 * vs;
             if (edge) {  // whatever the scales
               const bool in0 = 16 * c + j <= hi && 16 * c + j >= lo, in1 = 16 * c + j + 1 <= hi && 16 * c + j + 1 >= lo;

@@ -467,6 +467,38 @@ def test_attention_of_values_near_the_ends_of_f32(qd, fmt, heads, hk, hd, tokens
     _check(got, *attn_all(c, q, start, pos, heads // hk, 0.1, window))
 
 
+@pytest.mark.parametrize("size", [1e5, 1e8, 1e12])
+@pytest.mark.parametrize("heads,hk,hd,tokens,total,rows,window,room", UNEQUAL)
+def test_attention_of_huge_scores(qd, heads, hk, hd, tokens, total, rows, window, room, size):
+    """Scores so large that one position takes all the weight: its values come out.  A score is off by (hd + 16) 2^-24 of
+    sum |q k| (attn_ref); rows whose two largest scores are nearer than four times that say nothing but that they are
+    finite.  The weight is 1 in two parts and a sum, 2^-20 with room."""
+    rng = np.random.default_rng([31, heads, hd, tokens, total[0]])
+    c = Cache(rng, len(total), hk, hd, tokens, total, "i8", width=room and room // tokens)
+    kv, _ = _handle(qd, c)
+    start, pos = _starts(rows), np.array(total, np.int32) - np.array(rows, np.int32)
+    q = (rng.normal(size=(int(start[-1]), heads, hd)) * size).astype(np.float32)
+    out = _attn(qd, kv, dev(q), dev(start), dev(pos), heads, 0.5, window)
+    assert out.isfinite().all()
+    got, clear = out.cpu().numpy(), 0
+    for b in range(len(pos)):
+        for h in range(heads):
+            ck, sk, cv, sv = c.values(b, h // (heads // hk), int(pos[b]) + rows[b])
+            for i in range(rows[b]):
+                r, p = start[b] + i, int(pos[b]) + i
+                lo = max(0, p - window + 1) if window else 0
+                x = q[r, h].astype(np.float64)
+                s = (ck[lo : p + 1] @ x) * sk[lo : p + 1] * 0.5
+                off = (hd + 16) * 2.0**-24 * ((np.abs(ck[lo : p + 1]) @ np.abs(x)) * sk[lo : p + 1] * 0.5).max()
+                top = int(s.argmax())
+                if len(s) > 1 and s[top] - np.delete(s, top).max() < 4 * off + 40:
+                    continue
+                clear += 1
+                want = cv[lo + top] * sv[lo + top]
+                assert np.all(np.abs(got[r, h] - want) <= 2.0**-20 * np.abs(want)), (b, h, i)
+    assert clear >= len(q) * heads // 2
+
+
 @pytest.mark.parametrize("name", ["ks", "vs"])
 @pytest.mark.parametrize("hd,rows,window,room", [(64, 1, 20, None), (128, 40, 0, None), (64, 40, 20, None), (64, 300, 0, WIDE),
                                                  (128, 300, 20, WIDE)])
