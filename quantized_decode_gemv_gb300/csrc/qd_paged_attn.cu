@@ -292,7 +292,7 @@ __device__ __forceinline__ int64_t row_of(const AttnArgs& a, int hd, int64_t str
 // that an SM's registers hold do not hide.  A warp takes about 480 instructions for 4 KB of the cache (176 turn codes into
 // operands, 32 are products; starts and joins among them), of which an SM issues 1.5 to 2 of 4 a cycle, where HBM brings
 // 4 KB in 174 cycles.  The kernels of head dimension 128 spill (76 to 92 bytes a thread with 8 rows, 164 to 212 with 16).
-// 100 sequences of 32/8 heads of 128, 4000 positions on average: 165 us (floor 123); 131000 positions of one: 59 (40);
+// 100 sequences of 32/8 heads of 128, 4000 positions on average: 166 us (floor 123); 131000 positions of one: 59 (40);
 // 16 of 32/32 heads of 64, 2000 on average: 40 (20, and 8 of the starts and the join).  Against, at the time: tiles of 4 KB
 // at head dimension 128 178 us instead of 166, tiles of 8 KB at 64 46 instead of 40; four CTAs of 128 registers a
 // thread 253 (more spills) and 44; CTAs of two warps 227 and 39; q's fragments in registers 171 and 38;
@@ -841,8 +841,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(AttnArgs a) {
 // SM fill what is left.  The blocks of all walks, as long as each block's last row sees, are listed by a kernel
 // of one CTA and taken whole or cut evenly over the CTAs, in heads, sequences and blocks in turn.
 // What bounds it: the latency of a tile's chain between its three barriers (1.3 of 4 instructions a cycle; a tile
-// of 128 rows takes a CTA 3.5 us alone on an SM; 104 bytes a thread are spilled at head dimension 128).  8 heads of 128,
-// 1024 x 4 rows, 2040 positions: 137 to 141 us, of which the list 5 and the join that finds nothing 3 (floor 13: the
+// of 128 rows takes a CTA 3.5 us alone on an SM; 112 bytes a thread are spilled at head dimension 128).  8 heads of 128,
+// 1024 x 4 rows, 2040 positions: 137 to 142 us, of which the list 5 and the join that finds nothing 3 (floor 13: the
 // products once); in copies, of 136 us then, without the conversions 99 us, without the products too 76, with a quarter of
 // the sums too 67.  Against the same 136: walks cut 151 us, 17 of them the join; the next loads before the proxy fences 144;
 // four threads to a row, of 64 registers, 167; the values' codes through shared memory 143; blocks of 16 rows 277.  A
